@@ -26,6 +26,13 @@ Entry points (same names as the C ABI, minus the ``bsa_`` prefix):
 * :func:`set_wait_limit` (hang detection), :func:`debug_stall_next_forward`
   (its test hook)
 * :func:`block_sparse_attention`  convenience: mask + forward in one call
+* :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`  norm of query and key
+  heads and position rotation on the way from a projection to the attention,
+  and its gradients; :func:`rope_inv_freq` makes the frequencies
+* :func:`cache_append`, :func:`tree_attention`, :func:`cache_accept`  serving
+  over a paged cache: write new tokens, attend with one or a tree of drafted
+  tokens per sequence, keep the accepted ones
+* :func:`cache_resize`, :func:`cache_fork`, :func:`cache_compact`  its pages
 """
 
 from ._binding import (  # noqa: F401
@@ -55,4 +62,17 @@ from ._binding import (  # noqa: F401
     set_wait_limit,
     topk_blocks,
     validate_csr,
+)
+from .paged import (  # noqa: F401
+    cache_accept,
+    cache_append,
+    cache_compact,
+    cache_fork,
+    cache_resize,
+    tree_attention,
+)
+from .rope import (  # noqa: F401
+    qk_norm_rope,
+    qk_norm_rope_backward,
+    rope_inv_freq,
 )

@@ -47,6 +47,43 @@ class _ForwardArgs(ctypes.Structure):
                 ("causal", ctypes.c_int32), ("out_fp32", ctypes.c_int32)]
 
 
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_length", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
+_Stride3 = ctypes.c_int64 * 3
+
+
+class _NormRopeArgs(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_int32) for x in ("B", "N", "Hq", "Hkv", "D", "rotary_dim", "kv_repeat", "interleaved")]
+    _fields_ += [("eps", ctypes.c_float), ("gain", ctypes.c_float)]
+    _fields_ += [(x, ctypes.c_void_p) for x in ("q", "k", "v")]
+    _fields_ += [(x, _Stride3) for x in ("q_stride", "k_stride", "v_stride")]
+    _fields_ += [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("position_stride", ctypes.c_int64),
+                 ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class _NormRopeGrads(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_void_p) for x in ("dq", "dk", "dv", "q", "k", "v")]
+    _fields_ += [(x, _Stride3) for x in ("q_stride", "k_stride", "v_stride")]
+    _fields_ += [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class _PageCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+    _fields_ += [(x, ctypes.c_int32) for x in ("layers", "n_pages", "Hkv", "page", "D")]
+    _fields_ += [("page_table", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class _TreeArgs(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_int32) for x in ("B", "T", "Hq")]
+    _fields_ += [(x, ctypes.c_void_p) for x in ("q", "context_len", "draft_len", "tree_mask", "row_ptr", "col_idx")]
+    _fields_ += [("col_capacity", ctypes.c_int64), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                 ("scale", ctypes.c_float)]
+
+
 MAX_WINDOWS = 4
 
 
@@ -106,6 +143,21 @@ def lib():
                 "bsa_debug_stall_next_forward": ([i32], ctypes.c_int),
                 "bsa_forward_noalloc": ([PS, P, P, P, P, P, P, P, ctypes.c_float, i32, P], ctypes.c_int),
                 "bsa_release_workspace": ([], None),
+                "bsa_rope_inv_freq": ([ctypes.POINTER(_RopeSpec), P], ctypes.c_int),
+                "bsa_qk_norm_rope": ([ctypes.POINTER(_NormRopeArgs), P, P, P, P], ctypes.c_int),
+                "bsa_qk_norm_rope_backward_workspace": ([i32], i64),
+                "bsa_qk_norm_rope_backward": ([ctypes.POINTER(_NormRopeArgs), ctypes.POINTER(_NormRopeGrads), P, i64,
+                                               P], ctypes.c_int),
+                "bsa_cache_append": ([ctypes.POINTER(_NormRopeArgs), ctypes.POINTER(_PageCache), P, P, P, P],
+                                     ctypes.c_int),
+                "bsa_tree_attention_workspace": ([i32, i32, i32, i32, i32], i64),
+                "bsa_tree_attention": ([ctypes.POINTER(_TreeArgs), ctypes.POINTER(_PageCache), P, i64, P],
+                                       ctypes.c_int),
+                "bsa_cache_accept": ([ctypes.POINTER(_PageCache), P, P, P, i32, P, P], ctypes.c_int),
+                "bsa_cache_pages_workspace": ([i32, i32, i32], i64),
+                "bsa_cache_resize": ([ctypes.POINTER(_PageCache), P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_fork": ([ctypes.POINTER(_PageCache), P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_compact": ([ctypes.POINTER(_PageCache), P, P, P, i64, P], ctypes.c_int),
             }
             for name, (args, res) in sigs.items():
                 f = getattr(L, name)
@@ -124,6 +176,44 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+class _NoScope:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SCOPE = _NoScope()
+
+
+def _scope(device: torch.device, stream):
+    """Context in which a call on tensors of `device` allocates and launches:
+    the tensors' device, and `stream` (default: that device's current one), so
+    that what the call allocates belongs to the stream that uses it."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return _NO_SCOPE
+
+
+def _same_device(first: torch.Tensor, *ts: Optional[torch.Tensor]) -> torch.device:
+    if not first.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    d = first.device
+    for t in ts:
+        if t is not None and t.device != d:
+            raise ValueError("tensors on different devices: %s and %s" % (d, t.device))
+    return d
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -240,6 +240,48 @@ int to_pattern_set(const bsa_pattern_ex* pats, int32_t n_patterns, const int32_t
 namespace bsa {
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 int32_t take_forward_stall() { return g_stall_next.exchange(-1); }
+
+int device_context(int32_t** err, int* sm_count) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    DevState* d;
+    int st = dev_state(&d);
+    if (st != BSA_OK) return st;
+    if ((st = check_arch(d)) != BSA_OK) return st;
+    *err = d->err;
+    *sm_count = d->sm_count;
+    return BSA_OK;
+}
+
+int check_page_cache(const bsa_page_cache* c) {
+    if (!c || c->layers <= 0 || c->n_pages <= 0 || c->Hkv <= 0 || c->page <= 0 || c->D <= 0 || c->n_seqs <= 0 ||
+        c->max_pages <= 0)
+        return BSA_ERR_INVALID_ARG;
+    if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4))
+        return BSA_ERR_INVALID_ARG;
+    if ((c->D != 64 && c->D != 128) || (c->page != 64 && c->page != 128)) return BSA_ERR_UNSUPPORTED;
+    // rows of one layer, and slots of one sequence, fit an int
+    const int64_t heads = (int64_t)c->n_pages * c->Hkv;
+    if (heads > INT32_MAX / c->page || c->max_pages > INT32_MAX / c->page) return BSA_ERR_INVALID_ARG;
+    return BSA_OK;
+}
+
+int encode_rows_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows) {
+    return make_map(m, base, rows, D, box_rows);
+}
+
+int encode_token_rows_bf16(CUtensorMap* m, const void* base, uint64_t tokens, uint64_t heads, uint64_t D,
+                           uint32_t box_heads, uint32_t box_tokens) {
+    auto fn = encode_fn();
+    if (!fn) return BSA_ERR_CUDA;
+    cuuint64_t dims[3] = {D, heads, tokens};
+    cuuint64_t strides[2] = {D * 2, heads * D * 2};
+    cuuint32_t box[3] = {64, box_heads, box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BSA_OK : BSA_ERR_CUDA;
+}
 }  // namespace bsa
 
 extern "C" {

@@ -6,7 +6,21 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "bsa.h"
+
 namespace bsa {
+
+// The current device's error word and SM count (BSA_ERR_UNSUPPORTED on a
+// device the kernels are not built for).  Allocates the word on first use.
+int device_context(int32_t** err, int* sm_count);
+// Sizes, alignment and the 2^31 row limit of a paged cache's pools (the page
+// table is checked by the calls that read one).
+int check_page_cache(const bsa_page_cache* c);
+// 2-D bf16 view [rows, D] in boxes of 64 columns x box_rows rows, 128-byte swizzle.
+int encode_rows_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows);
+// 3-D bf16 view [tokens, heads, D] in boxes of 64 columns x box_heads x box_tokens, 128-byte swizzle.
+int encode_token_rows_bf16(CUtensorMap* m, const void* base, uint64_t tokens, uint64_t heads, uint64_t D,
+                           uint32_t box_heads, uint32_t box_tokens);
 
 struct FwdParams {
     const int32_t* row_ptr;

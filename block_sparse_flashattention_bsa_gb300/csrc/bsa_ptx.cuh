@@ -17,6 +17,8 @@ constexpr int ERR_BAD_COL = 2;
 constexpr int ERR_BAD_ROW = 4;
 constexpr int ERR_LAUNCH = 8;  // a kernel found its launch unusable (e.g. misaligned shared memory)
 constexpr int ERR_CAPACITY = 16;  // a buffer sized by the caller was smaller than the data (entries dropped)
+constexpr int ERR_BAD_PAGE = 32;  // a page-table entry, slot or sequence id out of range (access skipped)
+constexpr int ERR_PAGES = 64;     // a page request was refused (pool empty, bad or repeated sequence)
 
 // A wait that has not completed after this long is treated as a hang: the
 // kernel records ERR_TIMEOUT and returns instead of spinning forever.  The
@@ -111,6 +113,14 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
         ::"r"(smem_u32(smem_dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+// 3-D tiled load global -> shared, completion counted in bytes on `bar`.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                                            int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(smem_dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 

@@ -1,0 +1,665 @@
+// bsa_rope.cu -- what stands between a projection and the attention: the RMS
+// norm of every query and key head and the position rotation in one pass,
+// token-major rows in, head-major rows (or rows of a paged cache) out, and
+// the gradients of the head-major form.
+//
+// Mathematics, for a head row x of D values at position t:
+//   y = x * r * w,  r = 1 / sqrt(mean(x^2) + eps)          (no weight: y = x)
+//   a pair (y_a, y_b) of the first rotary_dim values, with its frequency f:
+//   z_a = gain * (y_a cos(t f) - y_b sin(t f)),  z_b = gain * (y_b cos(t f) + y_a sin(t f))
+// The angle is kept in turns: f / (2 pi) as a 64-bit fixed-point fraction,
+// multiplied by the position modulo 2^64 (integer arithmetic, so no range
+// reduction and no loss at far positions: the product is exact and the
+// fraction is good to 2^-53 of a turn per position); its top 32 bits give the
+// angle in [-pi, pi), where sin.approx / cos.approx are within 2^-20 of the
+// true values.  That is 2^11 times finer than the bf16 rounding of the result.
+//
+// Gradients, with dy the rotated-back gradient (by -t f, times gain), g = dy * w:
+//   dx = r g - x r^3 mean(g x),   dw = sum over rows of dy * x * r
+// (a repeated key or value head first sums the gradients of its copies, fp32).
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "bsa.h"
+#include "bsa_internal.h"
+#include "bsa_ptx.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kMaxPairs = 64;  // rotary_dim / 2 <= 64
+
+// Rows of one kind (q, k or v): token-major side and its head-major side.
+struct RopeSide {
+    const void* x;              // token-major rows
+    int64_t sb, sn, sh;         // its strides in elements
+    void* out;                  // forward: head-major rows (append: q only, token-major rows)
+    const void* dz;             // backward: head-major gradients
+    void* dx;                   // backward: token-major gradients
+    int64_t gb, gn, gh;         // strides of dx
+    const float* w;             // norm weight or null
+    float* partial;             // backward: per-CTA sums of the weight's gradient
+    int32_t H;                  // token-major heads
+    int32_t rep;                // head-major copies of each
+    int32_t ctas;               // CTAs working on this kind
+    int32_t rotate;             // 0 for values
+};
+
+struct RopeParams {
+    RopeSide side[3];
+    const double* inv_freq;
+    const int32_t* pos;
+    int64_t pos_sb;
+    int64_t tokens;  // B * N
+    int32_t N, rd;
+    float eps, gain;
+    // append: rows of k and v go to pages
+    void *k_cache, *v_cache;
+    const int32_t *page_table, *seq_ids, *slots;
+    int32_t n_seqs, max_pages, page, n_pages;
+    int32_t* err;
+};
+
+// Fraction of a turn per position, in units of 2^-64.
+__device__ __forceinline__ unsigned long long to_turns(double f) {
+    const double t = f * 0.15915494309189533577;  // 1 / (2 pi)
+    return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// A head row is spread over LPR = D / 16 lanes, 16 values (two 16-byte
+// chunks) each, placed so that both members of every pair sit in one lane:
+// halves (i, i + rd/2): chunks s and s + rd/16; interleaved (2i, 2i + 1):
+// chunks 2s and 2s + 1.  Either way lane s owns the pairs 8s .. 8s + 7, and
+// the lanes from rd/16 on own the values that are not rotated.
+template <int D, bool IL>
+struct Lane {
+    static constexpr int LPR = D / 16;
+    int s, ca, cb;
+    bool rot;
+    __device__ Lane(int rd) {
+        s = threadIdx.x % LPR;
+        const int nr = rd / 16;
+        rot = s < nr;
+        ca = (IL || !rot) ? 2 * s : s;
+        cb = (IL || !rot) ? 2 * s + 1 : s + nr;
+    }
+};
+
+// Sum over the LPR lanes of a row (every lane gets it).
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// cos and sin of this lane's 8 pairs at position pos, times gain.
+__device__ __forceinline__ void lane_angles(const unsigned long long* turns, int s, int pos, float gain, float* cs,
+                                            float* sn) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const unsigned long long t = turns[8 * s + e] * (unsigned long long)(long long)pos;
+        const float a = (float)(int)(unsigned)(t >> 32) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+        cs[e] = __cosf(a) * gain;
+        sn[e] = __sinf(a) * gain;
+    }
+}
+
+// The lane's pairs rotated by (cs, sn): f[0..7] is chunk a, f[8..15] chunk b.
+template <bool IL>
+__device__ __forceinline__ void rotate16(float* f, const float* cs, const float* sn) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int a = IL ? 2 * e : e, b = IL ? 2 * e + 1 : e + 8;
+        const float x = f[a], y = f[b];
+        f[a] = x * cs[e] - y * sn[e];
+        f[b] = y * cs[e] + x * sn[e];
+    }
+}
+
+__device__ __forceinline__ void load_turns(const RopeParams& p, unsigned long long* turns) {
+    for (int i = threadIdx.x; i < p.rd / 2; i += kRopeThreads) turns[i] = to_turns(p.inv_freq[i]);
+    __syncthreads();
+}
+
+// Which kind this CTA works on, and its index and count among that kind's CTAs.
+__device__ __forceinline__ int cta_side(const RopeParams& p, int* idx) {
+    int b = blockIdx.x, k = 0;
+    while (k < 2 && b >= p.side[k].ctas) b -= p.side[k++].ctas;
+    *idx = b;
+    return k;
+}
+
+// One CTA item: TB = 256 / LPR consecutive tokens times U heads.  A lane
+// group takes one token and loads its U rows at once (64 bytes a lane and
+// row in flight), so the angles are computed once for U rows; neighbouring
+// lane groups take neighbouring tokens, so the head-major stores of a head
+// run over TB consecutive rows.
+template <int D, int U, bool IL, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopeParams p) {
+    constexpr int LPR = D / 16, TB = kRopeThreads / LPR;
+    __shared__ unsigned long long turns[kMaxPairs];
+    int idx;
+    const int kind = cta_side(p, &idx);
+    const RopeSide& sd = p.side[kind];
+    const Lane<D, IL> ln(p.rd);
+    load_turns(p, turns);
+    float w[16];
+    const bool norm = sd.w != nullptr;
+    if (norm) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[e] = sd.w[ln.ca * 8 + e];
+            w[8 + e] = sd.w[ln.cb * 8 + e];
+        }
+    }
+    const int hgroups = (sd.H + U - 1) / U;
+    const int64_t items = (p.tokens + TB - 1) / TB * hgroups;
+    for (int64_t it = idx; it < items; it += sd.ctas) {
+        const int hg = (int)(it % hgroups);
+        const int64_t tok = it / hgroups * TB + threadIdx.x / LPR;
+        bool live = tok < p.tokens;
+        int seq = 0;
+        if (APPEND && live) {
+            seq = p.seq_ids[tok];
+            live = seq >= 0;
+        }
+        const int64_t b = live ? (int)tok / p.N : 0, n = live ? tok - b * p.N : 0;
+        const int h0 = hg * U;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sd.x) + b * sd.sb +
+                                                          n * sd.sn + h0 * sd.sh);
+        const int64_t sh8 = sd.sh / 8;
+        uint4 ra[U], rb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = live && h0 + u < sd.H;
+            ra[u] = on ? src[u * sh8 + ln.ca] : make_uint4(0, 0, 0, 0);
+            rb[u] = on ? src[u * sh8 + ln.cb] : make_uint4(0, 0, 0, 0);
+        }
+        float cs[8], sn[8];
+        const bool turn = sd.rotate && ln.rot;
+        if (turn && live) {
+            const int pos = p.pos ? p.pos[b * p.pos_sb + n] : (APPEND ? p.slots[tok] : (int)n);
+            lane_angles(turns, ln.s, pos, p.gain, cs, sn);
+        }
+        // where the row goes: base of head 0 and distance between heads, in 16-byte chunks
+        uint4* dst = nullptr;
+        int64_t dh = 0;
+        if (live) {
+            if (!APPEND) {
+                dst = reinterpret_cast<uint4*>(sd.out) + (b * sd.H * sd.rep * (int64_t)p.N + n) * (D / 8);
+                dh = (int64_t)p.N * (D / 8);
+            } else if (kind == 0) {
+                dst = reinterpret_cast<uint4*>(sd.out) + tok * sd.H * (D / 8);
+                dh = D / 8;
+            } else {
+                // a token outside the table, or a slot without a page, is reported and not written
+                const int slot = p.slots[tok];
+                int pg = -1;
+                if (seq < p.n_seqs && slot >= 0 && slot / p.page < p.max_pages)
+                    pg = p.page_table[(int64_t)seq * p.max_pages + slot / p.page];
+                if ((unsigned)pg < (unsigned)p.n_pages) {
+                    dst = reinterpret_cast<uint4*>(kind == 1 ? p.k_cache : p.v_cache) +
+                          ((int64_t)pg * sd.H * p.page + slot % p.page) * (D / 8);
+                    dh = (int64_t)p.page * (D / 8);
+                } else if (ln.s == 0 && h0 == 0) {
+                    atomicOr(p.err, ERR_BAD_PAGE);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint4 oa = ra[u], ob = rb[u];
+            if (sd.rotate) {
+                float f[16];
+                unpack8(ra[u], f);
+                unpack8(rb[u], f + 8);
+                if (norm) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
+                    const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] *= r * w[e];
+                }
+                if (turn) rotate16<IL>(f, cs, sn);
+                oa = pack8(f);
+                ob = pack8(f + 8);
+            }
+            if (dst && h0 + u < sd.H) {
+                const int copies = APPEND ? 1 : sd.rep;
+                uint4* d = dst + (int64_t)(h0 + u) * copies * dh;
+                for (int c = 0; c < copies; ++c) {
+                    d[c * dh + ln.ca] = oa;
+                    d[c * dh + ln.cb] = ob;
+                }
+            }
+        }
+    }
+}
+
+// The gradients: the same items; a row needs its dz rows (one per copy) and,
+// with a norm, its x row.  The weight's gradient is summed per lane over all
+// of the CTA's rows, then over the CTA's lanes, into one row of `partial` per
+// CTA, which reduce_weight_kernel adds in a fixed order.
+template <int D, int U, bool IL>
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const RopeParams p) {
+    constexpr int LPR = D / 16, TB = kRopeThreads / LPR;
+    __shared__ unsigned long long turns[kMaxPairs];
+    __shared__ float red[kRopeThreads / 32][D];
+    int idx;
+    const int kind = cta_side(p, &idx);
+    const RopeSide& sd = p.side[kind];
+    const Lane<D, IL> ln(p.rd);
+    griddep_launch_dependents();
+    load_turns(p, turns);
+    float w[16], acc[16];
+    const bool norm = sd.w != nullptr;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        acc[e] = 0.f;
+        w[e] = norm ? sd.w[(e < 8 ? ln.ca : ln.cb) * 8 + (e & 7)] : 1.f;
+    }
+    const int hgroups = (sd.H + U - 1) / U;
+    const int64_t items = (p.tokens + TB - 1) / TB * hgroups;
+    const int64_t sh8 = sd.sh / 8, gh8 = sd.gh / 8, zh8 = (int64_t)p.N * (D / 8);
+    for (int64_t it = idx; it < items; it += sd.ctas) {
+        const int hg = (int)(it % hgroups);
+        const int64_t tok = it / hgroups * TB + threadIdx.x / LPR;
+        const bool live = tok < p.tokens;
+        const int64_t b = live ? (int)tok / p.N : 0, n = live ? tok - b * p.N : 0;
+        const int h0 = hg * U;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sd.x) + b * sd.sb +
+                                                          n * sd.sn + h0 * sd.sh);
+        const uint4* dz = reinterpret_cast<const uint4*>(sd.dz) +
+                          ((b * sd.H + h0) * sd.rep * (int64_t)p.N + n) * (D / 8);
+        uint4 xa[U], xb[U], za[U], zb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = live && h0 + u < sd.H;
+            za[u] = on ? dz[u * sd.rep * zh8 + ln.ca] : make_uint4(0, 0, 0, 0);
+            zb[u] = on ? dz[u * sd.rep * zh8 + ln.cb] : make_uint4(0, 0, 0, 0);
+            xa[u] = on && norm ? src[u * sh8 + ln.ca] : make_uint4(0, 0, 0, 0);
+            xb[u] = on && norm ? src[u * sh8 + ln.cb] : make_uint4(0, 0, 0, 0);
+        }
+        float cs[8], sn[8];
+        const bool turn = sd.rotate && ln.rot;
+        if (turn && live) {
+            const int pos = p.pos ? p.pos[b * p.pos_sb + n] : (int)n;
+            lane_angles(turns, ln.s, pos, p.gain, cs, sn);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+        }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(sd.dx) + b * sd.gb + n * sd.gn + h0 * sd.gh);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = live && h0 + u < sd.H;
+            float g[16];
+            unpack8(za[u], g);
+            unpack8(zb[u], g + 8);
+            for (int c = 1; c < sd.rep; ++c) {
+                if (!on) break;
+                float t[16];
+                unpack8(dz[(u * sd.rep + c) * zh8 + ln.ca], t);
+                unpack8(dz[(u * sd.rep + c) * zh8 + ln.cb], t + 8);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) g[e] += t[e];
+            }
+            if (turn && live) rotate16<IL>(g, cs, sn);
+            if (norm) {
+                float x[16], ss = 0.f, sg = 0.f;
+                unpack8(xa[u], x);
+                unpack8(xb[u], x + 8);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    ss = fmaf(x[e], x[e], ss);
+                    sg = fmaf(g[e] * w[e], x[e], sg);
+                }
+                const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+                const float c = row_sum<LPR>(sg) * (1.f / D) * r * r * r;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (on) acc[e] = fmaf(g[e], x[e] * r, acc[e]);
+                    g[e] = g[e] * w[e] * r - x[e] * c;
+                }
+            }
+            if (on) {
+                dst[u * gh8 + ln.ca] = pack8(g);
+                dst[u * gh8 + ln.cb] = pack8(g + 8);
+            }
+        }
+    }
+    if (!norm) return;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+        if ((threadIdx.x & 31) < LPR) red[threadIdx.x / 32][(e < 8 ? ln.ca : ln.cb) * 8 + (e & 7)] = acc[e];
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += kRopeThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kRopeThreads / 32; ++k) s += red[k][d];
+        sd.partial[(int64_t)idx * D + d] = s;
+    }
+}
+
+// dw[d] = sum of rows[0 .. n) [d]; block 0: q, block 1: k.  Four columns a
+// thread, the rows dealt over the block, then one tree over shared memory.
+struct ReduceParams {
+    const float* rows[2];
+    float* out[2];
+    int32_t n[2];
+};
+template <int D>
+__global__ void __launch_bounds__(1024) reduce_weight_kernel(const ReduceParams p) {
+    constexpr int C4 = D / 4, G = 1024 / C4;
+    __shared__ float4 red[G][C4];
+    const int k = blockIdx.x, c = threadIdx.x % C4, g = threadIdx.x / C4;
+    griddep_wait();
+    if (!p.out[k]) return;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = g; i < p.n[k]; i += G) {
+        const float4 v = reinterpret_cast<const float4*>(p.rows[k])[(int64_t)i * C4 + c];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+    }
+    red[g][c] = a;
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (g < o) {
+            const float4 v = red[g + o][c];
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+            red[g][c] = a;
+        }
+    }
+    if (g == 0) reinterpret_cast<float4*>(p.out[k])[c] = a;
+}
+
+// CTAs of each kind, in proportion to the bytes it moves (two per SM in all),
+// none without an item.
+void deal_ctas(RopeParams* p, int D, int U, int sm_count, const double* bytes) {
+    const int TB = kRopeThreads / (D / 16);
+    const double all = bytes[0] + bytes[1] + bytes[2];
+    for (int k = 0; k < 3; ++k) {
+        RopeSide& sd = p->side[k];
+        const int64_t items = sd.H > 0 ? (p->tokens + TB - 1) / TB * ((sd.H + U - 1) / U) : 0;
+        const int64_t share = std::max<int64_t>(1, (int64_t)std::lround(2.0 * sm_count * bytes[k] / all));
+        sd.ctas = (int32_t)std::min(items, share);
+    }
+}
+
+constexpr int kRopeMaxCtas = 1024;  // bound on a kind's CTAs (two per SM), for the workspace
+
+cudaError_t launch_pdl(void (*kern)(const ReduceParams), int grid, int threads, const ReduceParams& p,
+                       cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <bool APPEND>
+cudaError_t launch_fwd(const RopeParams& p, int D, int U, bool il, cudaStream_t s) {
+    const unsigned grid = (unsigned)(p.side[0].ctas + p.side[1].ctas + p.side[2].ctas);
+    auto go = [&](auto kern) {
+        kern<<<grid, kRopeThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    };
+    if (D == 128) {
+        if (U == 4) return il ? go(norm_rope_kernel<128, 4, true, APPEND>) : go(norm_rope_kernel<128, 4, false, APPEND>);
+        return il ? go(norm_rope_kernel<128, 1, true, APPEND>) : go(norm_rope_kernel<128, 1, false, APPEND>);
+    }
+    if (U == 4) return il ? go(norm_rope_kernel<64, 4, true, APPEND>) : go(norm_rope_kernel<64, 4, false, APPEND>);
+    return il ? go(norm_rope_kernel<64, 1, true, APPEND>) : go(norm_rope_kernel<64, 1, false, APPEND>);
+}
+
+cudaError_t launch_bwd(const RopeParams& p, int D, bool il, cudaStream_t s) {
+    const unsigned grid = (unsigned)(p.side[0].ctas + p.side[1].ctas + p.side[2].ctas);
+    auto go = [&](auto kern) {
+        kern<<<grid, kRopeThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    };
+    if (D == 128) return il ? go(norm_rope_bwd_kernel<128, 2, true>) : go(norm_rope_bwd_kernel<128, 2, false>);
+    return il ? go(norm_rope_bwd_kernel<64, 2, true>) : go(norm_rope_bwd_kernel<64, 2, false>);
+}
+
+bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Token-major strides: rows start on 16 bytes, one element after another.
+bool strides_ok(const int64_t* st) {
+    for (int i = 0; i < 3; ++i)
+        if (st[i] < 0 || st[i] % 8) return false;
+    return true;
+}
+
+// Heads of a lane group's task: 4 share one computation of the angles; 1
+// spreads a small call over more CTAs.  4 wherever that still gives every SM
+// two CTAs' worth of items.
+int pick_heads(int64_t tokens, int D, int Hq, int Hkv, int sm_count) {
+    const int TB = kRopeThreads / (D / 16);
+    const int64_t items = (tokens + TB - 1) / TB * ((Hq + 3) / 4 + 2 * ((Hkv + 3) / 4));
+    return items >= 2 * (int64_t)sm_count ? 4 : 1;
+}
+
+int fill(const bsa_norm_rope_args* a, RopeParams* p) {
+    if (!a || a->B < 0 || a->N < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->D <= 0) return BSA_ERR_INVALID_ARG;
+    if (a->kv_repeat <= 0 || (int64_t)a->Hkv * a->kv_repeat > INT32_MAX) return BSA_ERR_INVALID_ARG;
+    if (a->rotary_dim < 0 || a->rotary_dim > a->D || a->rotary_dim % 16) return BSA_ERR_INVALID_ARG;
+    if (a->interleaved != 0 && a->interleaved != 1) return BSA_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.f) || !std::isfinite(a->eps) || !std::isfinite(a->gain)) return BSA_ERR_INVALID_ARG;
+    if (a->rotary_dim > 0 && (!a->inv_freq || !al(a->inv_freq, 8))) return BSA_ERR_INVALID_ARG;
+    if (!strides_ok(a->q_stride) || !strides_ok(a->k_stride) || (a->v && !strides_ok(a->v_stride)))
+        return BSA_ERR_INVALID_ARG;
+    if (!al(a->q, 16) || !al(a->k, 16) || !al(a->v, 16) || !al(a->positions, 4) || !al(a->q_weight, 4) ||
+        !al(a->k_weight, 4) || a->position_stride < 0)
+        return BSA_ERR_INVALID_ARG;
+    if (a->D != 64 && a->D != 128) return BSA_ERR_UNSUPPORTED;
+    p->tokens = (int64_t)a->B * a->N;
+    if (p->tokens > INT32_MAX) return BSA_ERR_INVALID_ARG;
+    const void* x[3] = {a->q, a->k, a->v};
+    const int64_t* st[3] = {a->q_stride, a->k_stride, a->v_stride};
+    for (int k = 0; k < 3; ++k) {
+        RopeSide& sd = p->side[k];
+        sd = RopeSide{};
+        sd.x = x[k];
+        sd.sb = st[k][0];
+        sd.sn = st[k][1];
+        sd.sh = st[k][2];
+        sd.H = k == 0 ? a->Hq : (k == 2 && !a->v ? 0 : a->Hkv);
+        sd.rep = k == 0 ? 1 : a->kv_repeat;
+        sd.rotate = k < 2;
+        sd.w = k == 0 ? a->q_weight : k == 1 ? a->k_weight : nullptr;
+    }
+    p->inv_freq = a->inv_freq;
+    p->pos = a->positions;
+    p->pos_sb = a->position_stride;
+    p->N = std::max(a->N, 1);
+    p->rd = a->rotary_dim;
+    p->eps = a->eps;
+    p->gain = a->gain;
+    return BSA_OK;
+}
+
+}  // namespace
+}  // namespace bsa
+
+extern "C" {
+
+int bsa_rope_inv_freq(const bsa_rope_spec* s, double* inv_freq) {
+    if (!s || !inv_freq) return BSA_ERR_INVALID_ARG;
+    if (s->rotary_dim <= 0 || s->rotary_dim % 2) return BSA_ERR_INVALID_ARG;
+    if (!(s->base > 0.0) || !std::isfinite(s->base) || !(s->factor > 0.0) || !std::isfinite(s->factor))
+        return BSA_ERR_INVALID_ARG;
+    if (s->scaling < BSA_ROPE_PLAIN || s->scaling > BSA_ROPE_BY_PARTS) return BSA_ERR_INVALID_ARG;
+    if (s->scaling == BSA_ROPE_BASE && s->rotary_dim <= 2) return BSA_ERR_INVALID_ARG;
+    if (s->scaling == BSA_ROPE_BY_PARTS &&
+        (!(s->original_length > 0.0) || !std::isfinite(s->original_length) || !std::isfinite(s->low) ||
+         !std::isfinite(s->high) || !(s->high > s->low)))
+        return BSA_ERR_INVALID_ARG;
+    const int n = s->rotary_dim / 2;
+    double base = s->base;
+    if (s->scaling == BSA_ROPE_BASE)
+        base *= std::pow(s->factor, (double)s->rotary_dim / (double)(s->rotary_dim - 2));
+    for (int i = 0; i < n; ++i) {
+        double f = std::pow(base, -2.0 * i / (double)s->rotary_dim);
+        if (s->scaling == BSA_ROPE_LINEAR) f /= s->factor;
+        if (s->scaling == BSA_ROPE_BY_PARTS) {
+            const double turns = s->original_length * f / 6.283185307179586476925;
+            const double ramp = std::min(1.0, std::max(0.0, (turns - s->low) / (s->high - s->low)));
+            f *= ramp + (1.0 - ramp) / s->factor;
+        }
+        inv_freq[i] = f;
+    }
+    return BSA_OK;
+}
+
+int bsa_qk_norm_rope(const bsa_norm_rope_args* a, void* q_out, void* k_out, void* v_out, bsa_stream_t stream) {
+    bsa::RopeParams p{};
+    int st = bsa::fill(a, &p);
+    if (st != BSA_OK) return st;
+    if (p.tokens == 0) return BSA_OK;
+    if (!a->q || !a->k || !q_out || !k_out || (a->v != nullptr) != (v_out != nullptr)) return BSA_ERR_INVALID_ARG;
+    if (!bsa::al(q_out, 16) || !bsa::al(k_out, 16) || !bsa::al(v_out, 16)) return BSA_ERR_INVALID_ARG;
+    int32_t* err;
+    int sms;
+    if ((st = bsa::device_context(&err, &sms)) != BSA_OK) return st;
+    void* out[3] = {q_out, k_out, v_out};
+    double bytes[3];
+    for (int k = 0; k < 3; ++k) {
+        p.side[k].out = out[k];
+        bytes[k] = (double)p.side[k].H * (1 + p.side[k].rep);
+    }
+    const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, sms);
+    bsa::deal_ctas(&p, a->D, U, sms, bytes);
+    const cudaError_t e =
+        bsa::launch_fwd<false>(p, a->D, U, a->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+int bsa_cache_append(const bsa_norm_rope_args* a, const bsa_page_cache* c, const int32_t* seq_ids,
+                     const int32_t* slots, void* q_out, bsa_stream_t stream) {
+    bsa::RopeParams p{};
+    int st = bsa::fill(a, &p);
+    if (st != BSA_OK) return st;
+    if ((st = bsa::check_page_cache(c)) != BSA_OK) return st;
+    if (a->B != 1 || a->kv_repeat != 1 || c->layers != 1 || c->Hkv != a->Hkv || c->D != a->D)
+        return BSA_ERR_INVALID_ARG;
+    if (p.tokens == 0) return BSA_OK;
+    if (!a->q || !a->k || !a->v || !q_out || !seq_ids || !slots || !c->page_table) return BSA_ERR_INVALID_ARG;
+    if (!bsa::al(q_out, 16) || !bsa::al(seq_ids, 4) || !bsa::al(slots, 4)) return BSA_ERR_INVALID_ARG;
+    int sms;
+    if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
+    p.side[0].out = q_out;
+    p.k_cache = c->k;
+    p.v_cache = c->v;
+    p.page_table = c->page_table;
+    p.seq_ids = seq_ids;
+    p.slots = slots;
+    p.n_seqs = c->n_seqs;
+    p.max_pages = c->max_pages;
+    p.page = c->page;
+    p.n_pages = c->n_pages;
+    const double bytes[3] = {(double)a->Hq, (double)a->Hkv, (double)a->Hkv};
+    const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, sms);
+    bsa::deal_ctas(&p, a->D, U, sms, bytes);
+    const cudaError_t e =
+        bsa::launch_fwd<true>(p, a->D, U, a->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+int64_t bsa_qk_norm_rope_backward_workspace(int32_t D) {
+    return D > 0 ? 2ll * bsa::kRopeMaxCtas * D * (int64_t)sizeof(float) : 0;
+}
+
+int bsa_qk_norm_rope_backward(const bsa_norm_rope_args* a, const bsa_norm_rope_grads* g, void* workspace,
+                              int64_t workspace_bytes, bsa_stream_t stream) {
+    bsa::RopeParams p{};
+    int st = bsa::fill(a, &p);
+    if (st != BSA_OK) return st;
+    if (!g) return BSA_ERR_INVALID_ARG;
+    const bool dw = a->q_weight || a->k_weight;
+    if ((a->q_weight != nullptr) != (g->q_weight != nullptr) || (a->k_weight != nullptr) != (g->k_weight != nullptr))
+        return BSA_ERR_INVALID_ARG;
+    if (!bsa::al(g->q_weight, 16) || !bsa::al(g->k_weight, 16) || !bsa::al(workspace, 16)) return BSA_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const void* dz[3] = {g->dq, g->dk, g->dv};
+    void* dx[3] = {g->q, g->k, g->v};
+    const int64_t* gs[3] = {g->q_stride, g->k_stride, g->v_stride};
+    if ((g->dv != nullptr) != (g->v != nullptr)) return BSA_ERR_INVALID_ARG;
+    p.side[2].H = g->dv ? a->Hkv : 0;
+    for (int k = 0; k < 3; ++k) {
+        if (k == 2 && !g->dv) continue;
+        const int32_t ext[3] = {a->B, a->N, k == 0 ? a->Hq : a->Hkv};
+        for (int i = 0; i < 3; ++i)  // written rows must not coincide
+            if (ext[i] > 1 && gs[k][i] == 0) return BSA_ERR_INVALID_ARG;
+        if (!bsa::strides_ok(gs[k]) || !bsa::al(dz[k], 16) || !bsa::al(dx[k], 16)) return BSA_ERR_INVALID_ARG;
+        if (p.tokens > 0 && (!dz[k] || !dx[k])) return BSA_ERR_INVALID_ARG;
+    }
+    if (p.tokens > 0 && ((a->q_weight && !a->q) || (a->k_weight && !a->k))) return BSA_ERR_INVALID_ARG;
+    if (dw && (!workspace || workspace_bytes < bsa_qk_norm_rope_backward_workspace(a->D))) return BSA_ERR_CAPACITY;
+    int32_t* err;
+    int sms;
+    if ((st = bsa::device_context(&err, &sms)) != BSA_OK) return st;
+    sms = std::min(sms, bsa::kRopeMaxCtas / 2);
+    if (p.tokens == 0) {
+        for (float* o : {g->q_weight, g->k_weight})
+            if (o && cudaMemsetAsync(o, 0, (size_t)a->D * sizeof(float), s) != cudaSuccess) return BSA_ERR_CUDA;
+        return BSA_OK;
+    }
+    double bytes[3];
+    for (int k = 0; k < 3; ++k) {
+        bsa::RopeSide& sd = p.side[k];
+        sd.dz = dz[k];
+        sd.dx = dx[k];
+        sd.gb = gs[k][0];
+        sd.gn = gs[k][1];
+        sd.gh = gs[k][2];
+        sd.partial = static_cast<float*>(workspace) + (int64_t)k * bsa::kRopeMaxCtas * a->D;
+        bytes[k] = (double)sd.H * (1 + sd.rep + (sd.w ? 1 : 0));
+    }
+    p.side[2].partial = nullptr;
+    bsa::deal_ctas(&p, a->D, 2, sms, bytes);
+    cudaError_t e = bsa::launch_bwd(p, a->D, a->interleaved != 0, s);
+    if (e == cudaSuccess && dw) {
+        bsa::ReduceParams r{{p.side[0].partial, p.side[1].partial},
+                            {g->q_weight, g->k_weight},
+                            {p.side[0].ctas, p.side[1].ctas}};
+        e = a->D == 128 ? bsa::launch_pdl(bsa::reduce_weight_kernel<128>, 2, 1024, r, s)
+                        : bsa::launch_pdl(bsa::reduce_weight_kernel<64>, 2, 1024, r, s);
+    }
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,823 @@
+// bsa_tree.cu -- attention of drafted tokens over a paged cache (one token per
+// sequence: decoding; a tree of up to 64: verification), for sm_103a.
+//
+// Mathematics: for the T * G query rows of a sequence that read one key head
+// (G query heads per key head), O = softmax(q K^T scale) V over the visible
+// slots in one pass, with the running maximum and sum of the softmax.  A slot
+// is visible when it is committed, or a draft whose bit is set in the row's
+// tree mask; with block lists, only inside listed pages.
+//
+// What bounds it: every K and V row is read once per row tile of 128 query
+// rows, 4 D bytes a slot, and used for 4 D T G flops; below ~280 flops per
+// byte (T G <= 128) memory is the limit, so the kernel is built to keep loads
+// in flight and everything else behind them.
+//
+// Work: a step is 128 key slots (one page of 128 or two of 64) of one row
+// tile.  All steps of the batch form one sequence of (unit, item, step), cut
+// into equal ranges, one per CTA: ragged lengths, long contexts with few rows
+// and large batches all load every SM alike.  An item that lies in one range
+// is written out directly; one that a range boundary cuts leaves an
+// unnormalised fp32 part (with its maximum and sum) per range in the
+// workspace, and merge_kernel joins the parts in range order -- no atomics,
+// so results do not depend on timing.
+//
+// One CTA per SM, 6 warps:
+//   warps 0-3  softmax, thread = query row (TMEM lane): S from TMEM, P (bf16)
+//              back over it, the rows' maximum and sum in registers; the
+//              running maximum is raised only when it grows by more than 2^8;
+//              at an item's end O from TMEM to global memory.
+//   warp 4     producer: walks the CTA's range, resolves pages and TMA-loads Q
+//              (two buffers) and the K / V tiles (a ring); publishes one
+//              description per step.
+//   warp 5     MMA: S = Q K^T and O += P V on tcgen05, M = 128 rows whatever
+//              T G is (the rows behind it compute on leftovers of shared
+//              memory and are never stored); the V rows of a page's unused
+//              slots are zeroed first, since 0 * NaN would reach O.
+
+#include <algorithm>
+#include <cmath>
+
+#include "bsa.h"
+#include "bsa_internal.h"
+#include "bsa_ptx.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kTreeThreads = 192;
+constexpr int kProducer = 4, kMma = 5;
+constexpr int kMaxUnits = 2048;   // units of one launch (their prefix sums sit in shared memory)
+constexpr int kMaxCtas = 160;     // partial slots are sized for this many
+constexpr int kMaxSlots = 12;     // K / V ring
+constexpr int kInfos = 8;         // step descriptions ahead
+constexpr int kTreeSmem = 232448;
+constexpr int kStep = 128;        // key slots per step
+
+enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };
+
+struct StepInfo {
+    int flags;
+    int slot0[2];  // first slot of each sub-block (64-slot pages: two)
+    int nv[2];     // its slots that hold something
+    int b, h, t0;  // sequence, key head, first drafted token of the row tile
+    int ctx, dl;
+    int part;      // -1: write the output, else the partial slot
+    int pad;
+};
+
+struct Meta {  // one per CTA: the item its range starts inside of
+    int start, end, per;  // start < 0: none
+    int b, h, t0, dl;
+    int pad;
+};
+
+struct TreeCtrl {
+    uint64_t t_full[kMaxSlots], t_empty[kMaxSlots];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t i_full[kInfos], i_empty[kInfos];
+    uint64_t drain;
+    StepInfo info[kInfos];
+    int red[8];
+    uint32_t tmem_base;
+    WaitFlag wf;
+    int prefix[kMaxUnits + 1];
+};
+
+struct TreeParams {
+    const int32_t *ctx, *dl, *row_ptr, *col_idx, *table;
+    const unsigned long long* mask;
+    int64_t col_cap;
+    int32_t B, T, Hq, Hkv, G, page, P, n_pages;
+    int32_t unit0, units;      // units of this launch
+    int32_t tq, RT;            // drafted tokens per row tile, row tiles
+    int32_t n_slots, q_box;    // ring slots, bytes of one 64-column box of Q
+    int32_t grid;
+    void* out;
+    float* lse;
+    float* part_o;             // [2 * grid][rows][D]
+    float2* part_ml;           // [2 * grid][rows]
+    Meta* meta;
+    int32_t* err;
+    float scale_log2;
+    unsigned long long wait_limit_ns;
+};
+
+__device__ __forceinline__ bool twait(uint64_t* bar, uint32_t parity, volatile WaitFlag* wf) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, wf));
+}
+
+// Sequence lengths as they are used: nothing negative, drafts at most T.
+__device__ __forceinline__ int seq_ctx(const TreeParams& p, int b) { return max(p.ctx[b], 0); }
+__device__ __forceinline__ int seq_dl(const TreeParams& p, int b) {
+    return p.dl ? min(max(p.dl[b], 0), p.T) : p.T;
+}
+
+// Pages a unit's row visits: listed entries, or the sequence's pages.
+__device__ int unit_pages(const TreeParams& p, int u, bool report) {
+    if (p.row_ptr) {
+        const int64_t beg = p.row_ptr[u], end = min((int64_t)p.row_ptr[u + 1], p.col_cap);
+        if (beg < 0 || end < beg || end - beg > p.P) {
+            if (report) atomicOr(p.err, ERR_BAD_ROW);
+            return 0;
+        }
+        return (int)(end - beg);
+    }
+    const int64_t len = (int64_t)seq_ctx(p, u) + seq_dl(p, u);
+    const int64_t n = (len + p.page - 1) / p.page;
+    if (n > p.P && report) atomicOr(p.err, ERR_BAD_PAGE);
+    return (int)min(n, (int64_t)p.P);
+}
+
+// Steps of one item of unit u; at least one, so that a row without any key
+// still passes through the pipeline and writes its zeros.
+__device__ __forceinline__ int unit_steps(const TreeParams& p, int u, bool report) {
+    const int ppt = kStep / p.page;
+    return max(1, (unit_pages(p, u, report) + ppt - 1) / ppt);
+}
+
+// Bit k: slot base + k is visible to a row with these draft bits.
+__device__ __forceinline__ unsigned long long visible64(int base, int ctx, unsigned long long bits) {
+    const int d = ctx - base;
+    if (d >= 64) return ~0ull;
+    if (d > 0) return ((1ull << d) - 1) | (bits << d);
+    return d > -64 ? bits >> -d : 0ull;
+}
+
+// ---------------------------------------------------------------- producer
+template <int D>
+__device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
+                              const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, int lo, int hi, int per,
+                              volatile WaitFlag* wf) {
+    constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX;
+    const int lane = threadIdx.x & 31;
+    const bool leader = elect_one();
+    const int ppt = kStep / p.page;
+    const int mult = p.row_ptr ? p.RT : p.Hkv * p.RT;
+    uint32_t slot = 0, phase = 0, nload = 0, g = 0, nq = 0;
+    bool ok = true;
+    Meta mt{-1, 0, per, 0, 0, 0, 0, 0};
+    if (lo < hi) {
+        // the unit that holds step lo: last u with prefix[u] <= lo
+        int u = 0;
+        for (int step = 1 << 10; step > 0; step >>= 1)
+            if (u + step < p.units && c->prefix[u + step] <= lo) u += step;
+        int per_item = (c->prefix[u + 1] - c->prefix[u]) / mult;
+        int k = (lo - c->prefix[u]) / per_item;
+        int pos = lo;
+        while (ok && pos < hi) {
+            const int gu = p.unit0 + u;  // unit of the whole call
+            const int b = p.row_ptr ? gu / p.Hkv : gu;
+            const int h = p.row_ptr ? gu % p.Hkv : k / p.RT;
+            const int t0 = (k % p.RT) * p.tq;
+            const int ctx = seq_ctx(p, b), dl = seq_dl(p, b);
+            const int64_t len = (int64_t)ctx + dl;
+            const int start = c->prefix[u] + k * per_item, end = start + per_item;
+            const int s0 = pos - start, s1 = min(end, hi) - start;
+            const bool whole = s0 == 0 && start + s1 == end;
+            const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
+            if (start < lo) mt = Meta{start, end, per, b, h, t0, dl, 0};
+            const int n = unit_pages(p, gu, false);
+            const int beg = p.row_ptr ? p.row_ptr[gu] : 0;
+            // Q of the item
+            const uint32_t qb = nq & 1;
+            if (!twait(&c->q_empty[qb], ((nq >> 1) & 1) ^ 1, wf)) {
+                ok = false;
+                break;
+            }
+            if (leader) {
+                mbar_arrive_expect_tx(&c->q_full[qb], (uint32_t)(p.tq * p.G * 128 * NBOX));
+#pragma unroll
+                for (int x = 0; x < NBOX; ++x)
+                    tma_load_3d(sQ + (qb * NBOX + x) * p.q_box, tq, &c->q_full[qb], x * 64, h * p.G, b * p.T + t0);
+            }
+            ++nq;
+            // steps, 32 pages resolved at a time
+            for (int e0 = s0 * ppt; e0 < s1 * ppt && ok; e0 += 32) {
+                const int e = e0 + lane;
+                int nv = 0, j = 0, y = -p.page;
+                if (e < n && e < s1 * ppt) {
+                    j = p.row_ptr ? p.col_idx[beg + e] : e;
+                    if ((unsigned)j >= (unsigned)p.P) {
+                        atomicOr(p.err, ERR_BAD_COL);
+                        j = 0;
+                    } else {
+                        nv = (int)min(max(len - (int64_t)j * p.page, (int64_t)0), (int64_t)p.page);
+                        if (nv > 0) {
+                            const int pg = p.table[(int64_t)b * p.P + j];
+                            if ((unsigned)pg < (unsigned)p.n_pages) {
+                                y = (pg * p.Hkv + h) * p.page;
+                            } else {
+                                atomicOr(p.err, ERR_BAD_PAGE);
+                                nv = 0;
+                            }
+                        }
+                    }
+                }
+                const int cnt = min(32, s1 * ppt - e0);
+                for (int q = 0; q < cnt && ok; q += ppt) {
+                    const int sl0 = __shfl_sync(0xffffffffu, j, q) * p.page, nv0 = __shfl_sync(0xffffffffu, nv, q);
+                    const int y0 = __shfl_sync(0xffffffffu, y, q);
+                    const int q1 = q + ppt - 1;  // the step's second page, if it has two
+                    const int sl1 = __shfl_sync(0xffffffffu, j, q1) * p.page, nv1 = __shfl_sync(0xffffffffu, nv, q1);
+                    const int y1 = __shfl_sync(0xffffffffu, y, q1);
+                    const int st = (e0 + q) / ppt;
+                    const uint32_t is = g % kInfos;
+                    if (!twait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        StepInfo& f = c->info[is];
+                        const bool plain = nv0 == p.page && sl0 + p.page <= ctx &&
+                                           (ppt == 1 || (nv1 == p.page && sl1 + p.page <= ctx));
+                        f.flags = (st == s0 ? kFirst : 0) | (st + 1 == s1 ? kLast : 0) | (plain ? 0 : kMask);
+                        f.slot0[0] = sl0;
+                        f.slot0[1] = ppt == 2 ? sl1 : sl0 + 64;
+                        f.nv[0] = nv0;
+                        f.nv[1] = ppt == 2 ? nv1 : nv0;
+                        f.b = b;
+                        f.h = h;
+                        f.t0 = t0;
+                        f.ctx = ctx;
+                        f.dl = dl;
+                        f.part = part;
+                        mbar_arrive(&c->i_full[is]);
+                    }
+                    __syncwarp();
+                    ++g;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!twait(&c->t_empty[slot], phase ^ 1, wf)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) {
+                            mbar_arrive_expect_tx(&c->t_full[slot], T_BYTES);
+#pragma unroll
+                            for (int x = 0; x < NBOX; ++x) {
+                                uint8_t* dst = sT + slot * T_BYTES + x * T_BOX;
+                                tma_load_2d(dst, kv ? tv : tk, &c->t_full[slot], x * 64, y0);
+                                if (ppt == 2) tma_load_2d(dst + 64 * 128, kv ? tv : tk, &c->t_full[slot], x * 64, y1);
+                            }
+                        }
+                        ++nload;
+                        if (++slot == (uint32_t)p.n_slots) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+            }
+            pos = start + s1;
+            if (++k == mult && pos < hi) {
+                k = 0;
+                ++u;
+                per_item = (c->prefix[u + 1] - c->prefix[u]) / mult;
+            }
+        }
+    }
+    if (ok) {
+        const uint32_t is = g % kInfos;
+        if (twait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf) && lane == 0) {
+            c->info[is].flags = kEnd;
+            mbar_arrive(&c->i_full[is]);
+        }
+    }
+    if (lane == 0) p.meta[blockIdx.x] = mt;
+    __syncwarp();
+    if (leader) {
+        // copies still in flight must land before the CTA exits
+        const uint32_t ns = (uint32_t)p.n_slots;
+        for (uint32_t n = nload > ns ? nload - ns : 0; n < nload; ++n)
+            mbar_wait_drain(&c->t_full[n % ns], (n / ns) & 1);
+        for (uint32_t n = nq > 2 ? nq - 2 : 0; n < nq; ++n) mbar_wait_drain(&c->q_full[n & 1], (n >> 1) & 1);
+    }
+}
+
+// ---------------------------------------------------------------- MMA
+template <int D>
+__device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, uint32_t tmem,
+                         volatile WaitFlag* wf) {
+    constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX;
+    constexpr uint64_t KDESC = sdesc_sw128_base(16, 1024), VDESC = sdesc_sw128_base(T_BOX, 1024);
+    constexpr uint32_t IQK = idesc_bf16_f32(128, kStep, false), IPV = idesc_bf16_f32(128, D, true);
+    constexpr int O_COL = 2 * kStep;
+    const int lane = threadIdx.x & 31;
+    const bool leader = elect_one();
+    uint32_t slot = 0, phase = 0, nq = 0;
+    bool pend = false, pfirst = false, ok = true;
+    uint32_t pslot = 0, pphase = 0, pg = 0;
+    int pnv0 = 0, pnv1 = 0;
+    auto step_slot = [&] {
+        if (++slot == (uint32_t)p.n_slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    auto issue_pv = [&]() -> bool {
+        const uint32_t sb = pg & 1;
+        if (!twait(&c->t_full[pslot], pphase, wf)) return false;
+        uint8_t* tile = sT + pslot * T_BYTES;
+        const int z0 = pnv0 > 0 && pnv0 < p.page ? pnv0 : p.page;  // rows z0 .. page of the first page
+        const int z1 = p.page == 64 && pnv1 > 0 && pnv1 < 64 ? pnv1 : 64;
+        if (z0 < p.page || z1 < 64) {
+            for (int x = lane; x < (p.page - z0) * 8 * NBOX; x += 32) {
+                const int row = z0 + x / (8 * NBOX), q = x % (8 * NBOX);
+                *reinterpret_cast<uint4*>(tile + (q >> 3) * T_BOX + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            for (int x = lane; x < (64 - z1) * 8 * NBOX; x += 32) {
+                const int row = 64 + z1 + x / (8 * NBOX), q = x % (8 * NBOX);
+                *reinterpret_cast<uint4*>(tile + (q >> 3) * T_BOX + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        if (!twait(&c->p_full[sb], (pg >> 1) & 1, wf)) return false;
+        tc_fence_after();
+        const uint64_t vdesc = VDESC + (smem_u32(tile) >> 4);
+        if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < kStep / 16; ++kk)
+                mma_ts(tmem + O_COL, tmem + sb * kStep + kk * 8, vdesc + (uint64_t)((kk * 16 * 128) >> 4), IPV,
+                       (pfirst && kk == 0) ? 0u : 1u);
+            mma_commit(&c->pv_done[sb]);
+            mma_commit(&c->t_empty[pslot]);
+        }
+        __syncwarp();
+        return true;
+    };
+    for (uint32_t g = 0; ok; ++g) {
+        const uint32_t is = g % kInfos;
+        if (!twait(&c->i_full[is], (g / kInfos) & 1, wf)) {
+            ok = false;
+            break;
+        }
+        const int flags = c->info[is].flags, nv0 = c->info[is].nv[0], nv1 = c->info[is].nv[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->i_empty[is]);
+        if (flags & kEnd) break;
+        const uint32_t qb = nq & 1;
+        if ((flags & kFirst) && !twait(&c->q_full[qb], (nq >> 1) & 1, wf)) {
+            ok = false;
+            break;
+        }
+        if (!twait(&c->t_full[slot], phase, wf)) {
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        const uint32_t sb = g & 1;
+        const uint64_t kdesc = KDESC + (smem_u32(sT + slot * T_BYTES) >> 4);
+        if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t qd = KDESC + (smem_u32(sQ + (qb * NBOX + (kk >> 2)) * p.q_box + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + sb * kStep, qd, kdesc + (uint64_t)(((kk >> 2) * T_BOX + (kk & 3) * 32) >> 4), IQK,
+                       kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&c->s_full[sb]);
+            mma_commit(&c->t_empty[slot]);
+            if (flags & kLast) mma_commit(&c->q_empty[qb]);
+        }
+        __syncwarp();
+        step_slot();
+        if (flags & kLast) ++nq;
+        if (pend && !issue_pv()) {
+            ok = false;
+            break;
+        }
+        pend = true;
+        pfirst = flags & kFirst;
+        pslot = slot;
+        pphase = phase;
+        pg = g;
+        pnv0 = nv0;
+        pnv1 = nv1;
+        step_slot();
+    }
+    if (ok && pend) issue_pv();
+    if (leader) {
+        mma_commit(&c->drain);
+        mbar_wait_drain(&c->drain, 0);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- softmax
+template <int D>
+__device__ void tree_softmax(const TreeParams& p, TreeCtrl* c, uint32_t tmem, volatile WaitFlag* wf) {
+    constexpr int O_COL = 2 * kStep;
+    const int row = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t t_o = tmem + lanes + O_COL;
+    const int rt = row / p.G, rg = row - rt * p.G;  // drafted token (in the tile) and query head of this row
+    const bool idle = warp * 32 >= p.tq * p.G;      // the whole warp lies behind the tile's rows
+    float m = -INFINITY, l = 0.f;
+    const f2 sl2 = {p.scale_log2, p.scale_log2};
+    for (uint32_t g = 0;; ++g) {
+        const uint32_t is = g % kInfos, sb = g & 1;
+        if (!twait(&c->i_full[is], (g / kInfos) & 1, wf)) break;
+        const StepInfo f = c->info[is];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->i_empty[is]);
+        if (f.flags & kEnd) break;
+        if (!twait(&c->s_full[sb], (g >> 1) & 1, wf)) break;
+        tc_fence_after();
+        const int t = f.t0 + rt;
+        if (f.flags & kFirst) {
+            m = -INFINITY;
+            l = 0.f;
+        }
+        if (!idle) {
+            const uint32_t t_s = tmem + lanes + sb * kStep;
+            uint32_t s[4][32];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_ld32(t_s + x * 32, s[x]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) reg_fence(s[x]);
+            if (f.flags & kMask) {
+                unsigned long long bits = 0;
+                if (t < f.dl) {
+                    bits = p.mask ? p.mask[(int64_t)f.b * p.T + t] : (2ull << t) - 1;
+                    if (f.dl < 64) bits &= (1ull << f.dl) - 1;
+                }
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const unsigned long long vis = f.nv[w] > 0 ? visible64(f.slot0[w], f.ctx, bits) : 0ull;
+                    const uint32_t v[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            if (!((v[x] >> q) & 1u)) s[2 * w + x][q] = __float_as_uint(-INFINITY);
+                }
+            }
+            float mx[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                mx[x] = __uint_as_float(s[x][0]);
+#pragma unroll
+                for (int q = 1; q < 31; q += 2)
+                    mx[x] = fmax3(mx[x], __uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1]));
+                mx[x] = fmaxf(mx[x], __uint_as_float(s[x][31]));
+            }
+            const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+            // raise the reference when it would grow by more than 2^8 (exact
+            // after the division by the sum, which uses the same reference)
+            const bool grow = top > m + 8.f || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float alpha = grow ? ex2_approx(m - top) : 1.f;
+                if (grow) {
+                    m = top;
+                    l *= alpha;
+                }
+                if (!(f.flags & kFirst)) {
+                    // O must hold every earlier step's product before it is scaled
+                    if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
+                    tc_fence_after();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + x * 32, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+                        tmem_st32(t_o + x * 32, o);
+                    }
+                }
+            }
+            __syncwarp();
+            const float ref = m == -INFINITY ? 0.f : m;
+            const f2 nm2 = {-ref, -ref};
+            f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const f2 a = fma2({__uint_as_float(s[x][2 * q]), __uint_as_float(s[x][2 * q + 1])}, sl2, nm2);
+                    const f2 e = {ex2_approx(a.x), ex2_approx(a.y)};
+                    sum[q & 1] = add2(sum[q & 1], e);
+                    pk[q] = pack_bf16x2(e.x, e.y);
+                }
+                tmem_st16(t_s + x * 16, pk);
+            }
+            const f2 all = add2(sum[0], sum[1]);
+            l += all.x + all.y;
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->p_full[sb]);
+        if (!(f.flags & kLast)) continue;
+        // the item's (or its part's) result
+        if (!twait(&c->pv_done[sb], (g >> 1) & 1, wf)) break;
+        tc_fence_after();
+        if (idle) continue;
+        const bool live = rt < p.tq && t < f.dl;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t orow = ((int64_t)f.b * p.T + t) * p.Hq + f.h * p.G + rg;
+        const int64_t prow = (int64_t)f.part * (p.tq * p.G) + row;
+        if (live) {
+            if (f.part < 0)
+                p.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+            else
+                p.part_ml[prow] = make_float2(m, l);
+        }
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(t_o + x * 32, o);
+            tmem_wait_ld();
+            reg_fence(o);
+            if (!live) continue;
+            if (f.part < 0) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + x * 32);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        w[y] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * y]) * inv,
+                                           __uint_as_float(o[8 * q + 2 * y + 1]) * inv);
+                    dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else {
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + x * 32);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, const TreeParams p) {
+    constexpr int NBOX = D / 64, T_BYTES = NBOX * kStep * 128;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) atomicOr(p.err, ERR_LAUNCH);
+        return;
+    }
+    uint8_t* sQ = smem;
+    uint8_t* sT = sQ + 2 * NBOX * p.q_box;
+    TreeCtrl* c = reinterpret_cast<TreeCtrl*>(sT + p.n_slots * T_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < kMaxSlots; ++x) {
+            mbar_init(&c->t_full[x], 1);
+            mbar_init(&c->t_empty[x], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&c->q_full[x], 1);
+            mbar_init(&c->q_empty[x], 1);
+            mbar_init(&c->s_full[x], 1);
+            mbar_init(&c->p_full[x], 4);
+            mbar_init(&c->pv_done[x], 1);
+        }
+        for (int x = 0; x < kInfos; ++x) {
+            mbar_init(&c->i_full[x], 1);
+            mbar_init(&c->i_empty[x], 5);
+        }
+        mbar_init(&c->drain, 1);
+        c->wf.abort = 0;
+        c->wf.limit_ns = p.wait_limit_ns;
+        fence_mbar_init();
+    }
+    if (warp == kMma) {
+        tmem_alloc(&c->tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == kProducer && lane == 0) {
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+    }
+    // prefix sums of the units' steps: every thread a run of units, then a scan
+    {
+        const int mult = p.row_ptr ? p.RT : p.Hkv * p.RT;
+        const int run = (p.units + kTreeThreads - 1) / kTreeThreads;
+        const int u0 = min(p.units, (int)threadIdx.x * run), u1 = min(p.units, u0 + run);
+        int sum = 0;
+        for (int u = u0; u < u1; ++u) {
+            sum += unit_steps(p, p.unit0 + u, blockIdx.x == 0) * mult;
+            c->prefix[u + 1] = sum;
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) c->red[warp] = incl;
+        __syncthreads();
+        int before = incl - sum;
+        for (int w = 0; w < warp; ++w) before += c->red[w];
+        for (int u = u0; u < u1; ++u) c->prefix[u + 1] += before;
+        if (threadIdx.x == 0) c->prefix[0] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c->tmem_base;
+    volatile WaitFlag* wf = &c->wf;
+    const int total = c->prefix[p.units];
+    const int per = (total + p.grid - 1) / p.grid;
+    const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
+    if (warp == kProducer)
+        tree_producer<D>(&tq, &tk, &tv, p, sQ, sT, c, lo, hi, per, wf);
+    else if (warp == kMma)
+        tree_mma<D>(p, sQ, sT, c, tmem, wf);
+    else
+        tree_softmax<D>(p, c, tmem, wf);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && c->wf.abort) atomicOr(p.err, ERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------- merge
+// Block x joins the item that the boundary in front of range x + 1 is the
+// first to cut; a warp per query row.  With parts i in range order:
+// m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
+    griddep_wait();
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const Meta mt = p.meta[c];
+    if (mt.start < 0) return;
+    // range c is full or the last one; range c - 1 is always full
+    const int rows = p.tq * p.G;
+    const int per = p.meta[0].per;
+    const int first = c - 1;
+    if (mt.start < first * per) return;  // an earlier boundary cuts it too
+    const int last = (mt.end - 1) / per;
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int t = mt.t0 + r / p.G;
+    if (r >= rows || t >= mt.dl) return;
+    auto slot_of = [&](int k) { return k == first && mt.start > first * per ? 2 * k + 1 : 2 * k; };
+    float m = -INFINITY;
+    for (int k = first + lane; k <= last; k += 32) m = fmaxf(m, p.part_ml[(int64_t)slot_of(k) * rows + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    constexpr int C = D / 32;
+    float acc[C];
+#pragma unroll
+    for (int x = 0; x < C; ++x) acc[x] = 0.f;
+    if (m > -INFINITY) {
+#pragma unroll 4
+        for (int k = first; k <= last; ++k) {
+            const int64_t pr = (int64_t)slot_of(k) * rows + r;
+            const float2 ml = p.part_ml[pr];
+            const float w = ex2_approx(ml.x - m);
+            l += w * ml.y;
+            if (C == 4) {
+                const float4 o = reinterpret_cast<const float4*>(p.part_o + pr * D)[lane];
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
+                acc[C - 2] += w * o.z;
+                acc[C - 1] += w * o.w;
+            } else {
+                const float2 o = reinterpret_cast<const float2*>(p.part_o + pr * D)[lane];
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
+            }
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int64_t orow = ((int64_t)mt.b * p.T + t) * p.Hq + mt.h * p.G + r % p.G;
+    if (lane == 0) p.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D;
+    if (C == 4)
+        reinterpret_cast<uint2*>(out)[lane] =
+            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[C - 2] * inv, acc[C - 1] * inv));
+    else
+        reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+}
+
+bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Drafted tokens of a row tile: as many as fit 128 rows.
+int tile_tokens(int T, int G) { return std::min(T, 128 / G); }
+
+int64_t ws_part_offset() { return (kMaxCtas * (int64_t)sizeof(Meta) + 255) / 256 * 256; }
+
+template <int D>
+int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, int units,
+                int chunk, size_t smem, cudaStream_t s) {
+    static_assert(sizeof(TreeCtrl) <= 12288, "control block too large");
+    if (cudaFuncSetAttribute(tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem) != cudaSuccess)
+        return BSA_ERR_CUDA;
+    for (int u0 = 0; u0 < units; u0 += chunk) {
+        p.unit0 = u0;
+        p.units = std::min(chunk, units - u0);
+        tree_kernel<D><<<p.grid, kTreeThreads, smem, s>>>(tq, tk, tv, p);
+        if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+        if (p.grid < 2) continue;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)p.grid - 1, (unsigned)((p.tq * p.G + 7) / 8));
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p) != cudaSuccess) return BSA_ERR_CUDA;
+    }
+    return BSA_OK;
+}
+
+}  // namespace
+}  // namespace bsa
+
+extern "C" {
+
+int64_t bsa_tree_attention_workspace(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D) {
+    if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv || Hq / Hkv > 128) return 0;
+    const int64_t rows = (int64_t)bsa::tile_tokens(T, Hq / Hkv) * (Hq / Hkv);
+    return bsa::ws_part_offset() + 2ll * bsa::kMaxCtas * rows * (D + 2) * (int64_t)sizeof(float);
+}
+
+int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* workspace, int64_t workspace_bytes,
+                       bsa_stream_t stream) {
+    if (!a) return BSA_ERR_INVALID_ARG;
+    int st = bsa::check_page_cache(c);
+    if (st != BSA_OK) return st;
+    if (a->B <= 0 || a->T <= 0 || a->Hq <= 0 || a->Hq % c->Hkv || c->layers != 1 || c->n_seqs != a->B)
+        return BSA_ERR_INVALID_ARG;
+    if (!a->q || !a->context_len || !a->out || !a->lse || !c->page_table) return BSA_ERR_INVALID_ARG;
+    if (!bsa::al(a->q, 16) || !bsa::al(a->out, 16) || !bsa::al(a->lse, 4) || !bsa::al(a->context_len, 4) ||
+        !bsa::al(a->draft_len, 4) || !bsa::al(a->tree_mask, 8) || !bsa::al(a->row_ptr, 4) || !bsa::al(a->col_idx, 4))
+        return BSA_ERR_INVALID_ARG;
+    if ((a->row_ptr != nullptr) != (a->col_idx != nullptr) || a->col_capacity < 0) return BSA_ERR_INVALID_ARG;
+    if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return BSA_ERR_INVALID_ARG;
+    if (a->T > BSA_MAX_DRAFT || a->Hq / c->Hkv > 128) return BSA_ERR_UNSUPPORTED;
+    if (!workspace || !bsa::al(workspace, 256)) return BSA_ERR_INVALID_ARG;
+    if (workspace_bytes < bsa_tree_attention_workspace(a->B, a->T, a->Hq, c->Hkv, c->D)) return BSA_ERR_CAPACITY;
+    bsa::TreeParams p{};
+    p.G = a->Hq / c->Hkv;
+    p.tq = bsa::tile_tokens(a->T, p.G);
+    p.RT = (a->T + p.tq - 1) / p.tq;
+    // the steps of one launch stay below 2^30 (sums and range ends fit an int)
+    const int64_t mult = a->row_ptr ? p.RT : (int64_t)c->Hkv * p.RT;
+    const int64_t most = ((int64_t)c->max_pages * c->page + bsa::kStep - 1) / bsa::kStep;
+    const int64_t units = a->row_ptr ? (int64_t)a->B * c->Hkv : a->B;
+    if ((int64_t)a->B * a->T > INT32_MAX || units >= INT32_MAX || mult * most > 1 << 30) return BSA_ERR_INVALID_ARG;
+    const int chunk = (int)std::min<int64_t>(bsa::kMaxUnits, (1 << 30) / (mult * most));
+    int sms;
+    if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
+    const int rows = p.tq * p.G, nbox = c->D / 64;
+    p.q_box = (rows + 7) / 8 * 1024;
+    const int tile = nbox * bsa::kStep * 128;
+    p.n_slots = std::min(bsa::kMaxSlots, (bsa::kTreeSmem - 12288 - 2 * nbox * p.q_box) / tile);
+    const size_t smem = (size_t)2 * nbox * p.q_box + (size_t)p.n_slots * tile + 12288;
+    CUtensorMap tq, tk, tv;
+    const uint64_t krows = (uint64_t)c->n_pages * c->Hkv * c->page;
+    if ((st = bsa::encode_token_rows_bf16(&tq, a->q, (uint64_t)a->B * a->T, a->Hq, c->D, p.G, p.tq)) != BSA_OK) return st;
+    if ((st = bsa::encode_rows_bf16(&tk, c->k, krows, c->D, c->page)) != BSA_OK) return st;
+    if ((st = bsa::encode_rows_bf16(&tv, c->v, krows, c->D, c->page)) != BSA_OK) return st;
+    p.ctx = a->context_len;
+    p.dl = a->draft_len;
+    p.row_ptr = a->row_ptr;
+    p.col_idx = a->col_idx;
+    p.table = c->page_table;
+    p.mask = reinterpret_cast<const unsigned long long*>(a->tree_mask);
+    p.col_cap = a->col_capacity;
+    p.B = a->B;
+    p.T = a->T;
+    p.Hq = a->Hq;
+    p.Hkv = c->Hkv;
+    p.page = c->page;
+    p.P = c->max_pages;
+    p.n_pages = c->n_pages;
+    p.grid = std::min(sms, bsa::kMaxCtas);
+    p.out = a->out;
+    p.lse = a->lse;
+    p.meta = static_cast<bsa::Meta*>(workspace);
+    p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + bsa::ws_part_offset());
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * bsa::kMaxCtas * rows * c->D);
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.wait_limit_ns = bsa::wait_limit_ns();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return c->D == 128 ? bsa::launch_tree<128>(tq, tk, tv, p, (int)units, chunk, smem, s)
+                       : bsa::launch_tree<64>(tq, tk, tv, p, (int)units, chunk, smem, s);
+}
+
+}  // extern "C"

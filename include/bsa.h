@@ -396,7 +396,10 @@ int bsa_validate_csr(const bsa_shape *sh, const int32_t *row_ptr, const int32_t 
  * skipped; bit 4 = malformed row_ptr row treated as empty; bit 8 = a kernel
  * found its launch unusable (misaligned shared memory) and did nothing.  bit 16 =
  * the CSR held more entries than the col_capacity given to bsa_backward (the
- * extra ones were dropped).
+ * extra ones were dropped); bit 32 = a paged-cache call met a page-table
+ * entry, slot, sequence id or draft index out of range (that access was
+ * skipped); bit 64 = a page request was refused (bsa_cache_resize,
+ * bsa_cache_fork).
  * Returns BSA_ERR_DEVICE_CHECK when the word was non-zero.
  */
 int bsa_device_error(int32_t *code_out);
@@ -559,6 +562,209 @@ int bsa_merge_partial_blocks(float *o_acc, float *lse_acc, const float *o_part, 
 
 /* y = bf16(x), round to nearest even; n % 8 == 0, x and y 16-byte aligned. */
 int bsa_convert_f32_bf16(const float *x, void *y, int64_t n, bsa_stream_t stream);
+
+/*
+ * From a projection to the attention, and the gradients back
+ * ---------------------------------------------------------
+ * bsa_qk_norm_rope: the RMS norm of every query and key head and the position
+ * rotation in one pass.  It reads token-major rows (views of a projection,
+ * any strides) and writes the head-major contiguous tensors that bsa_forward
+ * takes, key and value heads repeated kv_repeat times (bsa_forward has one
+ * key head per query head).  For a head row x at position t:
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (no weight: y = x)
+ *   of the first rotary_dim values, pair i is (y[i], y[i + rotary_dim/2]) or,
+ *   interleaved, (y[2i], y[2i+1]); with the angle t * inv_freq[i] it becomes
+ *   gain * (y_a cos - y_b sin, y_b cos + y_a sin); the rest stays as it is.
+ * Values are only moved.  Arithmetic in fp32, one rounding to bf16 at the end;
+ * angles are exact to 2^-20 for every int32 position (see csrc/bsa_rope.cu).
+ */
+#define BSA_ROPE_PLAIN 0     /* f_i = base^(-2i/rotary_dim) */
+#define BSA_ROPE_LINEAR 1    /* f_i / factor: positions interpolated */
+#define BSA_ROPE_BASE 2      /* base * factor^(rotary_dim/(rotary_dim-2)) */
+#define BSA_ROPE_BY_PARTS 3  /* f_i * (ramp + (1 - ramp)/factor), ramp from 0 to 1 as the turns
+                                original_length * f_i / (2 pi) go from low to high */
+typedef struct {
+    int32_t rotary_dim;      /* even, > 0 (> 2 for BSA_ROPE_BASE) */
+    int32_t scaling;         /* BSA_ROPE_* */
+    double base, factor;     /* > 0 */
+    double original_length;  /* BSA_ROPE_BY_PARTS: > 0 */
+    double low, high;        /* BSA_ROPE_BY_PARTS: low < high */
+} bsa_rope_spec;
+
+/* inv_freq: HOST double [rotary_dim / 2].  Host only. */
+int bsa_rope_inv_freq(const bsa_rope_spec *s, double *inv_freq);
+
+typedef struct {
+    int32_t B, N, Hq, Hkv, D;    /* D in {64, 128}; B * N may be 0 (nothing to do) */
+    int32_t rotary_dim;          /* 0 .. D, a multiple of 16; 0: no rotation */
+    int32_t kv_repeat;           /* >= 1 */
+    int32_t interleaved;         /* 0 or 1 */
+    float eps, gain;             /* eps >= 0 */
+    const void *q, *k, *v;       /* device bf16; row (b, n, h) at b*stride[0] + n*stride[1] + h*stride[2]
+                                    elements, its D values contiguous; strides multiples of 8, >= 0;
+                                    v may be NULL (then v_out is) */
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    const double *inv_freq;      /* device [rotary_dim / 2] */
+    const int32_t *positions;    /* device, position of (b, n) at b*position_stride + n; NULL: n
+                                    (bsa_cache_append: the slot) */
+    int64_t position_stride;
+    const float *q_weight, *k_weight;  /* device [D]; NULL: that side has no norm */
+} bsa_norm_rope_args;
+
+/*   q_out  device bf16 [B, Hq, N, D];  k_out, v_out  [B, Hkv*kv_repeat, N, D]; 16-byte aligned */
+int bsa_qk_norm_rope(const bsa_norm_rope_args *a, void *q_out, void *k_out, void *v_out, bsa_stream_t stream);
+
+/*
+ * Its gradients.  `a` as in the forward (q and k are read where that side has
+ * a norm; v is not read).  The copies of a repeated head are summed in fp32.
+ *   dq, dk, dv    device bf16 head-major (bsa_backward's results); dv may be NULL (then v is)
+ *   q, k, v       gradients, device bf16, token-major with their own strides
+ *                 (multiples of 8, not 0 where the extent is above 1)
+ *   q_weight, k_weight   device fp32 [D], 16-byte aligned; given exactly where `a` has the weight
+ *   workspace     device, bsa_qk_norm_rope_backward_workspace(D) bytes, 16-byte
+ *                 aligned, needed when there is a weight: partial sums of the
+ *                 weights' gradients, added in a fixed order.  Calls that overlap
+ *                 on the GPU need workspaces of their own.
+ */
+typedef struct {
+    const void *dq, *dk, *dv;
+    void *q, *k, *v;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    float *q_weight, *k_weight;
+} bsa_norm_rope_grads;
+int64_t bsa_qk_norm_rope_backward_workspace(int32_t D);
+int bsa_qk_norm_rope_backward(const bsa_norm_rope_args *a, const bsa_norm_rope_grads *g, void *workspace,
+                              int64_t workspace_bytes, bsa_stream_t stream);
+
+/*
+ * Paged key/value cache
+ * ---------------------
+ * A page holds `page` consecutive slots of one sequence (the attention's key
+ * block); slot s of sequence b lives in page page_table[b][s / page], row
+ * s % page.  The pools belong to the caller.  Unless said otherwise the calls
+ * work on one layer (layers = 1: pass the layer's part of a larger pool).
+ * Table entries, slots and ids are checked on the device: one out of range is
+ * skipped and reported by bsa_device_error (bit 32), never dereferenced.
+ */
+typedef struct {
+    void *k, *v;             /* device bf16 [layers, n_pages, Hkv, page, D], 16-byte aligned */
+    int32_t layers, n_pages, Hkv, page, D;  /* page in {64, 128}, D in {64, 128}; n_pages*Hkv*page < 2^31 */
+    int32_t *page_table;     /* device [n_seqs, max_pages]; -1: no page */
+    int32_t n_seqs, max_pages;
+} bsa_page_cache;
+
+/*
+ * bsa_qk_norm_rope for the new tokens of a served batch: the rotated queries
+ * go to q_out (token-major, what bsa_tree_attention takes), the rotated keys
+ * and the values straight into their pages.
+ *   a         B = 1, N = tokens, kv_repeat = 1; v is needed; positions NULL: the slots
+ *   seq_ids   device [tokens]: row of the page table; < 0: padding (nothing is read or written)
+ *   slots     device [tokens]: the sequence's slot to write
+ *   q_out     device bf16 [tokens, Hq, D]
+ * Two tokens with the same sequence and slot: either one's rows stay.
+ */
+int bsa_cache_append(const bsa_norm_rope_args *a, const bsa_page_cache *c, const int32_t *seq_ids,
+                     const int32_t *slots, void *q_out, bsa_stream_t stream);
+
+#define BSA_MAX_DRAFT 64
+
+/*
+ * Attention of drafted tokens over a paged cache (T = 1: plain decoding).
+ * Sequence b has context_len[b] committed slots and draft_len[b] drafted
+ * tokens in the slots behind them.  Draft t attends to every committed slot
+ * and to the drafts u whose bit is set in tree_mask[b][t] (its ancestors and
+ * itself); with block lists, only to those of them that lie in listed pages.
+ *   q            device bf16 [B, T, Hq, D];  query head h reads key head h / (Hq / Hkv)
+ *   context_len  device [B]
+ *   draft_len    device [B], 0 .. T; NULL: T.  Rows t >= draft_len[b] of out and
+ *                lse are left as they were.
+ *   tree_mask    device uint64 [B, T]; NULL: a chain (u <= t).  Bits from draft_len[b] on
+ *                are ignored.
+ *   row_ptr, col_idx   optional device CSR with rows r = b * Hkv + h: the logical
+ *                pages (slot / page) that row reads, distinct, in any order; entries
+ *                outside [0, max_pages) are skipped and flagged (bit 2), a decreasing
+ *                row_ptr counts as an empty row (bit 4).  Both NULL: every page.
+ *                col_capacity: entries col_idx holds; rows are read only below it.
+ *   out          device bf16 [B, T, Hq, D];  lse  device fp32 [B, T, Hq] (natural log;
+ *                -inf and O = 0 for a row that sees nothing)
+ * Slots behind the drafts, unlisted pages and pages of other sequences may
+ * hold anything, NaN included.  K and V of a sequence's own slots must be finite.
+ * Limits: 1 <= T <= BSA_MAX_DRAFT, Hq a multiple of Hkv, Hq / Hkv <= 128.
+ *   workspace    device, bsa_tree_attention_workspace(...) bytes, 256-byte aligned:
+ *                partial results of rows split over several SMs.  Calls that
+ *                overlap on the GPU need workspaces of their own.
+ */
+typedef struct {
+    int32_t B, T, Hq;
+    const void *q;
+    const int32_t *context_len, *draft_len;
+    const uint64_t *tree_mask;
+    const int32_t *row_ptr, *col_idx;
+    int64_t col_capacity;
+    void *out;
+    float *lse;
+    float scale;
+} bsa_tree_args;
+int64_t bsa_tree_attention_workspace(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D);
+int bsa_tree_attention(const bsa_tree_args *a, const bsa_page_cache *c, void *workspace, int64_t workspace_bytes,
+                       bsa_stream_t stream);
+
+/*
+ * After verification: the accepted drafts' K and V rows move up, so that the
+ * sequence is contiguous again: slot context_len[b] + i takes the row of slot
+ * context_len[b] + accepted[b][i] for i < n_accepted[b], in every layer, and
+ * new_len[b] = context_len[b] + n_accepted[b].
+ *   accepted    device int32 [n_seqs, T], the first n_accepted[b] strictly
+ *               increasing and in [0, T); a sequence whose list is not, or that
+ *               lacks a page for it, is reported (bit 32), keeps its rows and gets
+ *               new_len[b] = context_len[b]
+ *   n_accepted  device [n_seqs], 0 .. T;  new_len  device [n_seqs] (not context_len itself)
+ *   T           1 .. BSA_MAX_DRAFT
+ */
+int bsa_cache_accept(const bsa_page_cache *c, const int32_t *context_len, const int32_t *accepted,
+                     const int32_t *n_accepted, int32_t T, int32_t *new_len, bsa_stream_t stream);
+
+/*
+ * Pages of the pool.  page_ref (device int32 [n_pages]) counts the table
+ * entries that hold a page; 0 is free.  A row of the table holds its pages in
+ * front and -1 behind them.  All layers move together.  Requests are served in
+ * order from the pages that are free when the call starts, lowest number first
+ * (pages that the same call gives back are taken by later calls); the first
+ * one that finds too few, and every later one that needs any, is refused.
+ *   granted   device int32 [n]: 1 served, 0 refused; a refused request changes
+ *             nothing and sets bit 64 of the error word.  Refused too: an id outside
+ *             [0, n_seqs), lengths out of range, a row whose entries are no live
+ *             pages, and the later ones of several requests for the same sequence.
+ *   workspace device, bsa_cache_pages_workspace(n, n_seqs, n_pages) bytes, 256-byte aligned.
+ * Sequences that a call names, and their sources, must not be written by
+ * kernels that overlap with it.
+ *
+ * bsa_cache_resize: sequence seqs[i] keeps its first keep[i] slots and holds
+ * pages for capacity[i] >= keep[i] of them (0, 0 frees it).  From slot keep[i]
+ * on every page belongs to this sequence alone: shared ones are given back,
+ * and a shared page that is kept in part is copied.
+ * bsa_cache_fork: sequence dst[i], which holds no page, gets the first len[i]
+ * slots of src[i]: full pages are shared, the rows of a part-filled last page
+ * are copied to a page of its own.  One source may be forked several times.
+ */
+int64_t bsa_cache_pages_workspace(int32_t n, int32_t n_seqs, int32_t n_pages);
+int bsa_cache_resize(const bsa_page_cache *c, int32_t *page_ref, int32_t n, const int32_t *seqs, const int32_t *keep,
+                     const int32_t *capacity, int32_t *granted, void *workspace, int64_t workspace_bytes,
+                     bsa_stream_t stream);
+int bsa_cache_fork(const bsa_page_cache *c, int32_t *page_ref, int32_t n, const int32_t *src, const int32_t *dst,
+                   const int32_t *len, int32_t *granted, void *workspace, int64_t workspace_bytes,
+                   bsa_stream_t stream);
+
+/*
+ * Defragmentation: the live pages move to the front of the pool.  With L live
+ * pages, the k-th live page at L or above moves to the k-th free page below
+ * L; the whole table and page_ref follow.
+ *   new_page   device int32 [n_pages]: where each page went, -1 for free pages
+ * Workspace as above with n = 0.  Entries of the table outside [0, n_pages)
+ * are left alone; one that names a free page becomes -1 and is reported (bit 32).
+ */
+int bsa_cache_compact(const bsa_page_cache *c, int32_t *page_ref, int32_t *new_page, void *workspace,
+                      int64_t workspace_bytes, bsa_stream_t stream);
 
 /* Human-readable text of a bsa_status (static storage). */
 const char *bsa_status_string(int status);
