@@ -47,6 +47,9 @@ class _ForwardArgs(ctypes.Structure):
                 ("causal", ctypes.c_int32), ("out_fp32", ctypes.c_int32)]
 
 
+# Argument structures of the projection and paged-cache calls.  The Python
+# layer packs them with struct (rope.py, paged.py), three times faster than
+# filling these.
 class _RopeSpec(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
                 ("factor", ctypes.c_double), ("original_length", ctypes.c_double), ("low", ctypes.c_double),
@@ -143,21 +146,19 @@ def lib():
                 "bsa_debug_stall_next_forward": ([i32], ctypes.c_int),
                 "bsa_forward_noalloc": ([PS, P, P, P, P, P, P, P, ctypes.c_float, i32, P], ctypes.c_int),
                 "bsa_release_workspace": ([], None),
-                "bsa_rope_inv_freq": ([ctypes.POINTER(_RopeSpec), P], ctypes.c_int),
-                "bsa_qk_norm_rope": ([ctypes.POINTER(_NormRopeArgs), P, P, P, P], ctypes.c_int),
+                # struct arguments: packed bytes, or a ctypes structure by reference
+                "bsa_rope_inv_freq": ([P, P], ctypes.c_int),
+                "bsa_qk_norm_rope": ([P, P, P, P, P], ctypes.c_int),
                 "bsa_qk_norm_rope_backward_workspace": ([i32], i64),
-                "bsa_qk_norm_rope_backward": ([ctypes.POINTER(_NormRopeArgs), ctypes.POINTER(_NormRopeGrads), P, i64,
-                                               P], ctypes.c_int),
-                "bsa_cache_append": ([ctypes.POINTER(_NormRopeArgs), ctypes.POINTER(_PageCache), P, P, P, P],
-                                     ctypes.c_int),
+                "bsa_qk_norm_rope_backward": ([P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_append": ([P, P, P, P, P, P], ctypes.c_int),
                 "bsa_tree_attention_workspace": ([i32, i32, i32, i32, i32], i64),
-                "bsa_tree_attention": ([ctypes.POINTER(_TreeArgs), ctypes.POINTER(_PageCache), P, i64, P],
-                                       ctypes.c_int),
-                "bsa_cache_accept": ([ctypes.POINTER(_PageCache), P, P, P, i32, P, P], ctypes.c_int),
+                "bsa_tree_attention": ([P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_accept": ([P, P, P, P, i32, P, P], ctypes.c_int),
                 "bsa_cache_pages_workspace": ([i32, i32, i32], i64),
-                "bsa_cache_resize": ([ctypes.POINTER(_PageCache), P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
-                "bsa_cache_fork": ([ctypes.POINTER(_PageCache), P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
-                "bsa_cache_compact": ([ctypes.POINTER(_PageCache), P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_resize": ([P, P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_fork": ([P, P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_compact": ([P, P, P, P, i64, P], ctypes.c_int),
             }
             for name, (args, res) in sigs.items():
                 f = getattr(L, name)
@@ -189,31 +190,37 @@ class _NoScope:
 _NO_SCOPE = _NoScope()
 
 
-def _scope(device: torch.device, stream):
-    """Context in which a call on tensors of `device` allocates and launches:
-    the tensors' device, and `stream` (default: that device's current one), so
-    that what the call allocates belongs to the stream that uses it."""
+def _scope(index: int, stream):
+    """Context in which a call on tensors of CUDA device `index` allocates and
+    launches: that device, and `stream` (default: its current one), so that
+    what the call allocates belongs to the stream that uses it."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        if stream.device.index != index:
+            raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, index))
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
+    if index != torch.cuda.current_device():
+        return torch.cuda.device(index)
     return _NO_SCOPE
 
 
-def _same_device(first: torch.Tensor, *ts: Optional[torch.Tensor]) -> torch.device:
-    if not first.is_cuda:
+# Raw handle of a device's current stream.  (torch.cuda.current_stream builds a
+# stream object for it: 2.9 us a call against 0.1 us.)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _same_device(first: torch.Tensor, *ts: Optional[torch.Tensor]) -> int:
+    """CUDA device index of the tensors, which must share one."""
+    d = first.get_device()
+    if d < 0:
         raise ValueError("expected CUDA tensors")
-    d = first.device
     for t in ts:
-        if t is not None and t.device != d:
-            raise ValueError("tensors on different devices: %s and %s" % (d, t.device))
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors on different devices: cuda:%d and %s" % (d, t.device))
     return d
 
 
-def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _addr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -7,15 +7,18 @@ Marshalling only; contracts are in ``include/bsa.h`` and the kernels in
 
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import Optional, Tuple
 
 import torch
 
-from ._binding import (_NormRopeArgs, _NormRopeGrads, _RopeSpec, _Stride3, _addr, _check, _same_device, _scope,
-                       _stream, lib)
+from ._binding import _addr, _check, _raw_stream, _same_device, _scope, lib
 
 _SCALING = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
+_BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
+_SPEC = struct.Struct("@2i5d")              # bsa_rope_spec
+_ARGS = struct.Struct("@8i2f3P9qPPq2P")     # bsa_norm_rope_args
+_GRADS = struct.Struct("@6P9q2P")           # bsa_norm_rope_grads
 
 
 def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -29,66 +32,69 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: Optional[str]
     linear ramp between."""
     if scaling not in _SCALING:
         raise ValueError("scaling: None, 'linear', 'base' or 'by_parts'")
-    spec = _RopeSpec(int(rotary_dim), _SCALING[scaling], float(base), float(factor), float(original_length),
-                     float(low), float(high))
-    out = torch.empty(max(0, int(rotary_dim)) // 2, dtype=torch.float64)
-    _check("bsa_rope_inv_freq", lib().bsa_rope_inv_freq(ctypes.byref(spec), ctypes.c_void_p(out.data_ptr())))
+    spec = _SPEC.pack(int(rotary_dim), _SCALING[scaling], float(base), float(factor), float(original_length),
+                      float(low), float(high))
+    out = torch.empty(max(0, int(rotary_dim)) // 2, dtype=_F64)
+    _check("bsa_rope_inv_freq", lib().bsa_rope_inv_freq(spec, out.data_ptr() or None))
     return out.to(device)
 
 
 def _row_stride(t: torch.Tensor, what: str):
-    """(batch, token, head) strides in elements of a token-major bf16 tensor."""
-    if t.dtype != torch.bfloat16 or (t.stride(-1) != 1 and t.numel() > 0):
-        raise ValueError("%s: expected bf16 with contiguous head rows" % what)
-    # a dimension of one element has no stride worth checking
-    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
+    """(batch, token, head) strides in elements of a token-major bf16 tensor
+    ([tokens, heads, D]: batch 0).  An extent of one has no stride worth checking."""
+    if t.dtype is not _BF16:
+        raise ValueError("%s: expected bf16" % what)
+    if t.dim() == 4:
+        (b, n, h, _), (sb, sn, sh, sd) = t.shape, t.stride()
+    else:
+        (n, h, _), (sn, sh, sd) = t.shape, t.stride()
+        b, sb = 1, 0
+    if sd != 1:
+        raise ValueError("%s: head rows must be contiguous" % what)
+    return sb if b > 1 else 0, sn if n > 1 else 0, sh if h > 1 else 0
 
 
-def _side_args(q, k, v, inv_freq, positions, q_weight, k_weight, eps, gain, interleaved, kv_repeat, tokens_dims):
-    """Checks and C arguments shared by the forward, its gradients and the
-    cache append (tokens_dims: 2 for [B, N, H, D], 1 for [tokens, H, D])."""
-    nd = tokens_dims + 2
-    if q.dim() != nd or k.dim() != nd or (v is not None and v.shape != k.shape) \
-            or q.shape[:tokens_dims] != k.shape[:tokens_dims] or q.shape[-1] != k.shape[-1]:
+def _side_args(q, k, v, inv_freq, positions, q_weight, k_weight, eps, gain, interleaved, kv_repeat, batched):
+    """Checks and packed C arguments shared by the forward, its gradients and
+    the cache append (batched: [B, N, H, D], else [tokens, H, D])."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != (4 if batched else 3) or len(ks) != len(qs) or qs[:-2] != ks[:-2] or qs[-1] != ks[-1] \
+            or (v is not None and v.shape != ks):
         raise ValueError("expected q, k, v with one shape up to their number of heads (k, v alike)")
-    device = _same_device(q, k, v, inv_freq, positions, q_weight, k_weight)
-    Hq, D = q.shape[-2:]
-    B, N = q.shape[:2] if tokens_dims == 2 else (1, q.shape[0])
+    index = _same_device(q, k, v, inv_freq, positions, q_weight, k_weight)
+    if batched:
+        B, N, Hq, D = qs
+    else:
+        B, (N, Hq, D) = 1, qs
     rd = 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not _F64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq: contiguous float64 [rotary_dim / 2] (rope_inv_freq)")
         rd = 2 * inv_freq.numel()
     pos_stride = 0
     if positions is not None:
-        if positions.dtype != torch.int32 or (N > 1 and positions.stride(-1) != 1) or \
-                positions.shape[-1] != N or positions.dim() > tokens_dims or \
-                (positions.dim() == 2 and positions.shape[0] != B):
+        ps = positions.shape
+        if positions.dtype is not _I32 or not (ps == (N,) or (batched and ps == (B, N))) \
+                or (N > 1 and positions.stride(-1) != 1):
             raise ValueError("positions: int32 [N] or [B, N], one per token")
-        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+        pos_stride = positions.stride(0) if len(ps) == 2 and B > 1 else 0
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != torch.float32 or w.shape != (D,) or not w.is_contiguous()):
+        if w is not None and (w.dtype is not _F32 or w.shape != (D,) or not w.is_contiguous()):
             raise ValueError("norm weights: contiguous float32 [D]")
-    pad = [0] * (2 - tokens_dims)
-    st = [_Stride3(*(pad + _row_stride(t, n))) if t is not None else _Stride3() for t, n in
-          ((q, "q"), (k, "k"), (v, "v"))]
-    a = _NormRopeArgs(B, N, Hq, k.shape[-2], D, rd, int(kv_repeat), int(bool(interleaved)), float(eps), float(gain),
-                      _addr(q), _addr(k), _addr(v), st[0], st[1], st[2], _addr(inv_freq), _addr(positions),
-                      pos_stride, _addr(q_weight), _addr(k_weight))
-    return a, device, B, N, Hq, k.shape[-2], D
+    a = _ARGS.pack(B, N, Hq, ks[-2], D, rd, kv_repeat, 1 if interleaved else 0, eps, gain, q.data_ptr(),
+                   k.data_ptr(), _addr(v), *_row_stride(q, "q"), *_row_stride(k, "k"),
+                   *((0, 0, 0) if v is None else _row_stride(v, "v")), _addr(inv_freq), _addr(positions), pos_stride,
+                   _addr(q_weight), _addr(k_weight))
+    return a, index, B, N, Hq, ks[-2], D
 
 
-def _outputs(given, shapes, like):
-    """Contiguous bf16 tensors of `shapes`: the given ones, checked, or new ones."""
+def _output(given, shape, like):
+    """A contiguous bf16 tensor of `shape`: the given one, checked, or a new one."""
     if given is None:
-        return [None if s is None else torch.empty(s, dtype=torch.bfloat16, device=like.device) for s in shapes]
-    if len(given) != len(shapes):
-        raise ValueError("out: %d tensors" % len(shapes))
-    for t, s in zip(given, shapes):
-        if (t is None) != (s is None) or (t is not None and (t.shape != s or t.dtype != torch.bfloat16
-                                                             or not t.is_contiguous() or t.device != like.device)):
-            raise ValueError("out: contiguous bf16 tensors of shapes %s on %s" % (shapes, like.device))
-    return list(given)
+        return torch.empty(shape, dtype=_BF16, device=like.device)
+    if given.shape != shape or given.dtype is not _BF16 or not given.is_contiguous() or given.device != like.device:
+        raise ValueError("out: contiguous bf16 %s on %s" % (tuple(shape), like.device))
+    return given
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor] = None,
@@ -104,13 +110,18 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor] = N
 
     positions: int32 [N] or [B,N] (default 0..N-1).  inv_freq None: no
     rotation.  gain multiplies the rotated values.  out: (q, k, v) to write."""
-    a, device, B, N, Hq, Hkv, D = _side_args(q, k, v, inv_freq, positions, q_weight, k_weight, eps, gain,
-                                             interleaved, kv_repeat, 2)
-    kv = (B, Hkv * int(kv_repeat), N, D)
-    with _scope(device, stream):
-        oq, ok, ov = _outputs(out, [(B, Hq, N, D), kv, None if v is None else kv], q)
-        _check("bsa_qk_norm_rope", lib().bsa_qk_norm_rope(ctypes.byref(a), _addr(oq), _addr(ok), _addr(ov),
-                                                          _stream(None)))
+    a, index, B, N, Hq, Hkv, D = _side_args(q, k, v, inv_freq, positions, q_weight, k_weight, eps, gain,
+                                            interleaved, kv_repeat, True)
+    kv = (B, Hkv * kv_repeat, N, D)
+    oq, ok, ov = (None, None, None) if out is None else out
+    if v is None and ov is not None:
+        raise ValueError("out: no v to write")
+    with _scope(index, stream):
+        oq, ok = _output(oq, (B, Hq, N, D), q), _output(ok, kv, q)
+        ov = None if v is None else _output(ov, kv, q)
+        st = lib().bsa_qk_norm_rope(a, oq.data_ptr(), ok.data_ptr(), _addr(ov), _raw_stream(index))
+    if st:
+        _check("bsa_qk_norm_rope", st)
     return oq, ok, ov
 
 
@@ -126,30 +137,35 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, dv: Optional[torch
     Returns (q, k, v gradients, token-major bf16; q_weight, k_weight gradients,
     float32 or None).  out: the three token-major tensors to write, with any
     strides (slices of one gradient of a fused projection)."""
-    a, device, B, N, Hq, Hkv, D = _side_args(q, k, None, inv_freq, positions, q_weight, k_weight, eps, gain,
-                                             interleaved, kv_repeat, 2)
-    kv = (B, Hkv * int(kv_repeat), N, D)
+    a, index, B, N, Hq, Hkv, D = _side_args(q, k, None, inv_freq, positions, q_weight, k_weight, eps, gain,
+                                            interleaved, kv_repeat, True)
+    kv = (B, Hkv * kv_repeat, N, D)
     _same_device(q, dq, dk, dv)
     for t, s in ((dq, (B, Hq, N, D)), (dk, kv), (dv, kv)):
-        if t is not None and (t.shape != s or t.dtype != torch.bfloat16 or not t.is_contiguous()):
+        if t is not None and (t.shape != s or t.dtype is not _BF16 or not t.is_contiguous()):
             raise ValueError("dq, dk, dv: contiguous bf16 tensors of the forward's output shapes")
-    shapes = [(B, N, Hq, D), (B, N, Hkv, D), None if dv is None else (B, N, Hkv, D)]
-    with _scope(device, stream):
+    device = q.device
+    sq, sk = (B, N, Hq, D), (B, N, Hkv, D)
+    with _scope(index, stream):
         if out is None:
-            gq, gk, gv = (None if s is None else torch.empty(s, dtype=torch.bfloat16, device=device) for s in shapes)
+            gq = torch.empty(sq, dtype=_BF16, device=device)
+            gk = torch.empty(sk, dtype=_BF16, device=device)
+            gv = None if dv is None else torch.empty(sk, dtype=_BF16, device=device)
         else:
             gq, gk, gv = out
             _same_device(q, gq, gk, gv)
-            for t, s in zip((gq, gk, gv), shapes):
-                if (t is None) != (s is None) or (t is not None and t.shape != s):
-                    raise ValueError("out: token-major tensors of shapes %s" % (shapes,))
-        st = [_Stride3(*_row_stride(t, "out")) if t is not None else _Stride3() for t in (gq, gk, gv)]
-        gqw = torch.empty(D, dtype=torch.float32, device=device) if q_weight is not None else None
-        gkw = torch.empty(D, dtype=torch.float32, device=device) if k_weight is not None else None
-        n = int(lib().bsa_qk_norm_rope_backward_workspace(D)) if gqw is not None or gkw is not None else 0
+            if gq.shape != sq or gk.shape != sk or (gv is None) != (dv is None) or (gv is not None
+                                                                                    and gv.shape != sk):
+                raise ValueError("out: token-major tensors of shapes %s, %s, %s" % (sq, sk, sk))
+        gqw = torch.empty(D, dtype=_F32, device=device) if q_weight is not None else None
+        gkw = torch.empty(D, dtype=_F32, device=device) if k_weight is not None else None
+        L = lib()
+        n = int(L.bsa_qk_norm_rope_backward_workspace(D)) if gqw is not None or gkw is not None else 0
         ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-        g = _NormRopeGrads(_addr(dq), _addr(dk), _addr(dv), _addr(gq), _addr(gk), _addr(gv), st[0], st[1], st[2],
-                           _addr(gqw), _addr(gkw))
-        _check("bsa_qk_norm_rope_backward", lib().bsa_qk_norm_rope_backward(
-            ctypes.byref(a), ctypes.byref(g), _addr(ws), n, _stream(None)))
+        g = _GRADS.pack(dq.data_ptr(), dk.data_ptr(), _addr(dv), gq.data_ptr(), gk.data_ptr(), _addr(gv),
+                        *_row_stride(gq, "out"), *_row_stride(gk, "out"),
+                        *((0, 0, 0) if gv is None else _row_stride(gv, "out")), _addr(gqw), _addr(gkw))
+        st = L.bsa_qk_norm_rope_backward(a, g, _addr(ws), n, _raw_stream(index))
+    if st:
+        _check("bsa_qk_norm_rope_backward", st)
     return gq, gk, gv, gqw, gkw
