@@ -32,6 +32,11 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 64;  // rotary_dim / 2 <= 64
+constexpr int kFwdRows = 4;    // rows of a lane group's task (forward, large calls)
+constexpr int kFwdWaves = 8;   // forward CTAs per SM (two resident)
+constexpr int kBwdResident = 2, kBwdWaves = 4;  // the gradients' CTAs per SM: resident, in all
+constexpr int kBwdStages = 3;  // rows in a lane's ring
+constexpr int kBwdSmem = kBwdStages * 4 * kRopeThreads * 16;
 
 // Rows of one kind (q, k or v): token-major side and its head-major side.
 struct RopeSide {
@@ -47,6 +52,10 @@ struct RopeSide {
     int32_t rep;                // head-major copies of each
     int32_t ctas;               // CTAs working on this kind
     int32_t rotate;             // 0 for values
+    // backward: heads side by side in a CTA, tokens side by side, runs of such
+    // heads per task, tasks per token block, tasks in all
+    int32_t hs, toks, runs, splits, tasks;
+    int64_t z_copy, z_step, x_step, dx_step;  // bytes to the next copy; from the last copy's end, and on the token side, to the next row
 };
 
 struct RopeParams {
@@ -255,103 +264,232 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopePa
     }
 }
 
-// The gradients: the same items; a row needs its dz rows (one per copy) and,
-// with a norm, its x row.  The weight's gradient is summed per lane over all
-// of the CTA's rows, then over the CTA's lanes, into one row of `partial` per
-// CTA, which reduce_weight_kernel adds in a fixed order.
-template <int D, int U, bool IL>
-__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const RopeParams p) {
-    constexpr int LPR = D / 16, TB = kRopeThreads / LPR;
+// The gradients.  A CTA works on `hs` heads (a divisor of H, at most 8) of
+// `toks` consecutive tokens at a time, one row per lane group, so that both
+// sides are touched in runs: hs * D values of a token, toks * D of a head.  A
+// task is a block of tokens times `runs` such head groups, one after the
+// other, so a token's angles are computed once for them.  What a lane reads
+// of a row -- the two chunks of dz, one copy after the other, and of x --
+// goes through a ring of its own in shared memory (cp.async, kBwdStages rows
+// ahead, across task boundaries): registers hold one row only, and the loads
+// of three rows are always in flight behind the arithmetic.  No lane reads
+// another's slots, so the ring needs no barrier.
+// The weight's gradient is summed per lane over all of the CTA's rows, then
+// over the CTA's lanes, into one row of `partial` per CTA, which
+// reduce_weight_kernel adds in a fixed order.
+template <int D, bool REP>
+struct RowIter {
+    static constexpr int LPR = D / 16;
+    int task, left, c;  // task, rows left in it, copy of the row
+    bool live;          // the lane group has a token
+    const char *z, *x;
+    char* dst;
+
+    __device__ __forceinline__ void start(const RopeParams& p, const RopeSide& sd, int t, int* tok_out) {
+        task = t;
+        c = 0;
+        if (t >= sd.tasks) return;
+        const int tb = t / sd.splits, lg = threadIdx.x / LPR, sub = lg / sd.hs;
+        const int run0 = (t - tb * sd.splits) * sd.runs;
+        const int h = run0 * sd.hs + (lg - sub * sd.hs);
+        left = min(sd.runs, sd.H / sd.hs - run0);
+        const int64_t tok = (int64_t)tb * sd.toks + sub;
+        live = sub < sd.toks && tok < p.tokens;
+        const int64_t b = live ? (int)tok / p.N : 0, n = live ? tok - b * p.N : 0;
+        *tok_out = (int)(b * p.N + n);
+        x = static_cast<const char*>(sd.x) + 2 * (b * sd.sb + n * sd.sn + h * sd.sh);
+        dst = static_cast<char*>(sd.dx) + 2 * (b * sd.gb + n * sd.gn + h * sd.gh);
+        z = static_cast<const char*>(sd.dz) + ((b * sd.H + h) * sd.rep * (int64_t)p.N + n) * (D * 2);
+    }
+    // The next copy of the row, or the next row; true at the end of the task.
+    __device__ __forceinline__ bool next(const RopeSide& sd) {
+        if (REP) {
+            z += sd.z_copy;
+            if (++c < sd.rep) return false;
+            c = 0;
+        }
+        z += sd.z_step;
+        x += sd.x_step;
+        dst += sd.dx_step;
+        return --left == 0;
+    }
+};
+
+__device__ __forceinline__ void cp_async16(uint4* dst, const char* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, f2* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
+}
+__device__ __forceinline__ uint4 pack8(const f2* f) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+
+// Rotation of a lane's pairs, values two to a register pair (f[0..3] chunk a,
+// f[4..7] chunk b; cs and sn of pairs 2e, 2e + 1 in element e).
+template <bool IL>
+__device__ __forceinline__ void rotate16(f2* f, const f2* cs, const f2* sn) {
+    if (IL) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float c = e & 1 ? cs[e / 2].y : cs[e / 2].x, s = e & 1 ? sn[e / 2].y : sn[e / 2].x;
+            f[e] = {f[e].x * c - f[e].y * s, f[e].y * c + f[e].x * s};
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f2 a = f[e], b = f[e + 4], ns = {-sn[e].x, -sn[e].y};
+            f[e] = fma2(a, cs[e], mul2(b, ns));
+            f[e + 4] = fma2(b, cs[e], mul2(a, sn[e]));
+        }
+    }
+}
+
+// The rows of one kind that this CTA takes; acc: this lane's share of the
+// weight's gradient.  NORM: the kind has a weight; REP: its rows have copies.
+template <int D, bool IL, bool NORM, bool REP>
+__device__ __forceinline__ void bwd_rows(const RopeParams& p, const RopeSide& sd, int idx, uint4* ring,
+                                         const unsigned long long* turns, const float* wsh, f2* acc) {
+    constexpr int LPR = D / 16, C4 = kRopeThreads;
+    const Lane<D, IL> ln(p.rd);
+    RowIter<D, REP> pre, cur;
+    int tok = 0, pre_tok;
+    pre.start(p, sd, idx, &pre_tok);
+    cur.start(p, sd, idx, &tok);
+    uint4* mine = ring + threadIdx.x;
+    const int oa = ln.ca * 16, ob = ln.cb * 16;
+    auto fetch = [&](int stage) {
+        if (pre.task < sd.tasks) {
+            uint4* r = mine + stage * 4 * C4;
+            const int bytes = pre.live ? 16 : 0;
+            cp_async16(r, pre.z + oa, bytes);
+            cp_async16(r + C4, pre.z + ob, bytes);
+            if (NORM && (!REP || pre.c == 0)) {
+                cp_async16(r + 2 * C4, pre.x + oa, bytes);
+                cp_async16(r + 3 * C4, pre.x + ob, bytes);
+            }
+            if (pre.next(sd)) pre.start(p, sd, pre.task + sd.ctas, &pre_tok);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kBwdStages - 1; ++s) fetch(s);
+    __syncthreads();  // turns and weights
+    f2 cs[4], sn[4], g[8], x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = x[e] = {0.f, 0.f};
+    const bool turn = sd.rotate && ln.rot;
+    bool fresh = true;
+    int stage = 0;
+    while (cur.task < sd.tasks) {
+        if (fresh && turn) {
+            fresh = false;
+            float c[8], s[8];
+            lane_angles(turns, ln.s, p.pos ? p.pos[tok / p.N * p.pos_sb + tok % p.N] : tok % p.N, p.gain, c, s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = {c[2 * e], c[2 * e + 1]};
+                sn[e] = {-s[2 * e], -s[2 * e + 1]};
+            }
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 2) : "memory");
+        const uint4* r = mine + stage * 4 * C4;
+        if (!REP || cur.c == 0) {
+            unpack8(r[0], g);
+            unpack8(r[C4], g + 4);
+            if (NORM) {
+                unpack8(r[2 * C4], x);
+                unpack8(r[3 * C4], x + 4);
+            }
+        } else {
+            f2 t[8];
+            unpack8(r[0], t);
+            unpack8(r[C4], t + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = add2(g[e], t[e]);
+        }
+        // the slot read in the step before is free
+        fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
+        stage = stage + 1 == kBwdStages ? 0 : stage + 1;
+        char* dst = cur.dst;
+        const bool live = cur.live, more = REP && cur.c + 1 < sd.rep;
+        if (cur.next(sd)) {
+            cur.start(p, sd, cur.task + sd.ctas, &tok);
+            fresh = true;
+        }
+        if (more) continue;
+        if (turn) rotate16<IL>(g, cs, sn);
+        if (NORM) {
+            f2 ss = {0.f, 0.f}, sg = {0.f, 0.f}, gw[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 w4 = *reinterpret_cast<const float4*>(wsh + (q < 2 ? ln.ca : ln.cb) * 8 + (q & 1) * 4);
+                gw[2 * q] = mul2(g[2 * q], {w4.x, w4.y});
+                gw[2 * q + 1] = mul2(g[2 * q + 1], {w4.z, w4.w});
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fma2(x[e], x[e], ss);
+                sg = fma2(gw[e], x[e], sg);
+            }
+            const float rr = rsqrtf(row_sum<LPR>(ss.x + ss.y) * (1.f / D) + p.eps);
+            const float c = row_sum<LPR>(sg.x + sg.y) * (-1.f / D) * rr * rr * rr;
+            const float ra = live ? rr : 0.f;  // lanes without a token add nothing
+            const f2 r2 = {rr, rr}, c2 = {c, c}, a2 = {ra, ra};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                acc[e] = fma2(g[e], mul2(x[e], a2), acc[e]);
+                g[e] = fma2(x[e], c2, mul2(gw[e], r2));
+            }
+        }
+        if (live) {
+            *reinterpret_cast<uint4*>(dst + oa) = pack8(g);
+            *reinterpret_cast<uint4*>(dst + ob) = pack8(g + 4);
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <int D, bool IL>
+__global__ void __launch_bounds__(kRopeThreads, kBwdResident) norm_rope_bwd_kernel(const RopeParams p) {
+    constexpr int LPR = D / 16;
+    extern __shared__ uint4 ring[];  // [stage][dz a, dz b, x a, x b][thread]
     __shared__ unsigned long long turns[kMaxPairs];
     __shared__ float red[kRopeThreads / 32][D];
+    __shared__ __align__(16) float wsh[D];
     int idx;
-    const int kind = cta_side(p, &idx);
-    const RopeSide& sd = p.side[kind];
-    const Lane<D, IL> ln(p.rd);
+    const RopeSide& sd = p.side[cta_side(p, &idx)];
     griddep_launch_dependents();
-    load_turns(p, turns);
-    float w[16], acc[16];
-    const bool norm = sd.w != nullptr;
+    if (sd.w)
+        for (int d = threadIdx.x; d < D; d += kRopeThreads) wsh[d] = sd.w[d];
+    if (sd.rotate)
+        for (int i = threadIdx.x; i < p.rd / 2; i += kRopeThreads) turns[i] = to_turns(p.inv_freq[i]);
+    f2 acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = {0.f, 0.f};
+    if (!sd.w) {
+        if (sd.rep == 1)
+            bwd_rows<D, IL, false, false>(p, sd, idx, ring, turns, wsh, acc);
+        else
+            bwd_rows<D, IL, false, true>(p, sd, idx, ring, turns, wsh, acc);
+        return;
+    }
+    if (sd.rep == 1)
+        bwd_rows<D, IL, true, false>(p, sd, idx, ring, turns, wsh, acc);
+    else
+        bwd_rows<D, IL, true, true>(p, sd, idx, ring, turns, wsh, acc);
+    const Lane<D, IL> ln(p.rd);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        acc[e] = 0.f;
-        w[e] = norm ? sd.w[(e < 8 ? ln.ca : ln.cb) * 8 + (e & 7)] : 1.f;
-    }
-    const int hgroups = (sd.H + U - 1) / U;
-    const int64_t items = (p.tokens + TB - 1) / TB * hgroups;
-    const int64_t sh8 = sd.sh / 8, gh8 = sd.gh / 8, zh8 = (int64_t)p.N * (D / 8);
-    for (int64_t it = idx; it < items; it += sd.ctas) {
-        const int hg = (int)(it % hgroups);
-        const int64_t tok = it / hgroups * TB + threadIdx.x / LPR;
-        const bool live = tok < p.tokens;
-        const int64_t b = live ? (int)tok / p.N : 0, n = live ? tok - b * p.N : 0;
-        const int h0 = hg * U;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sd.x) + b * sd.sb +
-                                                          n * sd.sn + h0 * sd.sh);
-        const uint4* dz = reinterpret_cast<const uint4*>(sd.dz) +
-                          ((b * sd.H + h0) * sd.rep * (int64_t)p.N + n) * (D / 8);
-        uint4 xa[U], xb[U], za[U], zb[U];
+        float a = e & 1 ? acc[e / 2].y : acc[e / 2].x;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool on = live && h0 + u < sd.H;
-            za[u] = on ? dz[u * sd.rep * zh8 + ln.ca] : make_uint4(0, 0, 0, 0);
-            zb[u] = on ? dz[u * sd.rep * zh8 + ln.cb] : make_uint4(0, 0, 0, 0);
-            xa[u] = on && norm ? src[u * sh8 + ln.ca] : make_uint4(0, 0, 0, 0);
-            xb[u] = on && norm ? src[u * sh8 + ln.cb] : make_uint4(0, 0, 0, 0);
-        }
-        float cs[8], sn[8];
-        const bool turn = sd.rotate && ln.rot;
-        if (turn && live) {
-            const int pos = p.pos ? p.pos[b * p.pos_sb + n] : (int)n;
-            lane_angles(turns, ln.s, pos, p.gain, cs, sn);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
-        }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(sd.dx) + b * sd.gb + n * sd.gn + h0 * sd.gh);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool on = live && h0 + u < sd.H;
-            float g[16];
-            unpack8(za[u], g);
-            unpack8(zb[u], g + 8);
-            for (int c = 1; c < sd.rep; ++c) {
-                if (!on) break;
-                float t[16];
-                unpack8(dz[(u * sd.rep + c) * zh8 + ln.ca], t);
-                unpack8(dz[(u * sd.rep + c) * zh8 + ln.cb], t + 8);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) g[e] += t[e];
-            }
-            if (turn && live) rotate16<IL>(g, cs, sn);
-            if (norm) {
-                float x[16], ss = 0.f, sg = 0.f;
-                unpack8(xa[u], x);
-                unpack8(xb[u], x + 8);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    ss = fmaf(x[e], x[e], ss);
-                    sg = fmaf(g[e] * w[e], x[e], sg);
-                }
-                const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-                const float c = row_sum<LPR>(sg) * (1.f / D) * r * r * r;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    if (on) acc[e] = fmaf(g[e], x[e] * r, acc[e]);
-                    g[e] = g[e] * w[e] * r - x[e] * c;
-                }
-            }
-            if (on) {
-                dst[u * gh8 + ln.ca] = pack8(g);
-                dst[u * gh8 + ln.cb] = pack8(g + 8);
-            }
-        }
-    }
-    if (!norm) return;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-#pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-        if ((threadIdx.x & 31) < LPR) red[threadIdx.x / 32][(e < 8 ? ln.ca : ln.cb) * 8 + (e & 7)] = acc[e];
+        for (int o = LPR; o < 32; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if ((threadIdx.x & 31) < LPR) red[threadIdx.x / 32][(e < 8 ? ln.ca : ln.cb) * 8 + (e & 7)] = a;
     }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kRopeThreads) {
@@ -403,13 +541,13 @@ __global__ void __launch_bounds__(1024) reduce_weight_kernel(const ReduceParams 
 
 // CTAs of each kind, in proportion to the bytes it moves (two per SM in all),
 // none without an item.
-void deal_ctas(RopeParams* p, int D, int U, int sm_count, const double* bytes) {
+void deal_ctas(RopeParams* p, int D, int U, int ctas, const double* bytes) {
     const int TB = kRopeThreads / (D / 16);
     const double all = bytes[0] + bytes[1] + bytes[2];
     for (int k = 0; k < 3; ++k) {
         RopeSide& sd = p->side[k];
         const int64_t items = sd.H > 0 ? (p->tokens + TB - 1) / TB * ((sd.H + U - 1) / U) : 0;
-        const int64_t share = std::max<int64_t>(1, (int64_t)std::lround(2.0 * sm_count * bytes[k] / all));
+        const int64_t share = std::max<int64_t>(1, (int64_t)std::lround(ctas * bytes[k] / all));
         sd.ctas = (int32_t)std::min(items, share);
     }
 }
@@ -438,21 +576,53 @@ cudaError_t launch_fwd(const RopeParams& p, int D, int U, bool il, cudaStream_t 
         return cudaGetLastError();
     };
     if (D == 128) {
-        if (U == 4) return il ? go(norm_rope_kernel<128, 4, true, APPEND>) : go(norm_rope_kernel<128, 4, false, APPEND>);
+        if (U == kFwdRows) return il ? go(norm_rope_kernel<128, kFwdRows, true, APPEND>) : go(norm_rope_kernel<128, kFwdRows, false, APPEND>);
         return il ? go(norm_rope_kernel<128, 1, true, APPEND>) : go(norm_rope_kernel<128, 1, false, APPEND>);
     }
-    if (U == 4) return il ? go(norm_rope_kernel<64, 4, true, APPEND>) : go(norm_rope_kernel<64, 4, false, APPEND>);
+    if (U == kFwdRows) return il ? go(norm_rope_kernel<64, kFwdRows, true, APPEND>) : go(norm_rope_kernel<64, kFwdRows, false, APPEND>);
     return il ? go(norm_rope_kernel<64, 1, true, APPEND>) : go(norm_rope_kernel<64, 1, false, APPEND>);
+}
+
+// The gradients' tasks and CTAs of each kind: all heads of a token block in
+// one task unless that leaves the SMs short of tasks.
+void deal_tasks(RopeParams* p, int D, int sm_count, const double* bytes) {
+    const int groups = kRopeThreads / (D / 16);
+    const int ctas = std::min(kBwdWaves * sm_count, kRopeMaxCtas);
+    const double all = bytes[0] + bytes[1] + bytes[2];
+    for (int k = 0; k < 3; ++k) {
+        RopeSide& sd = p->side[k];
+        if (sd.H == 0) continue;
+        sd.hs = 1;
+        for (int d = 2; d <= 2; ++d)
+            if (sd.H % d == 0) sd.hs = d;
+        sd.toks = groups / sd.hs;
+        const int64_t blocks = (p->tokens + sd.toks - 1) / sd.toks;
+        const int64_t share = std::max<int64_t>(1, (int64_t)std::lround(ctas * bytes[k] / all));
+        const int32_t all_runs = sd.H / sd.hs;
+        // at least 8 tasks for each of the kind's CTAs, or single runs
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(all_runs, 8 * share / std::max<int64_t>(1, blocks)));
+        sd.runs = (int32_t)((all_runs + want - 1) / want);
+        sd.splits = (all_runs + sd.runs - 1) / sd.runs;
+        sd.tasks = (int32_t)(blocks * sd.splits);
+        sd.ctas = (int32_t)std::min<int64_t>(sd.tasks, share);
+        // from a row (of rep copies) to the one hs heads on; next() has moved past its copies already
+        sd.z_copy = sd.rep > 1 ? (int64_t)p->N * D * 2 : 0;
+        sd.z_step = (int64_t)sd.hs * sd.rep * p->N * D * 2 - sd.rep * sd.z_copy;
+        sd.x_step = 2 * sd.hs * sd.sh;
+        sd.dx_step = 2 * sd.hs * sd.gh;
+    }
 }
 
 cudaError_t launch_bwd(const RopeParams& p, int D, bool il, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.side[0].ctas + p.side[1].ctas + p.side[2].ctas);
     auto go = [&](auto kern) {
-        kern<<<grid, kRopeThreads, 0, s>>>(p);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+        if (e != cudaSuccess) return e;
+        kern<<<grid, kRopeThreads, kBwdSmem, s>>>(p);
         return cudaGetLastError();
     };
-    if (D == 128) return il ? go(norm_rope_bwd_kernel<128, 2, true>) : go(norm_rope_bwd_kernel<128, 2, false>);
-    return il ? go(norm_rope_bwd_kernel<64, 2, true>) : go(norm_rope_bwd_kernel<64, 2, false>);
+    if (D == 128) return il ? go(norm_rope_bwd_kernel<128, true>) : go(norm_rope_bwd_kernel<128, false>);
+    return il ? go(norm_rope_bwd_kernel<64, true>) : go(norm_rope_bwd_kernel<64, false>);
 }
 
 bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -469,8 +639,8 @@ bool strides_ok(const int64_t* st) {
 // two CTAs' worth of items.
 int pick_heads(int64_t tokens, int D, int Hq, int Hkv, int sm_count) {
     const int TB = kRopeThreads / (D / 16);
-    const int64_t items = (tokens + TB - 1) / TB * ((Hq + 3) / 4 + 2 * ((Hkv + 3) / 4));
-    return items >= 2 * (int64_t)sm_count ? 4 : 1;
+    const int64_t items = (tokens + TB - 1) / TB * ((Hq + kFwdRows - 1) / kFwdRows + 2 * ((Hkv + kFwdRows - 1) / kFwdRows));
+    return items >= 2 * (int64_t)sm_count ? kFwdRows : 1;
 }
 
 int fill(const bsa_norm_rope_args* a, RopeParams* p) {
@@ -487,7 +657,9 @@ int fill(const bsa_norm_rope_args* a, RopeParams* p) {
         return BSA_ERR_INVALID_ARG;
     if (a->D != 64 && a->D != 128) return BSA_ERR_UNSUPPORTED;
     p->tokens = (int64_t)a->B * a->N;
-    if (p->tokens > INT32_MAX) return BSA_ERR_INVALID_ARG;
+    // a kind's tasks, of at least one head of 4 tokens, are counted in an int
+    if (p->tokens > INT32_MAX || (p->tokens / 4 + 1) * std::max(a->Hq, a->Hkv) > INT32_MAX - (1 << 16))
+        return BSA_ERR_INVALID_ARG;
     const void* x[3] = {a->q, a->k, a->v};
     const int64_t* st[3] = {a->q_stride, a->k_stride, a->v_stride};
     for (int k = 0; k < 3; ++k) {
@@ -562,7 +734,7 @@ int bsa_qk_norm_rope(const bsa_norm_rope_args* a, void* q_out, void* k_out, void
         bytes[k] = (double)p.side[k].H * (1 + p.side[k].rep);
     }
     const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, sms);
-    bsa::deal_ctas(&p, a->D, U, sms, bytes);
+    bsa::deal_ctas(&p, a->D, U, bsa::kFwdWaves * sms, bytes);
     const cudaError_t e =
         bsa::launch_fwd<false>(p, a->D, U, a->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
@@ -593,7 +765,7 @@ int bsa_cache_append(const bsa_norm_rope_args* a, const bsa_page_cache* c, const
     p.n_pages = c->n_pages;
     const double bytes[3] = {(double)a->Hq, (double)a->Hkv, (double)a->Hkv};
     const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, sms);
-    bsa::deal_ctas(&p, a->D, U, sms, bytes);
+    bsa::deal_ctas(&p, a->D, U, bsa::kFwdWaves * sms, bytes);
     const cudaError_t e =
         bsa::launch_fwd<true>(p, a->D, U, a->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
@@ -632,7 +804,6 @@ int bsa_qk_norm_rope_backward(const bsa_norm_rope_args* a, const bsa_norm_rope_g
     int32_t* err;
     int sms;
     if ((st = bsa::device_context(&err, &sms)) != BSA_OK) return st;
-    sms = std::min(sms, bsa::kRopeMaxCtas / 2);
     if (p.tokens == 0) {
         for (float* o : {g->q_weight, g->k_weight})
             if (o && cudaMemsetAsync(o, 0, (size_t)a->D * sizeof(float), s) != cudaSuccess) return BSA_ERR_CUDA;
@@ -650,7 +821,7 @@ int bsa_qk_norm_rope_backward(const bsa_norm_rope_args* a, const bsa_norm_rope_g
         bytes[k] = (double)sd.H * (1 + sd.rep + (sd.w ? 1 : 0));
     }
     p.side[2].partial = nullptr;
-    bsa::deal_ctas(&p, a->D, 2, sms, bytes);
+    bsa::deal_tasks(&p, a->D, sms, bytes);
     cudaError_t e = bsa::launch_bwd(p, a->D, a->interleaved != 0, s);
     if (e == cudaSuccess && dw) {
         bsa::ReduceParams r{{p.side[0].partial, p.side[1].partial},
