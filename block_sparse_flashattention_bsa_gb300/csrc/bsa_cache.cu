@@ -416,15 +416,17 @@ __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const PageR
     }
 }
 
-// One CTA per (sequence, head, K or V, layer): every accepted row is loaded
-// before the first one is written, since a row's new place may hold one that
-// still has to move.
-constexpr int kAcceptThreads = 128;
+// One CTA per (sequence, K or V, layer), so that the chain of dependent reads
+// (length, list, table) is walked once for all heads.  Heads go in groups of
+// at most 2048 16-byte pieces; of a group every accepted row is loaded before
+// the first one is written, since a row's new place may hold one that still
+// has to move.
+constexpr int kAcceptThreads = 256;
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const PageReq p, const int32_t* ctx_len,
                                                                 const int32_t* accepted, const int32_t* n_acc, int T,
                                                                 int32_t* new_len) {
-    __shared__ int from[64], to[64];  // page rows: page * page_size + row, per slot
-    const int b = blockIdx.x, h = blockIdx.y >> 1, is_v = blockIdx.y & 1;
+    __shared__ int64_t from[64], to[64];  // of head 0, in 16-byte pieces
+    const int b = blockIdx.x, is_v = blockIdx.y & 1, layer = blockIdx.y >> 1;
     const int ctx = ctx_len[b], na = n_acc[b], tid = threadIdx.x;
     bool ok = ctx >= 0 && na >= 0 && na <= T && ctx <= p.max_pages * p.page;
     if (ok && tid < na) {
@@ -437,33 +439,39 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const PageReq p,
                 const int64_t j = s[k] / p.page;
                 const int e = j < p.max_pages ? p.table[(int64_t)b * p.max_pages + j] : -1;
                 if ((unsigned)e >= (unsigned)p.n_pages) ok = false;
-                else (k ? to : from)[tid] = e * p.page + (int)(s[k] % p.page);
+                else (k ? to : from)[tid] = ((int64_t)e * p.Hkv * p.page + s[k] % p.page) * p.row16;
             }
         }
     }
     ok = __syncthreads_and(ok);
-    if (tid == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+    if (tid == 0 && blockIdx.y == 0) {
         new_len[b] = ok ? ctx + na : ctx;
         if (!ok) atomicOr(p.err, ERR_BAD_PAGE);
     }
-    if (!ok) return;
-    uint4* pool = (is_v ? p.v : p.k) + (int64_t)blockIdx.z * p.n_pages * p.Hkv * p.page * p.row16;
-    const int chunks = na * p.row16;  // at most 64 * 16
-    uint4 t[8];
-    auto at = [&](int pr, int c) {
-        const int pg = pr / p.page, r = pr % p.page;
-        return pool + (((int64_t)pg * p.Hkv + h) * p.page + r) * p.row16 + c;
-    };
+    if (!ok || na == 0) return;
+    const int64_t head = (int64_t)p.page * p.row16;
+    uint4* pool = (is_v ? p.v : p.k) + (int64_t)layer * p.n_pages * p.Hkv * head;
+    const int per = na * p.row16, group = max(1, 8 * kAcceptThreads / per);  // per <= 1024
+    for (int h0 = 0; h0 < p.Hkv; h0 += group) {
+        const int chunks = min(group, p.Hkv - h0) * per;
+        uint4 t[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const int c = u * kAcceptThreads + tid;
-        if (c < chunks && from[c / p.row16] != to[c / p.row16]) t[u] = *at(from[c / p.row16], c % p.row16);
-    }
-    __syncthreads();
+        for (int u = 0; u < 8; ++u) {
+            const int c = u * kAcceptThreads + tid;
+            if (c < chunks) {
+                const int h = c / per, i = (c - h * per) / p.row16, q = c - h * per - i * p.row16;
+                if (from[i] != to[i]) t[u] = pool[(h0 + h) * head + from[i] + q];
+            }
+        }
+        __syncthreads();
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const int c = u * kAcceptThreads + tid;
-        if (c < chunks && from[c / p.row16] != to[c / p.row16]) *at(to[c / p.row16], c % p.row16) = t[u];
+        for (int u = 0; u < 8; ++u) {
+            const int c = u * kAcceptThreads + tid;
+            if (c < chunks) {
+                const int h = c / per, i = (c - h * per) / p.row16, q = c - h * per - i * p.row16;
+                if (from[i] != to[i]) pool[(h0 + h) * head + to[i] + q] = t[u];
+            }
+        }
     }
 }
 
@@ -582,9 +590,9 @@ int bsa_cache_accept(const bsa_page_cache* c, const int32_t* context_len, const 
         return BSA_ERR_INVALID_ARG;
     for (const void* x : {(const void*)context_len, (const void*)accepted, (const void*)n_accepted, (const void*)new_len})
         if (!bsa::al(x, 4)) return BSA_ERR_INVALID_ARG;
-    if (2ll * c->Hkv > 65535 || c->layers > 65535) return BSA_ERR_UNSUPPORTED;
+    if (2ll * c->layers > 65535) return BSA_ERR_UNSUPPORTED;
     if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
-    const dim3 grid((unsigned)c->n_seqs, (unsigned)(2 * c->Hkv), (unsigned)c->layers);
+    const dim3 grid((unsigned)c->n_seqs, (unsigned)(2 * c->layers));
     bsa::accept_kernel<<<grid, bsa::kAcceptThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
         p, context_len, accepted, n_accepted, T, new_len);
     return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;

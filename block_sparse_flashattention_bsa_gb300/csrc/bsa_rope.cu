@@ -33,7 +33,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 64;  // rotary_dim / 2 <= 64
 constexpr int kFwdRows = 4;    // rows of a lane group's task (forward, large calls)
-constexpr int kFwdWaves = 8;   // forward CTAs per SM (two resident)
+constexpr int kFwdWaves = 16;  // forward CTAs per SM (two resident)
 constexpr int kBwdResident = 2, kBwdWaves = 4;  // the gradients' CTAs per SM: resident, in all
 constexpr int kBwdStages = 3;  // rows in a lane's ring
 constexpr int kBwdSmem = kBwdStages * 4 * kRopeThreads * 16;
@@ -79,35 +79,41 @@ __device__ __forceinline__ unsigned long long to_turns(double f) {
     return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+__device__ __forceinline__ void unpack8(const uint4& v, f2* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const f2* f) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
 }
 
 // A head row is spread over LPR = D / 16 lanes, 16 values (two 16-byte
-// chunks) each, placed so that both members of every pair sit in one lane:
-// halves (i, i + rd/2): chunks s and s + rd/16; interleaved (2i, 2i + 1):
-// chunks 2s and 2s + 1.  Either way lane s owns the pairs 8s .. 8s + 7, and
-// the lanes from rd/16 on own the values that are not rotated.
+// chunks) each, placed so that both members of every pair sit in one lane and
+// neighbouring lanes own neighbouring chunks (32-byte sectors used whole: with
+// chunks 2s and 2s + 1 in lane s the 16K gradients took 132 us instead of 86):
+//   interleaved (2i, 2i + 1): chunks s and s + LPR; pairs 4s .. and 4 (s + LPR) ..
+//   halves (i, i + rd/2), nr = rd/16 lanes: chunks s and s + nr, pairs 8s .. 8s + 7;
+//   the other lanes own the values that are not rotated.
 template <int D, bool IL>
 struct Lane {
     static constexpr int LPR = D / 16;
     int s, ca, cb;
-    bool rot;
+    bool ra, rb;  // chunk a / b is rotated
     __device__ Lane(int rd) {
         s = threadIdx.x % LPR;
         const int nr = rd / 16;
-        rot = s < nr;
-        ca = (IL || !rot) ? 2 * s : s;
-        cb = (IL || !rot) ? 2 * s + 1 : s + nr;
+        if (IL) {
+            ca = s;
+            cb = s + LPR;
+            ra = ca < 2 * nr;
+            rb = cb < 2 * nr;
+        } else {
+            ra = rb = s < nr;
+            ca = ra ? s : s + nr;
+            cb = ra ? s + nr : s + LPR;
+        }
     }
 };
 
@@ -120,32 +126,46 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // cos and sin of this lane's 8 pairs at position pos, times gain.
+template <int LPR, bool IL>
 __device__ __forceinline__ void lane_angles(const unsigned long long* turns, int s, int pos, float gain, float* cs,
                                             float* sn) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const unsigned long long t = turns[8 * s + e] * (unsigned long long)(long long)pos;
+        const int i = IL ? 4 * s + e + (e < 4 ? 0 : 4 * LPR - 4) : 8 * s + e;
+        const unsigned long long t = turns[i] * (unsigned long long)(long long)pos;
         const float a = (float)(int)(unsigned)(t >> 32) * 1.46291807926715968e-9f;  // 2 pi / 2^32
         cs[e] = __cosf(a) * gain;
         sn[e] = __sinf(a) * gain;
     }
 }
 
-// The lane's pairs rotated by (cs, sn): f[0..7] is chunk a, f[8..15] chunk b.
+// The lane's pairs rotated: f[0..3] chunk a, f[4..7] chunk b, two values each;
+// cs and sn hold pairs 2e and 2e + 1 in element e.
 template <bool IL>
-__device__ __forceinline__ void rotate16(float* f, const float* cs, const float* sn) {
+__device__ __forceinline__ void rotate16(f2* f, const f2* cs, const f2* sn, bool ra, bool rb) {
+    if (IL) {
+        if (ra) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int a = IL ? 2 * e : e, b = IL ? 2 * e + 1 : e + 8;
-        const float x = f[a], y = f[b];
-        f[a] = x * cs[e] - y * sn[e];
-        f[b] = y * cs[e] + x * sn[e];
+            for (int e = 0; e < 4; ++e) {
+                const float c = e & 1 ? cs[e / 2].y : cs[e / 2].x, s = e & 1 ? sn[e / 2].y : sn[e / 2].x;
+                f[e] = {f[e].x * c - f[e].y * s, f[e].y * c + f[e].x * s};
+            }
+        }
+        if (rb) {
+#pragma unroll
+            for (int e = 4; e < 8; ++e) {
+                const float c = e & 1 ? cs[e / 2].y : cs[e / 2].x, s = e & 1 ? sn[e / 2].y : sn[e / 2].x;
+                f[e] = {f[e].x * c - f[e].y * s, f[e].y * c + f[e].x * s};
+            }
+        }
+    } else if (ra) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f2 a = f[e], b = f[e + 4], ns = {-sn[e].x, -sn[e].y};
+            f[e] = fma2(a, cs[e], mul2(b, ns));
+            f[e + 4] = fma2(b, cs[e], mul2(a, sn[e]));
+        }
     }
-}
-
-__device__ __forceinline__ void load_turns(const RopeParams& p, unsigned long long* turns) {
-    for (int i = threadIdx.x; i < p.rd / 2; i += kRopeThreads) turns[i] = to_turns(p.inv_freq[i]);
-    __syncthreads();
 }
 
 // Which kind this CTA works on, and its index and count among that kind's CTAs.
@@ -169,14 +189,16 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopePa
     const int kind = cta_side(p, &idx);
     const RopeSide& sd = p.side[kind];
     const Lane<D, IL> ln(p.rd);
-    load_turns(p, turns);
-    float w[16];
+    // the first rows are requested before the frequencies are waited for
+    const double freq = sd.rotate && threadIdx.x < p.rd / 2 ? p.inv_freq[threadIdx.x] : 0.0;
+    bool first = true;
+    f2 w[8];
     const bool norm = sd.w != nullptr;
     if (norm) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            w[e] = sd.w[ln.ca * 8 + e];
-            w[8 + e] = sd.w[ln.cb * 8 + e];
+            const float* we = sd.w + (e < 4 ? ln.ca : ln.cb) * 8 + (2 * e & 7);
+            w[e] = {we[0], we[1]};
         }
     }
     const int hgroups = (sd.H + U - 1) / U;
@@ -185,11 +207,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopePa
         const int hg = (int)(it % hgroups);
         const int64_t tok = it / hgroups * TB + threadIdx.x / LPR;
         bool live = tok < p.tokens;
-        int seq = 0;
-        if (APPEND && live) {
-            seq = p.seq_ids[tok];
-            live = seq >= 0;
-        }
+        const int seq = APPEND && live ? p.seq_ids[tok] : 0;
+        const int slot = APPEND && live ? p.slots[tok] : 0;
         const int64_t b = live ? (int)tok / p.N : 0, n = live ? tok - b * p.N : 0;
         const int h0 = hg * U;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sd.x) + b * sd.sb +
@@ -202,11 +221,23 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopePa
             ra[u] = on ? src[u * sh8 + ln.ca] : make_uint4(0, 0, 0, 0);
             rb[u] = on ? src[u * sh8 + ln.cb] : make_uint4(0, 0, 0, 0);
         }
-        float cs[8], sn[8];
-        const bool turn = sd.rotate && ln.rot;
+        if (APPEND) live = live && seq >= 0;  // padding: read, not written
+        const int pos = !live ? 0 : p.pos ? p.pos[b * p.pos_sb + n] : APPEND ? slot : (int)n;
+        if (first) {
+            first = false;
+            if (threadIdx.x < p.rd / 2) turns[threadIdx.x] = to_turns(freq);
+            __syncthreads();
+        }
+        f2 cs[4], sn[4];
+        const bool turn = sd.rotate && (ln.ra || ln.rb);
         if (turn && live) {
-            const int pos = p.pos ? p.pos[b * p.pos_sb + n] : (APPEND ? p.slots[tok] : (int)n);
-            lane_angles(turns, ln.s, pos, p.gain, cs, sn);
+            float c[8], s[8];
+            lane_angles<LPR, IL>(turns, ln.s, pos, p.gain, c, s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = {c[2 * e], c[2 * e + 1]};
+                sn[e] = {s[2 * e], s[2 * e + 1]};
+            }
         }
         // where the row goes: base of head 0 and distance between heads, in 16-byte chunks
         uint4* dst = nullptr;
@@ -220,7 +251,6 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopePa
                 dh = D / 8;
             } else {
                 // a token outside the table, or a slot without a page, is reported and not written
-                const int slot = p.slots[tok];
                 int pg = -1;
                 if (seq < p.n_seqs && slot >= 0 && slot / p.page < p.max_pages)
                     pg = p.page_table[(int64_t)seq * p.max_pages + slot / p.page];
@@ -237,20 +267,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopePa
         for (int u = 0; u < U; ++u) {
             uint4 oa = ra[u], ob = rb[u];
             if (sd.rotate) {
-                float f[16];
+                f2 f[8];
                 unpack8(ra[u], f);
-                unpack8(rb[u], f + 8);
+                unpack8(rb[u], f + 4);
                 if (norm) {
-                    float ss = 0.f;
+                    f2 ss = {0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
-                    const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+                    for (int e = 0; e < 8; ++e) ss = fma2(f[e], f[e], ss);
+                    const float r = rsqrtf(row_sum<LPR>(ss.x + ss.y) * (1.f / D) + p.eps);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] *= r * w[e];
+                    for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2({r, r}, w[e]));
                 }
-                if (turn) rotate16<IL>(f, cs, sn);
+                if (turn) rotate16<IL>(f, cs, sn, ln.ra, ln.rb);
                 oa = pack8(f);
-                ob = pack8(f + 8);
+                ob = pack8(f + 4);
             }
             if (dst && h0 + u < sd.H) {
                 const int copies = APPEND ? 1 : sd.rep;
@@ -320,36 +350,6 @@ __device__ __forceinline__ void cp_async16(uint4* dst, const char* src, int byte
                  : "memory");
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, f2* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
-}
-__device__ __forceinline__ uint4 pack8(const f2* f) {
-    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
-                      pack_bf16x2(f[3].x, f[3].y));
-}
-
-// Rotation of a lane's pairs, values two to a register pair (f[0..3] chunk a,
-// f[4..7] chunk b; cs and sn of pairs 2e, 2e + 1 in element e).
-template <bool IL>
-__device__ __forceinline__ void rotate16(f2* f, const f2* cs, const f2* sn) {
-    if (IL) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float c = e & 1 ? cs[e / 2].y : cs[e / 2].x, s = e & 1 ? sn[e / 2].y : sn[e / 2].x;
-            f[e] = {f[e].x * c - f[e].y * s, f[e].y * c + f[e].x * s};
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const f2 a = f[e], b = f[e + 4], ns = {-sn[e].x, -sn[e].y};
-            f[e] = fma2(a, cs[e], mul2(b, ns));
-            f[e + 4] = fma2(b, cs[e], mul2(a, sn[e]));
-        }
-    }
-}
-
 // The rows of one kind that this CTA takes; acc: this lane's share of the
 // weight's gradient.  NORM: the kind has a weight; REP: its rows have copies.
 template <int D, bool IL, bool NORM, bool REP>
@@ -383,14 +383,14 @@ __device__ __forceinline__ void bwd_rows(const RopeParams& p, const RopeSide& sd
     f2 cs[4], sn[4], g[8], x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = x[e] = {0.f, 0.f};
-    const bool turn = sd.rotate && ln.rot;
+    const bool turn = sd.rotate && (ln.ra || ln.rb);
     bool fresh = true;
     int stage = 0;
     while (cur.task < sd.tasks) {
         if (fresh && turn) {
             fresh = false;
             float c[8], s[8];
-            lane_angles(turns, ln.s, p.pos ? p.pos[tok / p.N * p.pos_sb + tok % p.N] : tok % p.N, p.gain, c, s);
+            lane_angles<LPR, IL>(turns, ln.s, p.pos ? p.pos[tok / p.N * p.pos_sb + tok % p.N] : tok % p.N, p.gain, c, s);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 cs[e] = {c[2 * e], c[2 * e + 1]};
@@ -423,7 +423,7 @@ __device__ __forceinline__ void bwd_rows(const RopeParams& p, const RopeSide& sd
             fresh = true;
         }
         if (more) continue;
-        if (turn) rotate16<IL>(g, cs, sn);
+        if (turn) rotate16<IL>(g, cs, sn, ln.ra, ln.rb);
         if (NORM) {
             f2 ss = {0.f, 0.f}, sg = {0.f, 0.f}, gw[8];
 #pragma unroll

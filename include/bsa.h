@@ -658,7 +658,7 @@ typedef struct {
  * go to q_out (token-major, what bsa_tree_attention takes), the rotated keys
  * and the values straight into their pages.
  *   a         B = 1, N = tokens, kv_repeat = 1; v is needed; positions NULL: the slots
- *   seq_ids   device [tokens]: row of the page table; < 0: padding (nothing is read or written)
+ *   seq_ids   device [tokens]: row of the page table; < 0: padding (nothing is written)
  *   slots     device [tokens]: the sequence's slot to write
  *   q_out     device bf16 [tokens, Hq, D]
  * Two tokens with the same sequence and slot: either one's rows stay.
