@@ -21,15 +21,20 @@
 // workspace, and merge_kernel joins the parts in range order -- no atomics,
 // so results do not depend on timing.
 //
-// One CTA per SM, 6 warps:
-//   warps 0-3  softmax, thread = query row (TMEM lane): S from TMEM, P (bf16)
-//              back over it, the rows' maximum and sum in registers; the
-//              running maximum is raised only when it grows by more than 2^8;
-//              at an item's end O from TMEM to global memory.
-//   warp 4     producer: walks the CTA's range, resolves pages and TMA-loads Q
+// One CTA per SM, 10 warps:
+//   warps 0-7  softmax, thread = query row (TMEM lane): warpgroup h takes
+//              columns 64 h .. 64 h + 63 of every step, with an O accumulator,
+//              a running maximum and a sum of its own, so that the two need not
+//              meet before an item's end (where both write half of the joined
+//              row) and a step's softmax takes half as long.  The maximum is
+//              raised only when it grows by more than 2^8.  P goes back over S
+//              as two bf16 parts, high and low, so that its rounding (2^-17)
+//              does not add to the result's; the second product costs tensor
+//              time that is not the limit.
+//   warp 8     producer: walks the CTA's range, resolves pages and TMA-loads Q
 //              (two buffers) and the K / V tiles (a ring); publishes one
 //              description per step.
-//   warp 5     MMA: S = Q K^T and O += P V on tcgen05, M = 128 rows whatever
+//   warp 9     MMA: S = Q K^T and O += P V on tcgen05, M = 128 rows whatever
 //              T G is (the rows behind it compute on leftovers of shared
 //              memory and are never stored); the V rows of a page's unused
 //              slots are zeroed first, since 0 * NaN would reach O.
@@ -44,8 +49,8 @@
 namespace bsa {
 namespace {
 
-constexpr int kTreeThreads = 192;
-constexpr int kProducer = 4, kMma = 5;
+constexpr int kTreeThreads = 320;
+constexpr int kProducer = 8, kMma = 9;
 constexpr int kMaxUnits = 2048;   // units of one launch (their prefix sums sit in shared memory)
 constexpr int kMaxCtas = 160;     // partial slots are sized for this many
 constexpr int kMaxSlots = 12;     // K / V ring
@@ -53,7 +58,7 @@ constexpr int kInfos = 8;         // step descriptions ahead
 constexpr int kTreeSmem = 232448;
 constexpr int kStep = 128;        // key slots per step
 
-enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };
+enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };  // kFirst, kLast: of an item
 
 struct StepInfo {
     int flags;
@@ -76,9 +81,11 @@ struct TreeCtrl {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t i_full[kInfos], i_empty[kInfos];
+    uint64_t st_full[4];             // per pair of warps with the same rows: both posted their sums
     uint64_t drain;
     StepInfo info[kInfos];
-    int red[8];
+    float2 stats[2][128];            // [half][row]: maximum and sum posted at an item's end
+    int red[kTreeThreads / 32];
     uint32_t tmem_base;
     WaitFlag wf;
     int prefix[kMaxUnits + 1];
@@ -338,9 +345,13 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
         const uint64_t vdesc = VDESC + (smem_u32(tile) >> 4);
         if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < kStep / 16; ++kk)
-                mma_ts(tmem + O_COL, tmem + sb * kStep + kk * 8, vdesc + (uint64_t)((kk * 16 * 128) >> 4), IPV,
-                       (pfirst && kk == 0) ? 0u : 1u);
+            for (int kk = 0; kk < 2 * kStep / 16; ++kk) {
+                // 16 keys, high parts of P, then the same keys' low parts;
+                // keys 0-63 into one accumulator, 64-127 into the other
+                const int k16 = kk >> 1, h = k16 >> 2;
+                mma_ts(tmem + O_COL + h * D, tmem + sb * kStep + (k16 >> 1) * 32 + (kk & 1) * 16 + (k16 & 1) * 8,
+                       vdesc + (uint64_t)((k16 * 16 * 128) >> 4), IPV, (pfirst && kk % 8 == 0) ? 0u : 1u);
+            }
             mma_commit(&c->pv_done[sb]);
             mma_commit(&c->t_empty[pslot]);
         }
@@ -405,63 +416,66 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
 }
 
 // ---------------------------------------------------------------- softmax
+// Columns whose bit is 0 score -infinity (whatever stood there, NaN included).
+__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t vis) {
+#pragma unroll
+    for (int q = 0; q < 32; ++q)
+        if (!((vis >> q) & 1u)) s[q] = __float_as_uint(-INFINITY);
+}
+
+// Warpgroup wh (threads 128 wh ..): columns 64 wh .. of every step.
 template <int D>
 __device__ void tree_softmax(const TreeParams& p, TreeCtrl* c, uint32_t tmem, volatile WaitFlag* wf) {
     constexpr int O_COL = 2 * kStep;
-    const int row = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wh = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const uint32_t t_o = tmem + lanes + O_COL;
+    const uint32_t t_o = tmem + lanes + O_COL + wh * D;
     const int rt = row / p.G, rg = row - rt * p.G;  // drafted token (in the tile) and query head of this row
     const bool idle = warp * 32 >= p.tq * p.G;      // the whole warp lies behind the tile's rows
     float m = -INFINITY, l = 0.f;
     const f2 sl2 = {p.scale_log2, p.scale_log2};
+    uint32_t items = 0;
     for (uint32_t g = 0;; ++g) {
         const uint32_t is = g % kInfos, sb = g & 1;
         if (!twait(&c->i_full[is], (g / kInfos) & 1, wf)) break;
-        const StepInfo f = c->info[is];
+        const int flags = c->info[is].flags, slot0 = c->info[is].slot0[wh], nv = c->info[is].nv[wh];
+        const int b = c->info[is].b, h = c->info[is].h, t = c->info[is].t0 + rt;
+        const int ctx = c->info[is].ctx, dl = c->info[is].dl, part = c->info[is].part;
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->i_empty[is]);
-        if (f.flags & kEnd) break;
+        if (flags & kEnd) break;
         if (!twait(&c->s_full[sb], (g >> 1) & 1, wf)) break;
         tc_fence_after();
-        const int t = f.t0 + rt;
-        if (f.flags & kFirst) {
+        if (flags & kFirst) {
             m = -INFINITY;
             l = 0.f;
         }
         if (!idle) {
-            const uint32_t t_s = tmem + lanes + sb * kStep;
-            uint32_t s[4][32];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(t_s + x * 32, s[x]);
+            const uint32_t t_s = tmem + lanes + sb * kStep + wh * 64;
+            uint32_t s[2][32];
+            tmem_ld32(t_s, s[0]);
+            tmem_ld32(t_s + 32, s[1]);
             tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 4; ++x) reg_fence(s[x]);
-            if (f.flags & kMask) {
+            reg_fence(s[0]);
+            reg_fence(s[1]);
+            if (flags & kMask) {
                 unsigned long long bits = 0;
-                if (t < f.dl) {
-                    bits = p.mask ? p.mask[(int64_t)f.b * p.T + t] : (2ull << t) - 1;
-                    if (f.dl < 64) bits &= (1ull << f.dl) - 1;
+                if (t < dl) {
+                    bits = p.mask ? p.mask[(int64_t)b * p.T + t] : (2ull << t) - 1;
+                    if (dl < 64) bits &= (1ull << dl) - 1;
                 }
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const unsigned long long vis = f.nv[w] > 0 ? visible64(f.slot0[w], f.ctx, bits) : 0ull;
-                    const uint32_t v[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            if (!((v[x] >> q) & 1u)) s[2 * w + x][q] = __float_as_uint(-INFINITY);
-                }
+                const unsigned long long v = nv > 0 ? visible64(slot0, ctx, bits) : 0ull;
+                hide(s[0], (uint32_t)v);
+                hide(s[1], (uint32_t)(v >> 32));
             }
             float mx[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                mx[x] = __uint_as_float(s[x][0]);
+                const uint32_t* v = s[x >> 1] + (x & 1) * 16;
+                mx[x] = __uint_as_float(v[0]);
 #pragma unroll
-                for (int q = 1; q < 31; q += 2)
-                    mx[x] = fmax3(mx[x], __uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1]));
-                mx[x] = fmaxf(mx[x], __uint_as_float(s[x][31]));
+                for (int q = 1; q < 15; q += 2) mx[x] = fmax3(mx[x], __uint_as_float(v[q]), __uint_as_float(v[q + 1]));
+                mx[x] = fmaxf(mx[x], __uint_as_float(v[15]));
             }
             const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
             // raise the reference when it would grow by more than 2^8 (exact
@@ -473,11 +487,10 @@ __device__ void tree_softmax(const TreeParams& p, TreeCtrl* c, uint32_t tmem, vo
                     m = top;
                     l *= alpha;
                 }
-                if (!(f.flags & kFirst)) {
+                if (!(flags & kFirst)) {
                     // O must hold every earlier step's product before it is scaled
                     if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
                     tc_fence_after();
-                    __syncwarp();
 #pragma unroll 1
                     for (int x = 0; x < D / 32; ++x) {
                         uint32_t o[32];
@@ -494,17 +507,22 @@ __device__ void tree_softmax(const TreeParams& p, TreeCtrl* c, uint32_t tmem, vo
             const float ref = m == -INFINITY ? 0.f : m;
             const f2 nm2 = {-ref, -ref};
             f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            // 32 columns of P in the columns of their S: 16 of high parts, 16 of low
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t pk[16];
+            for (int x = 0; x < 2; ++x) {
+                uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const f2 a = fma2({__uint_as_float(s[x][2 * q]), __uint_as_float(s[x][2 * q + 1])}, sl2, nm2);
                     const f2 e = {ex2_approx(a.x), ex2_approx(a.y)};
                     sum[q & 1] = add2(sum[q & 1], e);
-                    pk[q] = pack_bf16x2(e.x, e.y);
+                    hi[q] = pack_bf16x2(e.x, e.y);
+                    const f2 n = {-__uint_as_float(hi[q] << 16), -__uint_as_float(hi[q] & 0xffff0000u)};
+                    const f2 r = add2(e, n);
+                    lo[q] = pack_bf16x2(r.x, r.y);
                 }
-                tmem_st16(t_s + x * 16, pk);
+                tmem_st16(t_s + x * 32, hi);
+                tmem_st16(t_s + x * 32 + 16, lo);
             }
             const f2 all = add2(sum[0], sum[1]);
             l += all.x + all.y;
@@ -513,44 +531,64 @@ __device__ void tree_softmax(const TreeParams& p, TreeCtrl* c, uint32_t tmem, vo
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->p_full[sb]);
-        if (!(f.flags & kLast)) continue;
-        // the item's (or its part's) result
+        if (!(flags & kLast)) continue;
+        // the item's (or its part's) result: both halves' sums and accumulators
         if (!twait(&c->pv_done[sb], (g >> 1) & 1, wf)) break;
-        tc_fence_after();
+        c->stats[wh][row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->st_full[warp]);
+        if (!twait(&c->st_full[warp], items & 1, wf)) break;
+        ++items;
         if (idle) continue;
-        const bool live = rt < p.tq && t < f.dl;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t orow = ((int64_t)f.b * p.T + t) * p.Hq + f.h * p.G + rg;
-        const int64_t prow = (int64_t)f.part * (p.tq * p.G) + row;
-        if (live) {
-            if (f.part < 0)
-                p.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-            else
-                p.part_ml[prow] = make_float2(m, l);
+        const float2 ml = c->stats[wh ^ 1][row];
+        tc_fence_after();
+        const bool live = rt < p.tq && t < dl;
+        const float mm = fmaxf(m, ml.x);
+        float w0 = m == -INFINITY ? 0.f : ex2_approx(m - mm);
+        float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+        const float sum = wh ? ml.y * w1 + l * w0 : l * w0 + ml.y * w1;  // the same in both halves
+        const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
+        const int64_t prow = (int64_t)part * (p.tq * p.G) + row;
+        if (part < 0) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            w0 *= inv;
+            w1 *= inv;
+            if (live && wh == 0) p.lse[orow] = sum > 0.f ? (mm + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        } else if (live && wh == 0) {
+            p.part_ml[prow] = make_float2(mm, sum);
         }
+        const f2 w02 = {w0, w0}, w12 = {w1, w1};
+        // this half writes columns wh * D/2 .. of the row
+        const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
 #pragma unroll 1
-        for (int x = 0; x < D / 32; ++x) {
-            uint32_t o[32];
+        for (int x = 0; x < D / 64; ++x) {
+            uint32_t o[32], o1[32];
             __syncwarp();
-            tmem_ld32(t_o + x * 32, o);
+            tmem_ld32(t_a + x * 32, o);
+            tmem_ld32(t_b + x * 32, o1);
             tmem_wait_ld();
             reg_fence(o);
+            reg_fence(o1);
             if (!live) continue;
-            if (f.part < 0) {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + x * 32);
+            f2 v[16];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[4];
+            for (int q = 0; q < 16; ++q)
+                v[q] = fma2({__uint_as_float(o1[2 * q]), __uint_as_float(o1[2 * q + 1])}, w12,
+                            mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w02));
+            const int64_t col = wh * (D / 2) + x * 32;
+            if (part < 0) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        w[y] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * y]) * inv,
-                                           __uint_as_float(o[8 * q + 2 * y + 1]) * inv);
-                    dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int q = 0; q < 4; ++q)
+                    dst[q] = make_uint4(pack_bf16x2(v[4 * q].x, v[4 * q].y),
+                                        pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
+                                        pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
+                                        pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
             } else {
-                uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + x * 32);
+                float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                for (int q = 0; q < 8; ++q)
+                    dst[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
             }
         }
         tc_fence_before();
@@ -583,13 +621,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(&c->q_full[x], 1);
             mbar_init(&c->q_empty[x], 1);
             mbar_init(&c->s_full[x], 1);
-            mbar_init(&c->p_full[x], 4);
+            mbar_init(&c->p_full[x], 8);
             mbar_init(&c->pv_done[x], 1);
         }
         for (int x = 0; x < kInfos; ++x) {
             mbar_init(&c->i_full[x], 1);
-            mbar_init(&c->i_empty[x], 5);
+            mbar_init(&c->i_empty[x], 9);  // the MMA warp and the eight softmax warps
         }
+        for (int x = 0; x < 4; ++x) mbar_init(&c->st_full[x], 2);
         mbar_init(&c->drain, 1);
         c->wf.abort = 0;
         c->wf.limit_ns = p.wait_limit_ns;
@@ -653,51 +692,63 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // ---------------------------------------------------------------- merge
 // Block x joins the item that the boundary in front of range x + 1 is the
-// first to cut; a warp per query row.  With parts i in range order:
-// m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.
-template <int D>
+// first to cut, RB query rows of it, 8 / RB warps to a row (each takes every
+// (8 / RB)-th part; their sums meet in shared memory).  With parts i in range
+// order: m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.
+template <int D, int RB>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
+    constexpr int WPR = 8 / RB, C = D / 32;
+    __shared__ float red[WPR > 1 ? WPR : 1][D + 1];
     griddep_wait();
-    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Meta mt = p.meta[c];
     if (mt.start < 0) return;
-    // range c is full or the last one; range c - 1 is always full
-    const int rows = p.tq * p.G;
-    const int per = p.meta[0].per;
-    const int first = c - 1;
+    const int rows = p.tq * p.G, per = mt.per, first = c - 1;
     if (mt.start < first * per) return;  // an earlier boundary cuts it too
     const int last = (mt.end - 1) / per;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int r = blockIdx.y * RB + warp / WPR, part = warp % WPR;
     const int t = mt.t0 + r / p.G;
-    if (r >= rows || t >= mt.dl) return;
+    const bool on = r < rows && t < mt.dl;
+    if (WPR == 1 && !on) return;
     auto slot_of = [&](int k) { return k == first && mt.start > first * per ? 2 * k + 1 : 2 * k; };
-    float m = -INFINITY;
-    for (int k = first + lane; k <= last; k += 32) m = fmaxf(m, p.part_ml[(int64_t)slot_of(k) * rows + r].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
-    constexpr int C = D / 32;
-    float acc[C];
+    float m = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
     for (int x = 0; x < C; ++x) acc[x] = 0.f;
-    if (m > -INFINITY) {
+    if (on) {
+        for (int k = first + lane; k <= last; k += 32) m = fmaxf(m, p.part_ml[(int64_t)slot_of(k) * rows + r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (m > -INFINITY) {
 #pragma unroll 4
-        for (int k = first; k <= last; ++k) {
-            const int64_t pr = (int64_t)slot_of(k) * rows + r;
-            const float2 ml = p.part_ml[pr];
-            const float w = ex2_approx(ml.x - m);
-            l += w * ml.y;
-            if (C == 4) {
-                const float4 o = reinterpret_cast<const float4*>(p.part_o + pr * D)[lane];
-                acc[0] += w * o.x;
-                acc[1] += w * o.y;
-                acc[C - 2] += w * o.z;
-                acc[C - 1] += w * o.w;
-            } else {
-                const float2 o = reinterpret_cast<const float2*>(p.part_o + pr * D)[lane];
-                acc[0] += w * o.x;
-                acc[1] += w * o.y;
+            for (int k = first + part; k <= last; k += WPR) {
+                const int64_t pr = (int64_t)slot_of(k) * rows + r;
+                const float2 ml = p.part_ml[pr];
+                const float w = ex2_approx(ml.x - m);
+                l += w * ml.y;
+                if (C == 4) {
+                    const float4 o = reinterpret_cast<const float4*>(p.part_o + pr * D)[lane];
+                    acc[0] += w * o.x;
+                    acc[1] += w * o.y;
+                    acc[C - 2] += w * o.z;
+                    acc[C - 1] += w * o.w;
+                } else {
+                    const float2 o = reinterpret_cast<const float2*>(p.part_o + pr * D)[lane];
+                    acc[0] += w * o.x;
+                    acc[1] += w * o.y;
+                }
             }
+        }
+    }
+    if (WPR > 1) {
+#pragma unroll
+        for (int x = 0; x < C; ++x) red[part][lane * C + x] = acc[x];
+        if (lane == 0) red[part][D] = l;
+        __syncthreads();
+        if (part > 0 || !on) return;
+        for (int w = 1; w < WPR; ++w) {
+#pragma unroll
+            for (int x = 0; x < C; ++x) acc[x] += red[w][lane * C + x];
+            l += red[w][D];
         }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -721,7 +772,7 @@ int64_t ws_part_offset() { return (kMaxCtas * (int64_t)sizeof(Meta) + 255) / 256
 template <int D>
 int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, int units,
                 int chunk, size_t smem, cudaStream_t s) {
-    static_assert(sizeof(TreeCtrl) <= 12288, "control block too large");
+    static_assert(sizeof(TreeCtrl) <= 14336, "control block too large");
     if (cudaFuncSetAttribute(tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem) != cudaSuccess)
         return BSA_ERR_CUDA;
     for (int u0 = 0; u0 < units; u0 += chunk) {
@@ -731,7 +782,9 @@ int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
         if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
         if (p.grid < 2) continue;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)p.grid - 1, (unsigned)((p.tq * p.G + 7) / 8));
+        // few rows: their parts are dealt over eight warps; many: a warp each
+        const int rows = p.tq * p.G, rb = rows <= 16 ? 1 : 8;
+        cfg.gridDim = dim3((unsigned)p.grid - 1, (unsigned)((rows + rb - 1) / rb));
         cfg.blockDim = dim3(256);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
@@ -739,7 +792,8 @@ int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p) != cudaSuccess) return BSA_ERR_CUDA;
+        if (cudaLaunchKernelEx(&cfg, rb == 1 ? tree_merge_kernel<D, 1> : tree_merge_kernel<D, 8>, p) != cudaSuccess)
+            return BSA_ERR_CUDA;
     }
     return BSA_OK;
 }
@@ -786,8 +840,8 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     const int rows = p.tq * p.G, nbox = c->D / 64;
     p.q_box = (rows + 7) / 8 * 1024;
     const int tile = nbox * bsa::kStep * 128;
-    p.n_slots = std::min(bsa::kMaxSlots, (bsa::kTreeSmem - 12288 - 2 * nbox * p.q_box) / tile);
-    const size_t smem = (size_t)2 * nbox * p.q_box + (size_t)p.n_slots * tile + 12288;
+    p.n_slots = std::min(bsa::kMaxSlots, (bsa::kTreeSmem - 14336 - 2 * nbox * p.q_box) / tile);
+    const size_t smem = (size_t)2 * nbox * p.q_box + (size_t)p.n_slots * tile + 14336;
     CUtensorMap tq, tk, tv;
     const uint64_t krows = (uint64_t)c->n_pages * c->Hkv * c->page;
     if ((st = bsa::encode_token_rows_bf16(&tq, a->q, (uint64_t)a->B * a->T, a->Hq, c->D, p.G, p.tq)) != BSA_OK) return st;
