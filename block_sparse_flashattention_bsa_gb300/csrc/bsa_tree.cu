@@ -36,8 +36,7 @@
 //              description per step.
 //   warp 9     MMA: S = Q K^T and O += P V on tcgen05, M = 128 rows whatever
 //              T G is (the rows behind it compute on leftovers of shared
-//              memory and are never stored); the V rows of a page's unused
-//              slots are zeroed first, since 0 * NaN would reach O.
+//              memory and are never stored).
 
 #include <algorithm>
 #include <cmath>
@@ -54,7 +53,8 @@ constexpr int kProducer = 8, kMma = 9;
 constexpr int kMaxUnits = 2048;   // units of one launch (their prefix sums sit in shared memory)
 constexpr int kMaxCtas = 160;     // partial slots are sized for this many
 constexpr int kMaxSlots = 12;     // K / V ring
-constexpr int kInfos = 8;         // step descriptions ahead
+constexpr int kInfos = 8;         // step descriptions ahead (more than the ring's kMaxSlots / 2 steps)
+static_assert(2 * kInfos > kMaxSlots + 2, "a description could be overwritten before its MMA");
 constexpr int kTreeSmem = 232448;
 constexpr int kStep = 128;        // key slots per step
 
@@ -67,7 +67,7 @@ struct StepInfo {
     int b, h, t0;  // sequence, key head, first drafted token of the row tile
     int ctx, dl;
     int part;      // -1: write the output, else the partial slot
-    int pad;
+    int vslot;     // ring slot of the V tile, bit 31: its phase
 };
 
 struct Meta {  // one per CTA: the item its range starts inside of
@@ -162,7 +162,7 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
     const int ppt = kStep / p.page;
     const int mult = p.row_ptr ? p.RT : p.Hkv * p.RT;
     uint32_t slot = 0, phase = 0, nload = 0, g = 0, nq = 0;
-    bool ok = true;
+    bool ok = true, ended = false;
     Meta mt{-1, 0, per, 0, 0, 0, 0, 0};
     if (lo < hi) {
         // the unit that holds step lo: last u with prefix[u] <= lo
@@ -234,8 +234,9 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
+                    if (leader) {
                         StepInfo& f = c->info[is];
+                        // written before the K tile's barrier is armed, by the same lane
                         const bool plain = nv0 == p.page && sl0 + p.page <= ctx &&
                                            (ppt == 1 || (nv1 == p.page && sl1 + p.page <= ctx));
                         f.flags = (st == s0 ? kFirst : 0) | (st + 1 == s1 ? kLast : 0) | (plain ? 0 : kMask);
@@ -249,6 +250,8 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
                         f.ctx = ctx;
                         f.dl = dl;
                         f.part = part;
+                        const bool wrap = slot + 1 == (uint32_t)p.n_slots;
+                        f.vslot = (wrap ? 0 : slot + 1) | ((phase ^ (wrap ? 1u : 0u)) << 31);
                         mbar_arrive(&c->i_full[is]);
                     }
                     __syncwarp();
@@ -285,24 +288,35 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
         }
     }
     if (ok) {
+        // the end mark, for the softmax warps and, with a slot's barrier, for the MMA lane
         const uint32_t is = g % kInfos;
-        if (twait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf) && lane == 0) {
+        if (twait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf) && twait(&c->t_empty[slot], phase ^ 1, wf) &&
+            leader) {
             c->info[is].flags = kEnd;
             mbar_arrive(&c->i_full[is]);
+            mbar_arrive(&c->t_full[slot]);
+            ended = true;
         }
     }
     if (lane == 0) p.meta[blockIdx.x] = mt;
     __syncwarp();
     if (leader) {
-        // copies still in flight must land before the CTA exits
+        // copies still in flight must land before the CTA exits (the end mark
+        // used the slot of the oldest one, which was consumed before)
         const uint32_t ns = (uint32_t)p.n_slots;
-        for (uint32_t n = nload > ns ? nload - ns : 0; n < nload; ++n)
+        for (uint32_t n = nload > ns ? nload - ns + (ended ? 1 : 0) : (ended && nload == ns ? 1 : 0); n < nload; ++n)
             mbar_wait_drain(&c->t_full[n % ns], (n / ns) & 1);
         for (uint32_t n = nq > 2 ? nq - 2 : 0; n < nq; ++n) mbar_wait_drain(&c->q_full[n & 1], (n >> 1) & 1);
     }
 }
 
 // ---------------------------------------------------------------- MMA
+// One lane does everything: a wait of the whole warp (vote included) costs
+// ~130 cycles even when its barrier is ready, and four of them per step left
+// the tensor pipe idle half the time (64-wide heads: 232 us instead of 198 for
+// 1.07 GB of cache).  Step descriptions come with the K tile's barrier: the
+// producer writes them before it arms it, and does not come round to them
+// again before the ring has (kInfos is more than the ring's steps).
 template <int D>
 __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, uint32_t tmem,
                          volatile WaitFlag* wf) {
@@ -310,40 +324,14 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
     constexpr uint64_t KDESC = sdesc_sw128_base(16, 1024), VDESC = sdesc_sw128_base(T_BOX, 1024);
     constexpr uint32_t IQK = idesc_bf16_f32(128, kStep, false), IPV = idesc_bf16_f32(128, D, true);
     constexpr int O_COL = 2 * kStep;
-    const int lane = threadIdx.x & 31;
-    const bool leader = elect_one();
-    uint32_t slot = 0, phase = 0, nq = 0;
-    bool pend = false, pfirst = false, ok = true;
-    uint32_t pslot = 0, pphase = 0, pg = 0;
-    int pnv0 = 0, pnv1 = 0;
-    auto step_slot = [&] {
-        if (++slot == (uint32_t)p.n_slots) {
-            slot = 0;
-            phase ^= 1;
-        }
-    };
-    auto issue_pv = [&]() -> bool {
-        const uint32_t sb = pg & 1;
-        if (!twait(&c->t_full[pslot], pphase, wf)) return false;
-        uint8_t* tile = sT + pslot * T_BYTES;
-        const int z0 = pnv0 > 0 && pnv0 < p.page ? pnv0 : p.page;  // rows z0 .. page of the first page
-        const int z1 = p.page == 64 && pnv1 > 0 && pnv1 < 64 ? pnv1 : 64;
-        if (z0 < p.page || z1 < 64) {
-            for (int x = lane; x < (p.page - z0) * 8 * NBOX; x += 32) {
-                const int row = z0 + x / (8 * NBOX), q = x % (8 * NBOX);
-                *reinterpret_cast<uint4*>(tile + (q >> 3) * T_BOX + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            for (int x = lane; x < (64 - z1) * 8 * NBOX; x += 32) {
-                const int row = 64 + z1 + x / (8 * NBOX), q = x % (8 * NBOX);
-                *reinterpret_cast<uint4*>(tile + (q >> 3) * T_BOX + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        if (!twait(&c->p_full[sb], (pg >> 1) & 1, wf)) return false;
-        tc_fence_after();
-        const uint64_t vdesc = VDESC + (smem_u32(tile) >> 4);
-        if (leader) {
+    if (elect_one()) {
+        uint32_t slot = 0, phase = 0, nq = 0, pslot = 0, pphase = 0;
+        bool pend = false, pfirst = false;
+        auto issue_pv = [&](uint32_t pg) -> bool {
+            const uint32_t sb = pg & 1;
+            if (!mbar_wait(&c->t_full[pslot], pphase, wf) || !mbar_wait(&c->p_full[sb], (pg >> 1) & 1, wf)) return false;
+            tc_fence_after();
+            const uint64_t vdesc = VDESC + (smem_u32(sT + pslot * T_BYTES) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 2 * kStep / 16; ++kk) {
                 // 16 keys, high parts of P, then the same keys' low parts;
@@ -354,33 +342,19 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
             }
             mma_commit(&c->pv_done[sb]);
             mma_commit(&c->t_empty[pslot]);
-        }
-        __syncwarp();
-        return true;
-    };
-    for (uint32_t g = 0; ok; ++g) {
-        const uint32_t is = g % kInfos;
-        if (!twait(&c->i_full[is], (g / kInfos) & 1, wf)) {
-            ok = false;
-            break;
-        }
-        const int flags = c->info[is].flags, nv0 = c->info[is].nv[0], nv1 = c->info[is].nv[1];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->i_empty[is]);
-        if (flags & kEnd) break;
-        const uint32_t qb = nq & 1;
-        if ((flags & kFirst) && !twait(&c->q_full[qb], (nq >> 1) & 1, wf)) {
-            ok = false;
-            break;
-        }
-        if (!twait(&c->t_full[slot], phase, wf)) {
-            ok = false;
-            break;
-        }
-        tc_fence_after();
-        const uint32_t sb = g & 1;
-        const uint64_t kdesc = KDESC + (smem_u32(sT + slot * T_BYTES) >> 4);
-        if (leader) {
+            return true;
+        };
+        for (uint32_t g = 0;; ++g) {
+            if (!mbar_wait(&c->t_full[slot], phase, wf)) break;
+            const int flags = c->info[g % kInfos].flags;
+            if (flags & kEnd) {
+                if (pend) issue_pv(g - 1);
+                break;
+            }
+            const uint32_t sb = g & 1, qb = nq & 1;
+            if ((flags & kFirst) && !mbar_wait(&c->q_full[qb], (nq >> 1) & 1, wf)) break;
+            tc_fence_after();
+            const uint64_t kdesc = KDESC + (smem_u32(sT + slot * T_BYTES) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t qd = KDESC + (smem_u32(sQ + (qb * NBOX + (kk >> 2)) * p.q_box + (kk & 3) * 32) >> 4);
@@ -389,26 +363,25 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
             }
             mma_commit(&c->s_full[sb]);
             mma_commit(&c->t_empty[slot]);
-            if (flags & kLast) mma_commit(&c->q_empty[qb]);
+            if (flags & kLast) {
+                mma_commit(&c->q_empty[qb]);
+                ++nq;
+            }
+            if (pend && !issue_pv(g - 1)) break;
+            pend = true;
+            pfirst = flags & kFirst;
+            // the V tile follows in the ring
+            if (++slot == (uint32_t)p.n_slots) {
+                slot = 0;
+                phase ^= 1;
+            }
+            pslot = slot;
+            pphase = phase;
+            if (++slot == (uint32_t)p.n_slots) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
-        __syncwarp();
-        step_slot();
-        if (flags & kLast) ++nq;
-        if (pend && !issue_pv()) {
-            ok = false;
-            break;
-        }
-        pend = true;
-        pfirst = flags & kFirst;
-        pslot = slot;
-        pphase = phase;
-        pg = g;
-        pnv0 = nv0;
-        pnv1 = nv1;
-        step_slot();
-    }
-    if (ok && pend) issue_pv();
-    if (leader) {
         mma_commit(&c->drain);
         mbar_wait_drain(&c->drain, 0);
     }
@@ -425,7 +398,7 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t vis) {
 
 // Warpgroup wh (threads 128 wh ..): columns 64 wh .. of every step.
 template <int D>
-__device__ void tree_softmax(const TreeParams& p, TreeCtrl* c, uint32_t tmem, volatile WaitFlag* wf) {
+__device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint32_t tmem, volatile WaitFlag* wf) {
     constexpr int O_COL = 2 * kStep;
     const int wh = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -441,9 +414,24 @@ __device__ void tree_softmax(const TreeParams& p, TreeCtrl* c, uint32_t tmem, vo
         const int flags = c->info[is].flags, slot0 = c->info[is].slot0[wh], nv = c->info[is].nv[wh];
         const int b = c->info[is].b, h = c->info[is].h, t = c->info[is].t0 + rt;
         const int ctx = c->info[is].ctx, dl = c->info[is].dl, part = c->info[is].part;
+        const uint32_t vslot = (uint32_t)c->info[is].vslot;
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->i_empty[is]);
         if (flags & kEnd) break;
+        // The V rows of a page's unused slots are zeroed (this half's keys):
+        // their weights are 0, but 0 * NaN would reach O.  A page that holds
+        // nothing was not loaded, its rows are zeros already.
+        const int used = p.page == 64 ? nv : nv > 0 ? min(max(nv - wh * 64, 0), 64) : 64;
+        if (flags & kMask && used < 64 && (p.page == 128 || nv > 0)) {
+            if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
+            uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
+            for (int x = row; x < (64 - used) * 8 * (D / 64); x += 128) {
+                const int r = x / (D / 8), q = x % (D / 8);
+                *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+        }
         if (!twait(&c->s_full[sb], (g >> 1) & 1, wf)) break;
         tc_fence_after();
         if (flags & kFirst) {
@@ -626,7 +614,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         for (int x = 0; x < kInfos; ++x) {
             mbar_init(&c->i_full[x], 1);
-            mbar_init(&c->i_empty[x], 9);  // the MMA warp and the eight softmax warps
+            mbar_init(&c->i_empty[x], 8);  // the softmax warps
         }
         for (int x = 0; x < 4; ++x) mbar_init(&c->st_full[x], 2);
         mbar_init(&c->drain, 1);
@@ -679,7 +667,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     else if (warp == kMma)
         tree_mma<D>(p, sQ, sT, c, tmem, wf);
     else
-        tree_softmax<D>(p, c, tmem, wf);
+        tree_softmax<D>(p, sT, c, tmem, wf);
     __syncwarp();
     tc_fence_before();
     __syncthreads();

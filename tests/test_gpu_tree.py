@@ -308,3 +308,16 @@ def test_streams_graphs_and_overlap(bsa):
     ref = bsa.tree_attention(*a.dev, scale=a.scale)
     assert torch.equal(oa[0], ref[0]) and torch.equal(oa[1], ref[1]) and torch.equal(ob[0], rb[0])
     assert bsa.device_error() == 0
+
+
+def test_no_wait_runs_out(bsa):
+    """Whole calls stay far below the 2 s that a pipeline wait may last (an end
+    of the pipeline that waits in vain would still give the right numbers)."""
+    import time
+    c = Case(8, 1, 8, 2, 128, 128, [1500 + 100 * i for i in range(8)], mask=None)
+    c.run(bsa)
+    torch.cuda.synchronize()
+    t = time.monotonic()
+    bsa.tree_attention(*c.dev, scale=c.scale)
+    torch.cuda.synchronize()
+    assert time.monotonic() - t < 1.0 and bsa.device_error() == 0
