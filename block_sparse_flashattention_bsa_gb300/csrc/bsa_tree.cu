@@ -80,7 +80,7 @@ struct TreeCtrl {
     uint64_t t_full[kMaxSlots], t_empty[kMaxSlots];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t i_full[kInfos], i_empty[kInfos];
+    uint64_t i_empty[kInfos];
     uint64_t st_full[4];             // per pair of warps with the same rows: both posted their sums
     uint64_t drain;
     StepInfo info[kInfos];
@@ -252,7 +252,6 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
                         f.part = part;
                         const bool wrap = slot + 1 == (uint32_t)p.n_slots;
                         f.vslot = (wrap ? 0 : slot + 1) | ((phase ^ (wrap ? 1u : 0u)) << 31);
-                        mbar_arrive(&c->i_full[is]);
                     }
                     __syncwarp();
                     ++g;
@@ -288,12 +287,11 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
         }
     }
     if (ok) {
-        // the end mark, for the softmax warps and, with a slot's barrier, for the MMA lane
+        // the end mark, with a slot's barrier; the MMA lane passes it on
         const uint32_t is = g % kInfos;
         if (twait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf) && twait(&c->t_empty[slot], phase ^ 1, wf) &&
             leader) {
             c->info[is].flags = kEnd;
-            mbar_arrive(&c->i_full[is]);
             mbar_arrive(&c->t_full[slot]);
             ended = true;
         }
@@ -313,10 +311,12 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
 // ---------------------------------------------------------------- MMA
 // One lane does everything: a wait of the whole warp (vote included) costs
 // ~130 cycles even when its barrier is ready, and four of them per step left
-// the tensor pipe idle half the time (64-wide heads: 232 us instead of 198 for
-// 1.07 GB of cache).  Step descriptions come with the K tile's barrier: the
+// the tensor pipe idle half the time (4 contexts of 128K slots, 16 drafts, 8
+// key heads of 64: 232 us; 200 us now).  Step descriptions come with the K tile's barrier: the
 // producer writes them before it arms it, and does not come round to them
-// again before the ring has (kInfos is more than the ring's steps).
+// again before the ring has (kInfos is more than the ring's steps).  The lane
+// passes them on with its own arrival on the scores' barrier, so the softmax
+// has one wait per step.
 template <int D>
 __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, uint32_t tmem,
                          volatile WaitFlag* wf) {
@@ -348,7 +348,9 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
             if (!mbar_wait(&c->t_full[slot], phase, wf)) break;
             const int flags = c->info[g % kInfos].flags;
             if (flags & kEnd) {
-                if (pend) issue_pv(g - 1);
+                if (pend && !issue_pv(g - 1)) break;
+                mbar_arrive(&c->s_full[g & 1]);
+                mbar_arrive(&c->s_full[g & 1]);
                 break;
             }
             const uint32_t sb = g & 1, qb = nq & 1;
@@ -362,6 +364,7 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
                        kk > 0 ? 1u : 0u);
             }
             mma_commit(&c->s_full[sb]);
+            mbar_arrive(&c->s_full[sb]);  // what this lane has seen (the step's description) the softmax sees
             mma_commit(&c->t_empty[slot]);
             if (flags & kLast) {
                 mma_commit(&c->q_empty[qb]);
@@ -396,6 +399,28 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t vis) {
         if (!((vis >> q) & 1u)) s[q] = __float_as_uint(-INFINITY);
 }
 
+// p = 2^(s * sl2 - m) of 64 columns as bf16 high and low parts; their sum.
+// m = -infinity: nothing was visible yet (0 stands in, every p is 0).
+__device__ __forceinline__ f2 weights(const uint32_t (&s)[2][32], f2 sl2, float m, uint32_t (&hi)[2][16],
+                                      uint32_t (&lo)[2][16]) {
+    const float ref = m == -INFINITY ? 0.f : m;
+    const f2 nm2 = {-ref, -ref};
+    f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const f2 a = fma2({__uint_as_float(s[x][2 * q]), __uint_as_float(s[x][2 * q + 1])}, sl2, nm2);
+            const f2 e = {ex2_approx(a.x), ex2_approx(a.y)};
+            sum[q & 1] = add2(sum[q & 1], e);
+            hi[x][q] = pack_bf16x2(e.x, e.y);
+            const f2 n = {-__uint_as_float(hi[x][q] << 16), -__uint_as_float(hi[x][q] & 0xffff0000u)};
+            const f2 r = add2(e, n);
+            lo[x][q] = pack_bf16x2(r.x, r.y);
+        }
+    return add2(sum[0], sum[1]);
+}
+
 // Warpgroup wh (threads 128 wh ..): columns 64 wh .. of every step.
 template <int D>
 __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint32_t tmem, volatile WaitFlag* wf) {
@@ -410,51 +435,63 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint
     uint32_t items = 0;
     for (uint32_t g = 0;; ++g) {
         const uint32_t is = g % kInfos, sb = g & 1;
-        if (!twait(&c->i_full[is], (g / kInfos) & 1, wf)) break;
-        const int flags = c->info[is].flags, slot0 = c->info[is].slot0[wh], nv = c->info[is].nv[wh];
-        const int b = c->info[is].b, h = c->info[is].h, t = c->info[is].t0 + rt;
-        const int ctx = c->info[is].ctx, dl = c->info[is].dl, part = c->info[is].part;
-        const uint32_t vslot = (uint32_t)c->info[is].vslot;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->i_empty[is]);
-        if (flags & kEnd) break;
-        // The V rows of a page's unused slots are zeroed (this half's keys):
-        // their weights are 0, but 0 * NaN would reach O.  A page that holds
-        // nothing was not loaded, its rows are zeros already.
-        const int used = p.page == 64 ? nv : nv > 0 ? min(max(nv - wh * 64, 0), 64) : 64;
-        if (flags & kMask && used < 64 && (p.page == 128 || nv > 0)) {
-            if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
-            uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
-            for (int x = row; x < (64 - used) * 8 * (D / 64); x += 128) {
-                const int r = x / (D / 8), q = x % (D / 8);
-                *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-        }
+        const StepInfo& f = c->info[is];
         if (!twait(&c->s_full[sb], (g >> 1) & 1, wf)) break;
         tc_fence_after();
+        const int flags = f.flags;
+        if (flags & kEnd) break;
+        uint32_t vis[2] = {~0u, ~0u};  // visible slots among this half's
+        if (flags & kMask) {
+            const int t = f.t0 + rt, dl = f.dl, nv = f.nv[wh];
+            unsigned long long bits = 0;
+            if (t < dl) {
+                bits = p.mask ? p.mask[(int64_t)f.b * p.T + t] : (2ull << t) - 1;
+                if (dl < 64) bits &= (1ull << dl) - 1;
+            }
+            const unsigned long long v = nv > 0 ? visible64(f.slot0[wh], f.ctx, bits) : 0ull;
+            vis[0] = (uint32_t)v;
+            vis[1] = (uint32_t)(v >> 32);
+            // The V rows of a page's unused slots are zeroed (this half's
+            // keys): their weights are 0, but 0 * NaN would reach O.  A page
+            // that holds nothing was not loaded, its rows are zeros already.
+            const int used = p.page == 64 ? nv : min(max(nv - wh * 64, 0), 64);
+            if (nv > 0 && used < 64) {
+                const uint32_t vslot = (uint32_t)f.vslot;
+                if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
+                uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
+                for (int x = row; x < (64 - used) * 8 * (D / 64); x += 128) {
+                    const int r = x / (D / 8), q = x % (D / 8);
+                    *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+        }
+        int b = 0, h = 0, t = 0, dl = 0, part = 0;
+        if (flags & kLast) {
+            b = f.b;
+            h = f.h;
+            t = f.t0 + rt;
+            dl = f.dl;
+            part = f.part;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->i_empty[is]);
         if (flags & kFirst) {
             m = -INFINITY;
             l = 0.f;
         }
         if (!idle) {
             const uint32_t t_s = tmem + lanes + sb * kStep + wh * 64;
-            uint32_t s[2][32];
+            uint32_t s[2][32], hi[2][16], lo[2][16];
             tmem_ld32(t_s, s[0]);
             tmem_ld32(t_s + 32, s[1]);
             tmem_wait_ld();
             reg_fence(s[0]);
             reg_fence(s[1]);
             if (flags & kMask) {
-                unsigned long long bits = 0;
-                if (t < dl) {
-                    bits = p.mask ? p.mask[(int64_t)b * p.T + t] : (2ull << t) - 1;
-                    if (dl < 64) bits &= (1ull << dl) - 1;
-                }
-                const unsigned long long v = nv > 0 ? visible64(slot0, ctx, bits) : 0ull;
-                hide(s[0], (uint32_t)v);
-                hide(s[1], (uint32_t)(v >> 32));
+                hide(s[0], vis[0]);
+                hide(s[1], vis[1]);
             }
             float mx[4];
 #pragma unroll
@@ -467,7 +504,10 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint
             }
             const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
             // raise the reference when it would grow by more than 2^8 (exact
-            // after the division by the sum, which uses the same reference)
+            // after the division by the sum, which uses the same reference).
+            // Taking the weights before the maximum is known, and again where
+            // a score has outgrown the reference, was slower (128K trees of
+            // 64-wide heads 200 -> 238 us).
             const bool grow = top > m + 8.f || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grow)) {
                 const float alpha = grow ? ex2_approx(m - top) : 1.f;
@@ -491,29 +531,15 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint
                     }
                 }
             }
+            const f2 all = weights(s, sl2, m, hi, lo);
             __syncwarp();
-            const float ref = m == -INFINITY ? 0.f : m;
-            const f2 nm2 = {-ref, -ref};
-            f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            l += all.x + all.y;
             // 32 columns of P in the columns of their S: 16 of high parts, 16 of low
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const f2 a = fma2({__uint_as_float(s[x][2 * q]), __uint_as_float(s[x][2 * q + 1])}, sl2, nm2);
-                    const f2 e = {ex2_approx(a.x), ex2_approx(a.y)};
-                    sum[q & 1] = add2(sum[q & 1], e);
-                    hi[q] = pack_bf16x2(e.x, e.y);
-                    const f2 n = {-__uint_as_float(hi[q] << 16), -__uint_as_float(hi[q] & 0xffff0000u)};
-                    const f2 r = add2(e, n);
-                    lo[q] = pack_bf16x2(r.x, r.y);
-                }
-                tmem_st16(t_s + x * 32, hi);
-                tmem_st16(t_s + x * 32 + 16, lo);
+                tmem_st16(t_s + x * 32, hi[x]);
+                tmem_st16(t_s + x * 32 + 16, lo[x]);
             }
-            const f2 all = add2(sum[0], sum[1]);
-            l += all.x + all.y;
             tmem_wait_st();
         }
         tc_fence_before();
@@ -608,12 +634,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int x = 0; x < 2; ++x) {
             mbar_init(&c->q_full[x], 1);
             mbar_init(&c->q_empty[x], 1);
-            mbar_init(&c->s_full[x], 1);
+            mbar_init(&c->s_full[x], 2);  // the scores' commit and the MMA lane itself
             mbar_init(&c->p_full[x], 8);
             mbar_init(&c->pv_done[x], 1);
         }
         for (int x = 0; x < kInfos; ++x) {
-            mbar_init(&c->i_full[x], 1);
             mbar_init(&c->i_empty[x], 8);  // the softmax warps
         }
         for (int x = 0; x < 4; ++x) mbar_init(&c->st_full[x], 2);
