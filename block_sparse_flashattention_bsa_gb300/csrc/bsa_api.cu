@@ -252,6 +252,17 @@ int device_context(int32_t** err, int* sm_count) {
     return BSA_OK;
 }
 
+cudaError_t raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev % kMaxDevices);
+    if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 int check_page_cache(const bsa_page_cache* c) {
     if (!c || c->layers <= 0 || c->n_pages <= 0 || c->Hkv <= 0 || c->page <= 0 || c->D <= 0 || c->n_seqs <= 0 ||
         c->max_pages <= 0)

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "bsa.h"
 
 namespace bsa {
@@ -13,6 +15,9 @@ namespace bsa {
 // The current device's error word and SM count (BSA_ERR_UNSUPPORTED on a
 // device the kernels are not built for).  Allocates the word on first use.
 int device_context(int32_t** err, int* sm_count);
+// Raises a kernel's dynamic shared-memory limit, once per kernel and device
+// (`done`: one bit per device, a static of the caller).
+cudaError_t raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>* done);
 // Sizes, alignment and the 2^31 row limit of a paged cache's pools (the page
 // table is checked by the calls that read one).
 int check_page_cache(const bsa_page_cache* c);

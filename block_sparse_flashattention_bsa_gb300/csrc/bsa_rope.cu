@@ -615,8 +615,10 @@ void deal_tasks(RopeParams* p, int D, int sm_count, const double* bytes) {
 
 cudaError_t launch_bwd(const RopeParams& p, int D, bool il, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.side[0].ctas + p.side[1].ctas + p.side[2].ctas);
+    static std::atomic<uint64_t> raised[4];  // [D == 128][interleaved]
     auto go = [&](auto kern) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+        const cudaError_t e =
+            raise_smem_limit(reinterpret_cast<const void*>(kern), kBwdSmem, &raised[(D == 128) * 2 + il]);
         if (e != cudaSuccess) return e;
         kern<<<grid, kRopeThreads, kBwdSmem, s>>>(p);
         return cudaGetLastError();

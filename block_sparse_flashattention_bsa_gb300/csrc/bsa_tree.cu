@@ -794,7 +794,8 @@ template <int D>
 int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, int units,
                 int chunk, size_t smem, cudaStream_t s) {
     static_assert(sizeof(TreeCtrl) <= 14336, "control block too large");
-    if (cudaFuncSetAttribute(tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem) != cudaSuccess)
+    static std::atomic<uint64_t> raised{0};
+    if (raise_smem_limit(reinterpret_cast<const void*>(tree_kernel<D>), kTreeSmem, &raised) != cudaSuccess)
         return BSA_ERR_CUDA;
     for (int u0 = 0; u0 < units; u0 += chunk) {
         p.unit0 = u0;
