@@ -56,6 +56,7 @@ constexpr int kMaxSlots = 12;     // K / V ring
 constexpr int kInfos = 8;         // step descriptions ahead (more than the ring's kMaxSlots / 2 steps)
 static_assert(2 * kInfos > kMaxSlots + 2, "a description could be overwritten before its MMA");
 constexpr int kTreeSmem = 232448;
+constexpr int kCtrlBytes = 14336;
 constexpr int kStep = 128;        // key slots per step
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };  // kFirst, kLast: of an item
@@ -81,7 +82,7 @@ struct TreeCtrl {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t i_empty[kInfos];
-    uint64_t st_full[4];             // per pair of warps with the same rows: both posted their sums
+    uint64_t st_full[4], x_full[4];  // per pair of warps with the same rows: both posted their sums, their parts of O
     uint64_t drain;
     StepInfo info[kInfos];
     float2 stats[2][128];            // [half][row]: maximum and sum posted at an item's end
@@ -99,6 +100,7 @@ struct TreeParams {
     int32_t unit0, units;      // units of this launch
     int32_t tq, RT;            // drafted tokens per row tile, row tiles
     int32_t n_slots, q_box;    // ring slots, bytes of one 64-column box of Q
+    int32_t dup;               // TMEM lanes between a row and its copy for the second half's warps (0: none)
     int32_t grid;
     void* out;
     float* lse;
@@ -199,10 +201,13 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
                 break;
             }
             if (leader) {
-                mbar_arrive_expect_tx(&c->q_full[qb], (uint32_t)(p.tq * p.G * 128 * NBOX));
+                mbar_arrive_expect_tx(&c->q_full[qb], (uint32_t)(p.tq * p.G * 128 * NBOX * (p.dup ? 2 : 1)));
 #pragma unroll
-                for (int x = 0; x < NBOX; ++x)
-                    tma_load_3d(sQ + (qb * NBOX + x) * p.q_box, tq, &c->q_full[qb], x * 64, h * p.G, b * p.T + t0);
+                for (int x = 0; x < NBOX; ++x) {
+                    uint8_t* dst = sQ + (qb * NBOX + x) * p.q_box;
+                    tma_load_3d(dst, tq, &c->q_full[qb], x * 64, h * p.G, b * p.T + t0);
+                    if (p.dup) tma_load_3d(dst + p.dup * 128, tq, &c->q_full[qb], x * 64, h * p.G, b * p.T + t0);
+                }
             }
             ++nq;
             // steps, 32 pages resolved at a time
@@ -429,13 +434,16 @@ __device__ __forceinline__ f2 weights(const uint32_t (&s)[2][32], f2 sl2, float 
 
 // Warpgroup wh (threads 128 wh ..): columns 64 wh .. of every step.
 template <int D>
-__device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint32_t tmem, volatile WaitFlag* wf) {
+__device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeCtrl* c, uint32_t tmem,
+                             volatile WaitFlag* wf) {
     constexpr int O_COL = 2 * kStep;
-    const int wh = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5, lane = threadIdx.x & 31;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int wh = threadIdx.x >> 7, tl = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(tl & 96) << 16;
     const uint32_t t_o = tmem + lanes + O_COL + wh * D;
-    const int rt = row / p.G, rg = row - rt * p.G;  // drafted token (in the tile) and query head of this row
-    const bool idle = warp * 32 >= p.tq * p.G;      // the whole warp lies behind the tile's rows
+    // query row of this TMEM lane (the second half works on the copies, if there are any)
+    const int rows = p.tq * p.G, row = (tl - wh * p.dup) & 127, pair = row >> 5;
+    const int rt = row / p.G, rg = row - rt * p.G;  // its drafted token (in the tile) and query head
+    const bool idle = (row & 96) >= rows;           // the whole warp lies behind the tile's rows
     float m = -INFINITY, l = 0.f;
     const f2 sl2 = {p.scale_log2, p.scale_log2};
     uint32_t items = 0;
@@ -465,7 +473,7 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint
                 const uint32_t vslot = (uint32_t)f.vslot;
                 if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
                 uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
-                for (int x = row; x < (64 - used) * 8 * (D / 64); x += 128) {
+                for (int x = tl; x < (64 - used) * 8 * (D / 64); x += 128) {
                     const int r = x / (D / 8), q = x % (D / 8);
                     *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
@@ -556,19 +564,19 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint
         if (!twait(&c->pv_done[sb], (g >> 1) & 1, wf)) break;
         c->stats[wh][row] = make_float2(m, l);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->st_full[warp]);
-        if (!twait(&c->st_full[warp], items & 1, wf)) break;
+        if (lane == 0) mbar_arrive(&c->st_full[pair]);
+        if (!twait(&c->st_full[pair], items & 1, wf)) break;
         ++items;
         if (idle) continue;
         const float2 ml = c->stats[wh ^ 1][row];
         tc_fence_after();
-        const bool live = rt < p.tq && t < dl;
+        const bool live = row < rows && t < dl;
         const float mm = fmaxf(m, ml.x);
         float w0 = m == -INFINITY ? 0.f : ex2_approx(m - mm);
         float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
         const float sum = wh ? ml.y * w1 + l * w0 : l * w0 + ml.y * w1;  // the same in both halves
         const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
-        const int64_t prow = (int64_t)part * (p.tq * p.G) + row;
+        const int64_t prow = (int64_t)part * rows + row;
         if (part < 0) {
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
             w0 *= inv;
@@ -577,15 +585,49 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, TreeCtrl* c, uint
         } else if (live && wh == 0) {
             p.part_ml[prow] = make_float2(mm, sum);
         }
-        const f2 w02 = {w0, w0}, w12 = {w1, w1};
-        // this half writes columns wh * D/2 .. of the row
+        const f2 w02 = {w0, w0}, w12 = {p.dup ? 1.f : w1, p.dup ? 1.f : w1};
+        // This half writes columns wh * D/2 .. of the row.  With copies the
+        // other accumulator lies in other lanes: each half hands over its
+        // (weighted) part of the other's columns, [column / 4][row].
         const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
+        if (p.dup) {
+#pragma unroll 1
+            for (int x = 0; x < D / 64; ++x) {
+                uint32_t o[32];
+                tmem_ld32(t_o + (wh ^ 1) * (D / 2) + x * 32, o);
+                tmem_wait_ld();
+                reg_fence(o);
+                float4* dst = xo + (wh * (D / 8) + x * 8) * p.dup + row;
+                if (row < p.dup) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[q * p.dup] = make_float4(__uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
+                                                     __uint_as_float(o[4 * q + 2]) * w0,
+                                                     __uint_as_float(o[4 * q + 3]) * w0);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&c->x_full[pair]);
+            if (!twait(&c->x_full[pair], (items - 1) & 1, wf)) break;
+        }
 #pragma unroll 1
         for (int x = 0; x < D / 64; ++x) {
             uint32_t o[32], o1[32];
             __syncwarp();
             tmem_ld32(t_a + x * 32, o);
-            tmem_ld32(t_b + x * 32, o1);
+            if (p.dup) {
+                const float4* src = xo + ((wh ^ 1) * (D / 8) + x * 8) * p.dup + (row & (p.dup - 1));
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 f4 = src[q * p.dup];
+                    o1[4 * q] = __float_as_uint(f4.x);
+                    o1[4 * q + 1] = __float_as_uint(f4.y);
+                    o1[4 * q + 2] = __float_as_uint(f4.z);
+                    o1[4 * q + 3] = __float_as_uint(f4.w);
+                }
+            } else {
+                tmem_ld32(t_b + x * 32, o1);
+            }
             tmem_wait_ld();
             reg_fence(o);
             reg_fence(o1);
@@ -629,7 +671,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     uint8_t* sQ = smem;
     uint8_t* sT = sQ + 2 * NBOX * p.q_box;
-    TreeCtrl* c = reinterpret_cast<TreeCtrl*>(sT + p.n_slots * T_BYTES);
+    float4* xo = reinterpret_cast<float4*>(sT + p.n_slots * T_BYTES);
+    TreeCtrl* c = reinterpret_cast<TreeCtrl*>(sT + p.n_slots * T_BYTES + p.dup * D * 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
     // Prefix sums of the units' steps: every thread a run of units, then a
@@ -659,6 +702,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(&c->pv_done[x - 64], 1);
         } else if (x >= 96 && x < 100) {
             mbar_init(&c->st_full[x - 96], 2);
+            mbar_init(&c->x_full[x - 96], 2);
         } else if (x == 128) {
             mbar_init(&c->drain, 1);
             c->wf.abort = 0;
@@ -700,7 +744,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     else if (warp == kMma)
         tree_mma<D>(p, sQ, sT, c, tmem, wf);
     else
-        tree_softmax<D>(p, sT, c, tmem, wf);
+        tree_softmax<D>(p, sT, xo, c, tmem, wf);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -785,6 +829,20 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
 
 bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// TMEM lanes between the query rows and their copies, 0 for none.  TMEM ties a
+// warp to a quarter of the lanes, and a quarter to one of the SM's four
+// schedulers: with few rows both halves' warps share one, and its exponentials
+// are what a step of 64-wide heads waits for.  A second copy of Q in lanes of
+// its own puts the second half's warps on other schedulers: 4 contexts of 128K
+// slots, 64 rows: 200 -> 177 us; 96 ragged sequences up to 8K, 4 rows: 197 ->
+// 173 us.  At 128-wide heads a step has twice the bytes to hide the same
+// softmax, and the ring slot that the copies cost is worth more (4 rows: 290
+// us without, 293 with them).
+int row_copies(int rows, int D) {
+    if (D != 64 || rows > 64) return 0;
+    return rows <= 32 ? 32 : 64;
+}
+
 // Drafted tokens of a row tile: as many as fit 128 rows.
 int tile_tokens(int T, int G) { return std::min(T, 128 / G); }
 
@@ -793,7 +851,7 @@ int64_t ws_part_offset() { return (kMaxCtas * (int64_t)sizeof(Meta) + 255) / 256
 template <int D>
 int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, int units,
                 int chunk, size_t smem, cudaStream_t s) {
-    static_assert(sizeof(TreeCtrl) <= 14336, "control block too large");
+    static_assert(sizeof(TreeCtrl) <= kCtrlBytes, "control block too large");
     static std::atomic<uint64_t> raised{0};
     if (raise_smem_limit(reinterpret_cast<const void*>(tree_kernel<D>), kTreeSmem, &raised) != cudaSuccess)
         return BSA_ERR_CUDA;
@@ -860,10 +918,12 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     int sms;
     if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
     const int rows = p.tq * p.G, nbox = c->D / 64;
-    p.q_box = (rows + 7) / 8 * 1024;
+    p.dup = bsa::row_copies(rows, c->D);
+    p.q_box = p.dup * 128 + (rows + 7) / 8 * 1024;
     const int tile = nbox * bsa::kStep * 128;
-    p.n_slots = std::min(bsa::kMaxSlots, (bsa::kTreeSmem - 14336 - 2 * nbox * p.q_box) / tile);
-    const size_t smem = (size_t)2 * nbox * p.q_box + (size_t)p.n_slots * tile + 14336;
+    const int fixed = bsa::kCtrlBytes + 2 * nbox * p.q_box + p.dup * c->D * 4;
+    p.n_slots = std::min(bsa::kMaxSlots, (bsa::kTreeSmem - fixed) / tile);
+    const size_t smem = (size_t)p.n_slots * tile + fixed;
     CUtensorMap tq, tk, tv;
     const uint64_t krows = (uint64_t)c->n_pages * c->Hkv * c->page;
     if ((st = bsa::encode_token_rows_bf16(&tq, a->q, (uint64_t)a->B * a->T, a->Hq, c->D, p.G, p.tq)) != BSA_OK) return st;
