@@ -403,6 +403,12 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
 }
 
 // ---------------------------------------------------------------- softmax
+// Natural-log LSE of a row from its reference (log2) and sum: -infinity where
+// nothing was visible, NaN where the row's scores are not numbers.
+__device__ __forceinline__ float row_lse(float m, float sum) {
+    return sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994531f;
+}
+
 // Columns whose bit is 0 score -infinity (whatever stood there, NaN included).
 __device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t vis) {
 #pragma unroll
@@ -578,10 +584,10 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
         const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
         const int64_t prow = (int64_t)part * rows + row;
         if (part < 0) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
             w0 *= inv;
             w1 *= inv;
-            if (live && wh == 0) p.lse[orow] = sum > 0.f ? (mm + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            if (live && wh == 0) p.lse[orow] = row_lse(mm, sum);
         } else if (live && wh == 0) {
             p.part_ml[prow] = make_float2(mm, sum);
         }
@@ -783,24 +789,23 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
         for (int k = first + lane; k <= last; k += 32) m = fmaxf(m, p.part_ml[(int64_t)slot_of(k) * rows + r].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (m > -INFINITY) {
+        const float ref = m > -INFINITY ? m : 0.f;
 #pragma unroll 4
-            for (int k = first + part; k <= last; k += WPR) {
-                const int64_t pr = (int64_t)slot_of(k) * rows + r;
-                const float2 ml = p.part_ml[pr];
-                const float w = ex2_approx(ml.x - m);
-                l += w * ml.y;
-                if (C == 4) {
-                    const float4 o = reinterpret_cast<const float4*>(p.part_o + pr * D)[lane];
-                    acc[0] += w * o.x;
-                    acc[1] += w * o.y;
-                    acc[C - 2] += w * o.z;
-                    acc[C - 1] += w * o.w;
-                } else {
-                    const float2 o = reinterpret_cast<const float2*>(p.part_o + pr * D)[lane];
-                    acc[0] += w * o.x;
-                    acc[1] += w * o.y;
-                }
+        for (int k = first + part; k <= last; k += WPR) {
+            const int64_t pr = (int64_t)slot_of(k) * rows + r;
+            const float2 ml = p.part_ml[pr];
+            const float w = ex2_approx(ml.x - ref);  // 0 for a part that saw nothing
+            l += w * ml.y;
+            if (C == 4) {
+                const float4 o = reinterpret_cast<const float4*>(p.part_o + pr * D)[lane];
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
+                acc[C - 2] += w * o.z;
+                acc[C - 1] += w * o.w;
+            } else {
+                const float2 o = reinterpret_cast<const float2*>(p.part_o + pr * D)[lane];
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
             }
         }
     }
@@ -816,9 +821,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
             l += red[w][D];
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t orow = ((int64_t)mt.b * p.T + t) * p.Hq + mt.h * p.G + r % p.G;
-    if (lane == 0) p.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lane == 0) p.lse[orow] = row_lse(m, l);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D;
     if (C == 4)
         reinterpret_cast<uint2*>(out)[lane] =

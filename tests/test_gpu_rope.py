@@ -323,3 +323,59 @@ def test_append_bad_places_are_reported_and_skipped(bsa):
     want[1, :, 0] = 1
     want[2, :, 5] = 1
     assert torch.equal(vc, want) and torch.equal(kc, want)
+
+
+@pytest.mark.parametrize("order", ["heads first", "batch last", "expanded", "reversed dims of one"])
+def test_other_strides(bsa, order):
+    """Views whose strides are not those of a fused projection."""
+    B, N, H, D = 2, 37, 4, 64
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(B, N, H, D, generator=g).bfloat16().cuda()
+    if order == "heads first":
+        v = x.transpose(1, 2).contiguous().transpose(1, 2)
+    elif order == "batch last":
+        v = x.permute(1, 2, 0, 3).contiguous().permute(2, 0, 1, 3)
+    elif order == "expanded":
+        v = x[:, :, :1].expand(B, N, H, D)
+    else:
+        v = x[:1, :, :1].as_strided((1, N, 1, D), (5, H * D, 3, 1))
+    f = bsa.rope_inv_freq(64)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")[None].expand(v.shape[0], N)
+    w = torch.rand(D, device="cuda")
+    args = dict(positions=pos, q_weight=w, k_weight=w)
+    a = bsa.qk_norm_rope(v, v, v, f, **args)
+    b = bsa.qk_norm_rope(v.contiguous(), v.contiguous(), v.contiguous(), f, **args)
+    for s, t in zip(a, b):
+        assert torch.equal(s, t)
+    dz = [torch.randn_like(t) for t in a]
+    ga = bsa.qk_norm_rope_backward(*dz, v, v, f, **args)
+    gb = bsa.qk_norm_rope_backward(*dz, v.contiguous(), v.contiguous(), f, **args)
+    for s, t in zip(ga, gb):
+        assert torch.equal(s, t)
+
+
+def test_gpu_refusals(bsa):
+    """What only a CUDA tensor can get wrong: types, strides, shapes, streams, outputs."""
+    x = torch.zeros(1, 8, 4, 64, device="cuda", dtype=torch.bfloat16)
+    f, w = bsa.rope_inv_freq(64), torch.ones(64, device="cuda")
+    bad = [dict(inv_freq=f.float()), dict(inv_freq=f[::2]), dict(positions=torch.arange(8, device="cuda")),
+           dict(positions=torch.zeros(7, dtype=torch.int32, device="cuda")),
+           dict(positions=torch.zeros(2, 8, dtype=torch.int32, device="cuda")),
+           dict(positions=torch.zeros(8, dtype=torch.int32)), dict(q_weight=w[:32]), dict(q_weight=w.bfloat16()),
+           dict(k_weight=w.cpu()), dict(q=x.float()), dict(q=x.transpose(2, 3)), dict(k=x[:, :4]),
+           dict(k=x[..., :32]), dict(v=x[:, :, :2]), dict(out=(x, x, x)), dict(out=(x, x, None))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            bsa.qk_norm_rope(**{**dict(q=x, k=x, v=x, inv_freq=f), **kw})
+    for kw in (dict(kv_repeat=0), dict(eps=-1.0), dict(inv_freq=bsa.rope_inv_freq(24)),
+               dict(inv_freq=bsa.rope_inv_freq(80)), dict(q=torch.zeros(1, 8, 4, 68, device="cuda",
+                                                                       dtype=torch.bfloat16)[..., :64]),
+               dict(q=torch.zeros(2056, device="cuda", dtype=torch.bfloat16)[1:2049].view(1, 8, 4, 64))):
+        with pytest.raises(bsa.BsaError):
+            bsa.qk_norm_rope(**{**dict(q=x, k=x, v=x, inv_freq=f), **kw})
+    z = torch.zeros(1, 4, 8, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        bsa.qk_norm_rope_backward(z.transpose(1, 2), z, z, x, x, f)
+    with pytest.raises(bsa.BsaError):  # gradient rows that coincide
+        bsa.qk_norm_rope_backward(z, z, z, x, x, f, out=(x, x, x[:, :, :1].expand(1, 8, 4, 64)))
+    assert bsa.device_error() == 0

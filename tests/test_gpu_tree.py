@@ -321,3 +321,33 @@ def test_no_wait_runs_out(bsa):
     bsa.tree_attention(*c.dev, scale=c.scale)
     torch.cuda.synchronize()
     assert time.monotonic() - t < 1.0 and bsa.device_error() == 0
+
+
+def test_a_row_of_nan_stays_alone(bsa):
+    """A query row that is no number gives NaN (O and LSE) and leaves the others their bits;
+    contexts long enough to be split over SMs, and short ones."""
+    c = Case(2, 3, 8, 2, 128, 128, [5000, 40])
+    o, lse = c.run(bsa)
+    good = o.clone(), lse.clone()
+    c.q[0, 1, 2] = float("nan")
+    c.q[1, 2, 7, 5] = float("inf")
+    o, lse = c.run(bsa)
+    assert o[0, 1, 2].isnan().all() and lse[0, 1, 2].isnan()
+    assert o[1, 2, 7].isnan().all() and lse[1, 2, 7].isnan()
+    keep = torch.ones(2, 3, 8, dtype=torch.bool, device="cuda")
+    keep[0, 1, 2] = keep[1, 2, 7] = False
+    assert torch.equal(o[keep], good[0][keep]) and torch.equal(lse[keep], good[1][keep])
+
+
+@pytest.mark.parametrize("ctx,dl", [(-5, 2), (3, -1), (3, 99)])
+def test_lengths_out_of_range_are_clamped(bsa, ctx, dl):
+    """A negative context is empty, drafts are taken as 0 .. T."""
+    c = Case(1, 4, 2, 1, 64, 64, [10], dl=[4])
+    c.ctx, c.dl = [ctx], [dl]
+    o = torch.full((1, 4, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, 4, 2), 5.0, device="cuda")
+    c.run(bsa, out=o, lse=lse)
+    c.ctx, c.dl = [max(ctx, 0)], [min(max(dl, 0), 4)]
+    c.check(o, lse)
+    n = c.dl[0]
+    assert (o[0, n:] == 3).all() and (lse[0, n:] == 5).all() and bsa.device_error() == 0
