@@ -33,7 +33,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 64;  // rotary_dim / 2 <= 64
 constexpr int kFwdRows = 4;    // rows of a lane group's task (forward, large calls)
-constexpr int kFwdWaves = 16;  // forward CTAs per SM (two resident)
+constexpr int kFwdWaves = 8;   // forward CTAs per SM (two resident)
 constexpr int kBwdResident = 2, kBwdWaves = 4;  // the gradients' CTAs per SM: resident, in all
 constexpr int kBwdStages = 3;  // rows in a lane's ring
 constexpr int kBwdSmem = kBwdStages * 4 * kRopeThreads * 16;
@@ -182,7 +182,7 @@ __device__ __forceinline__ int cta_side(const RopeParams& p, int* idx) {
 // lane groups take neighbouring tokens, so the head-major stores of a head
 // run over TB consecutive rows.
 template <int D, int U, bool IL, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel(const RopeParams p) {
     constexpr int LPR = D / 16, TB = kRopeThreads / LPR;
     __shared__ unsigned long long turns[kMaxPairs];
     int idx;
@@ -539,8 +539,10 @@ __global__ void __launch_bounds__(1024) reduce_weight_kernel(const ReduceParams 
     if (g == 0) reinterpret_cast<float4*>(p.out[k])[c] = a;
 }
 
-// CTAs of each kind, in proportion to the bytes it moves (two per SM in all),
-// none without an item.
+// CTAs of each kind, in proportion to the bytes it moves, none without an item.
+// Several times what is resident: kinds and rows of unequal cost then even out
+// over the SMs (128K tokens, 48 heads, 4.83 GB: 920 us with two CTAs per SM in
+// all, 750 with eight; 16K tokens of 24 heads: 38.9 with eight, 40.7 with 16).
 void deal_ctas(RopeParams* p, int D, int U, int ctas, const double* bytes) {
     const int TB = kRopeThreads / (D / 16);
     const double all = bytes[0] + bytes[1] + bytes[2];
@@ -636,13 +638,14 @@ bool strides_ok(const int64_t* st) {
     return true;
 }
 
-// Heads of a lane group's task: 4 share one computation of the angles; 1
-// spreads a small call over more CTAs.  4 wherever that still gives every SM
-// two CTAs' worth of items.
+// Heads of a lane group's task.  Four share one computation of the angles and
+// read four rows at once; single heads spread a small call over more CTAs.
+// Four from half an item per SM on (2,048 tokens of 48 heads, then the
+// acceptance: 18.9 us, 23.8 with single heads; 512 tokens: 8.2 and 9.7).
 int pick_heads(int64_t tokens, int D, int Hq, int Hkv, int sm_count) {
     const int TB = kRopeThreads / (D / 16);
     const int64_t items = (tokens + TB - 1) / TB * ((Hq + kFwdRows - 1) / kFwdRows + 2 * ((Hkv + kFwdRows - 1) / kFwdRows));
-    return items >= 2 * (int64_t)sm_count ? kFwdRows : 1;
+    return 2 * items >= sm_count ? kFwdRows : 1;
 }
 
 int fill(const bsa_norm_rope_args* a, RopeParams* p) {
