@@ -175,13 +175,12 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
         int u = 0;
         for (int step = 1 << 10; step > 0; step >>= 1)
             if (u + step < p.units && c->prefix[u + step] <= lo) u += step;
-        int k = -1;  // item of the unit, found once its length is known
+        int per_item = (c->prefix[u + 1] - c->prefix[u]) / mult;
+        int k = (lo - c->prefix[u]) / per_item;  // item of the unit
         int pos = lo;
         while (ok && pos < hi) {
             const int gu = p.unit0 + u;  // unit of the whole call
             const int n = unit_pages(p, gu, false);
-            const int per_item = max(1, pages_to_steps(p, n));
-            if (k < 0) k = (lo - c->prefix[u]) / per_item;
             const int b = p.row_ptr ? gu / p.Hkv : gu;
             const int kr = p.RT == 1 ? k : k / p.RT;  // k = (key head, row tile), or the row tile alone
             const int h = p.row_ptr ? gu - b * p.Hkv : kr;
@@ -291,9 +290,10 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
                 }
             }
             pos = start + s1;
-            if (++k == mult) {
+            if (++k == mult && pos < hi) {
                 k = 0;
                 ++u;
+                per_item = (c->prefix[u + 1] - c->prefix[u]) / mult;
             }
         }
     }
@@ -323,11 +323,11 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
 // One lane does everything: a wait of the whole warp (vote included) costs
 // ~130 cycles even when its barrier is ready, and four of them per step left
 // the tensor pipe idle half the time (4 contexts of 128K slots, 16 drafts, 8
-// key heads of 64: 232 us; 200 us now).  Step descriptions come with the K tile's barrier: the
-// producer writes them before it arms it, and does not come round to them
-// again before the ring has (kInfos is more than the ring's steps).  The lane
-// passes them on with its own arrival on the scores' barrier, so the softmax
-// has one wait per step.
+// key heads of 64: 232 us; 200 us since).  Step descriptions come with the K
+// tile's barrier: the producer writes them before it arms it, and does not
+// come round to them again before the ring has (kInfos is more than the ring's
+// steps).  The lane passes them on with its own arrival on the scores'
+// barrier, so the softmax has one wait per step.
 template <int D>
 __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, uint32_t tmem,
                          volatile WaitFlag* wf) {

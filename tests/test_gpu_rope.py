@@ -379,3 +379,27 @@ def test_gpu_refusals(bsa):
     with pytest.raises(bsa.BsaError):  # gradient rows that coincide
         bsa.qk_norm_rope_backward(z, z, z, x, x, f, out=(x, x, x[:, :, :1].expand(1, 8, 4, 64)))
     assert bsa.device_error() == 0
+
+
+def test_far_rows(bsa):
+    """Token rows and pages whose offsets pass 2^31 bytes and 2^31 elements."""
+    n = 2 ** 31 // 128 + 3000  # rows of 128 values
+    pool = torch.empty(n, 128, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(40, 128, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    pool[-40:] = x
+    far = pool[-40:].view(1, 40, 1, 128)
+    near = x.view(1, 40, 1, 128)
+    f = bsa.rope_inv_freq(128)
+    assert far.storage_offset() > 2 ** 31
+    step = pool.as_strided((1, 2, 1, 128), (0, (n - 1) * 128, 0, 1))  # two tokens, the second one far
+    pool[0] = x[3]
+    for a, b in ((far, near), (step, torch.stack([x[3], x[-1]]).view(1, 2, 1, 128))):
+        za, zb = bsa.qk_norm_rope(a, a, a, f), bsa.qk_norm_rope(b, b, b, f)
+        assert all(torch.equal(s, t) for s, t in zip(za, zb))
+    # a cache of the same size: its last page
+    pages = n // 64
+    cache = pool[:pages * 64].view(pages, 1, 64, 128)
+    table = torch.tensor([[pages - 1]], dtype=torch.int32, device="cuda")
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bsa.cache_append(near[0, :1], near[0, :1], near[0, :1], cache, cache, table, one, one + 63, None)
+    assert torch.equal(cache[pages - 1, 0, 63], x[0]) and bsa.device_error() == 0

@@ -351,3 +351,29 @@ def test_lengths_out_of_range_are_clamped(bsa, ctx, dl):
     c.check(o, lse)
     n = c.dl[0]
     assert (o[0, n:] == 3).all() and (lse[0, n:] == 5).all() and bsa.device_error() == 0
+
+
+@pytest.mark.parametrize("D,page,T,Hq,Hkv", [(128, 64, 64, 8, 1), (64, 128, 40, 20, 4), (128, 128, 7, 96, 3),
+                                             (64, 64, 33, 4, 2)])
+def test_block_lists_of_several_row_tiles(bsa, D, page, T, Hq, Hkv):
+    c = Case(3, T, Hq, Hkv, D, page, [700, 3, 1234], dl=[T, T - 1, 2], lists=listed(0.6), seed=T)
+    o, lse = c.run(bsa)
+    c.check(o, lse)
+    assert bsa.device_error() == 0
+
+
+def test_far_pages(bsa):
+    """Rows whose offset in the pool passes 2^31 bytes and 2^30 elements: a pool of
+    5 GB of which a few pages are used."""
+    c = Case(2, 2, 8, 4, 128, 128, [400, 130], seed=4)
+    want = c.run(bsa)
+    n = 5 * 2 ** 30 // (4 * 128 * 128 * 2)
+    big = [torch.empty(n, 4, 128, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    used = c.kc.shape[0]
+    place = torch.arange(used) * (n // used) + (n // used - 1)
+    for pool, small in zip(big, (c.kc, c.vc)):
+        pool[place.cuda()] = small.cuda()
+    table = c.dev[3].clone()
+    table[table >= 0] = place.int().cuda()[table[table >= 0].long()]
+    got = bsa.tree_attention(c.dev[0], big[0], big[1], table, *c.dev[4:], scale=c.scale)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and bsa.device_error() == 0
