@@ -162,6 +162,8 @@ __device__ void check_requests(const PageReq& p, int64_t t, int64_t nt) {
 
 template <bool FORK>
 __global__ void __launch_bounds__(256) pages_check_kernel(const PageReq p) {
+    griddep_launch_dependents();
+    griddep_wait();
     check_requests<FORK>(p, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x);
 }
 
@@ -198,6 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PageReq 
     __shared__ long long red64[32];
     const int tid = threadIdx.x;
     griddep_launch_dependents();
+    griddep_wait();
     if (MODE) {
         check_requests<MODE == 2>(p, tid, kPlanThreads);
         __threadfence();
@@ -280,6 +283,7 @@ __device__ __forceinline__ int64_t unit_offset(const PageReq& p, int64_t sub, in
 template <bool FORK>
 __global__ void __launch_bounds__(kCopyThreads) pages_apply_kernel(const PageReq p, int table_ctas) {
     const int lane = threadIdx.x & 31;
+    griddep_launch_dependents();
     griddep_wait();
     if ((int)blockIdx.x < table_ctas) {
         const int wpc = kCopyThreads / 32;
@@ -353,6 +357,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageRe
     __shared__ int below;  // live pages among the first n_live
     const int tid = threadIdx.x;
     griddep_launch_dependents();
+    griddep_wait();
     int n_live = 0;
     for (int i0 = 0; i0 < p.n_pages; i0 += 4 * kPlanThreads) {
         int cnt = 0;
@@ -409,6 +414,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageRe
 
 __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const PageReq p, const int32_t* new_page,
                                                                      int table_ctas) {
+    griddep_launch_dependents();
     griddep_wait();
     const int moved = p.w.head[0];
     const int32_t *holes = p.w.free_list, *movers = p.w.ref0;
@@ -449,6 +455,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const PageReq p,
                                                                 const int32_t* accepted, const int32_t* n_acc, int T,
                                                                 int32_t* new_len) {
     __shared__ int64_t from[64], to[64];  // of head 0, in 16-byte pieces
+    griddep_launch_dependents();
+    griddep_wait();
     const int b = blockIdx.x, is_v = blockIdx.y & 1, layer = blockIdx.y >> 1;
     const int ctx = ctx_len[b], na = n_acc[b], tid = threadIdx.x;
     bool ok = ctx >= 0 && na >= 0 && na <= T && ctx <= p.max_pages * p.page;
@@ -519,22 +527,6 @@ int fill_req(const bsa_page_cache* c, PageReq* p) {
 
 bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Launched while the kernel before it is still running; it waits for that one
-// before it reads anything.
-template <typename... A>
-cudaError_t launch_after(void (*kern)(A...), unsigned grid, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n, const int32_t* a, const int32_t* b,
                 const int32_t* len, int32_t* granted, void* ws, int64_t ws_bytes, cudaStream_t s) {
     PageReq p;
@@ -562,21 +554,16 @@ int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n
     const int64_t units = (int64_t)n * c->layers * 2 * c->Hkv;
     const unsigned copy_ctas = (unsigned)std::min<int64_t>(units, 8ll * sms);
     const bool small = (int64_t)n * c->max_pages <= 16384 && c->n_pages <= 16384 && c->n_seqs <= 16384;
+    cudaError_t e;
     if (small) {
-        if (fork)
-            pages_plan_kernel<2><<<1, kPlanThreads, 0, s>>>(p);
-        else
-            pages_plan_kernel<1><<<1, kPlanThreads, 0, s>>>(p);
+        e = launch_after(fork ? pages_plan_kernel<2> : pages_plan_kernel<1>, dim3(1), kPlanThreads, 0, s, p);
     } else {
-        if (fork)
-            pages_check_kernel<true><<<grid, 256, 0, s>>>(p);
-        else
-            pages_check_kernel<false><<<grid, 256, 0, s>>>(p);
-        pages_plan_kernel<0><<<1, kPlanThreads, 0, s>>>(p);
+        e = launch_after(fork ? pages_check_kernel<true> : pages_check_kernel<false>, dim3(grid), 256, 0, s, p);
+        if (e == cudaSuccess) e = launch_after(pages_plan_kernel<0>, dim3(1), kPlanThreads, 0, s, p);
     }
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-    const cudaError_t e = fork ? launch_after(pages_apply_kernel<true>, table_ctas + copy_ctas, s, p, table_ctas)
-                               : launch_after(pages_apply_kernel<false>, table_ctas + copy_ctas, s, p, table_ctas);
+    if (e == cudaSuccess)
+        e = launch_after(fork ? pages_apply_kernel<true> : pages_apply_kernel<false>, dim3(table_ctas + copy_ctas),
+                         kCopyThreads, 0, s, p, table_ctas);
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -617,14 +604,14 @@ int bsa_cache_compact(const bsa_page_cache* c, int32_t* page_ref, int32_t* new_p
     p.ref = page_ref;
     p.w = bsa::split_ws(workspace, 0, c->n_seqs, c->n_pages);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    bsa::compact_plan_kernel<<<1, bsa::kPlanThreads, 0, s>>>(p, new_page);
+    cudaError_t e = bsa::launch_after(bsa::compact_plan_kernel, dim3(1), bsa::kPlanThreads, 0, s, p, new_page);
+    if (e != cudaSuccess) return BSA_ERR_CUDA;
     const int64_t entries = (int64_t)c->n_seqs * c->max_pages;
     const int table_ctas = (int)std::min<int64_t>((entries + 1023) / 1024, sms);
     const int64_t units = (int64_t)c->n_pages * c->layers * 2 * c->Hkv;
     const unsigned copy_ctas = (unsigned)std::min<int64_t>(units, 8ll * sms);
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-    const cudaError_t e =
-        bsa::launch_after(bsa::compact_apply_kernel, table_ctas + copy_ctas, s, p, (const int32_t*)new_page, table_ctas);
+    e = bsa::launch_after(bsa::compact_apply_kernel, dim3(table_ctas + copy_ctas), bsa::kCopyThreads, 0, s, p, new_page,
+                          table_ctas);
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -641,9 +628,10 @@ int bsa_cache_accept(const bsa_page_cache* c, const int32_t* context_len, const 
     if (2ll * c->layers > 65535) return BSA_ERR_UNSUPPORTED;
     if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
     const dim3 grid((unsigned)c->n_seqs, (unsigned)(2 * c->layers));
-    bsa::accept_kernel<<<grid, bsa::kAcceptThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        p, context_len, accepted, n_accepted, T, new_len);
-    return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    const cudaError_t e =
+        bsa::launch_after(bsa::accept_kernel, grid, bsa::kAcceptThreads, 0, reinterpret_cast<cudaStream_t>(stream), p,
+                          context_len, accepted, n_accepted, T, new_len);
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // extern "C"

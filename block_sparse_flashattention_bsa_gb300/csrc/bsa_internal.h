@@ -15,6 +15,26 @@ namespace bsa {
 // The current device's error word and SM count (BSA_ERR_UNSUPPORTED on a
 // device the kernels are not built for).  Allocates the word on first use.
 int device_context(int32_t** err, int* sm_count);
+// Launches `kern` so that it may be set up while the kernel before it on the
+// stream is still running (programmatic stream serialisation).  Every CTA of
+// such a kernel waits (griddep_wait) before its first access to global memory,
+// so the order of the stream holds as ever; what overlaps is the launch itself
+// and the kernel's own preparation.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Raises a kernel's dynamic shared-memory limit, once per kernel and device
 // (`done`: one bit per device, a static of the caller).
 cudaError_t raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>* done);

@@ -189,6 +189,8 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
     const int kind = cta_side(p, &idx);
     const RopeSide& sd = p.side[kind];
     const Lane<D, IL> ln(p.rd);
+    griddep_launch_dependents();
+    griddep_wait();
     // the first rows are requested before the frequencies are waited for
     const double freq = sd.rotate && threadIdx.x < p.rd / 2 ? p.inv_freq[threadIdx.x] : 0.0;
     bool first = true;
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident) norm_rope_bwd_kern
     int idx;
     const RopeSide& sd = p.side[cta_side(p, &idx)];
     griddep_launch_dependents();
+    griddep_wait();
     if (sd.w)
         for (int d = threadIdx.x; d < D; d += kRopeThreads) wsh[d] = sd.w[d];
     if (sd.rotate)
@@ -514,6 +517,7 @@ __global__ void __launch_bounds__(1024) reduce_weight_kernel(const ReduceParams 
     constexpr int C4 = D / 4, G = 1024 / C4;
     __shared__ float4 red[G][C4];
     const int k = blockIdx.x, c = threadIdx.x % C4, g = threadIdx.x / C4;
+    griddep_launch_dependents();
     griddep_wait();
     if (!p.out[k]) return;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -558,26 +562,11 @@ void deal_ctas(RopeParams* p, int D, int U, int ctas, const double* bytes) {
 
 constexpr int kRopeMaxCtas = 1024;  // bound on a kind's CTAs (two per SM), for the workspace
 
-cudaError_t launch_pdl(void (*kern)(const ReduceParams), int grid, int threads, const ReduceParams& p,
-                       cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 template <bool APPEND>
 cudaError_t launch_fwd(const RopeParams& p, int D, int U, bool il, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.side[0].ctas + p.side[1].ctas + p.side[2].ctas);
     auto go = [&](auto kern) {
-        kern<<<grid, kRopeThreads, 0, s>>>(p);
-        return cudaGetLastError();
+        return launch_after(kern, dim3(grid), kRopeThreads, 0, s, p);
     };
     if (D == 128) {
         if (U == kFwdRows) return il ? go(norm_rope_kernel<128, kFwdRows, true, APPEND>) : go(norm_rope_kernel<128, kFwdRows, false, APPEND>);
@@ -624,8 +613,7 @@ cudaError_t launch_bwd(const RopeParams& p, int D, bool il, cudaStream_t s) {
         const cudaError_t e =
             raise_smem_limit(reinterpret_cast<const void*>(kern), kBwdSmem, &raised[(D == 128) * 2 + il]);
         if (e != cudaSuccess) return e;
-        kern<<<grid, kRopeThreads, kBwdSmem, s>>>(p);
-        return cudaGetLastError();
+        return launch_after(kern, dim3(grid), kRopeThreads, kBwdSmem, s, p);
     };
     if (D == 128) return il ? go(norm_rope_bwd_kernel<128, true>) : go(norm_rope_bwd_kernel<128, false>);
     return il ? go(norm_rope_bwd_kernel<64, true>) : go(norm_rope_bwd_kernel<64, false>);
@@ -834,8 +822,8 @@ int bsa_qk_norm_rope_backward(const bsa_norm_rope_args* a, const bsa_norm_rope_g
         bsa::ReduceParams r{{p.side[0].partial, p.side[1].partial},
                             {g->q_weight, g->k_weight},
                             {p.side[0].ctas, p.side[1].ctas}};
-        e = a->D == 128 ? bsa::launch_pdl(bsa::reduce_weight_kernel<128>, 2, 1024, r, s)
-                        : bsa::launch_pdl(bsa::reduce_weight_kernel<64>, 2, 1024, r, s);
+        e = bsa::launch_after(a->D == 128 ? bsa::reduce_weight_kernel<128> : bsa::reduce_weight_kernel<64>, dim3(2), 1024,
+                              0, s, r);
     }
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

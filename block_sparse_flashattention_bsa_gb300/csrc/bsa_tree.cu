@@ -677,7 +677,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     constexpr int NBOX = D / 64, T_BYTES = NBOX * kStep * 128;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023) {
-        if (threadIdx.x == 0) atomicOr(p.err, ERR_LAUNCH);
+        griddep_wait();
+        if (threadIdx.x == 0) {
+            p.meta[blockIdx.x].start = -1;  // nothing to join
+            atomicOr(p.err, ERR_LAUNCH);
+        }
         return;
     }
     uint8_t* sQ = smem;
@@ -686,18 +690,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     TreeCtrl* c = reinterpret_cast<TreeCtrl*>(sT + p.n_slots * T_BYTES + p.dup * D * 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
-    // Prefix sums of the units' steps: every thread a run of units, then a
-    // scan.  The lengths are asked for first; barriers and tensor memory are
-    // set up while they are on their way (the first page is requested 2.0 us
-    // after the kernel's start instead of 3.8).
-    const int mult = p.row_ptr ? p.RT : p.Hkv * p.RT;
-    const int run = (p.units + kTreeThreads - 1) / kTreeThreads;
-    const int u0 = min(p.units, (int)threadIdx.x * run), u1 = min(p.units, u0 + run);
-    int sum = 0;
-    for (int u = u0; u < u1; ++u) {
-        sum += unit_steps(p, p.unit0 + u, blockIdx.x == 0) * mult;
-        c->prefix[u + 1] = sum;
-    }
     {
         const int x = threadIdx.x;
         if (x < kMaxSlots) {
@@ -722,14 +714,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         fence_mbar_init();
     }
-    if (warp == kMma) {
-        tmem_alloc(&c->tmem_base, 512);
-        tmem_relinquish();
-    }
     if (warp == kProducer && lane == 0) {
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
+    }
+    // Nothing before this line reads or writes global memory or takes tensor
+    // memory (which a kernel before this one may still want): only what is
+    // this CTA's own is set up while that one ends.
+    griddep_wait();
+    if (warp == kMma) {
+        tmem_alloc(&c->tmem_base, 512);
+        tmem_relinquish();
+    }
+    // prefix sums of the units' steps: every thread a run of units, then a scan
+    const int mult = p.row_ptr ? p.RT : p.Hkv * p.RT;
+    const int run = (p.units + kTreeThreads - 1) / kTreeThreads;
+    const int u0 = min(p.units, (int)threadIdx.x * run), u1 = min(p.units, u0 + run);
+    int sum = 0;
+    for (int u = u0; u < u1; ++u) {
+        sum += unit_steps(p, p.unit0 + u, blockIdx.x == 0) * mult;
+        c->prefix[u + 1] = sum;
     }
     int incl = sum;
 #pragma unroll
@@ -778,6 +783,7 @@ template <int D, int RB>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     constexpr int WPR = 8 / RB, C = D / 32;
     __shared__ float red[WPR > 1 ? WPR : 1][D + 1];
+    griddep_launch_dependents();
     griddep_wait();
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Meta mt = p.meta[c];
@@ -871,22 +877,14 @@ int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
     for (int u0 = 0; u0 < units; u0 += chunk) {
         p.unit0 = u0;
         p.units = std::min(chunk, units - u0);
-        tree_kernel<D><<<p.grid, kTreeThreads, smem, s>>>(tq, tk, tv, p);
-        if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+        cudaError_t e = launch_after(tree_kernel<D>, dim3((unsigned)p.grid), kTreeThreads, smem, s, tq, tk, tv, p);
+        if (e != cudaSuccess) return BSA_ERR_CUDA;
         if (p.grid < 2) continue;
-        cudaLaunchConfig_t cfg = {};
         // few rows: their parts are dealt over eight warps; many: a warp each
         const int rows = p.tq * p.G, rb = rows <= 16 ? 1 : 8;
-        cfg.gridDim = dim3((unsigned)p.grid - 1, (unsigned)((rows + rb - 1) / rb));
-        cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, rb == 1 ? tree_merge_kernel<D, 1> : tree_merge_kernel<D, 8>, p) != cudaSuccess)
-            return BSA_ERR_CUDA;
+        e = launch_after(rb == 1 ? tree_merge_kernel<D, 1> : tree_merge_kernel<D, 8>,
+                         dim3((unsigned)p.grid - 1, (unsigned)((rows + rb - 1) / rb)), 256, 0, s, p);
+        if (e != cudaSuccess) return BSA_ERR_CUDA;
     }
     return BSA_OK;
 }
