@@ -3,8 +3,10 @@
 A thin ctypes binding over ``libbsa.so`` (declared in ``include/bsa.h``).
 Every step of the computation runs in the library's CUDA kernels; this module
 only marshals torch tensors (device memory) and the current CUDA stream into
-the C ABI and turns status codes into exceptions.  There is no fallback: if
-the library is missing or the device is not sm_103, calls raise.
+the C ABI and turns status codes into exceptions (for the projection and
+paged-cache calls, whose kernels can be shorter than that in Python, compiled:
+``csrc/bsa_torch.cpp``).  There is no fallback: if the library is missing or
+the device is not sm_103, calls raise.
 
 Entry points (same names as the C ABI, minus the ``bsa_`` prefix):
 

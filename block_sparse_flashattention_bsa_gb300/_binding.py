@@ -47,9 +47,8 @@ class _ForwardArgs(ctypes.Structure):
                 ("causal", ctypes.c_int32), ("out_fp32", ctypes.c_int32)]
 
 
-# Argument structures of the projection and paged-cache calls.  The Python
-# layer packs them with struct (rope.py, paged.py), three times faster than
-# filling these.
+# Argument structures of the projection and paged-cache calls for callers of
+# the C ABI (the Python entry points fill them in csrc/bsa_torch.cpp).
 class _RopeSpec(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
                 ("factor", ctypes.c_double), ("original_length", ctypes.c_double), ("low", ctypes.c_double),
@@ -146,7 +145,7 @@ def lib():
                 "bsa_debug_stall_next_forward": ([i32], ctypes.c_int),
                 "bsa_forward_noalloc": ([PS, P, P, P, P, P, P, P, ctypes.c_float, i32, P], ctypes.c_int),
                 "bsa_release_workspace": ([], None),
-                # struct arguments: packed bytes, or a ctypes structure by reference
+                # struct arguments: a ctypes structure by reference
                 "bsa_rope_inv_freq": ([P, P], ctypes.c_int),
                 "bsa_qk_norm_rope": ([P, P, P, P, P], ctypes.c_int),
                 "bsa_qk_norm_rope_backward_workspace": ([i32], i64),
@@ -179,48 +178,40 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-class _NoScope:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
+_compiled = None
 
 
-_NO_SCOPE = _NoScope()
+def compiled():
+    """The compiled marshalling of the projection and paged-cache calls
+    (csrc/bsa_torch.cpp); raises if it has not been built."""
+    global _compiled
+    if _compiled is None:
+        lib()  # the library it is linked against
+        try:
+            from . import _bsa_torch
+        except ImportError as e:
+            raise RuntimeError("_bsa_torch.so is not built (run python -m "
+                               "block_sparse_flashattention_bsa_gb300.build)") from e
+        _compiled = _bsa_torch
+    return _compiled
 
 
-def _scope(index: int, stream):
-    """Context in which a call on tensors of CUDA device `index` allocates and
-    launches: that device, and `stream` (default: its current one), so that
-    what the call allocates belongs to the stream that uses it."""
-    if stream is not None:
-        if stream.device.index != index:
-            raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, index))
-        return torch.cuda.stream(stream)
-    if index != torch.cuda.current_device():
-        return torch.cuda.device(index)
-    return _NO_SCOPE
-
-
-# Raw handle of a device's current stream.  (torch.cuda.current_stream builds a
-# stream object for it: 2.9 us a call against 0.1 us.)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _same_device(first: torch.Tensor, *ts: Optional[torch.Tensor]) -> int:
-    """CUDA device index of the tensors, which must share one."""
-    d = first.get_device()
-    if d < 0:
-        raise ValueError("expected CUDA tensors")
-    for t in ts:
-        if t is not None and t.get_device() != d:
-            raise ValueError("tensors on different devices: cuda:%d and %s" % (d, t.device))
-    return d
-
-
-def _addr(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.data_ptr()
+def _call(fn, name: str, stream, *args):
+    """fn(*args) on `stream` (default: the current one of the tensors' device);
+    a status in place of a result is raised."""
+    if stream is None:
+        r = fn(*args)
+    else:
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                if t.get_device() != stream.device.index:
+                    raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+                break
+        with torch.cuda.stream(stream):
+            r = fn(*args)
+    if r.__class__ is int:
+        _check(name, r)
+    return r
 
 
 def _ptr(t: Optional[torch.Tensor]):

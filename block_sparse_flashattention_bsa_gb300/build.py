@@ -1,4 +1,6 @@
-"""Build libbsa.so (the CUDA kernels + C ABI) in-tree with nvcc for sm_103a.
+"""Build libbsa.so (the CUDA kernels + C ABI) in-tree with nvcc for sm_103a,
+and _bsa_torch.so (compiled marshalling of the projection and paged-cache
+calls, linked against it) with the host compiler.
 
 Usage: ``python -m block_sparse_flashattention_bsa_gb300.build [--force]``.
 Translation units compile in parallel into ``_build/`` at the repository
@@ -20,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsa.so")
+BINDING = os.path.join(PKG, "_bsa_torch.so")
+BINDING_SOURCE = "bsa_torch.cpp"
 
 SOURCES = ["bsa_api.cu", "bsa_fwd.cu", "bsa_mask.cu", "bsa_topk.cu", "bsa_noalloc.cu", "bsa_pair.cu", "bsa_bwd.cu", "bsa_fp8.cu", "bsa_shard.cu",
            "bsa_rope.cu", "bsa_cache.cu", "bsa_tree.cu"]
@@ -38,7 +42,7 @@ def nvcc() -> str:
 
 
 def _newest_input() -> float:
-    paths = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.join(INCLUDE, "bsa.h")]
+    paths = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BINDING_SOURCE]] + [os.path.join(INCLUDE, "bsa.h")]
     return max(os.path.getmtime(p) for p in paths)
 
 
@@ -55,18 +59,46 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-lpthread", "-ldl"]
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    troot = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "bsa_torch.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(troot, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(cuda, "include"), "-I", INCLUDE, "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (BINDING_SOURCE, r.stdout, r.stderr))
+    return obj
+
+
+def _link(cmd, out: str) -> None:
+    tmp = out + ".tmp.%d" % os.getpid()
+    r = subprocess.run([x if x != out else tmp for x in cmd], capture_output=True, text=True)
+    if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
-    os.replace(tmp, LIB)
+    os.replace(tmp, out)
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    newest = _newest_input()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
+        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+        bobj = binding.result()
+    _link([nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-lrt", "-lpthread", "-ldl"], LIB)
+    import torch
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _link([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING, bobj, "-L" + tlib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN",
+           "-Wl,-rpath," + tlib], BINDING)
     return LIB
 
 
