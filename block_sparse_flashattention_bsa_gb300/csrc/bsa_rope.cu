@@ -34,7 +34,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 64;  // rotary_dim / 2 <= 64
 constexpr int kFwdRows = 4;    // rows of a lane group's task (forward, large calls)
 constexpr int kFwdWaves = 8;   // forward CTAs per SM (two resident)
-constexpr int kBwdResident = 2, kBwdWaves = 4;  // the gradients' CTAs per SM: resident, in all
+constexpr int kBwdResident = 2;  // the gradients' CTAs per SM
 constexpr int kBwdStages = 3;  // rows in a lane's ring
 constexpr int kBwdSmem = kBwdStages * 4 * kRopeThreads * 16;
 
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
 // sides are touched in runs: hs * D values of a token, toks * D of a head.  A
 // task is a block of tokens times `runs` such head groups, one after the
 // other, so a token's angles are computed once for them.  What a lane reads
-// of a row -- the two chunks of dz, one copy after the other, and of x --
+// of a row -- two chunks of x and two of each copy's dz, two rows at a time --
 // goes through a ring of its own in shared memory (cp.async, kBwdStages rows
 // ahead, across task boundaries): registers hold one row only, and the loads
 // of three rows are always in flight behind the arithmetic.  No lane reads
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
 // reduce_weight_kernel adds in a fixed order.
 // Bound by DRAM: 16K tokens of 16 + 16 heads of 128 (537 MB): 87 us, 6.2 TB/s
 // (102 us with two rows per lane loaded into registers at a time).
-template <int D, bool REP>
+template <int D, bool NORM, bool REP>
 struct RowIter {
     static constexpr int LPR = D / 16;
     int task, left, c;  // task, rows left in it, copy of the row
@@ -335,11 +335,16 @@ struct RowIter {
         dst = static_cast<char*>(sd.dx) + 2 * (b * sd.gb + n * sd.gn + h * sd.gh);
         z = static_cast<const char*>(sd.dz) + ((b * sd.H + h) * sd.rep * (int64_t)p.N + n) * (D * 2);
     }
-    // The next copy of the row, or the next row; true at the end of the task.
+    // Copies of the row that this step takes: with x one, else two where there are two left.
+    __device__ __forceinline__ int copies(const RopeSide& sd) const {
+        return REP && !(NORM && c == 0) && c + 1 < sd.rep ? 2 : 1;
+    }
+    // The next copies of the row, or the next row; true at the end of the task.
     __device__ __forceinline__ bool next(const RopeSide& sd) {
         if (REP) {
-            z += sd.z_copy;
-            if (++c < sd.rep) return false;
+            const int n = copies(sd);
+            z += n * sd.z_copy;
+            if ((c += n) < sd.rep) return false;
             c = 0;
         }
         z += sd.z_step;
@@ -361,7 +366,7 @@ __device__ __forceinline__ void bwd_rows(const RopeParams& p, const RopeSide& sd
                                          const unsigned long long* turns, const float* wsh, f2* acc) {
     constexpr int LPR = D / 16, C4 = kRopeThreads;
     const Lane<D, IL> ln(p.rd);
-    RowIter<D, REP> pre, cur;
+    RowIter<D, NORM, REP> pre, cur;
     int tok = 0, pre_tok;
     pre.start(p, sd, idx, &pre_tok);
     cur.start(p, sd, idx, &tok);
@@ -376,6 +381,9 @@ __device__ __forceinline__ void bwd_rows(const RopeParams& p, const RopeSide& sd
             if (NORM && (!REP || pre.c == 0)) {
                 cp_async16(r + 2 * C4, pre.x + oa, bytes);
                 cp_async16(r + 3 * C4, pre.x + ob, bytes);
+            } else if (REP && pre.copies(sd) == 2) {
+                cp_async16(r + 2 * C4, pre.z + sd.z_copy + oa, bytes);
+                cp_async16(r + 3 * C4, pre.z + sd.z_copy + ob, bytes);
             }
             if (pre.next(sd)) pre.start(p, sd, pre.task + sd.ctas, &pre_tok);
         }
@@ -417,11 +425,18 @@ __device__ __forceinline__ void bwd_rows(const RopeParams& p, const RopeSide& sd
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = add2(g[e], t[e]);
         }
+        if (REP && cur.copies(sd) == 2) {
+            f2 t[8];
+            unpack8(r[2 * C4], t);
+            unpack8(r[3 * C4], t + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = add2(g[e], t[e]);
+        }
         // the slot read in the step before is free
         fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
         stage = stage + 1 == kBwdStages ? 0 : stage + 1;
         char* dst = cur.dst;
-        const bool live = cur.live, more = REP && cur.c + 1 < sd.rep;
+        const bool live = cur.live, more = REP && cur.c + cur.copies(sd) < sd.rep;
         if (cur.next(sd)) {
             cur.start(p, sd, cur.task + sd.ctas, &tok);
             fresh = true;
@@ -580,8 +595,13 @@ cudaError_t launch_fwd(const RopeParams& p, int D, int U, bool il, cudaStream_t 
 // one task unless that leaves the SMs short of tasks.
 void deal_tasks(RopeParams* p, int D, int sm_count, const double* bytes) {
     const int groups = kRopeThreads / (D / 16);
-    const int ctas = std::min(kBwdWaves * sm_count, kRopeMaxCtas);
     const double all = bytes[0] + bytes[1] + bytes[2];
+    // Four CTAs per SM even out kinds of unequal cost, two save the start of
+    // the second pair: four from 400 KB each on (537 MB: 86.1 us with four,
+    // 89.1 with two; 121 MB: 30.9 and 27.9; 134 MB: 30.0 and 28.3).
+    const double moved = all * p->tokens * D * 2;
+    const int waves = moved >= 4.0 * sm_count * 400e3 ? 4 : kBwdResident;
+    const int ctas = std::min(waves * sm_count, kRopeMaxCtas);
     for (int k = 0; k < 3; ++k) {
         RopeSide& sd = p->side[k];
         if (sd.H == 0) continue;
