@@ -225,22 +225,6 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
         }
         if (APPEND) live = live && seq >= 0;  // padding: read, not written
         const int pos = !live ? 0 : p.pos ? p.pos[b * p.pos_sb + n] : APPEND ? slot : (int)n;
-        if (first) {
-            first = false;
-            if (threadIdx.x < p.rd / 2) turns[threadIdx.x] = to_turns(freq);
-            __syncthreads();
-        }
-        f2 cs[4], sn[4];
-        const bool turn = sd.rotate && (ln.ra || ln.rb);
-        if (turn && live) {
-            float c[8], s[8];
-            lane_angles<LPR, IL>(turns, ln.s, pos, p.gain, c, s);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                cs[e] = {c[2 * e], c[2 * e + 1]};
-                sn[e] = {s[2 * e], s[2 * e + 1]};
-            }
-        }
         // where the row goes: base of head 0 and distance between heads, in 16-byte chunks
         uint4* dst = nullptr;
         int64_t dh = 0;
@@ -263,6 +247,22 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
                 } else if (ln.s == 0 && h0 == 0) {
                     atomicOr(p.err, ERR_BAD_PAGE);
                 }
+            }
+        }
+        if (first) {
+            first = false;
+            if (threadIdx.x < p.rd / 2) turns[threadIdx.x] = to_turns(freq);
+            __syncthreads();
+        }
+        f2 cs[4], sn[4];
+        const bool turn = sd.rotate && (ln.ra || ln.rb);
+        if (turn && live) {
+            float c[8], s[8];
+            lane_angles<LPR, IL>(turns, ln.s, pos, p.gain, c, s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = {c[2 * e], c[2 * e + 1]};
+                sn[e] = {s[2 * e], s[2 * e + 1]};
             }
         }
 #pragma unroll

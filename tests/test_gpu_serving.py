@@ -218,3 +218,73 @@ def test_decoding_step_in_a_graph(bsa):
         assert torch.equal(out, want), i
     assert graphed[2].tolist() == [s + 6 for s in start] == eager[2].tolist()
     assert torch.equal(graphed[0], eager[0]) and torch.equal(graphed[1], eager[1]) and bsa.device_error() == 0
+
+
+def test_calls_keep_nothing(bsa):
+    """Memory and reference counts are what they were after many calls, refused ones among them."""
+    import sys
+    x = torch.randn(1, 16, 6, 64, device="cuda").bfloat16()
+    q, k, v = x[:, :, :2], x[:, :, 2:4], x[:, :, 4:]
+    f, w = bsa.rope_inv_freq(64), torch.ones(64, device="cuda")
+    kc, vc = (torch.zeros(4, 2, 64, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = torch.arange(4, dtype=torch.int32, device="cuda").reshape(2, 2)
+    ref = torch.ones(4, dtype=torch.int32, device="cuda")
+    two, one = torch.tensor([70, 3], dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    out = torch.empty(2, 1, 4, 64, device="cuda", dtype=torch.bfloat16)
+    q1 = torch.randn(2, 1, 4, 64, device="cuda").bfloat16()
+
+    def everything():
+        z = bsa.qk_norm_rope(q, k, v, f, q_weight=w)
+        bsa.qk_norm_rope_backward(*z, q, k, f, q_weight=w)
+        bsa.cache_append(k[0], k[0], v[0], kc, vc, table, two.repeat(8) * 0, two.repeat(8) * 0, f)
+        assert bsa.tree_attention(q1, kc, vc, table, two, out=out)[0] is out
+        bsa.tree_attention(q1, kc, vc, table, two)
+        bsa.cache_accept(kc, vc, table, two, one.reshape(2, 1) * 0, one)
+        bsa.cache_resize(table, ref, one * 0, two, two, kc, vc)
+        bsa.cache_compact(table, ref, kc, vc)
+        for bad in (lambda: bsa.qk_norm_rope(q, k, v, [1.0]), lambda: bsa.qk_norm_rope(q, k, v, f, eps=-1.0),
+                    lambda: bsa.tree_attention(q1, kc, vc, table, None), lambda: bsa.cache_compact(table, ref, kc, out)):
+            with pytest.raises((ValueError, bsa.BsaError)):
+                bad()
+        with pytest.raises(TypeError):
+            bsa.qk_norm_rope(q, k, v, f, kv_repeat=1.5)
+
+    held = (x, q, k, v, f, w, kc, vc, table, ref, two, one, out, q1)
+    everything()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in held]
+    for _ in range(50):
+        everything()
+    torch.cuda.synchronize()
+    assert (torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in held]) == before
+    bsa.device_error()
+
+
+def test_calls_from_two_threads(bsa):
+    """Calls at once from two threads, each on its own stream, with results of their own."""
+    import threading
+    f = bsa.rope_inv_freq(128)
+    g = torch.Generator().manual_seed(2)
+    data = [torch.randn(1, 300 + 100 * i, 12, 128, generator=g).bfloat16().cuda() for i in range(2)]
+
+    def step(x):
+        return bsa.qk_norm_rope(x[:, :, :8], x[:, :, 8:10], x[:, :, 10:], f, kv_repeat=4)
+
+    want = [[t.clone() for t in step(x)] for x in data]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(200):
+                got = step(data[i])
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and bsa.device_error() == 0
