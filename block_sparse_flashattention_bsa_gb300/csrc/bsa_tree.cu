@@ -26,7 +26,7 @@
 // a plain copy; 96 ragged sequences up to 8,192 slots, one token each (1.8 GB):
 // 279 to 289 us; one sequence of 1,500 slots: 9.3 us.
 //
-// One CTA per SM, 10 warps:
+// One CTA per SM, 11 warps:
 //   warps 0-7  softmax, thread = query row (TMEM lane): warpgroup h takes
 //              columns 64 h .. 64 h + 63 of every step, with an O accumulator,
 //              a running maximum and a sum of its own, so that the two need not
@@ -36,12 +36,11 @@
 //              as two bf16 parts, high and low, so that its rounding (2^-17)
 //              does not add to the result's; the second product costs tensor
 //              time that is not the limit.
-//   warp 8     producer: walks the CTA's range, resolves pages and TMA-loads Q
-//              (two buffers) and the K / V tiles (a ring); publishes one
-//              description per step.
+//   warp 8     producer: walks the CTA's range, resolves pages and TMA-loads the
+//              K / V tiles (a ring); publishes one description per step.
+//   warp 10    loads an item's Q as soon as the item before has used its own.
 //   warp 9     MMA: S = Q K^T and O += P V on tcgen05, M = 128 rows whatever
-//              T G is (the rows behind it compute on leftovers of shared
-//              memory and are never stored).
+//              T G is (the rows behind it are zeros and are never stored).
 
 #include <algorithm>
 #include <cmath>
@@ -53,8 +52,8 @@
 namespace bsa {
 namespace {
 
-constexpr int kTreeThreads = 320;
-constexpr int kProducer = 8, kMma = 9;
+constexpr int kTreeThreads = 352;
+constexpr int kProducer = 8, kMma = 9, kQLoader = 10;
 constexpr int kMaxUnits = 2048;   // units of one launch (their prefix sums sit in shared memory)
 constexpr int kMaxCtas = 160;     // partial slots are sized for this many
 constexpr int kMaxSlots = 12;     // K / V ring
@@ -63,6 +62,10 @@ static_assert(2 * kInfos > kMaxSlots + 2, "a description could be overwritten be
 constexpr int kTreeSmem = 232448;
 constexpr int kCtrlBytes = 14336;
 constexpr int kStep = 128;        // key slots per step
+constexpr int kQBox = 128 * 128;  // one 64-column box of Q: 128 rows, those behind the item's zero
+constexpr int kQAhead = 4;        // items announced to the Q loader
+// Q buffers: two of 64-wide heads; of 128-wide ones a second buffer would cost a ring slot.
+__host__ __device__ constexpr int q_buffers(int D) { return D == 64 ? 2 : 1; }
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };  // kFirst, kLast: of an item
 
@@ -85,10 +88,12 @@ struct Meta {  // one per CTA: the item its range starts inside of
 struct TreeCtrl {
     uint64_t t_full[kMaxSlots], t_empty[kMaxSlots];
     uint64_t q_full[2], q_empty[2];
+    uint64_t qi_full[kQAhead], qi_empty[kQAhead];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t i_empty[kInfos];
     uint64_t st_full[4], x_full[4];  // per pair of warps with the same rows: both posted their sums, their parts of O
     uint64_t drain;
+    int2 qitem[kQAhead];             // first query head and token of an item's row tile; x < 0: no more
     StepInfo info[kInfos];
     float2 stats[2][128];            // [half][row]: maximum and sum posted at an item's end
     int red[kTreeThreads / 32];
@@ -104,7 +109,7 @@ struct TreeParams {
     int32_t B, T, Hq, Hkv, G, page, P, n_pages;
     int32_t unit0, units;      // units of this launch
     int32_t tq, RT;            // drafted tokens per row tile, row tiles
-    int32_t n_slots, q_box;    // ring slots, bytes of one 64-column box of Q
+    int32_t n_slots;           // ring slots
     int32_t dup;               // TMEM lanes between a row and its copy for the second half's warps (0: none)
     int32_t grid;
     void* out;
@@ -164,9 +169,8 @@ __device__ __forceinline__ unsigned long long visible64(int base, int ctx, unsig
 
 // ---------------------------------------------------------------- producer
 template <int D>
-__device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                              const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, int lo, int hi, int per,
-                              volatile WaitFlag* wf) {
+__device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, const TreeParams& p, uint8_t* sT,
+                              TreeCtrl* c, int lo, int hi, int per, volatile WaitFlag* wf) {
     constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX;
     const int lane = threadIdx.x & 31;
     const bool leader = elect_one();
@@ -198,20 +202,14 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
             if (start < lo) mt = Meta{start, end, per, b, h, t0, dl, 0};
             const int beg = p.row_ptr ? p.row_ptr[gu] : 0;
-            // Q of the item
-            const uint32_t qb = nq & 1;
-            if (!twait(&c->q_empty[qb], ((nq >> 1) & 1) ^ 1, wf)) {
+            // the Q loader's turn, as soon as its buffer is free
+            if (!twait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
                 ok = false;
                 break;
             }
             if (leader) {
-                mbar_arrive_expect_tx(&c->q_full[qb], (uint32_t)(p.tq * p.G * 128 * NBOX * (p.dup ? 2 : 1)));
-#pragma unroll
-                for (int x = 0; x < NBOX; ++x) {
-                    uint8_t* dst = sQ + (qb * NBOX + x) * p.q_box;
-                    tma_load_3d(dst, tq, &c->q_full[qb], x * 64, h * p.G, b * p.T + t0);
-                    if (p.dup) tma_load_3d(dst + p.dup * 128, tq, &c->q_full[qb], x * 64, h * p.G, b * p.T + t0);
-                }
+                c->qitem[nq % kQAhead] = make_int2(h * p.G, b * p.T + t0);
+                mbar_arrive(&c->qi_full[nq % kQAhead]);
             }
             ++nq;
             // steps, 32 pages resolved at a time
@@ -311,6 +309,10 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
             mbar_arrive(&c->t_full[slot]);
             ended = true;
         }
+        if (twait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf) && leader) {
+            c->qitem[nq % kQAhead] = make_int2(-1, 0);
+            mbar_arrive(&c->qi_full[nq % kQAhead]);
+        }
     }
     if (lane == 0) p.meta[blockIdx.x] = mt;
     __syncwarp();
@@ -320,8 +322,40 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
         const uint32_t ns = (uint32_t)p.n_slots;
         for (uint32_t n = nload > ns ? nload - ns + (ended ? 1 : 0) : (ended && nload == ns ? 1 : 0); n < nload; ++n)
             mbar_wait_drain(&c->t_full[n % ns], (n / ns) & 1);
-        for (uint32_t n = nq > 2 ? nq - 2 : 0; n < nq; ++n) mbar_wait_drain(&c->q_full[n & 1], (n >> 1) & 1);
     }
+}
+
+// ---------------------------------------------------------------- Q loader
+// One lane.  An item's queries go to rows 0 .. of a 128-row tile (and, with
+// copies, to rows dup ..); the other rows stay the zeros of the start: the
+// tensor cores work on 128 rows whatever there is, and zeros cost less power
+// than leftovers do (128K trees, 3,000 calls on end, where the power limit
+// lowers the clock: 319 -> 313 us).  A warp of its own, so that waiting for the
+// one buffer holds up no K / V tile.
+template <int D>
+__device__ void tree_q_loader(const CUtensorMap* tq, const TreeParams& p, uint8_t* sQ, TreeCtrl* c,
+                              volatile WaitFlag* wf) {
+    constexpr int NBOX = D / 64, NQB = q_buffers(D);
+    if (elect_one()) {
+        uint32_t n = 0;
+        for (;; ++n) {
+            const uint32_t qi = n % kQAhead, qb = n % NQB;
+            if (!mbar_wait(&c->qi_full[qi], (n / kQAhead) & 1, wf)) break;
+            const int2 it = c->qitem[qi];
+            mbar_arrive(&c->qi_empty[qi]);
+            if (it.x < 0 || !mbar_wait(&c->q_empty[qb], ((n / NQB) & 1) ^ 1, wf)) break;
+            mbar_arrive_expect_tx(&c->q_full[qb], (uint32_t)(p.tq * p.G * 128 * NBOX * (p.dup ? 2 : 1)));
+#pragma unroll
+            for (int x = 0; x < NBOX; ++x) {
+                uint8_t* dst = sQ + (qb * NBOX + x) * kQBox;
+                tma_load_3d(dst, tq, &c->q_full[qb], x * 64, it.x, it.y);
+                if (p.dup) tma_load_3d(dst + p.dup * 128, tq, &c->q_full[qb], x * 64, it.x, it.y);
+            }
+        }
+        // copies still in flight must land before the CTA exits
+        for (uint32_t m = n > NQB ? n - NQB : 0; m < n; ++m) mbar_wait_drain(&c->q_full[m % NQB], (m / NQB) & 1);
+    }
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- MMA
@@ -336,7 +370,7 @@ __device__ void tree_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
 template <int D>
 __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, uint32_t tmem,
                          volatile WaitFlag* wf) {
-    constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX;
+    constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX, NQB = q_buffers(D);
     constexpr uint64_t KDESC = sdesc_sw128_base(16, 1024), VDESC = sdesc_sw128_base(T_BOX, 1024);
     constexpr uint32_t IQK = idesc_bf16_f32(128, kStep, false), IPV = idesc_bf16_f32(128, D, true);
     constexpr int O_COL = 2 * kStep;
@@ -369,13 +403,13 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
                 mbar_arrive(&c->s_full[g & 1]);
                 break;
             }
-            const uint32_t sb = g & 1, qb = nq & 1;
-            if ((flags & kFirst) && !mbar_wait(&c->q_full[qb], (nq >> 1) & 1, wf)) break;
+            const uint32_t sb = g & 1, qb = nq % NQB;
+            if ((flags & kFirst) && !mbar_wait(&c->q_full[qb], (nq / NQB) & 1, wf)) break;
             tc_fence_after();
             const uint64_t kdesc = KDESC + (smem_u32(sT + slot * T_BYTES) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t qd = KDESC + (smem_u32(sQ + (qb * NBOX + (kk >> 2)) * p.q_box + (kk & 3) * 32) >> 4);
+                const uint64_t qd = KDESC + (smem_u32(sQ + (qb * NBOX + (kk >> 2)) * kQBox + (kk & 3) * 32) >> 4);
                 mma_ss(tmem + sb * kStep, qd, kdesc + (uint64_t)(((kk >> 2) * T_BOX + (kk & 3) * 32) >> 4), IQK,
                        kk > 0 ? 1u : 0u);
             }
@@ -685,7 +719,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         return;
     }
     uint8_t* sQ = smem;
-    uint8_t* sT = sQ + 2 * NBOX * p.q_box;
+    uint8_t* sT = sQ + q_buffers(D) * NBOX * kQBox;
     float4* xo = reinterpret_cast<float4*>(sT + p.n_slots * T_BYTES);
     TreeCtrl* c = reinterpret_cast<TreeCtrl*>(sT + p.n_slots * T_BYTES + p.dup * D * 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -706,6 +740,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         } else if (x >= 96 && x < 100) {
             mbar_init(&c->st_full[x - 96], 2);
             mbar_init(&c->x_full[x - 96], 2);
+            mbar_init(&c->qi_full[x - 96], 1);
+            mbar_init(&c->qi_empty[x - 96], 1);
         } else if (x == 128) {
             mbar_init(&c->drain, 1);
             c->wf.abort = 0;
@@ -713,6 +749,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             c->prefix[0] = 0;
         }
         fence_mbar_init();
+        for (int z = x; z < q_buffers(D) * NBOX * kQBox / 16; z += kTreeThreads)
+            reinterpret_cast<uint4*>(sQ)[z] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
     }
     if (warp == kProducer && lane == 0) {
         tma_prefetch_desc(&tq);
@@ -756,9 +795,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int per = (total + p.grid - 1) / p.grid;
     const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
     if (warp == kProducer)
-        tree_producer<D>(&tq, &tk, &tv, p, sQ, sT, c, lo, hi, per, wf);
+        tree_producer<D>(&tk, &tv, p, sT, c, lo, hi, per, wf);
     else if (warp == kMma)
         tree_mma<D>(p, sQ, sT, c, tmem, wf);
+    else if (warp == kQLoader)
+        tree_q_loader<D>(&tq, p, sQ, c, wf);
     else
         tree_softmax<D>(p, sT, xo, c, tmem, wf);
     __syncwarp();
@@ -930,9 +971,8 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
     const int rows = p.tq * p.G, nbox = c->D / 64;
     p.dup = bsa::row_copies(rows, c->D);
-    p.q_box = p.dup * 128 + (rows + 7) / 8 * 1024;
     const int tile = nbox * bsa::kStep * 128;
-    const int fixed = bsa::kCtrlBytes + 2 * nbox * p.q_box + p.dup * c->D * 4;
+    const int fixed = bsa::kCtrlBytes + bsa::q_buffers(c->D) * nbox * bsa::kQBox + p.dup * c->D * 4;
     p.n_slots = std::min(bsa::kMaxSlots, (bsa::kTreeSmem - fixed) / tile);
     const size_t smem = (size_t)p.n_slots * tile + fixed;
     CUtensorMap tq, tk, tv;
