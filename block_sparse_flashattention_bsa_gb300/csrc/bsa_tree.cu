@@ -492,214 +492,228 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
     float m = -INFINITY, l = 0.f;
     const f2 sl2 = {p.scale_log2, p.scale_log2};
     uint32_t items = 0;
+    // The item whose last product is still to come.  Its result is written after
+    // the next item's first weights are taken, which takes as long as that
+    // product does, and before those are handed over, since the next product
+    // starts O anew (96 sequences up to 600 slots: 51 -> 43 us).
+    bool pending = false;
+    float pm = 0.f, pl = 0.f;
+    int b = 0, h = 0, t = 0, dl = 0, part = 0;
     for (uint32_t g = 0;; ++g) {
         const uint32_t is = g % kInfos, sb = g & 1;
         const StepInfo& f = c->info[is];
         if (!twait(&c->s_full[sb], (g >> 1) & 1, wf)) break;
         tc_fence_after();
         const int flags = f.flags;
-        if (flags & kEnd) break;
-        uint32_t vis[2] = {~0u, ~0u};  // visible slots among this half's
-        if (flags & kMask) {
-            const int t = f.t0 + rt, dl = f.dl, nv = f.nv[wh];
-            unsigned long long bits = 0;
-            if (t < dl) {
-                bits = p.mask ? p.mask[(int64_t)f.b * p.T + t] : (2ull << t) - 1;
-                if (dl < 64) bits &= (1ull << dl) - 1;
-            }
-            const unsigned long long v = nv > 0 ? visible64(f.slot0[wh], f.ctx, bits) : 0ull;
-            vis[0] = (uint32_t)v;
-            vis[1] = (uint32_t)(v >> 32);
-            // The V rows of a page's unused slots are zeroed (this half's
-            // keys): their weights are 0, but 0 * NaN would reach O.  A page
-            // that holds nothing was not loaded, its rows are zeros already.
-            const int used = p.page == 64 ? nv : min(max(nv - wh * 64, 0), 64);
-            if (nv > 0 && used < 64) {
-                const uint32_t vslot = (uint32_t)f.vslot;
-                if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
-                uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
-                for (int x = tl; x < (64 - used) * 8 * (D / 64); x += 128) {
-                    const int r = x / (D / 8), q = x % (D / 8);
-                    *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
+        if (!(flags & kEnd)) {
+            uint32_t vis[2] = {~0u, ~0u};  // visible slots among this half's
+            if (flags & kMask) {
+                const int tok = f.t0 + rt, n = f.dl, nv = f.nv[wh];
+                unsigned long long bits = 0;
+                if (tok < n) {
+                    bits = p.mask ? p.mask[(int64_t)f.b * p.T + tok] : (2ull << tok) - 1;
+                    if (n < 64) bits &= (1ull << n) - 1;
                 }
-                fence_proxy_async_smem();
+                const unsigned long long v = nv > 0 ? visible64(f.slot0[wh], f.ctx, bits) : 0ull;
+                vis[0] = (uint32_t)v;
+                vis[1] = (uint32_t)(v >> 32);
+                // The V rows of a page's unused slots are zeroed (this half's
+                // keys): their weights are 0, but 0 * NaN would reach O.  A page
+                // that holds nothing was not loaded, its rows are zeros already.
+                const int used = p.page == 64 ? nv : min(max(nv - wh * 64, 0), 64);
+                if (nv > 0 && used < 64) {
+                    const uint32_t vslot = (uint32_t)f.vslot;
+                    if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
+                    uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
+                    for (int x = tl; x < (64 - used) * 8 * (D / 64); x += 128) {
+                        const int r = x / (D / 8), q = x % (D / 8);
+                        *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+            }
+            if (flags & kFirst) {
+                m = -INFINITY;
+                l = 0.f;
+            }
+            if (!idle) {
+                const uint32_t t_s = tmem + lanes + sb * kStep + wh * 64;
+                uint32_t s[2][32], hi[2][16], lo[2][16];
+                tmem_ld32(t_s, s[0]);
+                tmem_ld32(t_s + 32, s[1]);
+                tmem_wait_ld();
+                reg_fence(s[0]);
+                reg_fence(s[1]);
+                if (flags & kMask) {
+                    hide(s[0], vis[0]);
+                    hide(s[1], vis[1]);
+                }
+                float mx[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t* v = s[x >> 1] + (x & 1) * 16;
+                    mx[x] = __uint_as_float(v[0]);
+#pragma unroll
+                    for (int q = 1; q < 15; q += 2)
+                        mx[x] = fmax3(mx[x], __uint_as_float(v[q]), __uint_as_float(v[q + 1]));
+                    mx[x] = fmaxf(mx[x], __uint_as_float(v[15]));
+                }
+                const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                // raise the reference when it would grow by more than 2^8 (exact
+                // after the division by the sum, which uses the same reference).
+                // Taking the weights before the maximum is known, and again where
+                // a score has outgrown the reference, was slower (128K trees of
+                // 64-wide heads 200 -> 238 us).
+                const bool grow = top > m + 8.f || (m == -INFINITY && top > m);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float alpha = grow ? ex2_approx(m - top) : 1.f;
+                    if (grow) {
+                        m = top;
+                        l *= alpha;
+                    }
+                    if (!(flags & kFirst)) {
+                        // O must hold every earlier step's product before it is scaled
+                        if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < D / 32; ++x) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + x * 32, o);
+                            tmem_wait_ld();
+                            reg_fence(o);
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+                            tmem_st32(t_o + x * 32, o);
+                        }
+                    }
+                }
+                const f2 all = weights(s, sl2, m, hi, lo);
+                __syncwarp();
+                l += all.x + all.y;
+                // 32 columns of P in the columns of their S: 16 of high parts, 16 of low
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    tmem_st16(t_s + x * 32, hi[x]);
+                    tmem_st16(t_s + x * 32 + 16, lo[x]);
+                }
+                tmem_wait_st();
             }
         }
-        int b = 0, h = 0, t = 0, dl = 0, part = 0;
+        if (pending) {
+            pending = false;
+            // the item's (or its part's) result: both halves' sums and accumulators
+            if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
+            c->stats[wh][row] = make_float2(pm, pl);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->st_full[pair]);
+            if (!twait(&c->st_full[pair], items & 1, wf)) break;
+            ++items;
+            if (!idle) {
+                const float2 ml = c->stats[wh ^ 1][row];
+                tc_fence_after();
+                const bool live = row < rows && t < dl;
+                const float mm = fmaxf(pm, ml.x);
+                float w0 = pm == -INFINITY ? 0.f : ex2_approx(pm - mm);
+                float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+                const float sum = wh ? ml.y * w1 + pl * w0 : pl * w0 + ml.y * w1;  // the same in both halves
+                const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
+                const int64_t prow = (int64_t)part * rows + row;
+                if (part < 0) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+                    w0 *= inv;
+                    w1 *= inv;
+                    if (live && wh == 0) p.lse[orow] = row_lse(mm, sum);
+                } else if (live && wh == 0) {
+                    p.part_ml[prow] = make_float2(mm, sum);
+                }
+                const f2 w02 = {w0, w0}, w12 = {p.dup ? 1.f : w1, p.dup ? 1.f : w1};
+                // This half writes columns wh * D/2 .. of the row.  With copies the
+                // other accumulator lies in other lanes: each half hands over its
+                // (weighted) part of the other's columns, [column / 4][row].
+                const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
+                if (p.dup) {
+#pragma unroll 1
+                    for (int x = 0; x < D / 64; ++x) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + (wh ^ 1) * (D / 2) + x * 32, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+                        float4* dst = xo + (wh * (D / 8) + x * 8) * p.dup + row;
+                        if (row < p.dup) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                dst[q * p.dup] = make_float4(
+                                    __uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
+                                    __uint_as_float(o[4 * q + 2]) * w0, __uint_as_float(o[4 * q + 3]) * w0);
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(&c->x_full[pair]);
+                    if (!twait(&c->x_full[pair], (items - 1) & 1, wf)) break;
+                }
+#pragma unroll 1
+                for (int x = 0; x < D / 64; ++x) {
+                    uint32_t o[32], o1[32];
+                    __syncwarp();
+                    tmem_ld32(t_a + x * 32, o);
+                    if (p.dup) {
+                        const float4* src = xo + ((wh ^ 1) * (D / 8) + x * 8) * p.dup + (row & (p.dup - 1));
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float4 f4 = src[q * p.dup];
+                            o1[4 * q] = __float_as_uint(f4.x);
+                            o1[4 * q + 1] = __float_as_uint(f4.y);
+                            o1[4 * q + 2] = __float_as_uint(f4.z);
+                            o1[4 * q + 3] = __float_as_uint(f4.w);
+                        }
+                    } else {
+                        tmem_ld32(t_b + x * 32, o1);
+                    }
+                    tmem_wait_ld();
+                    reg_fence(o);
+                    reg_fence(o1);
+                    if (!live) continue;
+                    f2 v[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = fma2({__uint_as_float(o1[2 * q]), __uint_as_float(o1[2 * q + 1])}, w12,
+                                    mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w02));
+                    const int64_t col = wh * (D / 2) + x * 32;
+                    if (part < 0) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dst[q] = make_uint4(pack_bf16x2(v[4 * q].x, v[4 * q].y),
+                                                pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
+                                                pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
+                                                pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+                    }
+                }
+            }
+        }
+        if (flags & kEnd) break;
         if (flags & kLast) {
+            pending = true;
+            pm = m;
+            pl = l;
             b = f.b;
             h = f.h;
             t = f.t0 + rt;
             dl = f.dl;
             part = f.part;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->i_empty[is]);
-        if (flags & kFirst) {
-            m = -INFINITY;
-            l = 0.f;
-        }
-        if (!idle) {
-            const uint32_t t_s = tmem + lanes + sb * kStep + wh * 64;
-            uint32_t s[2][32], hi[2][16], lo[2][16];
-            tmem_ld32(t_s, s[0]);
-            tmem_ld32(t_s + 32, s[1]);
-            tmem_wait_ld();
-            reg_fence(s[0]);
-            reg_fence(s[1]);
-            if (flags & kMask) {
-                hide(s[0], vis[0]);
-                hide(s[1], vis[1]);
-            }
-            float mx[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint32_t* v = s[x >> 1] + (x & 1) * 16;
-                mx[x] = __uint_as_float(v[0]);
-#pragma unroll
-                for (int q = 1; q < 15; q += 2) mx[x] = fmax3(mx[x], __uint_as_float(v[q]), __uint_as_float(v[q + 1]));
-                mx[x] = fmaxf(mx[x], __uint_as_float(v[15]));
-            }
-            const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-            // raise the reference when it would grow by more than 2^8 (exact
-            // after the division by the sum, which uses the same reference).
-            // Taking the weights before the maximum is known, and again where
-            // a score has outgrown the reference, was slower (128K trees of
-            // 64-wide heads 200 -> 238 us).
-            const bool grow = top > m + 8.f || (m == -INFINITY && top > m);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float alpha = grow ? ex2_approx(m - top) : 1.f;
-                if (grow) {
-                    m = top;
-                    l *= alpha;
-                }
-                if (!(flags & kFirst)) {
-                    // O must hold every earlier step's product before it is scaled
-                    if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int x = 0; x < D / 32; ++x) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + x * 32, o);
-                        tmem_wait_ld();
-                        reg_fence(o);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
-                        tmem_st32(t_o + x * 32, o);
-                    }
-                }
-            }
-            const f2 all = weights(s, sl2, m, hi, lo);
-            __syncwarp();
-            l += all.x + all.y;
-            // 32 columns of P in the columns of their S: 16 of high parts, 16 of low
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                tmem_st16(t_s + x * 32, hi[x]);
-                tmem_st16(t_s + x * 32 + 16, lo[x]);
-            }
-            tmem_wait_st();
-        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->p_full[sb]);
-        if (!(flags & kLast)) continue;
-        // the item's (or its part's) result: both halves' sums and accumulators
-        if (!twait(&c->pv_done[sb], (g >> 1) & 1, wf)) break;
-        c->stats[wh][row] = make_float2(m, l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->st_full[pair]);
-        if (!twait(&c->st_full[pair], items & 1, wf)) break;
-        ++items;
-        if (idle) continue;
-        const float2 ml = c->stats[wh ^ 1][row];
-        tc_fence_after();
-        const bool live = row < rows && t < dl;
-        const float mm = fmaxf(m, ml.x);
-        float w0 = m == -INFINITY ? 0.f : ex2_approx(m - mm);
-        float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
-        const float sum = wh ? ml.y * w1 + l * w0 : l * w0 + ml.y * w1;  // the same in both halves
-        const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
-        const int64_t prow = (int64_t)part * rows + row;
-        if (part < 0) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-            w0 *= inv;
-            w1 *= inv;
-            if (live && wh == 0) p.lse[orow] = row_lse(mm, sum);
-        } else if (live && wh == 0) {
-            p.part_ml[prow] = make_float2(mm, sum);
+        if (lane == 0) {
+            mbar_arrive(&c->i_empty[is]);
+            mbar_arrive(&c->p_full[sb]);
         }
-        const f2 w02 = {w0, w0}, w12 = {p.dup ? 1.f : w1, p.dup ? 1.f : w1};
-        // This half writes columns wh * D/2 .. of the row.  With copies the
-        // other accumulator lies in other lanes: each half hands over its
-        // (weighted) part of the other's columns, [column / 4][row].
-        const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
-        if (p.dup) {
-#pragma unroll 1
-            for (int x = 0; x < D / 64; ++x) {
-                uint32_t o[32];
-                tmem_ld32(t_o + (wh ^ 1) * (D / 2) + x * 32, o);
-                tmem_wait_ld();
-                reg_fence(o);
-                float4* dst = xo + (wh * (D / 8) + x * 8) * p.dup + row;
-                if (row < p.dup) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[q * p.dup] = make_float4(__uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
-                                                     __uint_as_float(o[4 * q + 2]) * w0,
-                                                     __uint_as_float(o[4 * q + 3]) * w0);
-                }
-                __syncwarp();
-            }
-            if (lane == 0) mbar_arrive(&c->x_full[pair]);
-            if (!twait(&c->x_full[pair], (items - 1) & 1, wf)) break;
-        }
-#pragma unroll 1
-        for (int x = 0; x < D / 64; ++x) {
-            uint32_t o[32], o1[32];
-            __syncwarp();
-            tmem_ld32(t_a + x * 32, o);
-            if (p.dup) {
-                const float4* src = xo + ((wh ^ 1) * (D / 8) + x * 8) * p.dup + (row & (p.dup - 1));
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float4 f4 = src[q * p.dup];
-                    o1[4 * q] = __float_as_uint(f4.x);
-                    o1[4 * q + 1] = __float_as_uint(f4.y);
-                    o1[4 * q + 2] = __float_as_uint(f4.z);
-                    o1[4 * q + 3] = __float_as_uint(f4.w);
-                }
-            } else {
-                tmem_ld32(t_b + x * 32, o1);
-            }
-            tmem_wait_ld();
-            reg_fence(o);
-            reg_fence(o1);
-            if (!live) continue;
-            f2 v[16];
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-                v[q] = fma2({__uint_as_float(o1[2 * q]), __uint_as_float(o1[2 * q + 1])}, w12,
-                            mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w02));
-            const int64_t col = wh * (D / 2) + x * 32;
-            if (part < 0) {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    dst[q] = make_uint4(pack_bf16x2(v[4 * q].x, v[4 * q].y),
-                                        pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
-                                        pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
-                                        pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
-            } else {
-                float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    dst[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
-            }
-        }
-        tc_fence_before();
-        __syncwarp();
     }
 }
 
