@@ -95,7 +95,7 @@ struct TreeCtrl {
     uint64_t drain;
     int2 qitem[kQAhead];             // first query head and token of an item's row tile; x < 0: no more
     StepInfo info[kInfos];
-    float2 stats[2][128];            // [half][row]: maximum and sum posted at an item's end
+    float2 stats[2][2][128];         // [item parity][half][row]: maximum and sum posted at an item's end
     int red[kTreeThreads / 32];
     uint32_t tmem_base;
     WaitFlag wf;
@@ -182,22 +182,24 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
     if (lo < hi) {
         // the unit that holds step lo: last u with prefix[u] <= lo
         int u = 0;
-        for (int step = 1 << 10; step > 0; step >>= 1)
+        for (int step = 1 << (31 - __clz(p.units)); step > 0; step >>= 1)
             if (u + step < p.units && c->prefix[u + step] <= lo) u += step;
         int per_item = (c->prefix[u + 1] - c->prefix[u]) / mult;
         int k = (lo - c->prefix[u]) / per_item;  // item of the unit
         int pos = lo;
         while (ok && pos < hi) {
             const int gu = p.unit0 + u;  // unit of the whole call
-            const int n = unit_pages(p, gu, false);
             const int b = p.row_ptr ? gu / p.Hkv : gu;
+            const int start = c->prefix[u] + k * per_item, end = start + per_item;
+            const int s0 = pos - start, s1 = min(end, hi) - start;
+            // without a list an item's first pages do not wait for its length
+            const int pre = p.row_ptr ? 0 : p.table[(int64_t)b * p.P + min(s0 * ppt + lane, p.P - 1)];
+            const int n = unit_pages(p, gu, false);
             const int kr = p.RT == 1 ? k : k / p.RT;  // k = (key head, row tile), or the row tile alone
             const int h = p.row_ptr ? gu - b * p.Hkv : kr;
             const int t0 = (k - kr * p.RT) * p.tq;
             const int ctx = seq_ctx(p, b), dl = seq_dl(p, b);
             const uint32_t len = (uint32_t)ctx + dl;
-            const int start = c->prefix[u] + k * per_item, end = start + per_item;
-            const int s0 = pos - start, s1 = min(end, hi) - start;
             const bool whole = s0 == 0 && start + s1 == end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
             if (start < lo) mt = Meta{start, end, per, b, h, t0, dl, 0};
@@ -225,7 +227,7 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
                         const uint32_t first = (uint32_t)j << shift;
                         nv = len > first ? (int)min(len - first, (uint32_t)p.page) : 0;
                         if (nv > 0) {
-                            const int pg = p.table[(int64_t)b * p.P + j];
+                            const int pg = p.row_ptr || e0 > s0 * ppt ? p.table[(int64_t)b * p.P + j] : pre;
                             if ((unsigned)pg < (unsigned)p.n_pages) {
                                 y = (pg * p.Hkv + h) * p.page;
                             } else {
@@ -489,6 +491,8 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
     const int rows = p.tq * p.G, row = (tl - wh * p.dup) & 127, pair = row >> 5;
     const int rt = row / p.G, rg = row - rt * p.G;  // its drafted token (in the tile) and query head
     const bool idle = (row & 96) >= rows;           // the whole warp lies behind the tile's rows
+    // V's rows are zeroed by the idle warps, if there are any, else by all
+    const int busy = rows > 96 ? 0 : (rows + 31) & ~31;
     float m = -INFINITY, l = 0.f;
     const f2 sl2 = {p.scale_log2, p.scale_log2};
     uint32_t items = 0;
@@ -521,11 +525,11 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
                 // keys): their weights are 0, but 0 * NaN would reach O.  A page
                 // that holds nothing was not loaded, its rows are zeros already.
                 const int used = p.page == 64 ? nv : min(max(nv - wh * 64, 0), 64);
-                if (nv > 0 && used < 64) {
+                if (nv > 0 && used < 64 && row >= busy) {
                     const uint32_t vslot = (uint32_t)f.vslot;
                     if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
                     uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
-                    for (int x = tl; x < (64 - used) * 8 * (D / 64); x += 128) {
+                    for (int x = row - busy; x < (64 - used) * 8 * (D / 64); x += 128 - busy) {
                         const int r = x / (D / 8), q = x % (D / 8);
                         *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
@@ -600,105 +604,104 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
                 tmem_wait_st();
             }
         }
-        if (pending) {
-            pending = false;
+        if (pending && !idle) {
             // the item's (or its part's) result: both halves' sums and accumulators
-            if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
-            c->stats[wh][row] = make_float2(pm, pl);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->st_full[pair]);
             if (!twait(&c->st_full[pair], items & 1, wf)) break;
-            ++items;
-            if (!idle) {
-                const float2 ml = c->stats[wh ^ 1][row];
-                tc_fence_after();
-                const bool live = row < rows && t < dl;
-                const float mm = fmaxf(pm, ml.x);
-                float w0 = pm == -INFINITY ? 0.f : ex2_approx(pm - mm);
-                float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
-                const float sum = wh ? ml.y * w1 + pl * w0 : pl * w0 + ml.y * w1;  // the same in both halves
-                const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
-                const int64_t prow = (int64_t)part * rows + row;
-                if (part < 0) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-                    w0 *= inv;
-                    w1 *= inv;
-                    if (live && wh == 0) p.lse[orow] = row_lse(mm, sum);
-                } else if (live && wh == 0) {
-                    p.part_ml[prow] = make_float2(mm, sum);
-                }
-                const f2 w02 = {w0, w0}, w12 = {p.dup ? 1.f : w1, p.dup ? 1.f : w1};
-                // This half writes columns wh * D/2 .. of the row.  With copies the
-                // other accumulator lies in other lanes: each half hands over its
-                // (weighted) part of the other's columns, [column / 4][row].
-                const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
-                if (p.dup) {
-#pragma unroll 1
-                    for (int x = 0; x < D / 64; ++x) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + (wh ^ 1) * (D / 2) + x * 32, o);
-                        tmem_wait_ld();
-                        reg_fence(o);
-                        float4* dst = xo + (wh * (D / 8) + x * 8) * p.dup + row;
-                        if (row < p.dup) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                dst[q * p.dup] = make_float4(
-                                    __uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
-                                    __uint_as_float(o[4 * q + 2]) * w0, __uint_as_float(o[4 * q + 3]) * w0);
-                        }
-                        __syncwarp();
-                    }
-                    if (lane == 0) mbar_arrive(&c->x_full[pair]);
-                    if (!twait(&c->x_full[pair], (items - 1) & 1, wf)) break;
-                }
+            const float2 ml = c->stats[items & 1][wh ^ 1][row];
+            const bool live = row < rows && t < dl;
+            const float mm = fmaxf(pm, ml.x);
+            float w0 = pm == -INFINITY ? 0.f : ex2_approx(pm - mm);
+            float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+            const float sum = wh ? ml.y * w1 + pl * w0 : pl * w0 + ml.y * w1;  // the same in both halves
+            const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
+            const int64_t prow = (int64_t)part * rows + row;
+            if (part < 0) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+                w0 *= inv;
+                w1 *= inv;
+                if (live && wh == 0) p.lse[orow] = row_lse(mm, sum);
+            } else if (live && wh == 0) {
+                p.part_ml[prow] = make_float2(mm, sum);
+            }
+            const f2 w02 = {w0, w0}, w12 = {p.dup ? 1.f : w1, p.dup ? 1.f : w1};
+            if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
+            tc_fence_after();
+            // This half writes columns wh * D/2 .. of the row.  With copies the
+            // other accumulator lies in other lanes: each half hands over its
+            // (weighted) part of the other's columns, [column / 4][row].
+            const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
+            if (p.dup) {
 #pragma unroll 1
                 for (int x = 0; x < D / 64; ++x) {
-                    uint32_t o[32], o1[32];
-                    __syncwarp();
-                    tmem_ld32(t_a + x * 32, o);
-                    if (p.dup) {
-                        const float4* src = xo + ((wh ^ 1) * (D / 8) + x * 8) * p.dup + (row & (p.dup - 1));
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float4 f4 = src[q * p.dup];
-                            o1[4 * q] = __float_as_uint(f4.x);
-                            o1[4 * q + 1] = __float_as_uint(f4.y);
-                            o1[4 * q + 2] = __float_as_uint(f4.z);
-                            o1[4 * q + 3] = __float_as_uint(f4.w);
-                        }
-                    } else {
-                        tmem_ld32(t_b + x * 32, o1);
-                    }
+                    uint32_t o[32];
+                    tmem_ld32(t_o + (wh ^ 1) * (D / 2) + x * 32, o);
                     tmem_wait_ld();
                     reg_fence(o);
-                    reg_fence(o1);
-                    if (!live) continue;
-                    f2 v[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        v[q] = fma2({__uint_as_float(o1[2 * q]), __uint_as_float(o1[2 * q + 1])}, w12,
-                                    mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w02));
-                    const int64_t col = wh * (D / 2) + x * 32;
-                    if (part < 0) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            dst[q] = make_uint4(pack_bf16x2(v[4 * q].x, v[4 * q].y),
-                                                pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
-                                                pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
-                                                pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
+                    float4* dst = xo + (wh * (D / 8) + x * 8) * p.dup + row;
+                    if (row < p.dup) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+                            dst[q * p.dup] = make_float4(
+                                __uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
+                                __uint_as_float(o[4 * q + 2]) * w0, __uint_as_float(o[4 * q + 3]) * w0);
                     }
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&c->x_full[pair]);
+                if (!twait(&c->x_full[pair], items & 1, wf)) break;
+            }
+#pragma unroll 1
+            for (int x = 0; x < D / 64; ++x) {
+                uint32_t o[32], o1[32];
+                __syncwarp();
+                tmem_ld32(t_a + x * 32, o);
+                if (p.dup) {
+                    const float4* src = xo + ((wh ^ 1) * (D / 8) + x * 8) * p.dup + (row & (p.dup - 1));
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 f4 = src[q * p.dup];
+                        o1[4 * q] = __float_as_uint(f4.x);
+                        o1[4 * q + 1] = __float_as_uint(f4.y);
+                        o1[4 * q + 2] = __float_as_uint(f4.z);
+                        o1[4 * q + 3] = __float_as_uint(f4.w);
+                    }
+                } else {
+                    tmem_ld32(t_b + x * 32, o1);
+                }
+                tmem_wait_ld();
+                reg_fence(o);
+                reg_fence(o1);
+                if (!live) continue;
+                f2 v[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    v[q] = fma2({__uint_as_float(o1[2 * q]), __uint_as_float(o1[2 * q + 1])}, w12,
+                                mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w02));
+                const int64_t col = wh * (D / 2) + x * 32;
+                if (part < 0) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        dst[q] = make_uint4(pack_bf16x2(v[4 * q].x, v[4 * q].y),
+                                            pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
+                                            pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
+                                            pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
                 }
             }
         }
         if (flags & kEnd) break;
+        if (flags & kFirst) {
+            items += pending;
+            pending = false;
+        }
         if (flags & kLast) {
+            // two buffers: the other half may still be at the item before
+            c->stats[items & 1][wh][row] = make_float2(m, l);
             pending = true;
             pm = m;
             pl = l;
@@ -713,6 +716,7 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
         if (lane == 0) {
             mbar_arrive(&c->i_empty[is]);
             mbar_arrive(&c->p_full[sb]);
+            if ((flags & kLast) && !idle) mbar_arrive(&c->st_full[pair]);
         }
     }
 }
