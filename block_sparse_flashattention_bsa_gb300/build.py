@@ -97,7 +97,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     import torch
     tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
     _link([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING, bobj, "-L" + tlib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN",
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN",
            "-Wl,-rpath," + tlib], BINDING)
     return LIB
 
