@@ -99,7 +99,7 @@ struct TreeCtrl {
     int red[kTreeThreads / 32];
     uint32_t tmem_base;
     WaitFlag wf;
-    int prefix[kMaxUnits + 1];
+    int prefix[kMaxUnits + 1];       // sums of the units' steps per item
 };
 
 struct TreeParams {
@@ -180,32 +180,43 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
     bool ok = true, ended = false;
     Meta mt{-1, 0, per, 0, 0, 0, 0, 0};
     if (lo < hi) {
-        // the unit that holds step lo: last u with prefix[u] <= lo
+        // the unit that holds step lo: last u whose first step is not behind it
         int u = 0;
-        for (int step = 1 << (31 - __clz(p.units)); step > 0; step >>= 1)
-            if (u + step < p.units && c->prefix[u + step] <= lo) u += step;
-        int per_item = (c->prefix[u + 1] - c->prefix[u]) / mult;
-        int k = (lo - c->prefix[u]) / per_item;  // item of the unit
+        for (int span = p.units; span > 1;) {
+            const int stride = (span + 31) >> 5, off = lane * stride;
+            const bool le = off < span && c->prefix[u + off] * mult <= lo;
+            u += (__popc(__ballot_sync(0xffffffffu, le)) - 1) * stride;
+            span = min(stride, p.units - u);
+        }
+        int base = c->prefix[u], per_item = c->prefix[u + 1] - base;
+        int k = lo == base * mult ? 0 : (lo - base * mult) / per_item;  // item of the unit
         int pos = lo;
         while (ok && pos < hi) {
             const int gu = p.unit0 + u;  // unit of the whole call
             const int b = p.row_ptr ? gu / p.Hkv : gu;
-            const int start = c->prefix[u] + k * per_item, end = start + per_item;
+            const int ctx = seq_ctx(p, b), dl = seq_dl(p, b);
+            const uint32_t len = (uint32_t)ctx + dl;
+            const int start = base * mult + k * per_item, end = start + per_item;
             const int s0 = pos - start, s1 = min(end, hi) - start;
-            // without a list an item's first pages do not wait for its length
-            const int pre = p.row_ptr ? 0 : p.table[(int64_t)b * p.P + min(s0 * ppt + lane, p.P - 1)];
+            // the first pages are looked up before the item's length is known:
+            // list entries, or without a list the table's
+            const int64_t beg = p.row_ptr ? p.row_ptr[gu] : 0;
+            int pre = 0;
+            if (!p.row_ptr) {
+                pre = p.table[(int64_t)b * p.P + min(s0 * ppt + lane, p.P - 1)];
+            } else {
+                const int64_t at = min(beg + s0 * ppt + lane, p.col_cap - 1);
+                if (at >= 0) pre = p.col_idx[at];
+            }
             const int n = unit_pages(p, gu, false);
             const int kr = p.RT == 1 ? k : k / p.RT;  // k = (key head, row tile), or the row tile alone
             const int h = p.row_ptr ? gu - b * p.Hkv : kr;
             const int t0 = (k - kr * p.RT) * p.tq;
-            const int ctx = seq_ctx(p, b), dl = seq_dl(p, b);
-            const uint32_t len = (uint32_t)ctx + dl;
             const bool whole = s0 == 0 && start + s1 == end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
             if (start < lo) mt = Meta{start, end, per, b, h, t0, dl, 0};
-            const int beg = p.row_ptr ? p.row_ptr[gu] : 0;
             // the Q loader's turn, as soon as its buffer is free
-            if (!twait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
+            if (nq >= kQAhead && !twait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
                 ok = false;
                 break;
             }
@@ -219,7 +230,7 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
                 const int e = e0 + lane;
                 int nv = 0, j = 0, y = -p.page;
                 if (e < n && e < s1 * ppt) {
-                    j = p.row_ptr ? p.col_idx[beg + e] : e;
+                    j = !p.row_ptr ? e : e0 > s0 * ppt ? p.col_idx[beg + e] : pre;
                     if ((unsigned)j >= (unsigned)p.P) {
                         atomicOr(p.err, ERR_BAD_COL);
                         j = 0;
@@ -246,7 +257,7 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
                     const int y1 = __shfl_sync(0xffffffffu, y, q1);
                     const int st = (e0 + q) >> (ppt - 1);
                     const uint32_t is = g % kInfos;
-                    if (!twait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf)) {
+                    if (g >= kInfos && !twait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf)) {
                         ok = false;
                         break;
                     }
@@ -273,7 +284,7 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
                     ++g;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
-                        if (!twait(&c->t_empty[slot], phase ^ 1, wf)) {
+                        if (nload >= (uint32_t)p.n_slots && !twait(&c->t_empty[slot], phase ^ 1, wf)) {
                             ok = false;
                             break;
                         }
@@ -298,7 +309,8 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
             if (++k == mult && pos < hi) {
                 k = 0;
                 ++u;
-                per_item = (c->prefix[u + 1] - c->prefix[u]) / mult;
+                base = c->prefix[u];
+                per_item = c->prefix[u + 1] - base;
             }
         }
     }
@@ -790,7 +802,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int u0 = min(p.units, (int)threadIdx.x * run), u1 = min(p.units, u0 + run);
     int sum = 0;
     for (int u = u0; u < u1; ++u) {
-        sum += unit_steps(p, p.unit0 + u, blockIdx.x == 0) * mult;
+        sum += unit_steps(p, p.unit0 + u, blockIdx.x == 0);
         c->prefix[u + 1] = sum;
     }
     int incl = sum;
@@ -801,15 +813,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     if (lane == 31) c->red[warp] = incl;
     __syncthreads();
-    int before = incl - sum;
-    for (int w = 0; w < warp; ++w) before += c->red[w];
+    const int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? c->red[lane] : 0);
     for (int u = u0; u < u1; ++u) c->prefix[u + 1] += before;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c->tmem_base;
     volatile WaitFlag* wf = &c->wf;
-    const int total = c->prefix[p.units];
+    const int total = c->prefix[p.units] * mult;
     const int per = (total + p.grid - 1) / p.grid;
     const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
     if (warp == kProducer)
