@@ -4,9 +4,9 @@
 // device, so a serving loop never waits for it, and copies at the rate of
 // device memory.
 //
-// A request runs as three launches.  Check: one warp per request walks its
-// table row, finds whether it can be served and how many pages it takes, and
-// snapshots page_ref.  Plan: one CTA settles repeated sequences, adds up the
+// A request runs as three launches, few requests as two (check and plan in one
+// CTA).  Check: one warp per request walks its table row, finds whether it can
+// be served and how many pages it takes, and snapshots page_ref.  Plan: one CTA settles repeated sequences, adds up the
 // needs in request order and lists that many free pages, lowest first.
 // Apply: table and counts (a warp per request) and, in the other CTAs, the
 // rows of part-filled pages.  Every decision is taken on the snapshot and the
@@ -95,11 +95,9 @@ __device__ int row_held(const int32_t* row, int max_pages) {
     return max_pages;
 }
 
-// Check: thread t of nt (whole warps).
+// Check, one warp per request: thread t of nt (whole warps).
 template <bool FORK>
-__device__ void check_requests(const PageReq& p, int64_t t, int64_t nt) {
-    for (int64_t i = t; i < p.n_pages; i += nt) p.w.ref0[i] = p.ref[i];
-    for (int64_t i = t; i < p.n_seqs; i += nt) p.w.claim[i] = 0x7fffffff;
+__device__ void check_requests(const PageReq& p, int64_t t, int64_t nt, int32_t* needs) {
     const int lane = threadIdx.x & 31;
     for (int64_t i = t >> 5; i < p.n; i += nt >> 5) {
         int need = -1, src = -1, rows = 0;
@@ -153,7 +151,7 @@ __device__ void check_requests(const PageReq& p, int64_t t, int64_t nt) {
             }
         }
         if (lane == 0) {
-            p.w.need[i] = need;
+            needs[i] = need;
             p.w.src[i] = src;
             p.w.rows[i] = rows;
         }
@@ -164,7 +162,10 @@ template <bool FORK>
 __global__ void __launch_bounds__(256) pages_check_kernel(const PageReq p) {
     griddep_launch_dependents();
     griddep_wait();
-    check_requests<FORK>(p, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x);
+    const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, nt = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = t; i < p.n_pages; i += nt) p.w.ref0[i] = p.ref[i];
+    for (int64_t i = t; i < p.n_seqs; i += nt) p.w.claim[i] = 0x7fffffff;
+    check_requests<FORK>(p, t, nt, p.w.need);
 }
 
 // Inclusive sum of v over the CTA's threads in order; *total for everyone.
@@ -190,43 +191,64 @@ __device__ __forceinline__ T block_scan(T v, T* total, T* red) {
     return v + (warp ? before : 0);
 }
 
-// Plan.  MODE 0: after the check kernel; 1, 2: the check of a resize or a fork
-// first, in this CTA.  The separate check is for many requests or long rows;
-// where it is small, one launch less is worth more (32 requests of 16 pages in
-// a pool of 3,000: 10.1 to 12.4 us for the two kernels, 7.4 to 9.2 for this one).
-template <int MODE>
+// Requests in order: the later ones of a repeated sequence drop out, the needs
+// are added up, the first free pages listed and the answers given.  needs and
+// claims may lie in shared or global memory (barriers between the phases, and
+// fences for global memory, are the caller's).
+struct Plan {
+    const PageReq& p;
+    int32_t *needs, *claims, *offsets;
+
+    __device__ void claim() const {
+        for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
+            const int seq = p.a[i];
+            if ((unsigned)seq < (unsigned)p.n_seqs) atomicMin(&claims[seq], i);
+        }
+    }
+    // Sum of the needs (passes 31 bits where requests ask for far more than there is).
+    __device__ long long add_up(long long* red64) const {
+        long long sum = 0;
+        for (int i0 = 0; i0 < p.n; i0 += kPlanThreads) {
+            const int i = i0 + threadIdx.x;
+            int need = -1;
+            if (i < p.n) {
+                need = needs[i];
+                if (need >= 0 && static_cast<volatile int32_t*>(claims)[p.a[i]] != i) need = -1;
+                needs[i] = need;
+            }
+            long long total;
+            const long long v = max(need, 0);
+            const long long before = sum + block_scan(v, &total, red64) - v;
+            if (i < p.n) p.w.offset[i] = offsets[i] = (int)min(before, 0x7fffffffll);
+            sum += total;
+        }
+        return sum;
+    }
+    __device__ void answer(int have) const {
+        for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
+            const int need = needs[i];
+            const bool ok = need == 0 || (need > 0 && (int64_t)offsets[i] + need <= have);
+            p.granted[i] = ok;
+            if (!ok) {
+                p.w.rows[i] = 0;
+                atomicOr(p.err, ERR_PAGES);
+            }
+        }
+    }
+};
+
+// Plan after the check kernel.
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PageReq p) {
     __shared__ int red[32];
     __shared__ long long red64[32];
     const int tid = threadIdx.x;
     griddep_launch_dependents();
     griddep_wait();
-    if (MODE) {
-        check_requests<MODE == 2>(p, tid, kPlanThreads);
-        __threadfence();
-        __syncthreads();
-    }
-    for (int i = tid; i < p.n; i += kPlanThreads) {
-        const int seq = p.a[i];
-        if ((unsigned)seq < (unsigned)p.n_seqs) atomicMin(&p.w.claim[seq], i);
-    }
+    const Plan plan{p, p.w.need, p.w.claim, p.w.offset};
+    plan.claim();
     __threadfence();
     __syncthreads();
-    long long sum = 0;  // passes 31 bits where requests ask for far more than there is
-    for (int i0 = 0; i0 < p.n; i0 += kPlanThreads) {
-        const int i = i0 + tid;
-        int need = -1;
-        if (i < p.n) {
-            need = p.w.need[i];
-            if (need >= 0 && __ldcg(&p.w.claim[p.a[i]]) != i) need = -1;
-            p.w.need[i] = need;
-        }
-        long long total;
-        const long long v = max(need, 0);
-        const long long before = sum + block_scan(v, &total, red64) - v;
-        if (i < p.n) p.w.offset[i] = (int)min(before, 0x7fffffffll);
-        sum += total;
-    }
+    const long long sum = plan.add_up(red64);
     // the free pages, ascending, as many as are asked for
     int have = 0;
     for (int i0 = 0; i0 < p.n_pages && have < sum; i0 += 4 * kPlanThreads) {
@@ -244,15 +266,44 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PageReq 
             if (fr[u]) p.w.free_list[at++] = i0 + 4 * tid + u;
         have += total;
     }
-    for (int i = tid; i < p.n; i += kPlanThreads) {
-        const int need = p.w.need[i];
-        const bool ok = need == 0 || (need > 0 && (int64_t)p.w.offset[i] + need <= have);
-        p.granted[i] = ok;
-        if (!ok) {
-            p.w.rows[i] = 0;
-            atomicOr(p.err, ERR_PAGES);
-        }
+    plan.answer(have);
+}
+
+// Check and plan of few requests in one CTA, with what the phases hand on in
+// shared memory (free pages as bits).  32 requests of 16 pages in a pool of
+// 3,000: 10.1 to 12.4 us for the two kernels, 7.4 to 9.2 in one CTA over global
+// memory, 1.2 less in shared memory.  For many requests, long rows or a large
+// pool the check is worth the whole GPU.
+constexpr int kSmallRequests = 2048, kSmallSeqs = 4096, kSmallPages = 32 * kPlanThreads / 2;
+template <bool FORK>
+__global__ void __launch_bounds__(kPlanThreads) pages_small_kernel(const PageReq p) {
+    __shared__ int red[32];
+    __shared__ long long red64[32];
+    __shared__ int32_t needs[kSmallRequests], offsets[kSmallRequests], claims[kSmallSeqs];
+    __shared__ unsigned free_bits[kSmallPages / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    griddep_launch_dependents();
+    griddep_wait();
+    for (int i = tid; i < p.n_seqs; i += kPlanThreads) claims[i] = 0x7fffffff;
+    for (int i0 = tid - lane; i0 < p.n_pages; i0 += kPlanThreads) {
+        const int r = i0 + lane < p.n_pages ? p.ref[i0 + lane] : 1;
+        if (i0 + lane < p.n_pages) p.w.ref0[i0 + lane] = r;
+        const unsigned m = __ballot_sync(0xffffffffu, r == 0);
+        if (lane == 0) free_bits[i0 >> 5] = m;
     }
+    check_requests<FORK>(p, tid, kPlanThreads, needs);
+    __syncthreads();
+    const Plan plan{p, needs, claims, offsets};
+    plan.claim();
+    __syncthreads();
+    const long long sum = plan.add_up(red64);
+    // a word of free pages per thread
+    unsigned m = tid < (p.n_pages + 31) / 32 ? free_bits[tid] : 0;
+    int have;
+    const int cnt = __popc(m);
+    for (int at = block_scan(cnt, &have, red) - cnt; m && at < sum; ++at, m &= m - 1)
+        p.w.free_list[at] = tid * 32 + __ffs(m) - 1;
+    plan.answer(have);
 }
 
 // Copies `chunks` 16-byte pieces, the whole CTA, eight in flight per thread.
@@ -553,13 +604,14 @@ int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n
     const int table_ctas = (int)std::min<int64_t>((n + 7) / 8, sms);
     const int64_t units = (int64_t)n * c->layers * 2 * c->Hkv;
     const unsigned copy_ctas = (unsigned)std::min<int64_t>(units, 8ll * sms);
-    const bool small = (int64_t)n * c->max_pages <= 16384 && c->n_pages <= 16384 && c->n_seqs <= 16384;
+    const bool small = (int64_t)n * c->max_pages <= 16384 && n <= kSmallRequests && c->n_pages <= kSmallPages &&
+                       c->n_seqs <= kSmallSeqs;
     cudaError_t e;
     if (small) {
-        e = launch_after(fork ? pages_plan_kernel<2> : pages_plan_kernel<1>, dim3(1), kPlanThreads, 0, s, p);
+        e = launch_after(fork ? pages_small_kernel<true> : pages_small_kernel<false>, dim3(1), kPlanThreads, 0, s, p);
     } else {
         e = launch_after(fork ? pages_check_kernel<true> : pages_check_kernel<false>, dim3(grid), 256, 0, s, p);
-        if (e == cudaSuccess) e = launch_after(pages_plan_kernel<0>, dim3(1), kPlanThreads, 0, s, p);
+        if (e == cudaSuccess) e = launch_after(pages_plan_kernel, dim3(1), kPlanThreads, 0, s, p);
     }
     if (e == cudaSuccess)
         e = launch_after(fork ? pages_apply_kernel<true> : pages_apply_kernel<false>, dim3(table_ctas + copy_ctas),

@@ -191,6 +191,31 @@ def test_random_histories(bsa, seed, S, P, pages, layers, Hkv, page, D):
     bsa.device_error()
 
 
+@pytest.mark.parametrize("S,P,pages,n", [
+    (3, 300, 16384, 3), (3, 300, 16385, 3), (4096, 2, 70, 12), (4097, 2, 70, 12), (2100, 2, 4300, 2048),
+    (2100, 2, 4300, 2049)])
+def test_up_to_what_one_cta_takes_and_beyond(bsa, S, P, pages, n):
+    """The sizes where a request's check moves from one CTA to all of them."""
+    r = random.Random(S * P + n)
+    m = Model(S, P, pages, 1, 1, 64, 64, n)
+    half = r.sample(range(S), n)
+    do_resize(bsa, m, [(s, 0, r.randint(0, P * 64)) for s in half])
+    # scatter what is free over the whole pool, up to its last page
+    do_resize(bsa, m, [(s, 0, 0) for s in half[::2]] + [(half[-1], 0, 1)])
+    last = next(s for s in range(S) if m.held(s) == 0)
+    m.ref[pages - 1] += 1
+    m.table[last][0] = pages - 1
+    m.dr[pages - 1] += 1
+    m.dt[last, 0] = pages - 1
+    held = [s for s in range(S) if m.held(s)]
+    empty = [s for s in range(S) if not m.held(s)]
+    reqs = [(e, r.choice(held), r.randint(0, 64)) for e in empty]
+    do_fork(bsa, m, (reqs * 3)[:n])
+    do_compact(bsa, m)
+    do_resize(bsa, m, [(s, 0, 0) for s in range(S)][:n])
+    bsa.device_error()
+
+
 def test_refusals_set_the_error_word(bsa):
     m = Model(4, 4, 6, 1, 1)
     do_resize(bsa, m, [(0, 0, 256), (1, 0, 100)])       # the whole pool
