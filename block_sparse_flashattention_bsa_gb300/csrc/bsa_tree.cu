@@ -64,8 +64,10 @@ constexpr int kCtrlBytes = 14336;
 constexpr int kStep = 128;        // key slots per step
 constexpr int kQBox = 128 * 128;  // one 64-column box of Q: 128 rows, those behind the item's zero
 constexpr int kQAhead = 4;        // items announced to the Q loader
-// Q buffers: two of 64-wide heads; of 128-wide ones a second buffer would cost a ring slot.
-__host__ __device__ constexpr int q_buffers(int D) { return D == 64 ? 2 : 1; }
+// Where the splits hand over their accumulators (floats of a row), in bytes.
+__host__ __device__ constexpr int exchange_bytes(int D, int NS, int dup) {
+    return (NS == 4 ? 4 * 32 : dup) * D * 4;
+}
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };  // kFirst, kLast: of an item
 
@@ -87,15 +89,15 @@ struct Meta {  // one per CTA: the item its range starts inside of
 
 struct TreeCtrl {
     uint64_t t_full[kMaxSlots], t_empty[kMaxSlots];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full, q_empty;
     uint64_t qi_full[kQAhead], qi_empty[kQAhead];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t i_empty[kInfos];
-    uint64_t st_full[4], x_full[4];  // per pair of warps with the same rows: both posted their sums, their parts of O
+    uint64_t st_full[4], x_full[4];  // per group of warps with the same rows: all posted their sums, their parts of O
     uint64_t drain;
     int2 qitem[kQAhead];             // first query head and token of an item's row tile; x < 0: no more
     StepInfo info[kInfos];
-    float2 stats[2][2][128];         // [item parity][half][row]: maximum and sum posted at an item's end
+    float2 stats[2][256];            // [item parity][split][row]: maximum and sum posted at an item's end
     int red[kTreeThreads / 32];
     uint32_t tmem_base;
     WaitFlag wf;
@@ -110,7 +112,7 @@ struct TreeParams {
     int32_t unit0, units;      // units of this launch
     int32_t tq, RT;            // drafted tokens per row tile, row tiles
     int32_t n_slots;           // ring slots
-    int32_t dup;               // TMEM lanes between a row and its copy for the second half's warps (0: none)
+    int32_t dup;               // TMEM lanes between a row and its copies for the other splits' warps (0: none)
     int32_t grid;
     void* out;
     float* lse;
@@ -346,28 +348,27 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
 // than leftovers do (128K trees, 3,000 calls on end, where the power limit
 // lowers the clock: 319 -> 313 us).  A warp of its own, so that waiting for the
 // one buffer holds up no K / V tile.
-template <int D>
+template <int D, int NS>
 __device__ void tree_q_loader(const CUtensorMap* tq, const TreeParams& p, uint8_t* sQ, TreeCtrl* c,
                               volatile WaitFlag* wf) {
-    constexpr int NBOX = D / 64, NQB = q_buffers(D);
+    constexpr int NBOX = D / 64;
+    const int copies = p.dup ? NS : 1;
     if (elect_one()) {
         uint32_t n = 0;
         for (;; ++n) {
-            const uint32_t qi = n % kQAhead, qb = n % NQB;
+            const uint32_t qi = n % kQAhead;
             if (!mbar_wait(&c->qi_full[qi], (n / kQAhead) & 1, wf)) break;
             const int2 it = c->qitem[qi];
             mbar_arrive(&c->qi_empty[qi]);
-            if (it.x < 0 || !mbar_wait(&c->q_empty[qb], ((n / NQB) & 1) ^ 1, wf)) break;
-            mbar_arrive_expect_tx(&c->q_full[qb], (uint32_t)(p.tq * p.G * 128 * NBOX * (p.dup ? 2 : 1)));
+            if (it.x < 0 || !mbar_wait(&c->q_empty, (n & 1) ^ 1, wf)) break;
+            mbar_arrive_expect_tx(&c->q_full, (uint32_t)(p.tq * p.G * 128 * NBOX * copies));
 #pragma unroll
-            for (int x = 0; x < NBOX; ++x) {
-                uint8_t* dst = sQ + (qb * NBOX + x) * kQBox;
-                tma_load_3d(dst, tq, &c->q_full[qb], x * 64, it.x, it.y);
-                if (p.dup) tma_load_3d(dst + p.dup * 128, tq, &c->q_full[qb], x * 64, it.x, it.y);
-            }
+            for (int x = 0; x < NBOX; ++x)
+                for (int y = 0; y < copies; ++y)
+                    tma_load_3d(sQ + x * kQBox + y * p.dup * 128, tq, &c->q_full, x * 64, it.x, it.y);
         }
-        // copies still in flight must land before the CTA exits
-        for (uint32_t m = n > NQB ? n - NQB : 0; m < n; ++m) mbar_wait_drain(&c->q_full[m % NQB], (m / NQB) & 1);
+        // a copy still in flight must land before the CTA exits
+        if (n > 0) mbar_wait_drain(&c->q_full, (n - 1) & 1);
     }
     __syncwarp();
 }
@@ -381,10 +382,10 @@ __device__ void tree_q_loader(const CUtensorMap* tq, const TreeParams& p, uint8_
 // come round to them again before the ring has (kInfos is more than the ring's
 // steps).  The lane passes them on with its own arrival on the scores'
 // barrier, so the softmax has one wait per step.
-template <int D>
+template <int D, int NS>
 __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl* c, uint32_t tmem,
                          volatile WaitFlag* wf) {
-    constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX, NQB = q_buffers(D);
+    constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX;
     constexpr uint64_t KDESC = sdesc_sw128_base(16, 1024), VDESC = sdesc_sw128_base(T_BOX, 1024);
     constexpr uint32_t IQK = idesc_bf16_f32(128, kStep, false), IPV = idesc_bf16_f32(128, D, true);
     constexpr int O_COL = 2 * kStep;
@@ -399,10 +400,10 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
 #pragma unroll
             for (int kk = 0; kk < 2 * kStep / 16; ++kk) {
                 // 16 keys, high parts of P, then the same keys' low parts;
-                // keys 0-63 into one accumulator, 64-127 into the other
-                const int k16 = kk >> 1, h = k16 >> 2;
+                // an accumulator for every split's keys
+                const int k16 = kk >> 1, h = k16 / (8 / NS);
                 mma_ts(tmem + O_COL + h * D, tmem + sb * kStep + (k16 >> 1) * 32 + (kk & 1) * 16 + (k16 & 1) * 8,
-                       vdesc + (uint64_t)((k16 * 16 * 128) >> 4), IPV, (pfirst && kk % 8 == 0) ? 0u : 1u);
+                       vdesc + (uint64_t)((k16 * 16 * 128) >> 4), IPV, (pfirst && kk % (16 / NS) == 0) ? 0u : 1u);
             }
             mma_commit(&c->pv_done[sb]);
             mma_commit(&c->t_empty[pslot]);
@@ -417,13 +418,13 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
                 mbar_arrive(&c->s_full[g & 1]);
                 break;
             }
-            const uint32_t sb = g & 1, qb = nq % NQB;
-            if ((flags & kFirst) && !mbar_wait(&c->q_full[qb], (nq / NQB) & 1, wf)) break;
+            const uint32_t sb = g & 1;
+            if ((flags & kFirst) && !mbar_wait(&c->q_full, nq & 1, wf)) break;
             tc_fence_after();
             const uint64_t kdesc = KDESC + (smem_u32(sT + slot * T_BYTES) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t qd = KDESC + (smem_u32(sQ + (qb * NBOX + (kk >> 2)) * kQBox + (kk & 3) * 32) >> 4);
+                const uint64_t qd = KDESC + (smem_u32(sQ + (kk >> 2) * kQBox + (kk & 3) * 32) >> 4);
                 mma_ss(tmem + sb * kStep, qd, kdesc + (uint64_t)(((kk >> 2) * T_BOX + (kk & 3) * 32) >> 4), IQK,
                        kk > 0 ? 1u : 0u);
             }
@@ -431,7 +432,7 @@ __device__ void tree_mma(const TreeParams& p, uint8_t* sQ, uint8_t* sT, TreeCtrl
             mbar_arrive(&c->s_full[sb]);  // what this lane has seen (the step's description) the softmax sees
             mma_commit(&c->t_empty[slot]);
             if (flags & kLast) {
-                mma_commit(&c->q_empty[qb]);
+                mma_commit(&c->q_empty);
                 ++nq;
             }
             if (pend && !issue_pv(g - 1)) break;
@@ -469,15 +470,16 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t vis) {
         if (!((vis >> q) & 1u)) s[q] = __float_as_uint(-INFINITY);
 }
 
-// p = 2^(s * sl2 - m) of 64 columns as bf16 high and low parts; their sum.
+// p = 2^(s * sl2 - m) of 32 NG columns as bf16 high and low parts; their sum.
 // m = -infinity: nothing was visible yet (0 stands in, every p is 0).
-__device__ __forceinline__ f2 weights(const uint32_t (&s)[2][32], f2 sl2, float m, uint32_t (&hi)[2][16],
-                                      uint32_t (&lo)[2][16]) {
+template <int NG>
+__device__ __forceinline__ f2 weights(const uint32_t (&s)[NG][32], f2 sl2, float m, uint32_t (&hi)[NG][16],
+                                      uint32_t (&lo)[NG][16]) {
     const float ref = m == -INFINITY ? 0.f : m;
     const f2 nm2 = {-ref, -ref};
     f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < NG; ++x)
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
             const f2 a = fma2({__uint_as_float(s[x][2 * q]), __uint_as_float(s[x][2 * q + 1])}, sl2, nm2);
@@ -492,19 +494,25 @@ __device__ __forceinline__ f2 weights(const uint32_t (&s)[2][32], f2 sl2, float 
 }
 
 // Warpgroup wh (threads 128 wh ..): columns 64 wh .. of every step.
-template <int D>
+template <int D, int NS>
 __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeCtrl* c, uint32_t tmem,
                              volatile WaitFlag* wf) {
     constexpr int O_COL = 2 * kStep;
-    const int wh = threadIdx.x >> 7, tl = threadIdx.x & 127, lane = threadIdx.x & 31;
+    constexpr int NG = 4 / NS;  // 32-column groups of a split
+    const int wg = threadIdx.x >> 7, tl = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const int wh = NS == 4 ? tl >> 5 : wg;  // split
     const uint32_t lanes = (uint32_t)(tl & 96) << 16;
     const uint32_t t_o = tmem + lanes + O_COL + wh * D;
-    // query row of this TMEM lane (the second half works on the copies, if there are any)
-    const int rows = p.tq * p.G, row = (tl - wh * p.dup) & 127, pair = row >> 5;
+    // query row of this TMEM lane (the other splits work on the copies, if there are any)
+    const int rows = p.tq * p.G, row = NS == 4 ? lane : (tl - wh * p.dup) & 127, group = row >> 5;
     const int rt = row / p.G, rg = row - rt * p.G;  // its drafted token (in the tile) and query head
-    const bool idle = (row & 96) >= rows;           // the whole warp lies behind the tile's rows
-    // V's rows are zeroed by the idle warps, if there are any, else by all
+    // the whole warp lies behind the tile's rows, or its warpgroup is not needed
+    const bool idle = NS == 4 ? wg == 1 : (row & 96) >= rows;
+    // V's rows are zeroed by the idle warps, if there are any, else by all: this
+    // thread's number among them (below 0: none), their number
     const int busy = rows > 96 ? 0 : (rows + 31) & ~31;
+    const int zi = NS == 4 ? (wg ? tl : -1) : row - busy, zn = NS == 4 ? 128 : 128 - busy;
+    constexpr int SR = NS == 4 ? 32 : 128;  // rows of a split's sums
     float m = -INFINITY, l = 0.f;
     const f2 sl2 = {p.scale_log2, p.scale_log2};
     uint32_t items = 0;
@@ -513,7 +521,6 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
     // product does, and before those are handed over, since the next product
     // starts O anew (96 sequences up to 600 slots: 51 -> 43 us).
     bool pending = false;
-    float pm = 0.f, pl = 0.f;
     int b = 0, h = 0, t = 0, dl = 0, part = 0;
     for (uint32_t g = 0;; ++g) {
         const uint32_t is = g % kInfos, sb = g & 1;
@@ -522,31 +529,37 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
         tc_fence_after();
         const int flags = f.flags;
         if (!(flags & kEnd)) {
-            uint32_t vis[2] = {~0u, ~0u};  // visible slots among this half's
+            uint32_t vis[2] = {~0u, ~0u};  // visible slots among this split's
             if (flags & kMask) {
-                const int tok = f.t0 + rt, n = f.dl, nv = f.nv[wh];
+                const int half = wh * NG / 2, tok = f.t0 + rt, n = f.dl, nv = f.nv[half];
                 unsigned long long bits = 0;
                 if (tok < n) {
                     bits = p.mask ? p.mask[(int64_t)f.b * p.T + tok] : (2ull << tok) - 1;
                     if (n < 64) bits &= (1ull << n) - 1;
                 }
-                const unsigned long long v = nv > 0 ? visible64(f.slot0[wh], f.ctx, bits) : 0ull;
-                vis[0] = (uint32_t)v;
+                const unsigned long long v = nv > 0 ? visible64(f.slot0[half], f.ctx, bits) : 0ull;
+                vis[0] = (uint32_t)(NS == 4 && (wh & 1) ? v >> 32 : v);
                 vis[1] = (uint32_t)(v >> 32);
                 // The V rows of a page's unused slots are zeroed (this half's
                 // keys): their weights are 0, but 0 * NaN would reach O.  A page
                 // that holds nothing was not loaded, its rows are zeros already.
-                const int used = p.page == 64 ? nv : min(max(nv - wh * 64, 0), 64);
-                if (nv > 0 && used < 64 && row >= busy) {
+                if (zi >= 0) {
+                    const int h0 = NS == 4 ? 0 : wh, h1 = NS == 4 ? 2 : wh + 1;
                     const uint32_t vslot = (uint32_t)f.vslot;
-                    if (!twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf)) break;
-                    uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (wh * 64 + used) * 128;
-                    for (int x = row - busy; x < (64 - used) * 8 * (D / 64); x += 128 - busy) {
-                        const int r = x / (D / 8), q = x % (D / 8);
-                        *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
+                    bool landed = false;
+                    for (int hh = h0; hh < h1; ++hh) {
+                        const int used = p.page == 64 ? f.nv[hh] : min(max(f.nv[hh] - hh * 64, 0), 64);
+                        if (f.nv[hh] <= 0 || used >= 64) continue;
+                        if (!landed) landed = twait(&c->t_full[vslot & 0x7fffffffu], vslot >> 31, wf);
+                        if (!landed) break;
+                        uint8_t* tile = sT + (vslot & 0x7fffffffu) * (D / 64 * kStep * 128) + (hh * 64 + used) * 128;
+                        for (int x = zi; x < (64 - used) * 8 * (D / 64); x += zn) {
+                            const int r = x / (D / 8), q = x % (D / 8);
+                            *reinterpret_cast<uint4*>(tile + (q >> 3) * (kStep * 128) + r * 128 + (q & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
                     }
-                    fence_proxy_async_smem();
+                    if (landed) fence_proxy_async_smem();
                 }
             }
             if (flags & kFirst) {
@@ -554,20 +567,19 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
                 l = 0.f;
             }
             if (!idle) {
-                const uint32_t t_s = tmem + lanes + sb * kStep + wh * 64;
-                uint32_t s[2][32], hi[2][16], lo[2][16];
-                tmem_ld32(t_s, s[0]);
-                tmem_ld32(t_s + 32, s[1]);
-                tmem_wait_ld();
-                reg_fence(s[0]);
-                reg_fence(s[1]);
-                if (flags & kMask) {
-                    hide(s[0], vis[0]);
-                    hide(s[1], vis[1]);
-                }
-                float mx[4];
+                const uint32_t t_s = tmem + lanes + sb * kStep + wh * NG * 32;
+                uint32_t s[NG][32], hi[NG][16], lo[NG][16];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < NG; ++x) tmem_ld32(t_s + x * 32, s[x]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < NG; ++x) {
+                    reg_fence(s[x]);
+                    if (flags & kMask) hide(s[x], vis[x]);
+                }
+                float mx[2 * NG];
+#pragma unroll
+                for (int x = 0; x < 2 * NG; ++x) {
                     const uint32_t* v = s[x >> 1] + (x & 1) * 16;
                     mx[x] = __uint_as_float(v[0]);
 #pragma unroll
@@ -575,7 +587,9 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
                         mx[x] = fmax3(mx[x], __uint_as_float(v[q]), __uint_as_float(v[q + 1]));
                     mx[x] = fmaxf(mx[x], __uint_as_float(v[15]));
                 }
-                const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                float top = fmaxf(mx[0], mx[1]);
+                if (NG == 2) top = fmax3(top, mx[2 * NG - 2], mx[2 * NG - 1]);
+                top *= p.scale_log2;
                 // raise the reference when it would grow by more than 2^8 (exact
                 // after the division by the sum, which uses the same reference).
                 // Taking the weights before the maximum is known, and again where
@@ -609,7 +623,7 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
                 l += all.x + all.y;
                 // 32 columns of P in the columns of their S: 16 of high parts, 16 of low
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < NG; ++x) {
                     tmem_st16(t_s + x * 32, hi[x]);
                     tmem_st16(t_s + x * 32 + 16, lo[x]);
                 }
@@ -617,14 +631,21 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
             }
         }
         if (pending && !idle) {
-            // the item's (or its part's) result: both halves' sums and accumulators
-            if (!twait(&c->st_full[pair], items & 1, wf)) break;
-            const float2 ml = c->stats[items & 1][wh ^ 1][row];
+            // the item's (or its part's) result: every split's sums and accumulators
+            if (!twait(&c->st_full[group], items & 1, wf)) break;
             const bool live = row < rows && t < dl;
-            const float mm = fmaxf(pm, ml.x);
-            float w0 = pm == -INFINITY ? 0.f : ex2_approx(pm - mm);
-            float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
-            const float sum = wh ? ml.y * w1 + pl * w0 : pl * w0 + ml.y * w1;  // the same in both halves
+            const float2* st = c->stats[items & 1] + row;
+            float mm = st[0].x, sum = 0.f, w0 = 0.f, w1 = 0.f;  // w1: of the other half
+#pragma unroll
+            for (int x = 1; x < NS; ++x) mm = fmaxf(mm, st[x * SR].x);
+#pragma unroll
+            for (int x = 0; x < NS; ++x) {
+                const float2 ml = st[x * SR];
+                const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+                sum += ml.y * w;  // the same in every split
+                if (x == wh) w0 = w;
+                else w1 = w;
+            }
             const int64_t orow = ((int64_t)b * p.T + t) * p.Hq + h * p.G + rg;
             const int64_t prow = (int64_t)part * rows + row;
             if (part < 0) {
@@ -635,74 +656,119 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
             } else if (live && wh == 0) {
                 p.part_ml[prow] = make_float2(mm, sum);
             }
-            const f2 w02 = {w0, w0}, w12 = {p.dup ? 1.f : w1, p.dup ? 1.f : w1};
             if (!twait(&c->pv_done[sb ^ 1], ((g - 1) >> 1) & 1, wf)) break;
             tc_fence_after();
-            // This half writes columns wh * D/2 .. of the row.  With copies the
-            // other accumulator lies in other lanes: each half hands over its
-            // (weighted) part of the other's columns, [column / 4][row].
-            const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
-            if (p.dup) {
+            if constexpr (NS == 4) {
+                // every split lays its weighted accumulator down, [split][column / 4][row],
+                // and adds up and writes a quarter of the row's columns
 #pragma unroll 1
-                for (int x = 0; x < D / 64; ++x) {
+                for (int x = 0; x < D / 32; ++x) {
                     uint32_t o[32];
-                    tmem_ld32(t_o + (wh ^ 1) * (D / 2) + x * 32, o);
+                    tmem_ld32(t_o + x * 32, o);
                     tmem_wait_ld();
                     reg_fence(o);
-                    float4* dst = xo + (wh * (D / 8) + x * 8) * p.dup + row;
-                    if (row < p.dup) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            dst[q * p.dup] = make_float4(
-                                __uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
-                                __uint_as_float(o[4 * q + 2]) * w0, __uint_as_float(o[4 * q + 3]) * w0);
-                    }
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(&c->x_full[pair]);
-                if (!twait(&c->x_full[pair], items & 1, wf)) break;
-            }
-#pragma unroll 1
-            for (int x = 0; x < D / 64; ++x) {
-                uint32_t o[32], o1[32];
-                __syncwarp();
-                tmem_ld32(t_a + x * 32, o);
-                if (p.dup) {
-                    const float4* src = xo + ((wh ^ 1) * (D / 8) + x * 8) * p.dup + (row & (p.dup - 1));
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 f4 = src[q * p.dup];
-                        o1[4 * q] = __float_as_uint(f4.x);
-                        o1[4 * q + 1] = __float_as_uint(f4.y);
-                        o1[4 * q + 2] = __float_as_uint(f4.z);
-                        o1[4 * q + 3] = __float_as_uint(f4.w);
-                    }
-                } else {
-                    tmem_ld32(t_b + x * 32, o1);
-                }
-                tmem_wait_ld();
-                reg_fence(o);
-                reg_fence(o1);
-                if (!live) continue;
-                f2 v[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    v[q] = fma2({__uint_as_float(o1[2 * q]), __uint_as_float(o1[2 * q + 1])}, w12,
-                                mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w02));
-                const int64_t col = wh * (D / 2) + x * 32;
-                if (part < 0) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        dst[q] = make_uint4(pack_bf16x2(v[4 * q].x, v[4 * q].y),
-                                            pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
-                                            pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
-                                            pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
+                    float4* dst = xo + (wh * (D / 4) + x * 8) * 32 + row;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+                        dst[q * 32] = make_float4(__uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
+                                                  __uint_as_float(o[4 * q + 2]) * w0,
+                                                  __uint_as_float(o[4 * q + 3]) * w0);
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&c->x_full[group]);
+                if (!twait(&c->x_full[group], items & 1, wf)) break;
+                if (live) {
+                    const int64_t col = wh * (D / 4);
+                    float4 v[D / 16];
+#pragma unroll
+                    for (int q = 0; q < D / 16; ++q) {
+                        const float4* src = xo + (wh * (D / 16) + q) * 32 + row;
+                        v[q] = src[0];
+#pragma unroll
+                        for (int y = 1; y < NS; ++y) {
+                            const float4 o = src[y * (D / 4) * 32];
+                            v[q] = make_float4(v[q].x + o.x, v[q].y + o.y, v[q].z + o.z, v[q].w + o.w);
+                        }
+                    }
+                    if (part < 0) {
+                        uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
+#pragma unroll
+                        for (int q = 0; q < D / 16; ++q)
+                            dst[q] = make_uint2(pack_bf16x2(v[q].x, v[q].y), pack_bf16x2(v[q].z, v[q].w));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
+#pragma unroll
+                        for (int q = 0; q < D / 16; ++q) dst[q] = v[q];
+                    }
+                }
+            } else {
+                const f2 w02 = {w0, w0}, w12 = {p.dup ? 1.f : w1, p.dup ? 1.f : w1};
+                // This half writes columns wh * D/2 .. of the row.  With copies the
+                // other accumulator lies in other lanes: each half hands over its
+                // (weighted) part of the other's columns, [column / 4][row].
+                const uint32_t t_a = t_o + wh * (D / 2), t_b = tmem + lanes + O_COL + (wh ^ 1) * D + wh * (D / 2);
+                if (p.dup) {
+#pragma unroll 1
+                    for (int x = 0; x < D / 64; ++x) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + (wh ^ 1) * (D / 2) + x * 32, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+                        float4* dst = xo + (wh * (D / 8) + x * 8) * p.dup + row;
+                        if (row < p.dup) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                dst[q * p.dup] = make_float4(
+                                    __uint_as_float(o[4 * q]) * w0, __uint_as_float(o[4 * q + 1]) * w0,
+                                    __uint_as_float(o[4 * q + 2]) * w0, __uint_as_float(o[4 * q + 3]) * w0);
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(&c->x_full[group]);
+                    if (!twait(&c->x_full[group], items & 1, wf)) break;
+                }
+#pragma unroll 1
+                for (int x = 0; x < D / 64; ++x) {
+                    uint32_t o[32], o1[32];
+                    __syncwarp();
+                    tmem_ld32(t_a + x * 32, o);
+                    if (p.dup) {
+                        const float4* src = xo + ((wh ^ 1) * (D / 8) + x * 8) * p.dup + (row & (p.dup - 1));
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float4 f4 = src[q * p.dup];
+                            o1[4 * q] = __float_as_uint(f4.x);
+                            o1[4 * q + 1] = __float_as_uint(f4.y);
+                            o1[4 * q + 2] = __float_as_uint(f4.z);
+                            o1[4 * q + 3] = __float_as_uint(f4.w);
+                        }
+                    } else {
+                        tmem_ld32(t_b + x * 32, o1);
+                    }
+                    tmem_wait_ld();
+                    reg_fence(o);
+                    reg_fence(o1);
+                    if (!live) continue;
+                    f2 v[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = fma2({__uint_as_float(o1[2 * q]), __uint_as_float(o1[2 * q + 1])}, w12,
+                                    mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w02));
+                    const int64_t col = wh * (D / 2) + x * 32;
+                    if (part < 0) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dst[q] = make_uint4(pack_bf16x2(v[4 * q].x, v[4 * q].y),
+                                                pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
+                                                pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
+                                                pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+                    }
                 }
             }
         }
@@ -712,11 +778,9 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
             pending = false;
         }
         if (flags & kLast) {
-            // two buffers: the other half may still be at the item before
-            c->stats[items & 1][wh][row] = make_float2(m, l);
+            // two buffers: the other splits may still be at the item before
+            if (!idle) c->stats[items & 1][wh * SR + row] = make_float2(m, l);
             pending = true;
-            pm = m;
-            pl = l;
             b = f.b;
             h = f.h;
             t = f.t0 + rt;
@@ -728,13 +792,13 @@ __device__ void tree_softmax(const TreeParams& p, uint8_t* sT, float4* xo, TreeC
         if (lane == 0) {
             mbar_arrive(&c->i_empty[is]);
             mbar_arrive(&c->p_full[sb]);
-            if ((flags & kLast) && !idle) mbar_arrive(&c->st_full[pair]);
+            if ((flags & kLast) && !idle) mbar_arrive(&c->st_full[group]);
         }
     }
 }
 
 // ---------------------------------------------------------------- kernel
-template <int D>
+template <int D, int NS>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const TreeParams p) {
@@ -749,9 +813,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         return;
     }
     uint8_t* sQ = smem;
-    uint8_t* sT = sQ + q_buffers(D) * NBOX * kQBox;
+    uint8_t* sT = sQ + NBOX * kQBox;
     float4* xo = reinterpret_cast<float4*>(sT + p.n_slots * T_BYTES);
-    TreeCtrl* c = reinterpret_cast<TreeCtrl*>(sT + p.n_slots * T_BYTES + p.dup * D * 4);
+    TreeCtrl* c = reinterpret_cast<TreeCtrl*>(sT + p.n_slots * T_BYTES + exchange_bytes(D, NS, p.dup));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
     {
@@ -762,24 +826,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         } else if (x >= 32 && x < 32 + kInfos) {
             mbar_init(&c->i_empty[x - 32], 8);  // the softmax warps
         } else if (x >= 64 && x < 66) {
-            mbar_init(&c->q_full[x - 64], 1);
-            mbar_init(&c->q_empty[x - 64], 1);
             mbar_init(&c->s_full[x - 64], 2);  // the scores' commit and the MMA lane itself
             mbar_init(&c->p_full[x - 64], 8);
             mbar_init(&c->pv_done[x - 64], 1);
         } else if (x >= 96 && x < 100) {
-            mbar_init(&c->st_full[x - 96], 2);
-            mbar_init(&c->x_full[x - 96], 2);
+            mbar_init(&c->st_full[x - 96], NS);
+            mbar_init(&c->x_full[x - 96], NS);
             mbar_init(&c->qi_full[x - 96], 1);
             mbar_init(&c->qi_empty[x - 96], 1);
         } else if (x == 128) {
             mbar_init(&c->drain, 1);
+            mbar_init(&c->q_full, 1);
+            mbar_init(&c->q_empty, 1);
             c->wf.abort = 0;
             c->wf.limit_ns = p.wait_limit_ns;
             c->prefix[0] = 0;
         }
         fence_mbar_init();
-        for (int z = x; z < q_buffers(D) * NBOX * kQBox / 16; z += kTreeThreads)
+        for (int z = x; z < NBOX * kQBox / 16; z += kTreeThreads)
             reinterpret_cast<uint4*>(sQ)[z] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
@@ -826,11 +890,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp == kProducer)
         tree_producer<D>(&tk, &tv, p, sT, c, lo, hi, per, wf);
     else if (warp == kMma)
-        tree_mma<D>(p, sQ, sT, c, tmem, wf);
+        tree_mma<D, NS>(p, sQ, sT, c, tmem, wf);
     else if (warp == kQLoader)
-        tree_q_loader<D>(&tq, p, sQ, c, wf);
+        tree_q_loader<D, NS>(&tq, p, sQ, c, wf);
     else
-        tree_softmax<D>(p, sT, xo, c, tmem, wf);
+        tree_softmax<D, NS>(p, sT, xo, c, tmem, wf);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -937,17 +1001,17 @@ int tile_tokens(int T, int G) { return std::min(T, 128 / G); }
 
 int64_t ws_part_offset() { return (kMaxCtas * (int64_t)sizeof(Meta) + 255) / 256 * 256; }
 
-template <int D>
+template <int D, int NS>
 int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, int units,
                 int chunk, size_t smem, cudaStream_t s) {
     static_assert(sizeof(TreeCtrl) <= kCtrlBytes, "control block too large");
     static std::atomic<uint64_t> raised{0};
-    if (raise_smem_limit(reinterpret_cast<const void*>(tree_kernel<D>), kTreeSmem, &raised) != cudaSuccess)
+    if (raise_smem_limit(reinterpret_cast<const void*>(tree_kernel<D, NS>), kTreeSmem, &raised) != cudaSuccess)
         return BSA_ERR_CUDA;
     for (int u0 = 0; u0 < units; u0 += chunk) {
         p.unit0 = u0;
         p.units = std::min(chunk, units - u0);
-        cudaError_t e = launch_after(tree_kernel<D>, dim3((unsigned)p.grid), kTreeThreads, smem, s, tq, tk, tv, p);
+        cudaError_t e = launch_after(tree_kernel<D, NS>, dim3((unsigned)p.grid), kTreeThreads, smem, s, tq, tk, tv, p);
         if (e != cudaSuccess) return BSA_ERR_CUDA;
         if (p.grid < 2) continue;
         // few rows: their parts are dealt over eight warps; many: a warp each
@@ -1001,7 +1065,8 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     const int rows = p.tq * p.G, nbox = c->D / 64;
     p.dup = bsa::row_copies(rows, c->D);
     const int tile = nbox * bsa::kStep * 128;
-    const int fixed = bsa::kCtrlBytes + bsa::q_buffers(c->D) * nbox * bsa::kQBox + p.dup * c->D * 4;
+    const int splits = p.dup == 32 ? 4 : 2;
+    const int fixed = bsa::kCtrlBytes + nbox * bsa::kQBox + bsa::exchange_bytes(c->D, splits, p.dup);
     p.n_slots = std::min(bsa::kMaxSlots, (bsa::kTreeSmem - fixed) / tile);
     const size_t smem = (size_t)p.n_slots * tile + fixed;
     CUtensorMap tq, tk, tv;
@@ -1032,8 +1097,10 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.wait_limit_ns = bsa::wait_limit_ns();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return c->D == 128 ? bsa::launch_tree<128>(tq, tk, tv, p, (int)units, chunk, smem, s)
-                       : bsa::launch_tree<64>(tq, tk, tv, p, (int)units, chunk, smem, s);
+    auto launch = c->D == 128  ? bsa::launch_tree<128, 2>
+                  : splits == 4 ? bsa::launch_tree<64, 4>
+                                : bsa::launch_tree<64, 2>;
+    return launch(tq, tk, tv, p, (int)units, chunk, smem, s);
 }
 
 }  // extern "C"
