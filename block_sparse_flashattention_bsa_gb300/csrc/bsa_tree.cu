@@ -22,16 +22,21 @@
 // so results do not depend on timing.
 //
 // Measured: 4 contexts of 131,000 slots, 16 drafts, 32 query heads over 8 key
-// heads of 128 (2.15 GB of cache): 315 to 324 us, 6.6 to 6.8 TB/s, the rate of
+// heads of 128 (2.15 GB of cache): 311 to 321 us, 6.7 to 6.9 TB/s, the rate of
 // a plain copy; 96 ragged sequences up to 8,192 slots, one token each (1.8 GB):
-// 279 to 289 us; one sequence of 1,500 slots: 9.3 us.
+// 270 to 285 us; one sequence of 1,500 slots: 8.1 us.  Long contexts are bound
+// by DRAM (a step of 64 KB per SM every 1.4 us, 7 TB/s); ragged batches lose 5 %
+// to SMs that get less of it; short sequences are bound by the chain of an item
+// (first page, scores, weights, product, result: 3 us a time for two steps).
 //
 // One CTA per SM, 11 warps:
 //   warps 0-7  softmax, thread = query row (TMEM lane): warpgroup h takes
 //              columns 64 h .. 64 h + 63 of every step, with an O accumulator,
 //              a running maximum and a sum of its own, so that the two need not
 //              meet before an item's end (where both write half of the joined
-//              row) and a step's softmax takes half as long.  The maximum is
+//              row) and a step's softmax takes half as long.  64-wide heads with
+//              at most 32 rows: four splits of 32 columns, one to each of warps
+//              0-3, on copies of the rows.  The maximum is
 //              raised only when it grows by more than 2^8.  P goes back over S
 //              as two bf16 parts, high and low, so that its rounding (2^-17)
 //              does not add to the result's; the second product costs tensor
@@ -982,13 +987,15 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
 
 bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// TMEM lanes between the query rows and their copies, 0 for none.  TMEM ties a
+// TMEM lanes between the query rows and their copies, 0 for none; 32: four
+// splits of a step's columns, else two.  TMEM ties a
 // warp to a quarter of the lanes, and a quarter to one of the SM's four
 // schedulers: with few rows both halves' warps share one, and its exponentials
 // are what a step of 64-wide heads waits for.  A second copy of Q in lanes of
 // its own puts the second half's warps on other schedulers: 4 contexts of 128K
 // slots, 64 rows: 200 -> 177 us; 96 ragged sequences up to 8K, 4 rows: 197 ->
-// 173 us.  At 128-wide heads a step has twice the bytes to hide the same
+// 173 us.  Up to 32 rows there is room for four copies, a quarter of the columns
+// each (155.6 -> 153.6 us, listed trees 44.7 -> 43.8).  At 128-wide heads a step has twice the bytes to hide the same
 // softmax, and the ring slot that the copies cost is worth more (4 rows: 290
 // us without, 293 with them).
 int row_copies(int rows, int D) {

@@ -577,6 +577,8 @@ int bsa_convert_f32_bf16(const float *x, void *y, int64_t n, bsa_stream_t stream
  *   gain * (y_a cos - y_b sin, y_b cos + y_a sin); the rest stays as it is.
  * Values are only moved.  Arithmetic in fp32, one rounding to bf16 at the end;
  * angles are exact to 2^-20 for every int32 position (see csrc/bsa_rope.cu).
+ * Like the other calls, the first one on a device allocates its error word:
+ * make it before a stream capture.
  */
 #define BSA_ROPE_PLAIN 0     /* f_i = base^(-2i/rotary_dim) */
 #define BSA_ROPE_LINEAR 1    /* f_i / factor: positions interpolated */
@@ -661,7 +663,9 @@ typedef struct {
  *   seq_ids   device [tokens]: row of the page table; < 0: padding (nothing is written)
  *   slots     device [tokens]: the sequence's slot to write
  *   q_out     device bf16 [tokens, Hq, D]
- * Two tokens with the same sequence and slot: either one's rows stay.
+ * Two tokens with the same sequence and slot: either one's rows stay.  A page
+ * that several sequences share is written for all of them: bsa_cache_resize
+ * first gives each the pages from its length on for its own.
  */
 int bsa_cache_append(const bsa_norm_rope_args *a, const bsa_page_cache *c, const int32_t *seq_ids,
                      const int32_t *slots, void *q_out, bsa_stream_t stream);
