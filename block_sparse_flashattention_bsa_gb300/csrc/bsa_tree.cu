@@ -7,19 +7,23 @@
 // is visible when it is committed, or a draft whose bit is set in the row's
 // tree mask; with block lists, only inside listed pages.
 //
-// What bounds it: every K and V row is read once per row tile of 128 query
-// rows, 4 D bytes a slot, and used for 4 D T G flops; below ~280 flops per
-// byte (T G <= 128) memory is the limit, so the kernel is built to keep loads
-// in flight and everything else behind them.
+// What bounds it: every K and V row is read once, 4 D bytes a slot, and used
+// for 4 D T G flops; below ~280 flops per byte (T G <= 128) memory is the limit,
+// so the kernel is built to keep loads in flight and everything else behind
+// them.  With more rows the exponentials are (2,400 cycles for a step of 128).
 //
-// Work: a step is 128 key slots (one page of 128 or two of 64) of one row
-// tile.  All steps of the batch form one sequence of (unit, item, step), cut
-// into equal ranges, one per CTA: ragged lengths, long contexts with few rows
-// and large batches all load every SM alike.  An item that lies in one range
-// is written out directly; one that a range boundary cuts leaves an
-// unnormalised fp32 part (with its maximum and sum) per range in the
-// workspace, and merge_kernel joins the parts in range order -- no atomics,
-// so results do not depend on timing.
+// Work: a step is 128 key slots (one page of 128 or two of 64); an item the
+// steps of one key head of one sequence.  All steps of the batch form one
+// sequence of (unit, item, step), cut into equal ranges, one per CTA: ragged
+// lengths, long contexts with few rows and large batches all load every SM
+// alike.  Several row tiles: as many CTAs to a range, which read its pages at
+// about the same time, all but one of them from the L2 (ranges over (item, tile)
+// read them from DRAM once per tile: 40 drafts over 4 contexts of 128K, 160 rows
+// a head, 617 us against 551; 64 drafts, 1,024 rows, 635 against 515).  An item
+// that lies in one range is written out directly; one that a range boundary cuts
+// leaves an unnormalised fp32 part (with its maximum and sum) per range in the
+// workspace, and merge_kernel joins the parts in range order -- no atomics, so
+// results do not depend on timing.
 //
 // Measured: 4 contexts of 131,000 slots, 16 drafts, 32 query heads over 8 key
 // heads of 128 (2.15 GB of cache): 311 to 321 us, 6.7 to 6.9 TB/s, the rate of
@@ -118,7 +122,7 @@ struct TreeParams {
     int32_t tq, RT;            // drafted tokens per row tile, row tiles
     int32_t n_slots;           // ring slots
     int32_t dup;               // TMEM lanes between a row and its copies for the other splits' warps (0: none)
-    int32_t grid;
+    int32_t ranges;            // the grid is (RT, ranges)
     void* out;
     float* lse;
     float* part_o;             // [2 * grid][rows][D]
@@ -177,12 +181,12 @@ __device__ __forceinline__ unsigned long long visible64(int base, int ctx, unsig
 // ---------------------------------------------------------------- producer
 template <int D>
 __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, const TreeParams& p, uint8_t* sT,
-                              TreeCtrl* c, int lo, int hi, int per, volatile WaitFlag* wf) {
+                              TreeCtrl* c, int lo, int hi, int per, int t0, volatile WaitFlag* wf) {
     constexpr int NBOX = D / 64, T_BOX = kStep * 128, T_BYTES = NBOX * T_BOX;
     const int lane = threadIdx.x & 31;
     const bool leader = elect_one();
     const int ppt = p.page == 64 ? 2 : 1, shift = page_shift(p);
-    const int mult = p.row_ptr ? p.RT : p.Hkv * p.RT;
+    const int mult = p.row_ptr ? 1 : p.Hkv, cta = blockIdx.y * p.RT + blockIdx.x;
     uint32_t slot = 0, phase = 0, nload = 0, g = 0, nq = 0;
     bool ok = true, ended = false;
     Meta mt{-1, 0, per, 0, 0, 0, 0, 0};
@@ -216,11 +220,9 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
                 if (at >= 0) pre = p.col_idx[at];
             }
             const int n = unit_pages(p, gu, false);
-            const int kr = p.RT == 1 ? k : k / p.RT;  // k = (key head, row tile), or the row tile alone
-            const int h = p.row_ptr ? gu - b * p.Hkv : kr;
-            const int t0 = (k - kr * p.RT) * p.tq;
+            const int h = p.row_ptr ? gu - b * p.Hkv : k;
             const bool whole = s0 == 0 && start + s1 == end;
-            const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
+            const int part = whole ? -1 : 2 * cta + (pos == lo ? 0 : 1);
             if (start < lo) mt = Meta{start, end, per, b, h, t0, dl, 0};
             // the Q loader's turn, as soon as its buffer is free
             if (nq >= kQAhead && !twait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
@@ -335,7 +337,7 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
             mbar_arrive(&c->qi_full[nq % kQAhead]);
         }
     }
-    if (lane == 0) p.meta[blockIdx.x] = mt;
+    if (lane == 0) p.meta[cta] = mt;
     __syncwarp();
     if (leader) {
         // copies still in flight must land before the CTA exits (the end mark
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (smem_u32(smem) & 1023) {
         griddep_wait();
         if (threadIdx.x == 0) {
-            p.meta[blockIdx.x].start = -1;  // nothing to join
+            p.meta[blockIdx.y * p.RT + blockIdx.x].start = -1;  // nothing to join
             atomicOr(p.err, ERR_LAUNCH);
         }
         return;
@@ -866,12 +868,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tmem_relinquish();
     }
     // prefix sums of the units' steps: every thread a run of units, then a scan
-    const int mult = p.row_ptr ? p.RT : p.Hkv * p.RT;
+    const int mult = p.row_ptr ? 1 : p.Hkv;
     const int run = (p.units + kTreeThreads - 1) / kTreeThreads;
     const int u0 = min(p.units, (int)threadIdx.x * run), u1 = min(p.units, u0 + run);
     int sum = 0;
     for (int u = u0; u < u1; ++u) {
-        sum += unit_steps(p, p.unit0 + u, blockIdx.x == 0);
+        sum += unit_steps(p, p.unit0 + u, blockIdx.x + blockIdx.y == 0);
         c->prefix[u + 1] = sum;
     }
     int incl = sum;
@@ -890,10 +892,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t tmem = c->tmem_base;
     volatile WaitFlag* wf = &c->wf;
     const int total = c->prefix[p.units] * mult;
-    const int per = (total + p.grid - 1) / p.grid;
-    const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
+    const int range = blockIdx.y;
+    const int per = (total + p.ranges - 1) / p.ranges;
+    const int lo = min(total, range * per), hi = min(total, lo + per);
+    const int t0 = (int)blockIdx.x * p.tq;  // first drafted token of the CTA's rows
     if (warp == kProducer)
-        tree_producer<D>(&tk, &tv, p, sT, c, lo, hi, per, wf);
+        tree_producer<D>(&tk, &tv, p, sT, c, lo, hi, per, t0, wf);
     else if (warp == kMma)
         tree_mma<D, NS>(p, sQ, sT, c, tmem, wf);
     else if (warp == kQLoader)
@@ -911,8 +915,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge
-// Block x joins the item that the boundary in front of range x + 1 is the
-// first to cut, RB query rows of it, 8 / RB warps to a row (each takes every
+// Block (x, tile) joins the item that the boundary in front of range x + 1 is
+// the first to cut, RB query rows of it, 8 / RB warps to a row (each takes every
 // (8 / RB)-th part; their sums meet in shared memory).  With parts i in range
 // order: m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.
 // Bound by three dependent reads from the L2 (~2 us, and ~1 us after the last
@@ -924,8 +928,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     __shared__ float red[WPR > 1 ? WPR : 1][D + 1];
     griddep_launch_dependents();
     griddep_wait();
-    const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Meta mt = p.meta[c];
+    const int tile = blockIdx.z, c = blockIdx.x + 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Meta mt = p.meta[c * p.RT + tile];
     if (mt.start < 0) return;
     const int rows = p.tq * p.G, per = mt.per, first = c - 1;
     if (mt.start < first * per) return;  // an earlier boundary cuts it too
@@ -934,7 +939,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     const int t = mt.t0 + r / p.G;
     const bool on = r < rows && t < mt.dl;
     if (WPR == 1 && !on) return;
-    auto slot_of = [&](int k) { return k == first && mt.start > first * per ? 2 * k + 1 : 2 * k; };
+    auto slot_of = [&](int k) { return 2 * (k * p.RT + tile) + (k == first && mt.start > first * per ? 1 : 0); };
     float m = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
     for (int x = 0; x < C; ++x) acc[x] = 0.f;
@@ -1018,13 +1023,14 @@ int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
     for (int u0 = 0; u0 < units; u0 += chunk) {
         p.unit0 = u0;
         p.units = std::min(chunk, units - u0);
-        cudaError_t e = launch_after(tree_kernel<D, NS>, dim3((unsigned)p.grid), kTreeThreads, smem, s, tq, tk, tv, p);
+        cudaError_t e = launch_after(tree_kernel<D, NS>, dim3((unsigned)p.RT, (unsigned)p.ranges), kTreeThreads, smem,
+                                     s, tq, tk, tv, p);
         if (e != cudaSuccess) return BSA_ERR_CUDA;
-        if (p.grid < 2) continue;
+        if (p.ranges < 2) continue;
         // few rows: their parts are dealt over eight warps; many: a warp each
         const int rows = p.tq * p.G, rb = rows <= 16 ? 1 : 8;
         e = launch_after(rb == 1 ? tree_merge_kernel<D, 1> : tree_merge_kernel<D, 8>,
-                         dim3((unsigned)p.grid - 1, (unsigned)((rows + rb - 1) / rb)), 256, 0, s, p);
+                         dim3((unsigned)p.ranges - 1, (unsigned)((rows + rb - 1) / rb), (unsigned)p.RT), 256, 0, s, p);
         if (e != cudaSuccess) return BSA_ERR_CUDA;
     }
     return BSA_OK;
@@ -1062,7 +1068,7 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     p.tq = bsa::tile_tokens(a->T, p.G);
     p.RT = (a->T + p.tq - 1) / p.tq;
     // the steps of one launch stay below 2^30 (sums and range ends fit an int)
-    const int64_t mult = a->row_ptr ? p.RT : (int64_t)c->Hkv * p.RT;
+    const int64_t mult = a->row_ptr ? 1 : c->Hkv;
     const int64_t most = ((int64_t)c->max_pages * c->page + bsa::kStep - 1) / bsa::kStep;
     const int64_t units = a->row_ptr ? (int64_t)a->B * c->Hkv : a->B;
     if ((int64_t)a->B * a->T > INT32_MAX || units >= INT32_MAX || mult * most > 1 << 30) return BSA_ERR_INVALID_ARG;
@@ -1095,7 +1101,7 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     p.page = c->page;
     p.P = c->max_pages;
     p.n_pages = c->n_pages;
-    p.grid = std::min(sms, bsa::kMaxCtas);
+    p.ranges = std::max(1, std::min(sms, bsa::kMaxCtas) / p.RT);  // RT <= 64
     p.out = a->out;
     p.lse = a->lse;
     p.meta = static_cast<bsa::Meta*>(workspace);
