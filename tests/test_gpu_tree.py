@@ -377,3 +377,20 @@ def test_far_pages(bsa):
     table[table >= 0] = place.int().cuda()[table[table >= 0].long()]
     got = bsa.tree_attention(c.dev[0], big[0], big[1], table, *c.dev[4:], scale=c.scale)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and bsa.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq,Hkv", [
+    (1, 1, 1), (1, 31, 1), (4, 16, 2), (3, 11, 1), (8, 16, 2), (5, 13, 1), (1, 96, 1), (1, 97, 1), (2, 64, 1),
+    (3, 43, 1), (64, 16, 2), (64, 128, 1)])
+def test_row_counts(bsa, D, T, Hq, Hkv):
+    """Query rows of a key head on both sides of every change of layout (32, 64, 96
+    and 128 rows), and up to 64 tiles of 128."""
+    page = 64 if T % 2 else 128
+    c = Case(4, T, Hq, Hkv, D, page, [0, 127, 129, 1000], dl=[T, T, max(T - 1, 1), 1], seed=Hq + T)
+    got = []
+    for _ in range(2):  # rows behind the drafts stay as they were: zeros
+        o, lse = torch.zeros(4, T, Hq, D, dtype=torch.bfloat16).cuda(), torch.zeros(4, T, Hq).cuda()
+        got.append(c.run(bsa, out=o, lse=lse))
+    c.check(*got[0])
+    assert all(torch.equal(x, y) for x, y in zip(*got)) and bsa.device_error() == 0
