@@ -104,6 +104,7 @@ struct TreeCtrl {
     uint64_t i_empty[kInfos];
     uint64_t st_full[4], x_full[4];  // per group of warps with the same rows: all posted their sums, their parts of O
     uint64_t drain;
+    volatile uint32_t issued;        // steps the producer has issued
     int2 qitem[kQAhead];             // first query head and token of an item's row tile; x < 0: no more
     StepInfo info[kInfos];
     float2 stats[2][256];            // [item parity][split][row]: maximum and sum posted at an item's end
@@ -291,6 +292,7 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
                     }
                     __syncwarp();
                     ++g;
+                    if (leader) c->issued = g;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         if (nload >= (uint32_t)p.n_slots && !twait(&c->t_empty[slot], phase ^ 1, wf)) {
@@ -348,6 +350,15 @@ __device__ void tree_producer(const CUtensorMap* tk, const CUtensorMap* tv, cons
     }
 }
 
+// mbar_wait that leaves it to the caller what a wait beyond the limit means.
+__device__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity, volatile WaitFlag* wf) {
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 31u) == 0 && (wf->abort || globaltimer_ns() - t0 > wf->limit_ns)) return false;
+    }
+}
+
 // ---------------------------------------------------------------- Q loader
 // One lane.  An item's queries go to rows 0 .. of a 128-row tile (and, with
 // copies, to rows dup ..); the other rows stay the zeros of the start: the
@@ -364,7 +375,18 @@ __device__ void tree_q_loader(const CUtensorMap* tq, const TreeParams& p, uint8_
         uint32_t n = 0;
         for (;; ++n) {
             const uint32_t qi = n % kQAhead;
-            if (!mbar_wait(&c->qi_full[qi], (n / kQAhead) & 1, wf)) break;
+            // the next item is announced when this one's loads are through, which
+            // may take longer than a wait: the limit counts from the last step issued
+            bool there;
+            uint32_t seen;
+            do {
+                seen = c->issued;
+                there = mbar_wait_quiet(&c->qi_full[qi], (n / kQAhead) & 1, wf);
+            } while (!there && !wf->abort && c->issued != seen);
+            if (!there) {
+                wf->abort = 1;
+                break;
+            }
             const int2 it = c->qitem[qi];
             mbar_arrive(&c->qi_empty[qi]);
             if (it.x < 0 || !mbar_wait(&c->q_empty, (n & 1) ^ 1, wf)) break;
@@ -846,6 +868,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(&c->q_full, 1);
             mbar_init(&c->q_empty, 1);
             c->wf.abort = 0;
+            c->issued = 0;
             c->wf.limit_ns = p.wait_limit_ns;
             c->prefix[0] = 0;
         }

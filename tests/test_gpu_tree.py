@@ -394,3 +394,27 @@ def test_row_counts(bsa, D, T, Hq, Hkv):
         got.append(c.run(bsa, out=o, lse=lse))
     c.check(*got[0])
     assert all(torch.equal(x, y) for x, y in zip(*got)) and bsa.device_error() == 0
+
+
+def test_long_items_outlast_the_wait_limit(bsa):
+    """Contexts whose item keeps a CTA busy for longer than a pipeline wait may last
+    (all logical pages are a few physical ones)."""
+    B, P, n_pages = 4, 4000, 64
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(B, 2, 32, 128, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(n_pages, 8, 128, 128, generator=g).bfloat16().cuda() for _ in range(2))
+    table = torch.randint(0, n_pages, (B, P), generator=g).int().cuda()
+    ctx = torch.full((B,), P * 128 - 70, dtype=torch.int32).cuda()
+    want = bsa.tree_attention(q, k, v, table, ctx)
+    torch.cuda.synchronize()
+    t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    bsa.set_wait_limit(150_000)
+    try:
+        t0.record()
+        got = bsa.tree_attention(q, k, v, table, ctx)
+        t1.record()
+        torch.cuda.synchronize()
+    finally:
+        bsa.set_wait_limit(0)
+    assert bsa.device_error() == 0 and t0.elapsed_time(t1) > 0.3
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
