@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "bsa.h"
 #include "bsa_internal.h"
@@ -33,6 +34,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 64;  // rotary_dim / 2 <= 64
 constexpr int kFwdRows = 4;    // rows of a lane group's task (forward, large calls)
+constexpr int kAppendRows = 2; // the same of appending
 constexpr int kFwdWaves = 8;   // forward CTAs per SM (two resident)
 constexpr int kBwdResident = 2;  // the gradients' CTAs per SM
 constexpr int kBwdStages = 3;  // rows in a lane's ring
@@ -176,12 +178,32 @@ __device__ __forceinline__ int cta_side(const RopeParams& p, int* idx) {
     return k;
 }
 
+// The lane's two chunks of a row, normed and rotated in place.
+template <int D, bool IL>
+__device__ __forceinline__ void norm_rotate(uint4& a, uint4& b, bool norm, const f2* w, float eps, bool turn,
+                                            const f2* cs, const f2* sn, const Lane<D, IL>& ln) {
+    f2 f[8];
+    unpack8(a, f);
+    unpack8(b, f + 4);
+    if (norm) {
+        f2 ss = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fma2(f[e], f[e], ss);
+        const float r = rsqrtf(row_sum<D / 16>(ss.x + ss.y) * (1.f / D) + eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2({r, r}, w[e]));
+    }
+    if (turn) rotate16<IL>(f, cs, sn, ln.ra, ln.rb);
+    a = pack8(f);
+    b = pack8(f + 4);
+}
+
 // One CTA item: TB = 256 / LPR consecutive tokens times U heads.  A lane
 // group takes one token and loads its U rows at once (64 bytes a lane and
 // row in flight), so the angles are computed once for U rows; neighbouring
 // lane groups take neighbouring tokens, so the head-major stores of a head
 // run over TB consecutive rows.
-template <int D, int U, bool IL, bool APPEND>
+template <int D, int U, bool IL>
 __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel(const RopeParams p) {
     constexpr int LPR = D / 16, TB = kRopeThreads / LPR;
     __shared__ unsigned long long turns[kMaxPairs];
@@ -208,9 +230,7 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
     for (int64_t it = idx; it < items; it += sd.ctas) {
         const int hg = (int)(it % hgroups);
         const int64_t tok = it / hgroups * TB + threadIdx.x / LPR;
-        bool live = tok < p.tokens;
-        const int seq = APPEND && live ? p.seq_ids[tok] : 0;
-        const int slot = APPEND && live ? p.slots[tok] : 0;
+        const bool live = tok < p.tokens;
         const int64_t b = live ? (int)tok / p.N : 0, n = live ? tok - b * p.N : 0;
         const int h0 = hg * U;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sd.x) + b * sd.sb +
@@ -223,31 +243,13 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
             ra[u] = on ? src[u * sh8 + ln.ca] : make_uint4(0, 0, 0, 0);
             rb[u] = on ? src[u * sh8 + ln.cb] : make_uint4(0, 0, 0, 0);
         }
-        if (APPEND) live = live && seq >= 0;  // padding: read, not written
-        const int pos = !live ? 0 : p.pos ? p.pos[b * p.pos_sb + n] : APPEND ? slot : (int)n;
-        // where the row goes: base of head 0 and distance between heads, in 16-byte chunks
+        const int pos = !live ? 0 : p.pos ? p.pos[b * p.pos_sb + n] : (int)n;
+        // where the row goes: head 0, distance between heads, in 16-byte chunks
         uint4* dst = nullptr;
         int64_t dh = 0;
         if (live) {
-            if (!APPEND) {
-                dst = reinterpret_cast<uint4*>(sd.out) + (b * sd.H * sd.rep * (int64_t)p.N + n) * (D / 8);
-                dh = (int64_t)p.N * (D / 8);
-            } else if (kind == 0) {
-                dst = reinterpret_cast<uint4*>(sd.out) + tok * sd.H * (D / 8);
-                dh = D / 8;
-            } else {
-                // a token outside the table, or a slot without a page, is reported and not written
-                int pg = -1;
-                if (seq < p.n_seqs && slot >= 0 && slot / p.page < p.max_pages)
-                    pg = p.page_table[(int64_t)seq * p.max_pages + slot / p.page];
-                if ((unsigned)pg < (unsigned)p.n_pages) {
-                    dst = reinterpret_cast<uint4*>(kind == 1 ? p.k_cache : p.v_cache) +
-                          ((int64_t)pg * sd.H * p.page + slot % p.page) * (D / 8);
-                    dh = (int64_t)p.page * (D / 8);
-                } else if (ln.s == 0 && h0 == 0) {
-                    atomicOr(p.err, ERR_BAD_PAGE);
-                }
-            }
+            dst = reinterpret_cast<uint4*>(sd.out) + (b * sd.H * sd.rep * (int64_t)p.N + n) * (D / 8);
+            dh = (int64_t)p.N * (D / 8);
         }
         if (first) {
             first = false;
@@ -268,30 +270,148 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             uint4 oa = ra[u], ob = rb[u];
-            if (sd.rotate) {
-                f2 f[8];
-                unpack8(ra[u], f);
-                unpack8(rb[u], f + 4);
-                if (norm) {
-                    f2 ss = {0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fma2(f[e], f[e], ss);
-                    const float r = rsqrtf(row_sum<LPR>(ss.x + ss.y) * (1.f / D) + p.eps);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2({r, r}, w[e]));
-                }
-                if (turn) rotate16<IL>(f, cs, sn, ln.ra, ln.rb);
-                oa = pack8(f);
-                ob = pack8(f + 4);
-            }
+            if (sd.rotate) norm_rotate<D, IL>(oa, ob, norm, w, p.eps, turn, cs, sn, ln);
             if (dst && h0 + u < sd.H) {
-                const int copies = APPEND ? 1 : sd.rep;
+                const int copies = sd.rep;
                 uint4* d = dst + (int64_t)(h0 + u) * copies * dh;
                 for (int c = 0; c < copies; ++c) {
                     d[c * dh + ln.ca] = oa;
                     d[c * dh + ln.cb] = ob;
                 }
             }
+        }
+    }
+}
+
+// Appending.  A CTA's items are neighbours, heads first, so that a token's
+// angles and its page are looked up once for its heads, and the next item's
+// rows are on their way while this one's are worked on.  Queries stay
+// token-major; what the forward gains from neighbouring CTAs at neighbouring
+// tokens (runs of a head's rows) there is not, and reading is half of the
+// traffic, not a fifth: 32K tokens of 48 heads of 128 (805 MB) 159 us with the
+// forward's loop, 132 with this one, 6.1 TB/s (the forward 130 with its own, 151
+// with this one); 2,048 tokens 14.0 and 12.9, one token 2.8 and 2.4.
+template <int D, int U, bool IL>
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_append_kernel(const RopeParams p) {
+    constexpr int LPR = D / 16, TB = kRopeThreads / LPR;
+    __shared__ unsigned long long turns[kMaxPairs];
+    int idx;
+    const int kind = cta_side(p, &idx);
+    const RopeSide& sd = p.side[kind];
+    const Lane<D, IL> ln(p.rd);
+    griddep_launch_dependents();
+    griddep_wait();
+    const double freq = sd.rotate && threadIdx.x < p.rd / 2 ? p.inv_freq[threadIdx.x] : 0.0;
+    f2 w[8];
+    const bool norm = sd.w != nullptr;
+    if (norm) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float* we = sd.w + (e < 4 ? ln.ca : ln.cb) * 8 + (2 * e & 7);
+            w[e] = {we[0], we[1]};
+        }
+    }
+    const int hgroups = (sd.H + U - 1) / U;
+    const int64_t items = (p.tokens + TB - 1) / TB * hgroups;
+    const int64_t lo = items * idx / sd.ctas, hi = items * (idx + 1) / sd.ctas;
+    // A lane group's token: what it reads is requested by open(), where its rows
+    // go and its angles follow in place() when the token's turn has come.
+    struct Token {
+        const uint4* src;
+        int64_t tok;
+        int seq, slot, pos;
+        bool live;
+    };
+    auto open = [&](int64_t tb) {
+        Token t;
+        t.tok = tb * TB + threadIdx.x / LPR;
+        t.live = t.tok < p.tokens;
+        t.seq = t.live ? p.seq_ids[t.tok] : -1;
+        t.slot = t.live ? p.slots[t.tok] : 0;
+        t.pos = t.live && p.pos ? p.pos[t.tok] : t.slot;
+        t.src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sd.x) + (t.live ? t.tok * sd.sn : 0));
+        return t;
+    };
+    const int64_t sh8 = sd.sh / 8;
+    auto load = [&](const Token& t, int hg, uint4 (&a)[U], uint4 (&b)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = t.live && hg * U + u < sd.H;
+            const uint4* src = t.src + (hg * U + u) * sh8;
+            a[u] = on ? src[ln.ca] : make_uint4(0, 0, 0, 0);
+            b[u] = on ? src[ln.cb] : make_uint4(0, 0, 0, 0);
+        }
+    };
+    // where the row goes: base of head 0 and distance between heads, in 16-byte chunks
+    uint4* dst = nullptr;
+    int64_t dh = 0;
+    f2 cs[4], sn[4];
+    const bool turn = sd.rotate && (ln.ra || ln.rb);
+    auto place = [&](const Token& t) {
+        dst = nullptr;
+        if (t.seq < 0) return;  // padding: read, not written
+        if (kind == 0) {
+            dst = reinterpret_cast<uint4*>(sd.out) + t.tok * sd.H * (D / 8);
+            dh = D / 8;
+        } else {
+            // a token outside the table, or a slot without a page, is reported and not written
+            int pg = -1;
+            if (t.seq < p.n_seqs && t.slot >= 0 && t.slot / p.page < p.max_pages)
+                pg = p.page_table[(int64_t)t.seq * p.max_pages + t.slot / p.page];
+            if ((unsigned)pg < (unsigned)p.n_pages) {
+                dst = reinterpret_cast<uint4*>(kind == 1 ? p.k_cache : p.v_cache) +
+                      ((int64_t)pg * sd.H * p.page + t.slot % p.page) * (D / 8);
+                dh = (int64_t)p.page * (D / 8);
+            } else if (ln.s == 0) {
+                atomicOr(p.err, ERR_BAD_PAGE);
+            }
+        }
+        if (turn) {
+            float c[8], s[8];
+            lane_angles<LPR, IL>(turns, ln.s, t.pos, p.gain, c, s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = {c[2 * e], c[2 * e + 1]};
+                sn[e] = {s[2 * e], s[2 * e + 1]};
+            }
+        }
+    };
+    int64_t tb = lo / hgroups;
+    int hg = (int)(lo - tb * hgroups);
+    Token t;
+    uint4 ra[U], rb[U];
+    if (lo < hi) {
+        t = open(tb);
+        load(t, hg, ra, rb);
+    }
+    if (threadIdx.x < p.rd / 2) turns[threadIdx.x] = to_turns(freq);
+    __syncthreads();
+    if (lo < hi) place(t);
+    for (int64_t it = lo; it < hi; ++it) {
+        // the next item's rows are requested before this one's are worked on
+        uint4 na[U], nb[U];
+        const bool over = hg + 1 == hgroups, more = it + 1 < hi;
+        if (more) {
+            if (over) t = open(++tb);
+            load(t, over ? 0 : hg + 1, na, nb);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint4 oa = ra[u], ob = rb[u];
+            if (sd.rotate) norm_rotate<D, IL>(oa, ob, norm, w, p.eps, turn, cs, sn, ln);
+            if (dst && hg * U + u < sd.H) {
+                uint4* d = dst + (hg * U + u) * dh;
+                d[ln.ca] = oa;
+                d[ln.cb] = ob;
+            }
+        }
+        if (!more) break;
+        if (over) place(t);
+        hg = over ? 0 : hg + 1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ra[u] = na[u];
+            rb[u] = nb[u];
         }
     }
 }
@@ -566,11 +686,18 @@ __global__ void __launch_bounds__(1024) reduce_weight_kernel(const ReduceParams 
 // all, 750 with eight; 16K tokens of 24 heads: 38.9 with eight, 40.7 with 16).
 void deal_ctas(RopeParams* p, int D, int U, int ctas, const double* bytes) {
     const int TB = kRopeThreads / (D / 16);
-    const double all = bytes[0] + bytes[1] + bytes[2];
+    // a group of fewer than U heads takes as long as a whole one (32K tokens of
+    // 64 + 1 heads, forward: 236 us by bytes alone, 184)
+    double cost[3], all = 0;
+    for (int k = 0; k < 3; ++k) {
+        const int H = p->side[k].H;
+        cost[k] = H > 0 ? bytes[k] * ((H + U - 1) / U * U) / H : 0;
+        all += cost[k];
+    }
     for (int k = 0; k < 3; ++k) {
         RopeSide& sd = p->side[k];
         const int64_t items = sd.H > 0 ? (p->tokens + TB - 1) / TB * ((sd.H + U - 1) / U) : 0;
-        const int64_t share = std::max<int64_t>(1, (int64_t)std::lround(ctas * bytes[k] / all));
+        const int64_t share = std::max<int64_t>(1, (int64_t)std::lround(ctas * cost[k] / all));
         sd.ctas = (int32_t)std::min(items, share);
     }
 }
@@ -580,15 +707,20 @@ constexpr int kRopeMaxCtas = 1024;  // bound on a kind's CTAs (two per SM), for 
 template <bool APPEND>
 cudaError_t launch_fwd(const RopeParams& p, int D, int U, bool il, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.side[0].ctas + p.side[1].ctas + p.side[2].ctas);
-    auto go = [&](auto kern) {
-        return launch_after(kern, dim3(grid), kRopeThreads, 0, s, p);
+    auto go = [&](auto kern) { return launch_after(kern, dim3(grid), kRopeThreads, 0, s, p); };
+    auto pick = [&](auto d, auto u) {
+        if constexpr (APPEND)
+            return il ? go(norm_rope_append_kernel<d.value, u.value, true>)
+                      : go(norm_rope_append_kernel<d.value, u.value, false>);
+        else
+            return il ? go(norm_rope_kernel<d.value, u.value, true>) : go(norm_rope_kernel<d.value, u.value, false>);
     };
-    if (D == 128) {
-        if (U == kFwdRows) return il ? go(norm_rope_kernel<128, kFwdRows, true, APPEND>) : go(norm_rope_kernel<128, kFwdRows, false, APPEND>);
-        return il ? go(norm_rope_kernel<128, 1, true, APPEND>) : go(norm_rope_kernel<128, 1, false, APPEND>);
-    }
-    if (U == kFwdRows) return il ? go(norm_rope_kernel<64, kFwdRows, true, APPEND>) : go(norm_rope_kernel<64, kFwdRows, false, APPEND>);
-    return il ? go(norm_rope_kernel<64, 1, true, APPEND>) : go(norm_rope_kernel<64, 1, false, APPEND>);
+    constexpr std::integral_constant<int, APPEND ? kAppendRows : kFwdRows> many;
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 128> d128;
+    constexpr std::integral_constant<int, 64> d64;
+    if (D == 128) return U > 1 ? pick(d128, many) : pick(d128, one);
+    return U > 1 ? pick(d64, many) : pick(d64, one);
 }
 
 // The gradients' tasks and CTAs of each kind: all heads of a token block in
@@ -652,10 +784,19 @@ bool strides_ok(const int64_t* st) {
 // read four rows at once; single heads spread a small call over more CTAs.
 // Four from half an item per SM on (2,048 tokens of 48 heads, then the
 // acceptance: 18.9 us, 23.8 with single heads; 512 tokens: 8.2 and 9.7).
-int pick_heads(int64_t tokens, int D, int Hq, int Hkv, int sm_count) {
+int pick_heads(int64_t tokens, int D, int Hq, int Hkv, int rows, int sm_count) {
     const int TB = kRopeThreads / (D / 16);
-    const int64_t items = (tokens + TB - 1) / TB * ((Hq + kFwdRows - 1) / kFwdRows + 2 * ((Hkv + kFwdRows - 1) / kFwdRows));
-    return 2 * items >= sm_count ? kFwdRows : 1;
+    const int64_t items = (tokens + TB - 1) / TB * ((Hq + rows - 1) / rows + 2 * ((Hkv + rows - 1) / rows));
+    return 2 * items >= sm_count ? rows : 1;
+}
+
+// Appending: CTAs per SM.  Four start fewer times, six even out what the
+// kinds' items cost (2,048 tokens of 32 + 8 heads, 2.5 items a CTA of four: 12.9
+// us, with six 13.7; 32K of 32 + 32, 80 items: 300 and 255).
+int append_waves(int64_t tokens, int D, int Hq, int Hkv, int U, int sm_count) {
+    const int TB = kRopeThreads / (D / 16);
+    const int64_t items = (tokens + TB - 1) / TB * ((Hq + U - 1) / U + 2 * ((Hkv + U - 1) / U));
+    return items >= 64ll * sm_count ? 6 : 4;
 }
 
 int fill(const bsa_norm_rope_args* a, RopeParams* p) {
@@ -748,7 +889,7 @@ int bsa_qk_norm_rope(const bsa_norm_rope_args* a, void* q_out, void* k_out, void
         p.side[k].out = out[k];
         bytes[k] = (double)p.side[k].H * (1 + p.side[k].rep);
     }
-    const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, sms);
+    const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, bsa::kFwdRows, sms);
     bsa::deal_ctas(&p, a->D, U, bsa::kFwdWaves * sms, bytes);
     const cudaError_t e =
         bsa::launch_fwd<false>(p, a->D, U, a->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
@@ -778,9 +919,11 @@ int bsa_cache_append(const bsa_norm_rope_args* a, const bsa_page_cache* c, const
     p.max_pages = c->max_pages;
     p.page = c->page;
     p.n_pages = c->n_pages;
-    const double bytes[3] = {(double)a->Hq, (double)a->Hkv, (double)a->Hkv};
-    const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, sms);
-    bsa::deal_ctas(&p, a->D, U, bsa::kFwdWaves * sms, bytes);
+    // K and V: 1.2 for their pages' look-up (32K tokens of 64 + 1 heads 203 -> 192 us, of 32 + 8 133 -> 131)
+    const double bytes[3] = {(double)a->Hq, 1.2 * a->Hkv, 1.2 * a->Hkv};
+    const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, bsa::kAppendRows, sms);
+    const int waves = bsa::append_waves(p.tokens, a->D, a->Hq, a->Hkv, U, sms);
+    bsa::deal_ctas(&p, a->D, U, waves * sms, bytes);
     const cudaError_t e =
         bsa::launch_fwd<true>(p, a->D, U, a->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;

@@ -309,6 +309,36 @@ def test_append(bsa, tokens, Hq, Hkv, D, page, rd, il, norm, strided):
     np.testing.assert_array_equal(gk, K)  # nothing else was touched
 
 
+@pytest.mark.parametrize("tokens,Hq,Hkv,D,page", [(7001, 10, 3, 64, 64), (5003, 1, 1, 128, 128), (2309, 33, 2, 128, 64)])
+def test_append_of_many_tokens_is_that_of_few(bsa, tokens, Hq, Hkv, D, page):
+    """Items in a row and token blocks that end inside a CTA, padding and bad places among
+    them: the same rows bit for bit as from calls of a few tokens each."""
+    g = torch.Generator().manual_seed(tokens)
+    S, maxp = 40, -(-tokens // (40 * page)) + 2
+    table = torch.randperm(S * maxp, generator=g).reshape(S, maxp).int()
+    table[3, 1], table[5, 0] = -1, S * maxp
+    place = torch.randperm(S * maxp * page, generator=g)[:tokens]
+    seq, slot = (place // (maxp * page)).int(), (place % (maxp * page)).int()
+    seq[torch.rand(tokens, generator=g) < 0.1] = -1
+    seq[7], slot[11] = S, maxp * page
+    w = (1 + 0.3 * torch.randn(D, generator=g)).cuda()
+    x = torch.randn(tokens, Hq + 2 * Hkv, D, generator=g).bfloat16().cuda()
+    table, seq, slot = table.cuda(), seq.cuda(), slot.cuda()
+    f = bsa.rope_inv_freq(D)
+    got = []
+    for step in (tokens, 7):
+        kc, vc = (torch.zeros(S * maxp, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        q = torch.zeros(tokens, Hq, D, dtype=torch.bfloat16, device="cuda")
+        for i in range(0, tokens, step):
+            y = x[i:i + step]
+            bsa.cache_append(y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], kc, vc, table, seq[i:i + step],
+                             slot[i:i + step], f, q_weight=w, out=q[i:i + step])
+        assert bsa.device_error() == 32
+        got.append((q, kc, vc))
+    for s, t in zip(*got):
+        assert torch.equal(s, t) and int((s != 0).sum()) > s.numel() // (8 if s is got[0][0] else 40)
+
+
 def test_append_bad_places_are_reported_and_skipped(bsa):
     kc = torch.zeros(4, 2, 64, 64, device="cuda", dtype=torch.bfloat16)
     vc = torch.zeros_like(kc)
