@@ -780,10 +780,10 @@ bool strides_ok(const int64_t* st) {
     return true;
 }
 
-// Heads of a lane group's task.  Four share one computation of the angles and
-// read four rows at once; single heads spread a small call over more CTAs.
-// Four from half an item per SM on (2,048 tokens of 48 heads, then the
-// acceptance: 18.9 us, 23.8 with single heads; 512 tokens: 8.2 and 9.7).
+// Heads of a lane group's task: `rows` share one computation of the angles and
+// are read at once; single heads spread a small call over more CTAs.  Several
+// from half an item per SM on (with four, 2,048 tokens of 48 heads appended, then
+// accepted: 18.9 us, 23.8 with single heads; 512 tokens: 8.2 and 9.7).
 int pick_heads(int64_t tokens, int D, int Hq, int Hkv, int rows, int sm_count) {
     const int TB = kRopeThreads / (D / 16);
     const int64_t items = (tokens + TB - 1) / TB * ((Hq + rows - 1) / rows + 2 * ((Hkv + rows - 1) / rows));
