@@ -264,7 +264,7 @@ cudaError_t raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t
 }
 
 int check_page_cache(const bsa_page_cache* c) {
-    if (!c || c->layers <= 0 || c->n_pages <= 0 || c->Hkv <= 0 || c->page <= 0 || c->D <= 0 || c->n_seqs <= 0 ||
+    if (!c || c->layers <= 0 || c->n_pages <= 0 || c->Hkv <= 0 || c->page <= 0 || c->D <= 0 || c->n_seqs < 0 ||
         c->max_pages <= 0)
         return BSA_ERR_INVALID_ARG;
     if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4))

@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const PageReq p,
 int fill_req(const bsa_page_cache* c, PageReq* p) {
     int st = check_page_cache(c);
     if (st != BSA_OK) return st;
-    if (!c->page_table) return BSA_ERR_INVALID_ARG;
+    if (!c->page_table && c->n_seqs > 0) return BSA_ERR_INVALID_ARG;
     *p = PageReq{};
     p->table = c->page_table;
     p->n_seqs = c->n_seqs;
@@ -586,6 +586,7 @@ int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n
     if (st != BSA_OK) return st;
     if (n < 0) return BSA_ERR_INVALID_ARG;
     if (n == 0) return BSA_OK;
+    if (c->n_seqs == 0) return BSA_ERR_INVALID_ARG;
     if (!page_ref || !a || !b || !len || !granted) return BSA_ERR_INVALID_ARG;
     for (const void* x : {(const void*)page_ref, (const void*)a, (const void*)b, (const void*)len, (const void*)granted})
         if (!al(x, 4)) return BSA_ERR_INVALID_ARG;
@@ -649,6 +650,7 @@ int bsa_cache_compact(const bsa_page_cache* c, int32_t* page_ref, int32_t* new_p
     int sms;
     int st = bsa::fill_req(c, &p);
     if (st != BSA_OK) return st;
+    if (c->n_seqs == 0) return BSA_ERR_INVALID_ARG;  // the table is what says where the pages go
     if (!page_ref || !new_page || !bsa::al(page_ref, 4) || !bsa::al(new_page, 4)) return BSA_ERR_INVALID_ARG;
     if (!workspace || !bsa::al(workspace, 256)) return BSA_ERR_INVALID_ARG;
     if (workspace_bytes < bsa_cache_pages_workspace(0, c->n_seqs, c->n_pages)) return BSA_ERR_CAPACITY;
@@ -673,11 +675,13 @@ int bsa_cache_accept(const bsa_page_cache* c, const int32_t* context_len, const 
     int sms;
     int st = bsa::fill_req(c, &p);
     if (st != BSA_OK) return st;
-    if (T < 1 || T > BSA_MAX_DRAFT || !context_len || !accepted || !n_accepted || !new_len || new_len == context_len)
+    if (T < 1 || T > BSA_MAX_DRAFT) return BSA_ERR_INVALID_ARG;
+    if (2ll * c->layers > 65535) return BSA_ERR_UNSUPPORTED;
+    if (c->n_seqs == 0) return BSA_OK;
+    if (!context_len || !accepted || !n_accepted || !new_len || new_len == context_len)
         return BSA_ERR_INVALID_ARG;
     for (const void* x : {(const void*)context_len, (const void*)accepted, (const void*)n_accepted, (const void*)new_len})
         if (!bsa::al(x, 4)) return BSA_ERR_INVALID_ARG;
-    if (2ll * c->layers > 65535) return BSA_ERR_UNSUPPORTED;
     if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
     const dim3 grid((unsigned)c->n_seqs, (unsigned)(2 * c->layers));
     const cudaError_t e =

@@ -39,7 +39,8 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned threads, size_t
 // (`done`: one bit per device, a static of the caller).
 cudaError_t raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>* done);
 // Sizes, alignment and the 2^31 row limit of a paged cache's pools (the page
-// table is checked by the calls that read one).
+// table is checked by the calls that read one; no sequences pass: what that
+// means is theirs too).
 int check_page_cache(const bsa_page_cache* c);
 // 2-D bf16 view [rows, D] in boxes of 64 columns x box_rows rows, 128-byte swizzle.
 int encode_rows_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows);

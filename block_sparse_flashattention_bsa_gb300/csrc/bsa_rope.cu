@@ -905,6 +905,7 @@ int bsa_cache_append(const bsa_norm_rope_args* a, const bsa_page_cache* c, const
     if (a->B != 1 || a->kv_repeat != 1 || c->layers != 1 || c->Hkv != a->Hkv || c->D != a->D)
         return BSA_ERR_INVALID_ARG;
     if (p.tokens == 0) return BSA_OK;
+    if (c->n_seqs == 0) return BSA_ERR_INVALID_ARG;  // tokens of no sequence
     if (!a->q || !a->k || !a->v || !q_out || !seq_ids || !slots || !c->page_table) return BSA_ERR_INVALID_ARG;
     if (!bsa::al(q_out, 16) || !bsa::al(seq_ids, 4) || !bsa::al(slots, 4)) return BSA_ERR_INVALID_ARG;
     int sms;

@@ -1075,15 +1075,16 @@ int bsa_tree_attention(const bsa_tree_args* a, const bsa_page_cache* c, void* wo
     if (!a) return BSA_ERR_INVALID_ARG;
     int st = bsa::check_page_cache(c);
     if (st != BSA_OK) return st;
-    if (a->B <= 0 || a->T <= 0 || a->Hq <= 0 || a->Hq % c->Hkv || c->layers != 1 || c->n_seqs != a->B)
+    if (a->B < 0 || a->T <= 0 || a->Hq <= 0 || a->Hq % c->Hkv || c->layers != 1 || c->n_seqs != a->B)
         return BSA_ERR_INVALID_ARG;
-    if (!a->q || !a->context_len || !a->out || !a->lse || !c->page_table) return BSA_ERR_INVALID_ARG;
+    if (a->B > 0 && (!a->q || !a->context_len || !a->out || !a->lse || !c->page_table)) return BSA_ERR_INVALID_ARG;
     if (!bsa::al(a->q, 16) || !bsa::al(a->out, 16) || !bsa::al(a->lse, 4) || !bsa::al(a->context_len, 4) ||
         !bsa::al(a->draft_len, 4) || !bsa::al(a->tree_mask, 8) || !bsa::al(a->row_ptr, 4) || !bsa::al(a->col_idx, 4))
         return BSA_ERR_INVALID_ARG;
     if ((a->row_ptr != nullptr) != (a->col_idx != nullptr) || a->col_capacity < 0) return BSA_ERR_INVALID_ARG;
     if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return BSA_ERR_INVALID_ARG;
     if (a->T > BSA_MAX_DRAFT || a->Hq / c->Hkv > 128) return BSA_ERR_UNSUPPORTED;
+    if (a->B == 0) return BSA_OK;
     if (!workspace || !bsa::al(workspace, 256)) return BSA_ERR_INVALID_ARG;
     if (workspace_bytes < bsa_tree_attention_workspace(a->B, a->T, a->Hq, c->Hkv, c->D)) return BSA_ERR_CAPACITY;
     bsa::TreeParams p{};

@@ -647,6 +647,9 @@ int bsa_qk_norm_rope_backward(const bsa_norm_rope_args *a, const bsa_norm_rope_g
  * work on one layer (layers = 1: pass the layer's part of a larger pool).
  * Table entries, slots and ids are checked on the device: one out of range is
  * skipped and reported by bsa_device_error (bit 32), never dereferenced.
+ * n_seqs may be 0 (and page_table NULL) where that leaves nothing to do: no
+ * tokens, B = 0, no requests, acceptance over no sequences.  Such a call returns
+ * BSA_OK once its sizes are checked.
  */
 typedef struct {
     void *k, *v;             /* device bf16 [layers, n_pages, Hkv, page, D], 16-byte aligned */
@@ -693,7 +696,7 @@ int bsa_cache_append(const bsa_norm_rope_args *a, const bsa_page_cache *c, const
  *                -inf and O = 0 for a row that sees nothing)
  * Slots behind the drafts, unlisted pages and pages of other sequences may
  * hold anything, NaN included.  K and V of a sequence's own slots must be finite.
- * Limits: 1 <= T <= BSA_MAX_DRAFT, Hq a multiple of Hkv, Hq / Hkv <= 128.
+ * Limits: B >= 0 (0: nothing to do), 1 <= T <= BSA_MAX_DRAFT, Hq a multiple of Hkv, Hq / Hkv <= 128.
  *   workspace    device, bsa_tree_attention_workspace(...) bytes, 256-byte aligned:
  *                partial results of rows split over several SMs.  Calls that
  *                overlap on the GPU need workspaces of their own.
