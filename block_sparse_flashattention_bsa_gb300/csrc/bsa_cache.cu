@@ -578,6 +578,12 @@ int fill_req(const bsa_page_cache* c, PageReq* p) {
 
 bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two int32 vectors share a byte.
+bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + 4 * (uint64_t)nb && y < x + 4 * (uint64_t)na;
+}
+
 int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n, const int32_t* a, const int32_t* b,
                 const int32_t* len, int32_t* granted, void* ws, int64_t ws_bytes, cudaStream_t s) {
     PageReq p;
@@ -592,6 +598,11 @@ int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n
         if (!al(x, 4)) return BSA_ERR_INVALID_ARG;
     if (!ws || !al(ws, 256)) return BSA_ERR_INVALID_ARG;
     if (ws_bytes < bsa_cache_pages_workspace(n, c->n_seqs, c->n_pages)) return BSA_ERR_CAPACITY;
+    // the requests are read again once they are answered
+    for (const int32_t* x : {a, b, len})
+        if (meet(granted, n, x, n)) return BSA_ERR_INVALID_ARG;
+    if (meet(granted, n, page_ref, c->n_pages) || meet(granted, n, c->page_table, (int64_t)c->n_seqs * c->max_pages))
+        return BSA_ERR_INVALID_ARG;
     if ((st = device_context(&p.err, &sms)) != BSA_OK) return st;
     p.ref = page_ref;
     p.n = n;
@@ -654,6 +665,9 @@ int bsa_cache_compact(const bsa_page_cache* c, int32_t* page_ref, int32_t* new_p
     if (!page_ref || !new_page || !bsa::al(page_ref, 4) || !bsa::al(new_page, 4)) return BSA_ERR_INVALID_ARG;
     if (!workspace || !bsa::al(workspace, 256)) return BSA_ERR_INVALID_ARG;
     if (workspace_bytes < bsa_cache_pages_workspace(0, c->n_seqs, c->n_pages)) return BSA_ERR_CAPACITY;
+    if (bsa::meet(new_page, c->n_pages, page_ref, c->n_pages) ||
+        bsa::meet(new_page, c->n_pages, c->page_table, (int64_t)c->n_seqs * c->max_pages))
+        return BSA_ERR_INVALID_ARG;
     if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
     p.ref = page_ref;
     p.w = bsa::split_ws(workspace, 0, c->n_seqs, c->n_pages);
@@ -678,10 +692,14 @@ int bsa_cache_accept(const bsa_page_cache* c, const int32_t* context_len, const 
     if (T < 1 || T > BSA_MAX_DRAFT) return BSA_ERR_INVALID_ARG;
     if (2ll * c->layers > 65535) return BSA_ERR_UNSUPPORTED;
     if (c->n_seqs == 0) return BSA_OK;
-    if (!context_len || !accepted || !n_accepted || !new_len || new_len == context_len)
-        return BSA_ERR_INVALID_ARG;
+    if (!context_len || !accepted || !n_accepted || !new_len) return BSA_ERR_INVALID_ARG;
     for (const void* x : {(const void*)context_len, (const void*)accepted, (const void*)n_accepted, (const void*)new_len})
         if (!bsa::al(x, 4)) return BSA_ERR_INVALID_ARG;
+    // every CTA of a sequence reads these, one of them writes the new length
+    const int64_t S = c->n_seqs;
+    if (bsa::meet(new_len, S, context_len, S) || bsa::meet(new_len, S, n_accepted, S) ||
+        bsa::meet(new_len, S, accepted, S * T) || bsa::meet(new_len, S, c->page_table, S * c->max_pages))
+        return BSA_ERR_INVALID_ARG;
     if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
     const dim3 grid((unsigned)c->n_seqs, (unsigned)(2 * c->layers));
     const cudaError_t e =

@@ -57,7 +57,8 @@ def cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
                  stream=None) -> torch.Tensor:
     """Moves the rows of the accepted drafts (accepted int32 [n_seqs,T], the
     first n_accepted[b] strictly increasing) up behind the committed slots, in
-    every layer of the pools; returns the new lengths context_len + n_accepted."""
+    every layer of the pools; returns the new lengths context_len + n_accepted
+    (in new_len, if given: a tensor that overlaps none of the others)."""
     return _call(compiled().cache_accept, "bsa_cache_accept", stream, k_cache, v_cache, page_table, context_len,
                  accepted, n_accepted, new_len)
 

@@ -577,6 +577,7 @@ int bsa_convert_f32_bf16(const float *x, void *y, int64_t n, bsa_stream_t stream
  *   gain * (y_a cos - y_b sin, y_b cos + y_a sin); the rest stays as it is.
  * Values are only moved.  Arithmetic in fp32, one rounding to bf16 at the end;
  * angles are exact to 2^-20 for every int32 position (see csrc/bsa_rope.cu).
+ * Outputs must not overlap inputs.
  * Like the other calls, the first one on a device allocates its error word:
  * make it before a stream capture.
  */
@@ -650,6 +651,8 @@ int bsa_qk_norm_rope_backward(const bsa_norm_rope_args *a, const bsa_norm_rope_g
  * n_seqs may be 0 (and page_table NULL) where that leaves nothing to do: no
  * tokens, B = 0, no requests, acceptance over no sequences.  Such a call returns
  * BSA_OK once its sizes are checked.
+ * Outputs and workspaces must not overlap inputs or one another; the int32
+ * outputs (granted, new_page, new_len) are refused where they do.
  */
 typedef struct {
     void *k, *v;             /* device bf16 [layers, n_pages, Hkv, page, D], 16-byte aligned */
@@ -725,7 +728,7 @@ int bsa_tree_attention(const bsa_tree_args *a, const bsa_page_cache *c, void *wo
  *               increasing and in [0, T); a sequence whose list is not, or that
  *               lacks a page for it, is reported (bit 32), keeps its rows and gets
  *               new_len[b] = context_len[b]
- *   n_accepted  device [n_seqs], 0 .. T;  new_len  device [n_seqs] (not context_len itself)
+ *   n_accepted  device [n_seqs], 0 .. T;  new_len  device [n_seqs]
  *   T           1 .. BSA_MAX_DRAFT
  */
 int bsa_cache_accept(const bsa_page_cache *c, const int32_t *context_len, const int32_t *accepted,

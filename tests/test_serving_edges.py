@@ -48,3 +48,38 @@ def test_no_sequences_with_something_to_do(L):
     for kw in (dict(n_seqs=-1), dict(k=None), dict(layers=0), dict(max_pages=0)):
         assert L.bsa_cache_accept(ctypes.byref(empty(**kw)), None, None, None, 4, None, None) == INVALID
     assert L.bsa_cache_accept(ctypes.byref(empty(page=96)), None, None, None, 4, None, None) == UNSUP
+
+
+# ------------------------------------------------------------ outputs over inputs
+def test_accept_refuses_lengths_written_over_what_it_reads(L):
+    """Several CTAs read a sequence's entries; one of them writes its new length."""
+    c, A, M, N, S = 3 * 4, 1 << 21, 1 << 22, 1 << 23, 1 << 24   # bytes of a vector; addresses
+
+    def accept(new):
+        return L.bsa_cache_accept(ctypes.byref(cache(page_table=S)), N, A, M, 4, new, None)
+
+    for base, size in ((N, c), (M, c), (A, 4 * c), (S, 4 * c)):   # lengths, counts, lists, the table
+        for at in (base, base + size - 4, base - c + 4):
+            assert accept(at) == INVALID, hex(at)
+
+
+@pytest.mark.parametrize("call", ["bsa_cache_resize", "bsa_cache_fork"])
+def test_requests_refuse_answers_written_over_what_they_read(L, call):
+    """The last kernel of a request reads the vectors again, after the answers."""
+    A, B, C, R, S = (1 << k for k in range(21, 26))
+    n = L.bsa_cache_pages_workspace(5, 3, 16)
+
+    def request(granted):
+        return getattr(L, call)(ctypes.byref(cache(page_table=S)), R, 5, A, B, C, granted, FAKE, n, None)
+
+    for base, size in ((A, 20), (B, 20), (C, 20), (R, 64), (S, 48)):
+        for at in (base, base + size - 4, base - 16):
+            assert request(at) == INVALID, hex(at)
+
+
+def test_compact_refuses_a_map_written_over_what_it_reads(L):
+    R, S = 1 << 21, 1 << 22
+    n = L.bsa_cache_pages_workspace(0, 3, 16)
+    for base, size in ((R, 64), (S, 48)):
+        for at in (base, base + size - 4, base - 60):
+            assert L.bsa_cache_compact(ctypes.byref(cache(page_table=S)), R, at, FAKE, n, None) == INVALID, hex(at)
