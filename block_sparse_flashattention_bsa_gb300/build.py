@@ -41,9 +41,10 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _newest_input() -> float:
-    paths = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BINDING_SOURCE]] + [os.path.join(INCLUDE, "bsa.h")]
-    return max(os.path.getmtime(p) for p in paths)
+def _fresh(target: str, sources) -> bool:
+    """Whether target is there and no older than its sources."""
+    paths = [os.path.join(CSRC, s) for s in sources] + [os.path.join(INCLUDE, "bsa.h")]
+    return os.path.exists(target) and os.path.getmtime(target) >= max(os.path.getmtime(p) for p in paths)
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -62,7 +63,7 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 def _compile_binding() -> str:
     import sysconfig
 
-    import torch
+    torch = _torch()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     troot = os.path.dirname(torch.__file__)
     obj = os.path.join(BUILD, "bsa_torch.o")
@@ -84,21 +85,37 @@ def _link(cmd, out: str) -> None:
     os.replace(tmp, out)
 
 
+def _torch():
+    try:
+        import torch
+        return torch
+    except ImportError:
+        return None
+
+
+def _link_binding(obj: str) -> None:
+    tlib = os.path.join(os.path.dirname(_torch().__file__), "lib")
+    _link([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING, obj, "-L" + tlib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN",
+           "-Wl,-rpath," + tlib], BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    newest = _newest_input()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
+    """Builds what is missing or older than its sources.  libbsa.so needs nvcc
+    alone and is linked whether or not _bsa_torch.so can be; without torch,
+    which _bsa_torch.so is for, only libbsa.so is built."""
+    lib = force or not _fresh(LIB, SOURCES + HEADERS)
+    binding = _torch() is not None and (force or not _fresh(BINDING, [BINDING_SOURCE]))
+    if not lib and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
-        bobj = binding.result()
-    _link([nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-lrt", "-lpthread", "-ldl"], LIB)
-    import torch
-    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    _link([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING, bobj, "-L" + tlib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN",
-           "-Wl,-rpath," + tlib], BINDING)
+        bobj = ex.submit(_compile_binding) if binding else None
+        if lib:
+            objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+            _link([nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-lrt", "-lpthread", "-ldl"], LIB)
+        if binding:
+            _link_binding(bobj.result())
     return LIB
 
 
