@@ -24,6 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsa.so")
 BINDING = os.path.join(PKG, "_bsa_torch.so")
 BINDING_SOURCE = "bsa_torch.cpp"
+BINDING_RECORD = "bsa_torch.made_for"  # in BUILD: the torch and the Python that the binding was compiled for
 
 SOURCES = ["bsa_api.cu", "bsa_fwd.cu", "bsa_mask.cu", "bsa_topk.cu", "bsa_noalloc.cu", "bsa_pair.cu", "bsa_bwd.cu", "bsa_fp8.cu", "bsa_shard.cu",
            "bsa_rope.cu", "bsa_cache.cu", "bsa_tree.cu"]
@@ -93,19 +94,35 @@ def _torch():
         return None
 
 
+def _made_for() -> str:
+    torch = _torch()
+    return "%s\n%s\n%s\n" % (torch.__version__, os.path.dirname(torch.__file__), sys.version)
+
+
+def _binding_fresh() -> bool:
+    try:
+        with open(os.path.join(BUILD, BINDING_RECORD)) as f:
+            return f.read() == _made_for() and _fresh(BINDING, [BINDING_SOURCE])
+    except OSError:
+        return False
+
+
 def _link_binding(obj: str) -> None:
     tlib = os.path.join(os.path.dirname(_torch().__file__), "lib")
     _link([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING, obj, "-L" + tlib, "-ltorch_python", "-ltorch",
            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN",
            "-Wl,-rpath," + tlib], BINDING)
+    with open(os.path.join(BUILD, BINDING_RECORD), "w") as f:
+        f.write(_made_for())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Builds what is missing or older than its sources.  libbsa.so needs nvcc
+    """Builds what is missing or older than its sources (the binding also where
+    torch or Python is not what it was compiled for).  libbsa.so needs nvcc
     alone and is linked whether or not _bsa_torch.so can be; without torch,
     which _bsa_torch.so is for, only libbsa.so is built."""
     lib = force or not _fresh(LIB, SOURCES + HEADERS)
-    binding = _torch() is not None and (force or not _fresh(BINDING, [BINDING_SOURCE]))
+    binding = _torch() is not None and (force or not _binding_fresh())
     if not lib and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -63,3 +63,31 @@ def test_the_library_does_not_need_torch(B, monkeypatch):
     monkeypatch.setitem(B.sys.modules, "torch", None)  # import torch raises ImportError
     assert B.build() == B.LIB
     assert os.path.exists(B.LIB) and not os.path.exists(B.BINDING) and "bsa_torch.cpp" not in B.made
+
+
+@pytest.mark.parametrize("change", ["torch", "python", "no record"])
+def test_the_binding_follows_torch_and_python(B, monkeypatch, change):
+    """The binding is compiled against one torch and one Python: with another of
+    either it is built again, and the library is not."""
+    import torch
+    B.build()
+    B.made.clear()
+    if change == "torch":
+        monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    elif change == "python":
+        monkeypatch.setattr(B.sys, "version", "3.99.0 " + B.sys.version)
+    else:
+        os.remove(os.path.join(B.BUILD, B.BINDING_RECORD))
+    assert B.build() == B.LIB and B.made == ["bsa_torch.cpp", "_bsa_torch.so"]
+    B.made.clear()
+    assert B.build() == B.LIB and B.made == []
+
+
+def test_a_binding_that_failed_is_not_taken_for_the_new_one(B, monkeypatch):
+    import torch
+    B.build()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    monkeypatch.setattr(B, "binding_rc", 1)
+    for _ in range(2):
+        with pytest.raises(RuntimeError, match="bsa_torch.cpp"):
+            B.build()
