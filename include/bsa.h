@@ -669,7 +669,9 @@ typedef struct {
  *   seq_ids   device [tokens]: row of the page table; < 0: padding (nothing is written)
  *   slots     device [tokens]: the sequence's slot to write
  *   q_out     device bf16 [tokens, Hq, D]
- * Two tokens with the same sequence and slot: either one's rows stay.  A page
+ * Two tokens with the same sequence and slot leave pieces of either there (each
+ * 16 bytes of each head are from one of them, K and V apart); no other slot is
+ * affected, but the row is none to attend to.  A page
  * that several sequences share is written for all of them: bsa_cache_resize
  * first gives each the pages from its length on for its own.
  */

@@ -45,3 +45,33 @@ def test_an_empty_batch_passes_through_a_serving_step(bsa, lists):
     with pytest.raises(bsa.BsaError):  # a token of no sequence
         y = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
         bsa.cache_append(y, y, y, kc, vc, table, i32(0), i32(0), f)
+
+
+@pytest.mark.parametrize("page,D", [(64, 128), (128, 64)])
+def test_two_tokens_of_one_slot_leave_pieces_of_either(bsa, page, D):
+    """No order among them, but nothing of a third row and no other slot touched."""
+    n, H = 300, 3
+    g = torch.Generator(device="cuda").manual_seed(page)
+    x = torch.randn(n, 4 + 2 * H, D, generator=g, device="cuda").bfloat16()
+    seq = torch.arange(n, device="cuda", dtype=torch.int32) % 3
+    slot = torch.arange(n, device="cuda", dtype=torch.int32) // 3
+    table = torch.arange(3 * 4, device="cuda", dtype=torch.int32).view(3, 4)
+    f, w = bsa.rope_inv_freq(D), torch.rand(D, generator=g, device="cuda")
+
+    def append(rows, seq, slot, pools):
+        y = x[rows]
+        bsa.cache_append(y[:, :4], y[:, 4:4 + H], y[:, 4 + H:], *pools, table, seq[rows], slot[rows], f,
+                         positions=torch.arange(n, device="cuda", dtype=torch.int32)[rows], q_weight=w, k_weight=w)
+        return pools
+
+    pools = lambda: [torch.zeros(12, H, page, D, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    one, other = [r for r in range(n) if r != 250], [r for r in range(n) if r != 10]
+    seq[250], slot[250] = seq[10], slot[10]
+    both = append(list(range(n)), seq, slot, pools())
+    for got, a, b in zip(both, append(one, seq, slot, pools()), append(other, seq, slot, pools())):
+        pieces = [t.view(12, H, page, D // 8, 8) for t in (got, a, b)]
+        from_a, from_b = (pieces[0] == pieces[1]).all(-1), (pieces[0] == pieces[2]).all(-1)
+        assert (from_a | from_b).all()
+        apart = ~(pieces[1] == pieces[2]).all(-1)
+        assert int(apart.sum()) == H * D // 8  # the two tokens' slot, nothing else
+    assert bsa.device_error() == 0
