@@ -29,8 +29,8 @@ def cache_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: tor
     k, v [tokens,Hkv,D], any strides) belongs to slot slots[i] of sequence
     seq_ids[i] (< 0: padding, skipped), and its rotated key and its value go to
     that slot's page; two tokens of one slot leave pieces of either there.
-    positions default to the slots (a tree's drafts give
-    their depth).  Returns the rotated queries [tokens,Hq,D]."""
+    positions default to the slots (a tree's drafts give their depth).  Returns
+    the rotated queries [tokens,Hq,D]."""
     return _call(compiled().cache_append, "bsa_cache_append", stream, q, k, v, inv_freq, positions, q_weight, k_weight,
                  eps, gain, interleaved, 1, k_cache, v_cache, page_table, seq_ids, slots, out)
 

@@ -693,9 +693,10 @@ int bsa_cache_append(const bsa_norm_rope_args *a, const bsa_page_cache *c, const
  *   tree_mask    device uint64 [B, T]; NULL: a chain (u <= t).  Bits from draft_len[b] on
  *                are ignored.
  *   row_ptr, col_idx   optional device CSR with rows r = b * Hkv + h: the logical
- *                pages (slot / page) that row reads, distinct, in any order; entries
- *                outside [0, max_pages) are skipped and flagged (bit 2), a decreasing
- *                row_ptr counts as an empty row (bit 4).  Both NULL: every page.
+ *                pages (slot / page) that row reads, distinct, in any order, at most
+ *                max_pages of them; entries outside [0, max_pages) are skipped and flagged
+ *                (bit 2), a longer row or a decreasing row_ptr counts as an empty row
+ *                (bit 4).  Both NULL: every page.
  *                col_capacity: entries col_idx holds; rows are read only below it.
  *   out          device bf16 [B, T, Hq, D];  lse  device fp32 [B, T, Hq] (natural log;
  *                -inf and O = 0 for a row that sees nothing)

@@ -75,3 +75,29 @@ def test_two_tokens_of_one_slot_leave_pieces_of_either(bsa, page, D):
         apart = ~(pieces[1] == pieces[2]).all(-1)
         assert int(apart.sum()) == H * D // 8  # the two tokens' slot, nothing else
     assert bsa.device_error() == 0
+
+
+@pytest.mark.parametrize("page", [64, 128])
+def test_listed_rows_hold_at_most_max_pages_entries(bsa, page):
+    """Lists of a fixed width: up to max_pages entries those outside the table are
+    skipped and reported; a longer row is malformed and counts as empty."""
+    from test_gpu_tree import Case
+    c = Case(2, 2, 4, 2, 64, page, [5 * page - 9, 3 * page], lists=lambda b, h, held, g: list(range(held)), seed=page)
+    P = c.table.shape[1]
+    held = [int((c.table[b] >= 0).sum()) for b in range(2)]
+    rows = [list(range(held[r // 2])) for r in range(4)]
+
+    def lists(rows):
+        c.rp = torch.tensor([0] + [len(x) for x in rows]).cumsum(0).int()
+        c.ci = torch.tensor([j for x in rows for j in x], dtype=torch.int32)
+
+    pad = lambda x, n: x + [-1] * (n - len(x))
+    lists([pad(x, P) for x in rows])
+    c.check(*c.run(bsa))
+    assert bsa.device_error() == 2
+    lists([pad(rows[0], P), pad(rows[1], P + 1), rows[2], pad(rows[3], P + 5)])
+    o, lse = c.run(bsa)
+    assert bsa.device_error() == 2 | 4
+    lists([pad(rows[0], P), [], rows[2], []])
+    c.check(o, lse)
+    assert (o[0, :, 2:] == 0).all() and torch.isneginf(lse[0, :, 2:]).all()
