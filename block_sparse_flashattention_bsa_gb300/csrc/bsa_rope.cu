@@ -199,8 +199,8 @@ __device__ __forceinline__ void norm_rotate(uint4& a, uint4& b, bool norm, const
 }
 
 // One CTA item: TB = 256 / LPR consecutive tokens times U heads.  A lane
-// group takes one token and loads its U rows at once (64 bytes a lane and
-// row in flight), so the angles are computed once for U rows; neighbouring
+// group takes one token and loads its U rows at once (32 bytes a lane and
+// row), so the angles are computed once for U rows; neighbouring
 // lane groups take neighbouring tokens, so the head-major stores of a head
 // run over TB consecutive rows.
 template <int D, int U, bool IL>
@@ -416,15 +416,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_append_kernel(const
     }
 }
 
-// The gradients.  A CTA works on `hs` heads (a divisor of H, at most 8) of
+// The gradients.  A CTA works on `hs` heads (two where H is even, else one) of
 // `toks` consecutive tokens at a time, one row per lane group, so that both
 // sides are touched in runs: hs * D values of a token, toks * D of a head.  A
 // task is a block of tokens times `runs` such head groups, one after the
 // other, so a token's angles are computed once for them.  What a lane reads
-// of a row -- two chunks of x and two of each copy's dz, two rows at a time --
-// goes through a ring of its own in shared memory (cp.async, kBwdStages rows
-// ahead, across task boundaries): registers hold one row only, and the loads
-// of three rows are always in flight behind the arithmetic.  No lane reads
+// of a row -- two chunks of dz and two of x, or two of another copy's dz -- goes
+// through a ring of its own in shared memory (cp.async, across task
+// boundaries): registers hold one row only, and the loads of the next two are
+// in flight behind the arithmetic.  No lane reads
 // another's slots, so the ring needs no barrier.
 // The weight's gradient is summed per lane over all of the CTA's rows, then
 // over the CTA's lanes, into one row of `partial` per CTA, which
@@ -702,7 +702,7 @@ void deal_ctas(RopeParams* p, int D, int U, int ctas, const double* bytes) {
     }
 }
 
-constexpr int kRopeMaxCtas = 1024;  // bound on a kind's CTAs (two per SM), for the workspace
+constexpr int kRopeMaxCtas = 1024;  // the gradients' CTAs are held to this: rows of the workspace a kind has
 
 template <bool APPEND>
 cudaError_t launch_fwd(const RopeParams& p, int D, int U, bool il, cudaStream_t s) {
@@ -730,16 +730,15 @@ void deal_tasks(RopeParams* p, int D, int sm_count, const double* bytes) {
     const double all = bytes[0] + bytes[1] + bytes[2];
     // Four CTAs per SM even out kinds of unequal cost, two save the start of
     // the second pair: four from 400 KB each on (537 MB: 86.1 us with four,
-    // 89.1 with two; 121 MB: 30.9 and 27.9; 134 MB: 30.0 and 28.3).
+    // 89.1 with two; 121 MB: 30.9 and 27.9; 134 MB: 30.0 and 28.3; nothing was
+    // measured between 134 and 537 MB, where the turn is).
     const double moved = all * p->tokens * D * 2;
     const int waves = moved >= 4.0 * sm_count * 400e3 ? 4 : kBwdResident;
     const int ctas = std::min(waves * sm_count, kRopeMaxCtas);
     for (int k = 0; k < 3; ++k) {
         RopeSide& sd = p->side[k];
         if (sd.H == 0) continue;
-        sd.hs = 1;
-        for (int d = 2; d <= 2; ++d)
-            if (sd.H % d == 0) sd.hs = d;
+        sd.hs = sd.H % 2 == 0 ? 2 : 1;  // 8 side by side: 98 us for the 537 MB above
         sd.toks = groups / sd.hs;
         const int64_t blocks = (p->tokens + sd.toks - 1) / sd.toks;
         const int64_t share = std::max<int64_t>(1, (int64_t)std::lround(ctas * bytes[k] / all));
@@ -792,7 +791,8 @@ int pick_heads(int64_t tokens, int D, int Hq, int Hkv, int rows, int sm_count) {
 
 // Appending: CTAs per SM.  Four start fewer times, six even out what the
 // kinds' items cost (2,048 tokens of 32 + 8 heads, 2.5 items a CTA of four: 12.9
-// us, with six 13.7; 32K of 32 + 32, 80 items: 300 and 255).
+// us, with six 13.7; 32K of 32 + 32, 80 items: 300 and 255; the turn lies
+// somewhere between).
 int append_waves(int64_t tokens, int D, int Hq, int Hkv, int U, int sm_count) {
     const int TB = kRopeThreads / (D / 16);
     const int64_t items = (tokens + TB - 1) / TB * ((Hq + U - 1) / U + 2 * ((Hkv + U - 1) / U));

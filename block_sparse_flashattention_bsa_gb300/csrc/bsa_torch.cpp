@@ -2,10 +2,11 @@
 // calls (rope.py, paged.py): checks torch tensors, takes outputs and
 // workspaces from torch's allocator, fills the C ABI's structs and calls
 // libbsa.so on the tensors' device and its current stream.  The same steps in
-// Python took longer than the kernels of a small call: appending one token 27
-// us (11 now, of which the views of its inputs are 5), one decoding step 17 (9,
-// the GPU's own time), gradients of 8K packed tokens 45 (30, the same).  No
-// arithmetic, no state.
+// Python took longer than the kernels of a small call.  Calls in a row on the
+// same tensors: appending one token 27 us (12 now, of which the views of a fused
+// projection are 4.5; with new inputs from call to call 17), one decoding step
+// 17 (9, the GPU's own time), gradients of 8K packed tokens 45 (29, the same).
+// No arithmetic, no state.
 //
 // Every function takes its arguments by position and returns its result, or
 // the bsa_status as an int where the library refused; what a check here
