@@ -108,7 +108,8 @@ def draw(rng: random.Random):
         cost = lambda: T * (min(ctx + T, window + sinks + 64) if window else ctx + T) * Hq * D
         while cost() > most:
             T, ctx = T // 2, ctx // 2
-        B = _log(rng, 1, max(1, min(48, most // cost(), 4 * 32768 * 8 * 128 // ((ctx + T) * Hkv * D))))
+        B = _log(rng, 1, max(1, min(48, most // cost(), 4 * 32768 * 8 * 128 // ((ctx + T) * Hkv * D),
+                               8192 * 16 * 8 * 128 // (T * Hq * D))))
     return dict(op=op, mix=mix, B=B, T=T, ctx=ctx, ragged=rng.random() < 0.6, Hq=Hq, Hkv=Hkv, D=D, page=page, q8=q8,
                 window=window, sinks=sinks)
 
