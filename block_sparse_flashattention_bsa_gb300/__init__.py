@@ -34,7 +34,12 @@ Entry points (same names as the C ABI, minus the ``bsa_`` prefix):
 * :func:`cache_append`, :func:`tree_attention`, :func:`cache_accept`  serving
   over a paged cache: write new tokens, attend with one or a tree of drafted
   tokens per sequence, keep the accepted ones
+* :func:`chunk_attention`  attention of chunks of new tokens (or one token a
+  sequence) over a paged cache, over all slots or a sliding window with sinks
 * :func:`cache_resize`, :func:`cache_fork`, :func:`cache_compact`  its pages
+* :func:`cache_read`  ranges of a cache back as what :func:`forward` takes; the
+  cache calls, `chunk_attention` and this one also take caches of 8-bit rows
+  (e4m3 codes, a power of two per row)
 """
 
 from ._binding import (  # noqa: F401
@@ -70,7 +75,9 @@ from .paged import (  # noqa: F401
     cache_append,
     cache_compact,
     cache_fork,
+    cache_read,
     cache_resize,
+    chunk_attention,
     tree_attention,
 )
 from .rope import (  # noqa: F401

@@ -86,6 +86,21 @@ class _TreeArgs(ctypes.Structure):
                  ("scale", ctypes.c_float)]
 
 
+class _PageScales(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class _ReadArgs(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_int32) for x in ("R", "n", "kv_repeat")]
+    _fields_ += [(x, ctypes.c_void_p) for x in ("seq_ids", "first", "len", "k", "v")]
+
+
+class _ChunkArgs(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_int32) for x in ("B", "tokens", "Hq")]
+    _fields_ += [(x, ctypes.c_void_p) for x in ("q", "q_ptr", "context_len", "out", "lse")]
+    _fields_ += [("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
 MAX_WINDOWS = 4
 
 
@@ -158,6 +173,14 @@ def lib():
                 "bsa_cache_resize": ([P, P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
                 "bsa_cache_fork": ([P, P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
                 "bsa_cache_compact": ([P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_append_fp8": ([P, P, P, P, P, P, P], ctypes.c_int),
+                "bsa_cache_accept_fp8": ([P, P, P, P, P, i32, P, P], ctypes.c_int),
+                "bsa_cache_resize_fp8": ([P, P, P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_fork_fp8": ([P, P, P, i32, P, P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_compact_fp8": ([P, P, P, P, P, i64, P], ctypes.c_int),
+                "bsa_cache_read": ([P, P, P, P], ctypes.c_int),
+                "bsa_chunk_attention_workspace": ([i32, i32, i32, i32, i32], i64),
+                "bsa_chunk_attention": ([P, P, P, P, i64, P], ctypes.c_int),
             }
             for name, (args, res) in sigs.items():
                 f = getattr(L, name)

@@ -27,8 +27,8 @@ BINDING_SOURCE = "bsa_torch.cpp"
 BINDING_RECORD = "bsa_torch.made_for"  # in BUILD: the torch and the Python that the binding was compiled for
 
 SOURCES = ["bsa_api.cu", "bsa_fwd.cu", "bsa_mask.cu", "bsa_topk.cu", "bsa_noalloc.cu", "bsa_pair.cu", "bsa_bwd.cu", "bsa_fp8.cu", "bsa_shard.cu",
-           "bsa_rope.cu", "bsa_cache.cu", "bsa_tree.cu"]
-HEADERS = ["bsa_ptx.cuh", "bsa_internal.h"]
+           "bsa_rope.cu", "bsa_cache.cu", "bsa_tree.cu", "bsa_read.cu", "bsa_chunk.cu", "bsa_decode.cu"]
+HEADERS = ["bsa_ptx.cuh", "bsa_internal.h", "bsa_q8.cuh", "bsa_chunk.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -276,8 +276,26 @@ int check_page_cache(const bsa_page_cache* c) {
     return BSA_OK;
 }
 
+int check_page_scales(const bsa_page_cache*, const bsa_page_scales* s) {
+    // 16 bytes: the scales of a page's rows are copied in bulk
+    return s->k && s->v && aligned(s->k, 16) && aligned(s->v, 16) ? BSA_OK : BSA_ERR_INVALID_ARG;
+}
+
 int encode_rows_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows) {
     return make_map(m, base, rows, D, box_rows);
+}
+
+int encode_rows_e4m3(CUtensorMap* m, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return BSA_ERR_CUDA;
+    cuuint64_t dims[2] = {D, rows};
+    cuuint64_t strides[1] = {D};
+    cuuint32_t box[2] = {(cuuint32_t)D, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BSA_OK : BSA_ERR_CUDA;
 }
 
 int encode_token_rows_bf16(CUtensorMap* m, const void* base, uint64_t tokens, uint64_t heads, uint64_t D,

@@ -67,6 +67,7 @@ struct PageReq {
     PageWs w;
     // copies
     uint4 *k, *v;
+    uint8_t *ks, *vs;            // 8-bit pools: a scale byte per row (else null)
     int32_t layers, Hkv, row16;  // row16: 16-byte chunks of a row
 };
 
@@ -323,12 +324,20 @@ __device__ __forceinline__ void copy_rows(const uint4* src, uint4* dst, int chun
     }
 }
 
-// Rows of (copy, layer, K or V, head) number `unit` of a list of page copies.
-__device__ __forceinline__ int64_t unit_offset(const PageReq& p, int64_t sub, int pg, bool* is_v) {
+// First row of (copy, layer, K or V, head) number `unit` of a list of page copies.
+__device__ __forceinline__ int64_t unit_row(const PageReq& p, int64_t sub, int pg, bool* is_v) {
     const int h = (int)(sub % p.Hkv);
     const int64_t lk = sub / p.Hkv;
     *is_v = lk & 1;
-    return (((lk >> 1) * p.n_pages + pg) * p.Hkv + h) * (int64_t)p.page * p.row16;
+    return (((lk >> 1) * p.n_pages + pg) * p.Hkv + h) * (int64_t)p.page;
+}
+
+// `rows` rows from row s to row d of a pool, with their scales (a page has at most 128).
+__device__ __forceinline__ void copy_page_rows(const PageReq& p, int64_t s, int64_t d, int rows, bool is_v) {
+    uint4* pool = is_v ? p.v : p.k;
+    uint8_t* scale = is_v ? p.vs : p.ks;
+    if (scale && (int)threadIdx.x < rows) scale[d + threadIdx.x] = scale[s + threadIdx.x];
+    copy_rows(pool + s * p.row16, pool + d * p.row16, rows * p.row16);
 }
 
 template <bool FORK>
@@ -395,10 +404,9 @@ __global__ void __launch_bounds__(kCopyThreads) pages_apply_kernel(const PageReq
         const int rows = p.w.rows[i];
         if (!rows) continue;
         bool is_v;
-        const int64_t s = unit_offset(p, x - i * per, p.w.src[i], &is_v);
-        const int64_t d = unit_offset(p, x - i * per, p.w.free_list[p.w.offset[i]], &is_v);
-        uint4* pool = is_v ? p.v : p.k;
-        copy_rows(pool + s, pool + d, rows * p.row16);
+        const int64_t s = unit_row(p, x - i * per, p.w.src[i], &is_v);
+        const int64_t d = unit_row(p, x - i * per, p.w.free_list[p.w.offset[i]], &is_v);
+        copy_page_rows(p, s, d, rows, is_v);
     }
 }
 
@@ -488,10 +496,9 @@ __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const PageR
     for (int64_t x = blockIdx.x - table_ctas; x < moved * per; x += gridDim.x - table_ctas) {
         const int i = (int)(x / per);
         bool is_v;
-        const int64_t s = unit_offset(p, x - i * per, movers[i], &is_v);
-        const int64_t d = unit_offset(p, x - i * per, holes[i], &is_v);
-        uint4* pool = is_v ? p.v : p.k;
-        copy_rows(pool + s, pool + d, p.page * p.row16);
+        const int64_t s = unit_row(p, x - i * per, movers[i], &is_v);
+        const int64_t d = unit_row(p, x - i * per, holes[i], &is_v);
+        copy_page_rows(p, s, d, p.page, is_v);
     }
 }
 
@@ -555,12 +562,26 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const PageReq p,
             }
         }
     }
+    // the rows' scales, whole heads at a time: all of a head's are read before one is written
+    uint8_t* scale = is_v ? p.vs : p.ks;
+    if (!scale) return;
+    scale += (int64_t)layer * p.n_pages * p.Hkv * p.page;
+    const int heads = kAcceptThreads / na, i = tid % na;
+    for (int h0 = 0; h0 < p.Hkv; h0 += heads) {
+        const int h = h0 + tid / na;
+        const bool on = tid < heads * na && h < p.Hkv;
+        uint8_t e = 0;
+        if (on) e = scale[(int64_t)h * p.page + from[i] / p.row16];
+        __syncthreads();
+        if (on) scale[(int64_t)h * p.page + to[i] / p.row16] = e;
+    }
 }
 
 // What the page calls share: sizes, pools, workspace.
-int fill_req(const bsa_page_cache* c, PageReq* p) {
+int fill_req(const bsa_page_cache* c, const bsa_page_scales* scales, PageReq* p) {
     int st = check_page_cache(c);
     if (st != BSA_OK) return st;
+    if (scales && (st = check_page_scales(c, scales)) != BSA_OK) return st;
     if (!c->page_table && c->n_seqs > 0) return BSA_ERR_INVALID_ARG;
     *p = PageReq{};
     p->table = c->page_table;
@@ -572,7 +593,11 @@ int fill_req(const bsa_page_cache* c, PageReq* p) {
     p->v = static_cast<uint4*>(c->v);
     p->layers = c->layers;
     p->Hkv = c->Hkv;
-    p->row16 = c->D / 8;
+    p->row16 = scales ? c->D / 16 : c->D / 8;
+    if (scales) {
+        p->ks = static_cast<uint8_t*>(scales->k);
+        p->vs = static_cast<uint8_t*>(scales->v);
+    }
     return BSA_OK;
 }
 
@@ -584,11 +609,12 @@ bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
     return x < y + 4 * (uint64_t)nb && y < x + 4 * (uint64_t)na;
 }
 
-int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n, const int32_t* a, const int32_t* b,
-                const int32_t* len, int32_t* granted, void* ws, int64_t ws_bytes, cudaStream_t s) {
+int run_request(bool fork, const bsa_page_cache* c, const bsa_page_scales* scales, int32_t* page_ref, int32_t n,
+                const int32_t* a, const int32_t* b, const int32_t* len, int32_t* granted, void* ws, int64_t ws_bytes,
+                cudaStream_t s) {
     PageReq p;
     int sms;
-    int st = fill_req(c, &p);
+    int st = fill_req(c, scales, &p);
     if (st != BSA_OK) return st;
     if (n < 0) return BSA_ERR_INVALID_ARG;
     if (n == 0) return BSA_OK;
@@ -631,6 +657,56 @@ int run_request(bool fork, const bsa_page_cache* c, int32_t* page_ref, int32_t n
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
+int run_compact(const bsa_page_cache* c, const bsa_page_scales* scales, int32_t* page_ref, int32_t* new_page,
+                void* workspace, int64_t workspace_bytes, cudaStream_t s) {
+    PageReq p;
+    int sms;
+    int st = fill_req(c, scales, &p);
+    if (st != BSA_OK) return st;
+    if (c->n_seqs == 0) return BSA_ERR_INVALID_ARG;  // the table is what says where the pages go
+    if (!page_ref || !new_page || !al(page_ref, 4) || !al(new_page, 4)) return BSA_ERR_INVALID_ARG;
+    if (!workspace || !al(workspace, 256)) return BSA_ERR_INVALID_ARG;
+    if (workspace_bytes < bsa_cache_pages_workspace(0, c->n_seqs, c->n_pages)) return BSA_ERR_CAPACITY;
+    if (meet(new_page, c->n_pages, page_ref, c->n_pages) ||
+        meet(new_page, c->n_pages, c->page_table, (int64_t)c->n_seqs * c->max_pages))
+        return BSA_ERR_INVALID_ARG;
+    if ((st = device_context(&p.err, &sms)) != BSA_OK) return st;
+    p.ref = page_ref;
+    p.w = split_ws(workspace, 0, c->n_seqs, c->n_pages);
+    cudaError_t e = launch_after(compact_plan_kernel, dim3(1), kPlanThreads, 0, s, p, new_page);
+    if (e != cudaSuccess) return BSA_ERR_CUDA;
+    const int64_t entries = (int64_t)c->n_seqs * c->max_pages;
+    const int table_ctas = (int)std::min<int64_t>((entries + 1023) / 1024, sms);
+    const int64_t units = (int64_t)c->n_pages * c->layers * 2 * c->Hkv;
+    const unsigned copy_ctas = (unsigned)std::min<int64_t>(units, 8ll * sms);
+    e = launch_after(compact_apply_kernel, dim3(table_ctas + copy_ctas), kCopyThreads, 0, s, p, new_page, table_ctas);
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+int run_accept(const bsa_page_cache* c, const bsa_page_scales* scales, const int32_t* context_len,
+               const int32_t* accepted, const int32_t* n_accepted, int32_t T, int32_t* new_len, cudaStream_t s) {
+    PageReq p;
+    int sms;
+    int st = fill_req(c, scales, &p);
+    if (st != BSA_OK) return st;
+    if (T < 1 || T > BSA_MAX_DRAFT) return BSA_ERR_INVALID_ARG;
+    if (2ll * c->layers > 65535) return BSA_ERR_UNSUPPORTED;
+    if (c->n_seqs == 0) return BSA_OK;
+    if (!context_len || !accepted || !n_accepted || !new_len) return BSA_ERR_INVALID_ARG;
+    for (const void* x : {(const void*)context_len, (const void*)accepted, (const void*)n_accepted, (const void*)new_len})
+        if (!al(x, 4)) return BSA_ERR_INVALID_ARG;
+    // every CTA of a sequence reads these, one of them writes the new length
+    const int64_t S = c->n_seqs;
+    if (meet(new_len, S, context_len, S) || meet(new_len, S, n_accepted, S) ||
+        meet(new_len, S, accepted, S * T) || meet(new_len, S, c->page_table, S * c->max_pages))
+        return BSA_ERR_INVALID_ARG;
+    if ((st = device_context(&p.err, &sms)) != BSA_OK) return st;
+    const dim3 grid((unsigned)c->n_seqs, (unsigned)(2 * c->layers));
+    const cudaError_t e =
+        launch_after(accept_kernel, grid, kAcceptThreads, 0, s, p, context_len, accepted, n_accepted, T, new_len);
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace bsa
 
@@ -644,68 +720,58 @@ int64_t bsa_cache_pages_workspace(int32_t n, int32_t n_seqs, int32_t n_pages) {
 int bsa_cache_resize(const bsa_page_cache* c, int32_t* page_ref, int32_t n, const int32_t* seqs, const int32_t* keep,
                      const int32_t* capacity, int32_t* granted, void* workspace, int64_t workspace_bytes,
                      bsa_stream_t stream) {
-    return bsa::run_request(false, c, page_ref, n, seqs, keep, capacity, granted, workspace, workspace_bytes,
+    return bsa::run_request(false, c, nullptr, page_ref, n, seqs, keep, capacity, granted, workspace, workspace_bytes,
                             reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bsa_cache_fork(const bsa_page_cache* c, int32_t* page_ref, int32_t n, const int32_t* src, const int32_t* dst,
                    const int32_t* len, int32_t* granted, void* workspace, int64_t workspace_bytes,
                    bsa_stream_t stream) {
-    return bsa::run_request(true, c, page_ref, n, dst, src, len, granted, workspace, workspace_bytes,
+    return bsa::run_request(true, c, nullptr, page_ref, n, dst, src, len, granted, workspace, workspace_bytes,
                             reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bsa_cache_compact(const bsa_page_cache* c, int32_t* page_ref, int32_t* new_page, void* workspace,
                       int64_t workspace_bytes, bsa_stream_t stream) {
-    bsa::PageReq p;
-    int sms;
-    int st = bsa::fill_req(c, &p);
-    if (st != BSA_OK) return st;
-    if (c->n_seqs == 0) return BSA_ERR_INVALID_ARG;  // the table is what says where the pages go
-    if (!page_ref || !new_page || !bsa::al(page_ref, 4) || !bsa::al(new_page, 4)) return BSA_ERR_INVALID_ARG;
-    if (!workspace || !bsa::al(workspace, 256)) return BSA_ERR_INVALID_ARG;
-    if (workspace_bytes < bsa_cache_pages_workspace(0, c->n_seqs, c->n_pages)) return BSA_ERR_CAPACITY;
-    if (bsa::meet(new_page, c->n_pages, page_ref, c->n_pages) ||
-        bsa::meet(new_page, c->n_pages, c->page_table, (int64_t)c->n_seqs * c->max_pages))
-        return BSA_ERR_INVALID_ARG;
-    if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
-    p.ref = page_ref;
-    p.w = bsa::split_ws(workspace, 0, c->n_seqs, c->n_pages);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = bsa::launch_after(bsa::compact_plan_kernel, dim3(1), bsa::kPlanThreads, 0, s, p, new_page);
-    if (e != cudaSuccess) return BSA_ERR_CUDA;
-    const int64_t entries = (int64_t)c->n_seqs * c->max_pages;
-    const int table_ctas = (int)std::min<int64_t>((entries + 1023) / 1024, sms);
-    const int64_t units = (int64_t)c->n_pages * c->layers * 2 * c->Hkv;
-    const unsigned copy_ctas = (unsigned)std::min<int64_t>(units, 8ll * sms);
-    e = bsa::launch_after(bsa::compact_apply_kernel, dim3(table_ctas + copy_ctas), bsa::kCopyThreads, 0, s, p, new_page,
-                          table_ctas);
-    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    return bsa::run_compact(c, nullptr, page_ref, new_page, workspace, workspace_bytes,
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bsa_cache_accept(const bsa_page_cache* c, const int32_t* context_len, const int32_t* accepted,
                      const int32_t* n_accepted, int32_t T, int32_t* new_len, bsa_stream_t stream) {
-    bsa::PageReq p;
-    int sms;
-    int st = bsa::fill_req(c, &p);
-    if (st != BSA_OK) return st;
-    if (T < 1 || T > BSA_MAX_DRAFT) return BSA_ERR_INVALID_ARG;
-    if (2ll * c->layers > 65535) return BSA_ERR_UNSUPPORTED;
-    if (c->n_seqs == 0) return BSA_OK;
-    if (!context_len || !accepted || !n_accepted || !new_len) return BSA_ERR_INVALID_ARG;
-    for (const void* x : {(const void*)context_len, (const void*)accepted, (const void*)n_accepted, (const void*)new_len})
-        if (!bsa::al(x, 4)) return BSA_ERR_INVALID_ARG;
-    // every CTA of a sequence reads these, one of them writes the new length
-    const int64_t S = c->n_seqs;
-    if (bsa::meet(new_len, S, context_len, S) || bsa::meet(new_len, S, n_accepted, S) ||
-        bsa::meet(new_len, S, accepted, S * T) || bsa::meet(new_len, S, c->page_table, S * c->max_pages))
-        return BSA_ERR_INVALID_ARG;
-    if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
-    const dim3 grid((unsigned)c->n_seqs, (unsigned)(2 * c->layers));
-    const cudaError_t e =
-        bsa::launch_after(bsa::accept_kernel, grid, bsa::kAcceptThreads, 0, reinterpret_cast<cudaStream_t>(stream), p,
-                          context_len, accepted, n_accepted, T, new_len);
-    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    return bsa::run_accept(c, nullptr, context_len, accepted, n_accepted, T, new_len,
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+int bsa_cache_resize_fp8(const bsa_page_cache* c, const bsa_page_scales* scales, int32_t* page_ref, int32_t n,
+                         const int32_t* seqs, const int32_t* keep, const int32_t* capacity, int32_t* granted,
+                         void* workspace, int64_t workspace_bytes, bsa_stream_t stream) {
+    if (!scales) return BSA_ERR_INVALID_ARG;
+    return bsa::run_request(false, c, scales, page_ref, n, seqs, keep, capacity, granted, workspace, workspace_bytes,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int bsa_cache_fork_fp8(const bsa_page_cache* c, const bsa_page_scales* scales, int32_t* page_ref, int32_t n,
+                       const int32_t* src, const int32_t* dst, const int32_t* len, int32_t* granted, void* workspace,
+                       int64_t workspace_bytes, bsa_stream_t stream) {
+    if (!scales) return BSA_ERR_INVALID_ARG;
+    return bsa::run_request(true, c, scales, page_ref, n, dst, src, len, granted, workspace, workspace_bytes,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int bsa_cache_compact_fp8(const bsa_page_cache* c, const bsa_page_scales* scales, int32_t* page_ref,
+                          int32_t* new_page, void* workspace, int64_t workspace_bytes, bsa_stream_t stream) {
+    if (!scales) return BSA_ERR_INVALID_ARG;
+    return bsa::run_compact(c, scales, page_ref, new_page, workspace, workspace_bytes,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int bsa_cache_accept_fp8(const bsa_page_cache* c, const bsa_page_scales* scales, const int32_t* context_len,
+                         const int32_t* accepted, const int32_t* n_accepted, int32_t T, int32_t* new_len,
+                         bsa_stream_t stream) {
+    if (!scales) return BSA_ERR_INVALID_ARG;
+    return bsa::run_accept(c, scales, context_len, accepted, n_accepted, T, new_len,
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

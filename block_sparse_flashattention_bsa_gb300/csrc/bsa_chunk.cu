@@ -1,0 +1,971 @@
+// bsa_chunk.cu -- attention of chunks of new tokens over a paged cache (a prompt
+// behind a cached prefix, ragged batches), over all slots or a sliding window with
+// sinks, bf16 or 8-bit pools.
+//
+// Mathematics: O = softmax(q K^T scale) V over the slots u <= s a token in slot s
+// sees (with a window w: u > s - w or u < sinks), in one pass over the slots with
+// the running maximum and sum of the softmax.  The G query heads of a key head are
+// rows of the same tile: row t * G + g is head g of the tile's token t.
+//
+// What bounds it: 4 D flops for every (row, slot) pair, the tensor cores; the
+// exponentials (one a pair) and, for 8-bit rows, the conversions run beside them.
+//
+// Work: an item is two tiles of 128 rows of one key head of one sequence (both
+// tiles use every K / V tile that is loaded); a step 128 slots.  plan_kernel lists
+// the items' steps, heads outermost; the steps of the whole batch are cut into
+// equal ranges, one per CTA, so that one long chunk loads the SMs as evenly as
+// many short ones.  Items that a range boundary cuts leave unnormalised fp32
+// parts, which the merge joins in range order: results do not depend on timing.
+//
+// One CTA per SM:
+//   warps 0-3, 4-7  softmax of tile A, B: thread = row (TMEM lane).  S in
+//              registers, P back over it in bf16.  O is rescaled in TMEM only when
+//              the maximum grows by more than 2^8.
+//   warp 8     producer: walks the range, resolves pages, TMA-loads K / V tiles
+//   warp 9     MMA: S = Q K^T and O += P V on tcgen05; while one tile's softmax
+//              runs, the other tile's products do:
+//              ... PV_A(j-1) QK_A(j) PV_B(j-1) QK_B(j) PV_A(j) ...
+//   warp 10    loads an item's Q tiles as soon as the item before has used its own
+//   warp 11    bf16: zeroes V rows behind the last token (they may hold NaN)
+//   warps 12-15  8-bit: convert tiles to bf16 (code * 2^e, exact), thread = row
+
+#include <algorithm>
+#include <cmath>
+
+#include "bsa.h"
+#include "bsa_chunk.cuh"
+#include "bsa_q8.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kSmem = 232448;
+constexpr int kCtrl = 2560;
+constexpr int kInfos = 4;
+constexpr int kQAhead = 4;
+constexpr int kMaxTiles = 12;
+constexpr int kProducer = 8, kMma = 9, kQLoader = 10, kFixer = 11, kConverter = 12;
+constexpr int kRows = 256;  // rows of an item
+
+enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8, kFix = 16 };
+
+struct StepInfo {
+    int flags;
+    int base, have;      // first slot; halves that lie in a page
+    int row0, n, h;      // first token (row of q), tokens, key head of the item
+    int pos0, end;       // slot of its first token, slot behind the sequence's last one
+    int part;            // -1: write the output, else the partial slot
+};
+
+// A row group of the plan: two tiles of tokens of one sequence.
+struct Group {
+    int b, t0, steps, cum;  // cum: steps of the groups before it
+};
+struct PlanHead {
+    int groups, steps;  // steps of all groups, of one key head
+    int pad[62];
+};
+
+struct Ctrl {
+    uint64_t t_full[kMaxTiles], t_empty[kMaxTiles];   // bf16 tiles
+    uint64_t r_full[kMaxTiles], r_empty[kMaxTiles];   // 8-bit tiles
+    uint64_t q_full[2], q_empty[2];
+    uint64_t qi_full[kQAhead], qi_empty[kQAhead];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t i_empty[kInfos];
+    uint64_t fix_full, drain;
+    volatile uint32_t issued;        // steps the producer has issued
+    int2 qitem[kQAhead];             // first query head and token of an item; x < 0: no more
+    StepInfo info[kInfos];
+    uint32_t tmem_base;
+    WaitFlag wf;
+};
+static_assert(sizeof(Ctrl) <= kCtrl, "control block too large");
+
+struct ChunkParams {
+    ChunkCommon c;
+    int32_t tq;                // tokens of a tile
+    const PlanHead* head;
+    const Group* groups;
+    PartMeta* meta;
+    float* part_o;             // [2 * grid][256][D]
+    float2* part_ml;           // [2 * grid][256]
+};
+
+template <int D, bool Q8>
+struct Cfg {
+    static constexpr int THREADS = Q8 ? 512 : 384;
+    static constexpr int NBOX = D / 64;
+    static constexpr int QBOX = 128 * 128, QTILE = NBOX * QBOX;
+    static constexpr int BOX = kTile * 128, TILE = NBOX * BOX;
+    static constexpr int RAW = kTile * D;              // an 8-bit tile
+    static constexpr int FREE = kSmem - kCtrl - 2 * QTILE;
+    // 8-bit: three bf16 tiles, the rest holds what is in flight
+    static constexpr int NRAW = Q8 ? ((FREE - 3 * TILE) / (RAW + kTile) > kMaxTiles ? kMaxTiles
+                                                                                    : (FREE - 3 * TILE) / (RAW + kTile))
+                                   : 0;
+    static constexpr int NT = Q8 ? 3 : (FREE / TILE > kMaxTiles ? kMaxTiles : FREE / TILE);
+    static constexpr int SMEM = 2 * QTILE + NT * TILE + NRAW * (RAW + kTile) + kCtrl;
+    static constexpr int O_COL = 2 * kTile;
+    static_assert(SMEM <= kSmem && NT >= 3 && (!Q8 || NRAW >= 2), "shared memory");
+};
+
+// ---------------------------------------------------------------- plan
+// One CTA: the row groups of the sequences that are not short, and the running
+// sum of their steps.  Sequences in order, a warp each (lanes are groups).
+__global__ void __launch_bounds__(1024) plan_kernel(const ChunkCommon p, PlanHead* head, Group* groups, int cap, int tq) {
+    __shared__ int red[32];
+    __shared__ int first[1024 + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_launch_dependents();
+    griddep_wait();
+    int done = 0;  // groups of the sequences before
+    for (int b0 = 0; b0 < p.B; b0 += 1024) {
+        const int b = b0 + tid;
+        int cnt = 0;
+        if (b < p.B) {
+            const Seq s = sequence(p, b, true);
+            if (s.n * (int64_t)p.G > kShortRows) cnt = (s.n + 2 * tq - 1) / (2 * tq);
+        }
+        int incl = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) red[warp] = incl;
+        __syncthreads();
+        incl += __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
+        first[tid] = done + incl - cnt;
+        if (tid == 1023) first[1024] = done + incl;
+        __syncthreads();
+        for (int u = warp; u < min(1024, p.B - b0); u += 32) {
+            const int at = first[u], n = first[u + 1] - at;
+            if (n == 0) continue;
+            const Seq s = sequence(p, b0 + u, false);
+            for (int i = lane; i < n && at + i < cap; i += 32) {
+                const int t0 = i * 2 * tq, pos = s.ctx + t0;
+                groups[at + i] = Group{b0 + u, t0, visible_span(p, pos, s.ctx + min(s.n, t0 + 2 * tq)).steps, 0};
+            }
+        }
+        done = first[1024];
+        __syncthreads();
+    }
+    if (done > cap) {  // overlapping sequences: more rows than there are
+        if (tid == 0) atomicOr(p.err, ERR_CAPACITY);
+        done = cap;
+    }
+    __threadfence_block();
+    __syncthreads();
+    int before = 0;
+    for (int g0 = 0; g0 < done; g0 += 1024) {
+        const int g = g0 + tid, steps = g < done ? groups[g].steps : 0;
+        int incl = steps;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) red[warp] = incl;
+        __syncthreads();
+        incl += __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
+        if (g < done) groups[g].cum = before + incl - steps;
+        before += __reduce_add_sync(0xffffffffu, red[lane]);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        head->groups = done;
+        head->steps = before;
+    }
+}
+
+// ---------------------------------------------------------------- producer
+template <int D, bool Q8>
+__device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const ChunkParams& p, uint8_t* sT, uint8_t* sS,
+                         Ctrl* c, int S1, int n_groups, int lo, int hi, int per, volatile WaitFlag* wf) {
+    using C = Cfg<D, Q8>;
+    constexpr uint32_t NS = Q8 ? C::NRAW : C::NT;
+    constexpr int ROWB = Q8 ? D : 128, NBOX = Q8 ? 1 : C::NBOX, BOX = kTile * ROWB, TILE = NBOX * BOX;
+    const ChunkCommon& cc = p.c;
+    uint64_t* full = Q8 ? c->r_full : c->t_full;
+    uint64_t* empty = Q8 ? c->r_empty : c->t_empty;
+    const int lane = threadIdx.x & 31, ppt = kTile / cc.page;
+    const bool leader = elect_one();
+    uint32_t slot = 0, phase = 0, nload = 0, g = 0, nq = 0;
+    bool ok = true, ended = false;
+    PartMeta mt{-1, 0, per, 0, 0, 0, {0, 0}};
+    if (lo < hi) {
+        int h = lo / S1;
+        const int in = lo - h * S1;
+        int u = 0;  // the group that holds step lo of head h: last one whose first step is not behind it
+        for (int span = n_groups; span > 1;) {
+            const int stride = (span + 31) >> 5, off = lane * stride;
+            const bool le = off < span && p.groups[u + off].cum <= in;
+            u += (__popc(__ballot_sync(0xffffffffu, le)) - 1) * stride;
+            span = min(stride, n_groups - u);
+        }
+        int pos = lo;
+        while (ok && pos < hi) {
+            const Group gr = p.groups[u];
+            const int b = gr.b;
+            const Seq sq = sequence(cc, b, false);
+            const int n = min(sq.n - gr.t0, 2 * p.tq), first = sq.ctx + gr.t0, last = first + n;
+            const int vis0 = first_slot(cc, first);
+            const Span sp = visible_span(cc, first, last);
+            const int start = h * S1 + gr.cum, end = start + gr.steps;
+            const int s0 = pos - start, s1 = min(end, hi) - start;
+            const bool whole = s0 == 0 && start + s1 == end;
+            const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
+            if (start < lo) mt = PartMeta{start, end, per, sq.row0 + gr.t0, n, h, {0, 0}};
+            // the Q loader's turn, as soon as its buffers are free
+            if (nq >= kQAhead && !warp_wait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
+                ok = false;
+                break;
+            }
+            if (leader) {
+                c->qitem[nq % kQAhead] = make_int2(h * cc.G, sq.row0 + gr.t0);
+                mbar_arrive(&c->qi_full[nq % kQAhead]);
+            }
+            ++nq;
+            for (int e0 = s0 * ppt; e0 < s1 * ppt && ok; e0 += 32) {
+                const int e = e0 + lane, est = e / ppt;  // 32 pages resolved at a time
+                const int j = sp.tile(est) * ppt + e % ppt;
+                const int y = est < s1 ? page_row(cc, b, h, j, vis0, last) : -1;
+                const int cnt = min(32, s1 * ppt - e0);
+                for (int q = 0; q < cnt && ok; q += ppt) {
+                    const int st = (e0 + q) / ppt;
+                    const int y0 = __shfl_sync(0xffffffffu, y, q), y1 = __shfl_sync(0xffffffffu, y, q + ppt - 1);
+                    const uint32_t is = g % kInfos;
+                    if (g >= kInfos && !warp_wait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) {
+                        StepInfo& f = c->info[is];
+                        const int base = sp.tile(st) * kTile;
+                        const int have = ppt == 1 ? (y0 >= 0 ? 3 : 0) : (y0 >= 0 ? 1 : 0) | (y1 >= 0 ? 2 : 0);
+                        // every row sees all of it: up to the first token, inside the last one's window
+                        const bool plain = have == 3 && base + kTile <= first + 1 &&
+                                           (cc.window <= 0 || base > last - 1 - cc.window || base + kTile <= cc.sinks);
+                        f.flags = (st == s0 ? kFirst : 0) | (st + 1 == s1 ? kLast : 0) | (plain ? 0 : kMask) |
+                                  (base + kTile > sq.ctx + sq.n ? kFix : 0);
+                        f.base = base;
+                        f.have = have;
+                        f.row0 = sq.row0 + gr.t0;
+                        f.n = n;
+                        f.h = h;
+                        f.pos0 = first;
+                        f.end = sq.ctx + sq.n;
+                        f.part = part;
+                    }
+                    __syncwarp();
+                    ++g;
+                    if (leader) c->issued = g;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (nload >= NS && !warp_wait(&empty[slot], phase ^ 1, wf)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) {
+                            const uint8_t* sc = kv ? cc.vs : cc.ks;
+                            uint32_t bytes = TILE;
+                            if (Q8) bytes += (y0 >= 0 ? cc.page : 0) + (ppt == 2 && y1 >= 0 ? cc.page : 0);
+                            mbar_arrive_expect_tx(&full[slot], bytes);
+#pragma unroll
+                            for (int x = 0; x < NBOX; ++x) {
+                                uint8_t* dst = sT + slot * TILE + x * BOX;
+                                tma_load_2d(dst, kv ? tv : tk, &full[slot], x * 64, y0 >= 0 ? y0 : -cc.page);
+                                if (ppt == 2)
+                                    tma_load_2d(dst + 64 * ROWB, kv ? tv : tk, &full[slot], x * 64,
+                                                y1 >= 0 ? y1 : -cc.page);
+                            }
+                            if (Q8) {
+                                if (y0 >= 0) bulk_load(sS + slot * kTile, sc + y0, cc.page, &full[slot]);
+                                if (ppt == 2 && y1 >= 0)
+                                    bulk_load(sS + slot * kTile + 64, sc + y1, cc.page, &full[slot]);
+                            }
+                        }
+                        ++nload;
+                        if (++slot == NS) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+            }
+            pos = start + s1;
+            if (++u == n_groups && pos < hi) {
+                u = 0;
+                ++h;
+            }
+        }
+    }
+    if (ok) {
+        // the end mark, with a slot's barrier; the converters and the MMA lane pass it on
+        const uint32_t is = g % kInfos;
+        if ((g < kInfos || warp_wait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf)) &&
+            (nload < NS || warp_wait(&empty[slot], phase ^ 1, wf)) && leader) {
+            c->info[is].flags = kEnd;
+            mbar_arrive(&full[slot]);
+            ended = true;
+        }
+        if ((nq < kQAhead || warp_wait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) && leader) {
+            c->qitem[nq % kQAhead] = make_int2(-1, 0);
+            mbar_arrive(&c->qi_full[nq % kQAhead]);
+        }
+    }
+    if (lane == 0) p.meta[blockIdx.x] = mt;
+    __syncwarp();
+    if (leader) {
+        // copies still in flight must land before the CTA exits (the end mark used
+        // the slot of the oldest one, which was consumed before)
+        for (uint32_t x = nload > NS ? nload - NS : 0; x < nload; ++x) {
+            if (ended && x % NS == nload % NS) continue;
+            mbar_wait_drain(&full[x % NS], (x / NS) & 1);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- Q loader
+// One lane.  Tile B's queries follow tile A's; rows behind a tile's tokens * G
+// stay the zeros of the start (or another tile's queries: they are not stored).
+template <int D>
+__device__ void q_loader(const CUtensorMap* tq, const ChunkParams& p, uint8_t* sQ, Ctrl* c, volatile WaitFlag* wf) {
+    constexpr int NBOX = D / 64, QBOX = 128 * 128;
+    if (elect_one()) {
+        uint32_t n = 0;  // items
+        uint32_t loads[2] = {0, 0};
+        for (;; ++n) {
+            const uint32_t qi = n % kQAhead;
+            // the next item is announced when this one's loads are through, which may take
+            // longer than a wait: the limit counts from the last step issued
+            bool there;
+            uint32_t seen;
+            do {
+                seen = c->issued;
+                const unsigned long long t0 = globaltimer_ns();
+                there = false;
+                for (uint32_t it = 1; !there; ++it) {
+                    there = mbar_try_wait(&c->qi_full[qi], (n / kQAhead) & 1);
+                    if ((it & 31u) == 0 && (wf->abort || globaltimer_ns() - t0 > wf->limit_ns)) break;
+                }
+            } while (!there && !wf->abort && c->issued != seen);
+            if (!there) {
+                wf->abort = 1;
+                break;
+            }
+            const int2 it = c->qitem[qi];
+            mbar_arrive(&c->qi_empty[qi]);
+            if (it.x < 0) break;
+            bool ok = true;
+            for (int t = 0; t < 2 && ok; ++t) {
+                ok = mbar_wait(&c->q_empty[t], (n & 1) ^ 1, wf);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&c->q_full[t], (uint32_t)(p.tq * p.c.G * 128 * NBOX));
+                ++loads[t];
+#pragma unroll
+                for (int x = 0; x < NBOX; ++x)
+                    tma_load_3d(sQ + (t * NBOX + x) * QBOX, tq, &c->q_full[t], x * 64, it.x, it.y + t * p.tq);
+            }
+            if (!ok) break;
+        }
+        // a copy still in flight must land before the CTA exits
+        for (int t = 0; t < 2; ++t)
+            if (loads[t] > 0) mbar_wait_drain(&c->q_full[t], (loads[t] - 1) & 1);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- MMA
+template <int D, bool Q8>
+__device__ void mma_lane(uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem, volatile WaitFlag* wf) {
+    using C = Cfg<D, Q8>;
+    constexpr uint64_t KDESC = sdesc_sw128_base(16, 1024), VDESC = sdesc_sw128_base(C::BOX, 1024);
+    constexpr uint32_t IQK = idesc_bf16_f32(128, kTile, false), IPV = idesc_bf16_f32(128, D, true);
+    if (elect_one()) {
+        uint32_t slot = 0, phase = 0, vslot = 0, vphase = 0, items = 0, fixes = 0;
+        bool pend = false;
+        int pflags = 0;
+        auto next = [&]() {
+            if (++slot == (uint32_t)C::NT) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        auto qk = [&](int t, uint32_t ks) {
+            const uint64_t kd = KDESC + (smem_u32(sT + ks * C::TILE) >> 4);
+            const uint64_t qd = KDESC + (smem_u32(sQ + t * C::QTILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + t * kTile, qd + off, kd + off, IQK, kk > 0);
+            }
+            mma_commit(&c->s_full[t]);
+            mbar_arrive(&c->s_full[t]);
+        };
+        auto pv = [&](int t, uint32_t g) -> bool {
+            if (t == 0) {
+                if (!mbar_wait(&c->t_full[vslot], vphase, wf)) return false;
+                if (!Q8 && (pflags & kFix)) {
+                    if (!mbar_wait(&c->fix_full, fixes & 1, wf)) return false;
+                    ++fixes;
+                }
+            }
+            if (!mbar_wait(&c->p_full[t], g & 1, wf)) return false;
+            tc_fence_after();
+            const uint64_t vd = VDESC + (smem_u32(sT + vslot * C::TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+                mma_ts(tmem + C::O_COL + t * D, tmem + t * kTile + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), IPV,
+                       ((pflags & kFirst) && kk == 0) ? 0u : 1u);
+            if (t == 1) mma_commit(&c->t_empty[vslot]);
+            if (pflags & kLast) mma_commit(&c->o_full[t]);
+            return true;
+        };
+        for (uint32_t g = 0;; ++g) {
+            if (pend && !pv(0, g - 1)) break;
+            if (!mbar_wait(&c->t_full[slot], phase, wf)) break;
+            const int flags = c->info[g % kInfos].flags;
+            if (flags & kEnd) {
+                if (pend && !pv(1, g - 1)) break;
+                for (int t = 0; t < 2; ++t) {
+                    mbar_arrive(&c->s_full[t]);
+                    mbar_arrive(&c->s_full[t]);
+                }
+                break;
+            }
+            const uint32_t ks = slot;
+            if ((flags & kFirst) && !mbar_wait(&c->q_full[0], items & 1, wf)) break;
+            tc_fence_after();
+            qk(0, ks);
+            if (flags & kLast) mma_commit(&c->q_empty[0]);
+            if (pend && !pv(1, g - 1)) break;
+            if ((flags & kFirst) && !mbar_wait(&c->q_full[1], items & 1, wf)) break;
+            tc_fence_after();
+            qk(1, ks);
+            mma_commit(&c->t_empty[ks]);
+            if (flags & kLast) {
+                mma_commit(&c->q_empty[1]);
+                ++items;
+            }
+            next();
+            vslot = slot;
+            vphase = phase;
+            next();
+            pflags = flags;
+            pend = true;
+        }
+        mma_commit(&c->drain);
+        mbar_wait_drain(&c->drain, 0);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- fixer
+// bf16: V rows behind the last token become zeros before the product reads them.
+template <int D>
+__device__ void fixer(uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
+    using C = Cfg<D, false>;
+    const int lane = threadIdx.x & 31;
+    uint32_t slot = 0, phase = 0;
+    auto next = [&]() {
+        if (++slot == (uint32_t)C::NT) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    for (uint32_t g = 0;; ++g) {
+        if (!warp_wait(&c->t_full[slot], phase, wf)) return;
+        const uint32_t is = g % kInfos;
+        const int flags = c->info[is].flags, left = c->info[is].end - c->info[is].base;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->i_empty[is]);
+        if (flags & kEnd) return;
+        next();
+        if (flags & kFix) {
+            if (!warp_wait(&c->t_full[slot], phase, wf)) return;
+            const int from = max(left, 0);
+#pragma unroll
+            for (int x = 0; x < C::NBOX; ++x)
+                for (int i = from * 8 + lane; i < kTile * 8; i += 32)
+                    reinterpret_cast<uint4*>(sT + slot * C::TILE + x * C::BOX)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->fix_full);
+        }
+        next();
+    }
+}
+
+// ---------------------------------------------------------------- converters
+// Thread = row of a tile: its codes times 2^e, in bf16, into the tile that the
+// products read; 16-byte pieces, both sides in their copy's swizzle.
+template <int D>
+__device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
+    using C = Cfg<D, true>;
+    const int lane = threadIdx.x & 31, row = threadIdx.x - kConverter * 32;
+    uint32_t rs = 0, rphase = 0, ts = 0, tphase = 1;
+    for (uint32_t n = 0;; ++n) {
+        if (!warp_wait(&c->r_full[rs], rphase, wf)) return;
+        if (!warp_wait(&c->t_empty[ts], tphase, wf)) return;
+        const bool end = (n & 1) == 0 && (c->info[(n >> 1) % kInfos].flags & kEnd);
+        if (!end) {
+            const uint8_t* src = sR + rs * C::RAW + row * D;
+            uint8_t* dst = sT + ts * C::TILE + row * 128;
+            const uint32_t e = sS[rs * kTile + row];
+            const uint32_t f1 = scale_first(e) * 0x10001u, f2_ = scale_rest(e) * 0x10001u;
+            const bool two = __any_sync(0xffffffffu, e > kOneStep);
+            const int rx = D == 64 ? (row >> 1) & 3 : row & 7, wx = row & 7;
+            uint4 v[D / 16];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) v[i] = *reinterpret_cast<const uint4*>(src + ((i ^ rx) << 4));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o[2 * k] = mul_bf16x2(spread_odd(__byte_perm(w[k], 0, 0x1404)), f1);
+                    o[2 * k + 1] = mul_bf16x2(spread_odd(__byte_perm(w[k], 0, 0x3424)), f1);
+                }
+                if (two) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2_);
+                }
+                uint8_t* box = dst + (i >> 2) * C::BOX;
+                const int ch = (i & 3) * 2;
+                *reinterpret_cast<uint4*>(box + ((ch ^ wx) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(box + (((ch + 1) ^ wx) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&c->r_empty[rs]);
+            mbar_arrive(&c->t_full[ts]);
+        }
+        if (end) return;
+        if (++rs == (uint32_t)C::NRAW) {
+            rs = 0;
+            rphase ^= 1;
+        }
+        if (++ts == (uint32_t)C::NT) {
+            ts = 0;
+            tphase ^= 1;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- softmax
+template <int D, bool Q8>
+__device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile WaitFlag* wf) {
+    using C = Cfg<D, Q8>;
+    const ChunkCommon& cc = p.c;
+    const int t = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(row & 96) << 16;
+    const uint32_t t_s = tmem + lanes + t * kTile, t_o = tmem + lanes + C::O_COL + t * D;
+    const int tok = t * p.tq + row / cc.G, hd = row % cc.G;  // the row's token of the item, head of the group
+    const bool in_tile = row < p.tq * cc.G;
+    float m = -INFINITY, l = 0.f;
+    uint32_t items = 0;
+    const f2 sl2 = {cc.scale_log2, cc.scale_log2};
+    for (uint32_t g = 0;; ++g) {
+        if (!warp_wait(&c->s_full[t], g & 1, wf)) return;
+        tc_fence_after();
+        const uint32_t is = g % kInfos;
+        const StepInfo& f = c->info[is];
+        const int flags = f.flags;
+        if (flags & kEnd) return;
+        if (flags & kFirst) {
+            m = -INFINITY;
+            l = 0.f;
+        }
+        // Columns 64 .. 127 first, then 0 .. 63, which stay in registers for the
+        // weights (P of columns c goes over columns c / 2, so 0 .. 63 come first there).
+        uint32_t s[2][32];
+        Seen seen;
+        if (flags & kMask) seen = seen_slots(cc, f.base, in_tile && tok < f.n ? f.pos0 + tok : -1, f.have);
+        auto load = [&](int half) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) tmem_ld32(t_s + half * 64 + x * 32, s[x]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) reg_fence(s[x]);
+            if (flags & kMask) {
+                const unsigned long long vis = half ? seen.w[1] : seen.w[0];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int q = 0; q < 32; ++q)
+                        if (!(((uint32_t)(vis >> (32 * x)) >> q) & 1u)) s[x][q] = __float_as_uint(-INFINITY);
+            }
+        };
+        float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+            load(half);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int q = 0; q < 32; q += 2)
+                    a[(q >> 1) & 3] = fmax3(a[(q >> 1) & 3], __uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1]));
+        }
+        const float top = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * cc.scale_log2;
+        // The reference follows the maximum only where it grows by more than 2^8
+        // (exact after the final division).  The product before this step's scores
+        // has completed: O is at rest.
+        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+            const float up = fmaxf(m, top);
+            const float w = up == -INFINITY ? 1.f : ex2_approx(m - up);
+            if (!(flags & kFirst)) {
+                const f2 w2 = {w, w};
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + x * 32, o);
+                    tmem_wait_ld();
+                    reg_fence(o);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const f2 v = mul2({__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])}, w2);
+                        o[2 * q] = __float_as_uint(v.x);
+                        o[2 * q + 1] = __float_as_uint(v.y);
+                    }
+                    tmem_st32(t_o + x * 32, o);
+                }
+            }
+            l *= w;
+            m = up;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const f2 nm2 = {-ref, -ref};
+        f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half) load(1);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const f2 v = fma2({__uint_as_float(s[x][2 * q]), __uint_as_float(s[x][2 * q + 1])}, sl2, nm2);
+                    const f2 e = {ex2_approx(v.x), ex2_approx(v.y)};
+                    sum[q & 1] = add2(sum[q & 1], e);
+                    pk[q] = pack_bf16x2(e.x, e.y);
+                }
+                tmem_st16(t_s + half * 32 + x * 16, pk);
+            }
+        }
+        const f2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
+        const int n = f.n, part = f.part;
+        const int64_t row0 = f.row0;
+        const int h = f.h;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&c->i_empty[is]);
+            mbar_arrive(&c->p_full[t]);
+        }
+        if (!(flags & kLast)) continue;
+        // The item's end: its row, normalised, or a part of it.
+        if (!warp_wait(&c->o_full[t], items & 1, wf)) return;
+        tc_fence_after();
+        ++items;
+        const bool live = in_tile && tok < n;
+        const float w = part >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const int64_t orow = (row0 + tok) * cc.Hq + h * cc.G + hd;
+        const int64_t prow = (int64_t)part * kRows + threadIdx.x;
+        if (live) {
+            if (part < 0)
+                cc.lse[orow] = lse_of(m, l);
+            else
+                p.part_ml[prow] = make_float2(m, l);
+        }
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(t_o + x * 32, o);
+            tmem_wait_ld();
+            reg_fence(o);
+            if (!live) continue;
+            if (part < 0) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cc.out) + orow * D + x * 32);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * i]) * w, __uint_as_float(o[8 * q + 2 * i + 1]) * w);
+                    dst[q] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            } else {
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + x * 32);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+        }
+        __syncwarp();
+        tc_fence_before();
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                 const __grid_constant__ CUtensorMap tv, const ChunkParams p) {
+    using C = Cfg<D, Q8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {
+        griddep_wait();
+        if (threadIdx.x == 0) {
+            p.meta[blockIdx.x].start = -1;
+            atomicOr(p.c.err, ERR_LAUNCH);
+        }
+        return;
+    }
+    uint8_t* sQ = smem;
+    uint8_t* sT = sQ + 2 * C::QTILE;
+    uint8_t* sR = sT + C::NT * C::TILE;
+    uint8_t* sS = sR + C::NRAW * C::RAW;
+    Ctrl* c = reinterpret_cast<Ctrl*>(sS + C::NRAW * kTile);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_launch_dependents();
+    {
+        const int x = threadIdx.x;
+        if (x < kMaxTiles) {
+            mbar_init(&c->t_full[x], Q8 ? 4 : 1);  // the converters' warps, or the copy
+            mbar_init(&c->t_empty[x], 1);
+            mbar_init(&c->r_full[x], 1);
+            mbar_init(&c->r_empty[x], 4);
+        } else if (x >= 32 && x < 32 + kInfos) {
+            mbar_init(&c->i_empty[x - 32], Q8 ? 8 : 9);  // the softmax warps and the fixer
+        } else if (x >= 64 && x < 66) {
+            mbar_init(&c->q_full[x - 64], 1);
+            mbar_init(&c->q_empty[x - 64], 1);
+            mbar_init(&c->s_full[x - 64], 2);  // the scores' commit and the MMA lane itself
+            mbar_init(&c->p_full[x - 64], 4);
+            mbar_init(&c->o_full[x - 64], 1);
+        } else if (x >= 96 && x < 96 + kQAhead) {
+            mbar_init(&c->qi_full[x - 96], 1);
+            mbar_init(&c->qi_empty[x - 96], 1);
+        } else if (x == 128) {
+            mbar_init(&c->fix_full, 1);
+            mbar_init(&c->drain, 1);
+            c->wf.abort = 0;
+            c->wf.limit_ns = p.c.wait_limit_ns;
+            c->issued = 0;
+        }
+        fence_mbar_init();
+        for (int z = x; z < 2 * C::QTILE / 16; z += C::THREADS)
+            reinterpret_cast<uint4*>(sQ)[z] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    if (warp == kProducer && lane == 0) {
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+    }
+    // Nothing before this line reads or writes global memory or takes tensor memory.
+    griddep_wait();
+    if (warp == kMma) {
+        tmem_alloc(&c->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c->tmem_base;
+    volatile WaitFlag* wf = &c->wf;
+    const int S1 = p.head->steps, n_groups = p.head->groups;
+    const int total = S1 * p.c.Hkv;
+    const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
+    // 8-bit: 128 registers a thread at launch; the softmax's 256 threads take 184,
+    // the others' 256 keep 72: 184 + 72 = 2 * 128.
+    if (warp < 8) {
+        if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        softmax<D, Q8>(p, c, tmem, wf);
+    } else {
+        if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kProducer)
+            producer<D, Q8>(&tk, &tv, p, Q8 ? sR : sT, sS, c, S1, n_groups, lo, hi, per, wf);
+        else if (warp == kMma)
+            mma_lane<D, Q8>(sQ, sT, c, tmem, wf);
+        else if (warp == kQLoader)
+            q_loader<D>(&tq, p, sQ, c, wf);
+        else if (warp == kFixer) {
+            if (!Q8) fixer<D>(sT, c, wf);
+        } else
+            converter<D>(sR, sS, sT, c, wf);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && c->wf.abort) atomicOr(p.c.err, ERR_TIMEOUT);
+}
+
+bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int tile_tokens(int G) { return 128 / G; }
+
+// The workspace: both kernels' part descriptions, the plan, the parts.
+struct Layout {
+    int64_t short_meta, short_o, short_ml, meta, head, groups, o, ml, bytes;
+    int32_t cap;
+};
+int64_t up(int64_t x) { return (x + 255) / 256 * 256; }
+Layout layout(int64_t B, int64_t tokens, int G, int D) {
+    Layout w{};
+    int64_t at = 0;
+    auto take = [&](int64_t n) {
+        const int64_t x = at;
+        at = up(at + n);
+        return x;
+    };
+    const int64_t parts = 2 * kChunkMaxCtas;
+    w.short_meta = take(kChunkMaxCtas * (int64_t)sizeof(PartMeta));
+    w.short_o = take(parts * kShortRows * D * 4);
+    w.short_ml = take(parts * kShortRows * 8);
+    if (tokens * G > kShortRows) {
+        // a sequence's groups: its tokens over 2 tq, rounded up
+        const int64_t cap = tokens / (2 * tile_tokens(G)) + std::min(B, tokens);
+        w.cap = (int32_t)std::min<int64_t>(cap, INT32_MAX);
+        w.meta = take(kChunkMaxCtas * (int64_t)sizeof(PartMeta));
+        w.head = take(sizeof(PlanHead));
+        w.groups = take(cap * (int64_t)sizeof(Group));
+        w.o = take(parts * kRows * D * 4);
+        w.ml = take(parts * kRows * 8);
+    }
+    w.bytes = at;
+    return w;
+}
+
+template <int D, bool Q8>
+int go(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, int ctas, cudaStream_t s) {
+    using C = Cfg<D, Q8>;
+    static std::atomic<uint64_t> raised{0};
+    if (raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<D, Q8>), C::SMEM, &raised) != cudaSuccess)
+        return BSA_ERR_CUDA;
+    if (Q8) {
+        // the register split takes all of what 512 threads of 128 are given: with less it would wait forever
+        static std::atomic<int> regs{0};
+        if (regs.load() == 0) {
+            cudaFuncAttributes at;
+            if (cudaFuncGetAttributes(&at, chunk_kernel<D, Q8>) != cudaSuccess) return BSA_ERR_CUDA;
+            regs.store(at.numRegs);
+        }
+        if (regs.load() < 128) return BSA_ERR_UNSUPPORTED;
+    }
+    cudaError_t e = launch_after(chunk_kernel<D, Q8>, dim3((unsigned)ctas), C::THREADS, C::SMEM, s, tq, tk, tv, p);
+    if (e == cudaSuccess && ctas > 1)
+        e = launch_after(chunk_merge_kernel<D, kRows, 8>, dim3((unsigned)ctas - 1, kRows / 8), 256, 0, s, p.c, p.meta,
+                         p.part_o, p.part_ml, p.tq);
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace bsa
+
+extern "C" {
+
+int64_t bsa_chunk_attention_workspace(int32_t B, int32_t tokens, int32_t Hq, int32_t Hkv, int32_t D) {
+    if (B <= 0 || tokens <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv || Hq / Hkv > 128) return 0;
+    return bsa::layout(B, tokens, Hq / Hkv, D).bytes;
+}
+
+int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const bsa_page_scales* scales,
+                        void* workspace, int64_t workspace_bytes, bsa_stream_t stream) {
+    using namespace bsa;
+    if (!a) return BSA_ERR_INVALID_ARG;
+    int st = check_page_cache(c);
+    if (st != BSA_OK) return st;
+    if (scales && (st = check_page_scales(c, scales)) != BSA_OK) return st;
+    if (a->B < 0 || a->tokens < 0 || a->Hq <= 0 || a->Hq % c->Hkv || c->layers != 1 || c->n_seqs != a->B)
+        return BSA_ERR_INVALID_ARG;
+    if (!a->q_ptr && a->tokens != a->B) return BSA_ERR_INVALID_ARG;
+    if (a->window < 0 || a->sinks < 0 || !(a->scale > 0.f) || !std::isfinite(a->scale)) return BSA_ERR_INVALID_ARG;
+    if (!al(a->q, 16) || !al(a->out, 16) || !al(a->lse, 4) || !al(a->context_len, 4) || !al(a->q_ptr, 4))
+        return BSA_ERR_INVALID_ARG;
+    if (a->Hq / c->Hkv > 128) return BSA_ERR_UNSUPPORTED;
+    if (a->B > 0 && a->tokens > 0 && (!a->q || !a->context_len || !a->out || !a->lse || !c->page_table))
+        return BSA_ERR_INVALID_ARG;
+    if (a->B == 0 || a->tokens == 0) return BSA_OK;
+    const int G = a->Hq / c->Hkv;
+    const Layout w = layout(a->B, a->tokens, G, c->D);
+    // the steps of the chunks stay below 2^30 (sums and range ends fit an int)
+    const int64_t most = ((int64_t)c->max_pages * c->page + kTile - 1) / kTile;
+    if (c->Hkv * most > 1 << 30 || (w.cap > 0 && w.cap * (double)most * c->Hkv > (double)(1 << 30)))
+        return BSA_ERR_INVALID_ARG;
+    if (!workspace || !al(workspace, 256)) return BSA_ERR_INVALID_ARG;
+    if (workspace_bytes < w.bytes) return BSA_ERR_CAPACITY;
+    ChunkCommon p{};
+    int sms;
+    if ((st = device_context(&p.err, &sms)) != BSA_OK) return st;
+    p.ctx = a->context_len;
+    p.q_ptr = a->q_ptr;
+    p.table = c->page_table;
+    p.ks = scales ? static_cast<const uint8_t*>(scales->k) : nullptr;
+    p.vs = scales ? static_cast<const uint8_t*>(scales->v) : nullptr;
+    p.B = a->B;
+    p.tokens = a->tokens;
+    p.Hq = a->Hq;
+    p.Hkv = c->Hkv;
+    p.G = G;
+    p.page = c->page;
+    p.P = c->max_pages;
+    p.n_pages = c->n_pages;
+    p.window = a->window;
+    p.sinks = a->sinks;
+    p.out = a->out;
+    p.lse = a->lse;
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.wait_limit_ns = wait_limit_ns();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    // single tokens of more heads than a short sequence's rows are chunks too
+    if (G <= kShortRows) {
+        ShortLaunch L{};
+        L.c = p;
+        L.k = c->k;
+        L.v = c->v;
+        L.q = a->q;
+        L.D = c->D;
+        L.sms = sms;
+        L.meta = reinterpret_cast<PartMeta*>(ws + w.short_meta);
+        L.part_o = reinterpret_cast<float*>(ws + w.short_o);
+        L.part_ml = reinterpret_cast<float2*>(ws + w.short_ml);
+        if ((st = launch_short(L, s)) != BSA_OK) return st;
+        if (!a->q_ptr || (int64_t)a->tokens * G <= kShortRows) return BSA_OK;  // there is no other sequence
+    }
+    ChunkParams cp{};
+    cp.c = p;
+    cp.tq = tile_tokens(G);
+    cp.head = reinterpret_cast<const PlanHead*>(ws + w.head);
+    cp.groups = reinterpret_cast<const Group*>(ws + w.groups);
+    cp.meta = reinterpret_cast<PartMeta*>(ws + w.meta);
+    cp.part_o = reinterpret_cast<float*>(ws + w.o);
+    cp.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    CUtensorMap tq, tk, tv;
+    const uint64_t krows = (uint64_t)c->n_pages * c->Hkv * c->page;
+    auto encode = scales ? encode_rows_e4m3 : encode_rows_bf16;
+    if ((st = encode_token_rows_bf16(&tq, a->q, (uint64_t)a->tokens, a->Hq, c->D, G, cp.tq)) != BSA_OK) return st;
+    if ((st = encode(&tk, c->k, krows, c->D, c->page)) != BSA_OK) return st;
+    if ((st = encode(&tv, c->v, krows, c->D, c->page)) != BSA_OK) return st;
+    if (launch_after(plan_kernel, dim3(1), 1024, 0, s, p, reinterpret_cast<PlanHead*>(ws + w.head),
+                     reinterpret_cast<Group*>(ws + w.groups), w.cap, cp.tq) != cudaSuccess)
+        return BSA_ERR_CUDA;
+    const int ctas = std::min(sms, kChunkMaxCtas);
+    if (c->D == 128) return scales ? go<128, true>(tq, tk, tv, cp, ctas, s) : go<128, false>(tq, tk, tv, cp, ctas, s);
+    return scales ? go<64, true>(tq, tk, tv, cp, ctas, s) : go<64, false>(tq, tk, tv, cp, ctas, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,221 @@
+// bsa_chunk.cuh -- what the kernels of the attention of new tokens share: the
+// sequences, which tiles of slots they see, and how the parts of a row that
+// several CTAs worked on are handed to the merge.
+#pragma once
+
+#include <limits.h>
+#include <math.h>
+
+#include "bsa_internal.h"
+#include "bsa_ptx.cuh"
+
+namespace bsa {
+
+constexpr int kTile = 128;            // key slots of a step
+constexpr int kChunkMaxCtas = 160;    // parts are sized for this many
+constexpr int kShortRows = 16;        // query rows of a key head up to which a sequence is "short"
+
+struct ChunkCommon {
+    const int32_t *ctx, *q_ptr, *table;
+    const uint8_t *ks, *vs;           // 8-bit pools: the rows' scales
+    int32_t B, tokens, Hq, Hkv, G, page, P, n_pages;
+    int32_t window, sinks;
+    void* out;
+    float* lse;
+    int32_t* err;
+    float scale_log2;
+    unsigned long long wait_limit_ns;
+};
+
+// The item that a CTA's range of steps starts inside of (start < 0: none): its
+// first step and the one behind its last, the steps of a range, its rows.
+struct PartMeta {
+    int start, end, per;
+    int row0, n;   // first token (row of q) and tokens
+    int h;
+    int pad[2];
+};
+
+struct Seq {
+    int row0, n, ctx;
+};
+
+// New tokens of sequence b; none where q_ptr makes no sense or positions leave an int.
+__device__ __forceinline__ Seq sequence(const ChunkCommon& p, int b, bool report) {
+    Seq s{b, 1, max(p.ctx[b], 0)};
+    if (p.q_ptr) {
+        const int lo = p.q_ptr[b], hi = p.q_ptr[b + 1];
+        if (lo < 0 || hi < lo || hi > p.tokens) {
+            if (report) atomicOr(p.err, ERR_BAD_ROW);
+            return Seq{0, 0, 0};
+        }
+        s.row0 = lo;
+        s.n = hi - lo;
+    }
+    if (s.n > 0 && s.ctx > INT_MAX - 1024 - s.n) {
+        if (report) atomicOr(p.err, ERR_BAD_PAGE);
+        s.n = 0;
+    }
+    if (report && s.n > 0 && s.ctx + s.n > p.P * p.page) atomicOr(p.err, ERR_BAD_PAGE);
+    return s;
+}
+
+// Tiles of slots that the tokens in slots first .. end - 1 see: the sinks' and,
+// from lo_tile on, those of their windows.
+struct Span {
+    int sink_tiles, lo_tile, steps;
+    __device__ __forceinline__ int tile(int step) const {
+        return step < sink_tiles ? step : lo_tile + step - sink_tiles;
+    }
+};
+__device__ __forceinline__ int first_slot(const ChunkCommon& p, int first) {
+    return p.window > 0 ? max(0, first - p.window + 1) : 0;
+}
+__device__ __forceinline__ Span visible_span(const ChunkCommon& p, int first, int end) {
+    end = min(end, p.P * p.page);
+    Span s;
+    s.lo_tile = first_slot(p, first) / kTile;
+    const int tiles = (int)(((unsigned)end + kTile - 1) / kTile);
+    s.sink_tiles = p.window > 0 ? min((int)(((unsigned)min(p.sinks, end) + kTile - 1) / kTile), s.lo_tile) : 0;
+    // at least one, so that rows which see nothing pass through and write their zeros
+    s.steps = max(1, s.sink_tiles + max(0, tiles - s.lo_tile));
+    return s;
+}
+
+// Slots u that a token in slot pos sees among base .. base + 127, as bits of two words.
+struct Seen {
+    unsigned long long w[2];
+};
+__device__ __forceinline__ unsigned long long below(int n) {  // bits 0 .. n - 1
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+// have: bit h set where the tile's half h lies in a page.
+__device__ __forceinline__ Seen seen_slots(const ChunkCommon& p, int base, int pos, int have) {
+    Seen s;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int b = base + 64 * h;
+        unsigned long long m = below(pos + 1 - b);
+        if (p.window > 0) m &= ~below(max(pos - p.window + 1, 0) - b) | below(p.sinks - b);
+        s.w[h] = (have >> h) & 1 ? m : 0ull;
+    }
+    return s;
+}
+
+// Page j of sequence b for tokens that see from slot lo to slot end - 1 (and the
+// sinks): its first row in the pools, or -1 where nothing of it is seen or it is
+// not there (reported).
+__device__ __forceinline__ int page_row(const ChunkCommon& p, int b, int h, int j, int lo, int end) {
+    const unsigned s0 = (unsigned)j * p.page;
+    if (j >= p.P || s0 >= (unsigned)end) return -1;
+    if (s0 + p.page <= (unsigned)lo && !(p.window > 0 && s0 < (unsigned)p.sinks)) return -1;
+    const int pg = p.table[(int64_t)b * p.P + j];
+    if ((unsigned)pg >= (unsigned)p.n_pages) {
+        atomicOr(p.err, ERR_BAD_PAGE);
+        return -1;
+    }
+    return (pg * p.Hkv + h) * p.page;
+}
+
+// Natural-log LSE of a row from its reference (log2) and sum.
+__device__ __forceinline__ float lse_of(float m, float sum) {
+    return sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994531f;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile WaitFlag* wf) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, wf));
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, bytes % 16 == 0), counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+struct ShortLaunch {
+    ChunkCommon c;
+    const void *k, *v, *q;
+    int32_t D, sms;
+    PartMeta* meta;
+    float* part_o;
+    float2* part_ml;
+};
+// Sequences whose new tokens make at most kShortRows rows of a key head (csrc/bsa_decode.cu).
+int launch_short(const ShortLaunch& L, cudaStream_t s);
+
+// Joins the parts that the boundary in front of range x + 1 is the first to cut:
+// with parts i in range order, m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i /
+// sum w_i l_i.  A CTA takes RB rows, 8 / RB warps to a row (each every (8 / RB)-th
+// part).  Rows of an item: ROWS, in tiles of 128 with tq tokens of G rows each
+// (ROWS = 16: one tile).  Bound by dependent reads from the L2.
+template <int D, int ROWS, int RB>
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkCommon p, const PartMeta* meta, const float* part_o,
+                                                          const float2* part_ml, int tq) {
+    constexpr int WPR = 8 / RB, C = D / 32;
+    __shared__ float red[WPR > 1 ? WPR : 1][D + 1];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const PartMeta mt = meta[blockIdx.x + 1];
+    const int first = blockIdx.x;
+    if (mt.start < 0 || mt.start < first * mt.per) return;  // not cut here, or by an earlier boundary too
+    const int last = (mt.end - 1) / mt.per;
+    const int r = blockIdx.y * RB + warp / WPR, part = warp % WPR;
+    const int i = r & 127, t = (r >> 7) * tq + i / p.G;
+    const bool on = r < ROWS && i < tq * p.G && t < mt.n;
+    if (WPR == 1 && !on) return;
+    auto slot_of = [&](int k) { return 2 * k + (k == first && mt.start > first * mt.per ? 1 : 0); };
+    float m = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+    for (int x = 0; x < C; ++x) acc[x] = 0.f;
+    if (on) {
+        for (int k = first + lane; k <= last; k += 32) m = fmaxf(m, part_ml[(int64_t)slot_of(k) * ROWS + r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = m > -INFINITY ? m : 0.f;
+#pragma unroll 4
+        for (int k = first + part; k <= last; k += WPR) {
+            const int64_t pr = (int64_t)slot_of(k) * ROWS + r;
+            const float2 ml = part_ml[pr];
+            const float w = ex2_approx(ml.x - ref);  // 0 for a part that saw nothing
+            l += w * ml.y;
+            const float* src = part_o + pr * D + lane * C;
+            if (C == 4) {
+                const float4 o = *reinterpret_cast<const float4*>(src);
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
+                acc[C - 2] += w * o.z;
+                acc[C - 1] += w * o.w;
+            } else {
+                const float2 o = *reinterpret_cast<const float2*>(src);
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
+            }
+        }
+    }
+    if (WPR > 1) {
+#pragma unroll
+        for (int x = 0; x < C; ++x) red[part][lane * C + x] = acc[x];
+        if (lane == 0) red[part][D] = l;
+        __syncthreads();
+        if (part > 0 || !on) return;
+        for (int w = 1; w < WPR; ++w) {
+#pragma unroll
+            for (int x = 0; x < C; ++x) acc[x] += red[w][lane * C + x];
+            l += red[w][D];
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t orow = (int64_t)(mt.row0 + t) * p.Hq + mt.h * p.G + i % p.G;
+    if (lane == 0) p.lse[orow] = lse_of(m, l);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D;
+    if (C == 4)
+        reinterpret_cast<uint2*>(out)[lane] =
+            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[C - 2] * inv, acc[C - 1] * inv));
+    else
+        reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+}
+
+}  // namespace bsa

@@ -42,8 +42,12 @@ cudaError_t raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t
 // table is checked by the calls that read one; no sequences pass: what that
 // means is theirs too).
 int check_page_cache(const bsa_page_cache* c);
+// The scales of an 8-bit cache that check_page_cache has passed.
+int check_page_scales(const bsa_page_cache* c, const bsa_page_scales* s);
 // 2-D bf16 view [rows, D] in boxes of 64 columns x box_rows rows, 128-byte swizzle.
 int encode_rows_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows);
+// The same of e4m3 rows: whole rows of D bytes, D-byte swizzle (64 or 128).
+int encode_rows_e4m3(CUtensorMap* m, const void* base, uint64_t rows, uint64_t D, uint32_t box_rows);
 // 3-D bf16 view [tokens, heads, D] in boxes of 64 columns x box_heads x box_tokens, 128-byte swizzle.
 int encode_token_rows_bf16(CUtensorMap* m, const void* base, uint64_t tokens, uint64_t heads, uint64_t D,
                            uint32_t box_heads, uint32_t box_tokens);

@@ -27,6 +27,7 @@
 #include "bsa.h"
 #include "bsa_internal.h"
 #include "bsa_ptx.cuh"
+#include "bsa_q8.cuh"
 
 namespace bsa {
 namespace {
@@ -70,6 +71,7 @@ struct RopeParams {
     float eps, gain;
     // append: rows of k and v go to pages
     void *k_cache, *v_cache;
+    uint8_t *k_scale, *v_scale;  // 8-bit pools: a scale per row
     const int32_t *page_table, *seq_ids, *slots;
     int32_t n_seqs, max_pages, page, n_pages;
     int32_t* err;
@@ -178,11 +180,11 @@ __device__ __forceinline__ int cta_side(const RopeParams& p, int* idx) {
     return k;
 }
 
-// The lane's two chunks of a row, normed and rotated in place.
+// The lane's two chunks of a row, normed and rotated, in fp32.
 template <int D, bool IL>
-__device__ __forceinline__ void norm_rotate(uint4& a, uint4& b, bool norm, const f2* w, float eps, bool turn,
-                                            const f2* cs, const f2* sn, const Lane<D, IL>& ln) {
-    f2 f[8];
+__device__ __forceinline__ void norm_rotate_f32(const uint4& a, const uint4& b, f2 (&f)[8], bool norm, const f2* w,
+                                                float eps, bool turn, const f2* cs, const f2* sn,
+                                                const Lane<D, IL>& ln) {
     unpack8(a, f);
     unpack8(b, f + 4);
     if (norm) {
@@ -194,8 +196,35 @@ __device__ __forceinline__ void norm_rotate(uint4& a, uint4& b, bool norm, const
         for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2({r, r}, w[e]));
     }
     if (turn) rotate16<IL>(f, cs, sn, ln.ra, ln.rb);
+}
+
+// The same in place, rounded to bf16.
+template <int D, bool IL>
+__device__ __forceinline__ void norm_rotate(uint4& a, uint4& b, bool norm, const f2* w, float eps, bool turn,
+                                            const f2* cs, const f2* sn, const Lane<D, IL>& ln) {
+    f2 f[8];
+    norm_rotate_f32<D, IL>(a, b, f, norm, w, eps, turn, cs, sn, ln);
     a = pack8(f);
     b = pack8(f + 4);
+}
+
+// Scale exponent of the row whose 16 values each of LPR lanes hold, and the
+// lane's codes, eight bytes for each chunk: one rounding from the fp32 values.
+template <int LPR>
+__device__ __forceinline__ int quantise16(const f2 (&f)[8], uint2& a, uint2& b) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmax3(m, fabsf(f[e].x), fabsf(f[e].y));
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int ex = row_exponent(m);
+    const float inv = exp2_int(-ex);
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = e4m3x2(f[e].x * inv, f[e].y * inv);
+    a = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    b = make_uint2(h[4] | h[5] << 16, h[6] | h[7] << 16);
+    return ex;
 }
 
 // One CTA item: TB = 256 / LPR consecutive tokens times U heads.  A lane
@@ -291,7 +320,7 @@ __global__ void __launch_bounds__(kRopeThreads, U == 1 ? 3 : 2) norm_rope_kernel
 // traffic, not a fifth: 32K tokens of 48 heads of 128 (805 MB) 159 us with the
 // forward's loop, 132 with this one, 6.1 TB/s (the forward 130 with its own, 151
 // with this one); 2,048 tokens 14.0 and 12.9, one token 2.8 and 2.4.
-template <int D, int U, bool IL>
+template <int D, int U, bool IL, bool Q8>
 __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_append_kernel(const RopeParams p) {
     constexpr int LPR = D / 16, TB = kRopeThreads / LPR;
     __shared__ unsigned long long turns[kMaxPairs];
@@ -342,8 +371,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_append_kernel(const
             b[u] = on ? src[ln.cb] : make_uint4(0, 0, 0, 0);
         }
     };
-    // where the row goes: base of head 0 and distance between heads, in 16-byte chunks
+    // where the row goes: base of head 0 and distance between heads, in chunks
+    // (16 bytes; rows of an 8-bit pool: 8)
     uint4* dst = nullptr;
+    uint8_t* dscale = nullptr;  // 8-bit pools: the scale of head 0
     int64_t dh = 0;
     f2 cs[4], sn[4];
     const bool turn = sd.rotate && (ln.ra || ln.rb);
@@ -359,9 +390,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_append_kernel(const
             if (t.seq < p.n_seqs && t.slot >= 0 && t.slot / p.page < p.max_pages)
                 pg = p.page_table[(int64_t)t.seq * p.max_pages + t.slot / p.page];
             if ((unsigned)pg < (unsigned)p.n_pages) {
-                dst = reinterpret_cast<uint4*>(kind == 1 ? p.k_cache : p.v_cache) +
-                      ((int64_t)pg * sd.H * p.page + t.slot % p.page) * (D / 8);
+                const int64_t row = (int64_t)pg * sd.H * p.page + t.slot % p.page;
                 dh = (int64_t)p.page * (D / 8);
+                if (Q8) {
+                    dst = reinterpret_cast<uint4*>(reinterpret_cast<uint2*>(kind == 1 ? p.k_cache : p.v_cache) +
+                                                   row * (D / 8));
+                    dscale = (kind == 1 ? p.k_scale : p.v_scale) + row;
+                } else {
+                    dst = reinterpret_cast<uint4*>(kind == 1 ? p.k_cache : p.v_cache) + row * (D / 8);
+                }
             } else if (ln.s == 0) {
                 atomicOr(p.err, ERR_BAD_PAGE);
             }
@@ -398,6 +435,24 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_append_kernel(const
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             uint4 oa = ra[u], ob = rb[u];
+            if (Q8 && kind > 0) {
+                f2 f[8];
+                if (sd.rotate) {
+                    norm_rotate_f32<D, IL>(oa, ob, f, norm, w, p.eps, turn, cs, sn, ln);
+                } else {
+                    unpack8(oa, f);
+                    unpack8(ob, f + 4);
+                }
+                uint2 qa, qb;
+                const int ex = quantise16<LPR>(f, qa, qb);
+                if (dst && hg * U + u < sd.H) {
+                    uint2* d = reinterpret_cast<uint2*>(dst) + (hg * U + u) * dh;
+                    d[ln.ca] = qa;
+                    d[ln.cb] = qb;
+                    if (ln.s == 0) dscale[(int64_t)(hg * U + u) * p.page] = (uint8_t)(ex + 127);
+                }
+                continue;
+            }
             if (sd.rotate) norm_rotate<D, IL>(oa, ob, norm, w, p.eps, turn, cs, sn, ln);
             if (dst && hg * U + u < sd.H) {
                 uint4* d = dst + (hg * U + u) * dh;
@@ -704,14 +759,14 @@ void deal_ctas(RopeParams* p, int D, int U, int ctas, const double* bytes) {
 
 constexpr int kRopeMaxCtas = 1024;  // the gradients' CTAs are held to this: rows of the workspace a kind has
 
-template <bool APPEND>
+template <bool APPEND, bool Q8 = false>
 cudaError_t launch_fwd(const RopeParams& p, int D, int U, bool il, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.side[0].ctas + p.side[1].ctas + p.side[2].ctas);
     auto go = [&](auto kern) { return launch_after(kern, dim3(grid), kRopeThreads, 0, s, p); };
     auto pick = [&](auto d, auto u) {
         if constexpr (APPEND)
-            return il ? go(norm_rope_append_kernel<d.value, u.value, true>)
-                      : go(norm_rope_append_kernel<d.value, u.value, false>);
+            return il ? go(norm_rope_append_kernel<d.value, u.value, true, Q8>)
+                      : go(norm_rope_append_kernel<d.value, u.value, false, Q8>);
         else
             return il ? go(norm_rope_kernel<d.value, u.value, true>) : go(norm_rope_kernel<d.value, u.value, false>);
     };
@@ -840,6 +895,46 @@ int fill(const bsa_norm_rope_args* a, RopeParams* p) {
     return BSA_OK;
 }
 
+// Appending to bf16 pools, or (scales) 8-bit ones.
+int append(const bsa_norm_rope_args* a, const bsa_page_cache* c, const bsa_page_scales* scales, const int32_t* seq_ids,
+           const int32_t* slots, void* q_out, cudaStream_t stream) {
+    RopeParams p{};
+    int st = fill(a, &p);
+    if (st != BSA_OK) return st;
+    if ((st = check_page_cache(c)) != BSA_OK) return st;
+    if (scales && (st = check_page_scales(c, scales)) != BSA_OK) return st;
+    if (a->B != 1 || a->kv_repeat != 1 || c->layers != 1 || c->Hkv != a->Hkv || c->D != a->D)
+        return BSA_ERR_INVALID_ARG;
+    if (p.tokens == 0) return BSA_OK;
+    if (c->n_seqs == 0) return BSA_ERR_INVALID_ARG;  // tokens of no sequence
+    if (!a->q || !a->k || !a->v || !q_out || !seq_ids || !slots || !c->page_table) return BSA_ERR_INVALID_ARG;
+    if (!al(q_out, 16) || !al(seq_ids, 4) || !al(slots, 4)) return BSA_ERR_INVALID_ARG;
+    int sms;
+    if ((st = device_context(&p.err, &sms)) != BSA_OK) return st;
+    p.side[0].out = q_out;
+    p.k_cache = c->k;
+    p.v_cache = c->v;
+    if (scales) {
+        p.k_scale = static_cast<uint8_t*>(scales->k);
+        p.v_scale = static_cast<uint8_t*>(scales->v);
+    }
+    p.page_table = c->page_table;
+    p.seq_ids = seq_ids;
+    p.slots = slots;
+    p.n_seqs = c->n_seqs;
+    p.max_pages = c->max_pages;
+    p.page = c->page;
+    p.n_pages = c->n_pages;
+    // K and V: 1.2 for their pages' look-up (32K tokens of 64 + 1 heads 203 -> 192 us, of 32 + 8 133 -> 131)
+    const double bytes[3] = {(double)a->Hq, 1.2 * a->Hkv, 1.2 * a->Hkv};
+    const int U = pick_heads(p.tokens, a->D, a->Hq, a->Hkv, kAppendRows, sms);
+    const int waves = append_waves(p.tokens, a->D, a->Hq, a->Hkv, U, sms);
+    deal_ctas(&p, a->D, U, waves * sms, bytes);
+    const cudaError_t e = scales ? launch_fwd<true, true>(p, a->D, U, a->interleaved != 0, stream)
+                                 : launch_fwd<true>(p, a->D, U, a->interleaved != 0, stream);
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace bsa
 
@@ -898,36 +993,13 @@ int bsa_qk_norm_rope(const bsa_norm_rope_args* a, void* q_out, void* k_out, void
 
 int bsa_cache_append(const bsa_norm_rope_args* a, const bsa_page_cache* c, const int32_t* seq_ids,
                      const int32_t* slots, void* q_out, bsa_stream_t stream) {
-    bsa::RopeParams p{};
-    int st = bsa::fill(a, &p);
-    if (st != BSA_OK) return st;
-    if ((st = bsa::check_page_cache(c)) != BSA_OK) return st;
-    if (a->B != 1 || a->kv_repeat != 1 || c->layers != 1 || c->Hkv != a->Hkv || c->D != a->D)
-        return BSA_ERR_INVALID_ARG;
-    if (p.tokens == 0) return BSA_OK;
-    if (c->n_seqs == 0) return BSA_ERR_INVALID_ARG;  // tokens of no sequence
-    if (!a->q || !a->k || !a->v || !q_out || !seq_ids || !slots || !c->page_table) return BSA_ERR_INVALID_ARG;
-    if (!bsa::al(q_out, 16) || !bsa::al(seq_ids, 4) || !bsa::al(slots, 4)) return BSA_ERR_INVALID_ARG;
-    int sms;
-    if ((st = bsa::device_context(&p.err, &sms)) != BSA_OK) return st;
-    p.side[0].out = q_out;
-    p.k_cache = c->k;
-    p.v_cache = c->v;
-    p.page_table = c->page_table;
-    p.seq_ids = seq_ids;
-    p.slots = slots;
-    p.n_seqs = c->n_seqs;
-    p.max_pages = c->max_pages;
-    p.page = c->page;
-    p.n_pages = c->n_pages;
-    // K and V: 1.2 for their pages' look-up (32K tokens of 64 + 1 heads 203 -> 192 us, of 32 + 8 133 -> 131)
-    const double bytes[3] = {(double)a->Hq, 1.2 * a->Hkv, 1.2 * a->Hkv};
-    const int U = bsa::pick_heads(p.tokens, a->D, a->Hq, a->Hkv, bsa::kAppendRows, sms);
-    const int waves = bsa::append_waves(p.tokens, a->D, a->Hq, a->Hkv, U, sms);
-    bsa::deal_ctas(&p, a->D, U, waves * sms, bytes);
-    const cudaError_t e =
-        bsa::launch_fwd<true>(p, a->D, U, a->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    return bsa::append(a, c, nullptr, seq_ids, slots, q_out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int bsa_cache_append_fp8(const bsa_norm_rope_args* a, const bsa_page_cache* c, const bsa_page_scales* scales,
+                         const int32_t* seq_ids, const int32_t* slots, void* q_out, bsa_stream_t stream) {
+    if (!scales) return BSA_ERR_INVALID_ARG;
+    return bsa::append(a, c, scales, seq_ids, slots, q_out, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int64_t bsa_qk_norm_rope_backward_workspace(int32_t D) {

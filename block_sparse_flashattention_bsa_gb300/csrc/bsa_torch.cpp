@@ -302,14 +302,36 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* o, Py_ssize_t n) {
 }
 
 // ------------------------------------------------------------ paged cache
-bsa_page_cache pool(T kc, T vc, T table, bool layers) {
+// The scales of 8-bit pools (`given` false: bf16 pools).
+struct Scales {
+    bsa_page_scales s{};
+    bool given = false;
+    const bsa_page_scales* ptr() const { return given ? &s : nullptr; }
+};
+
+bsa_page_cache pool(T kc, T vc, T table, bool layers, T ks, T vs, Scales* scales) {
     const int64_t nd = kc->dim();
     want(kc->sizes() == vc->sizes() && (nd == 4 || (layers && nd == 5)),
          layers ? "expected k_cache and v_cache of one shape [n_pages, Hkv, page, D] or [layers, n_pages, Hkv, page, D]"
                 : "expected k_cache and v_cache of one shape [n_pages, Hkv, page, D]");
-    want(kc->scalar_type() == at::kBFloat16 && vc->scalar_type() == at::kBFloat16 && kc->is_contiguous() &&
-             vc->is_contiguous(),
-         "expected contiguous bf16 caches");
+    want((ks != nullptr) == (vs != nullptr), "k_scale and v_scale come together");
+    scales->given = ks != nullptr;
+    if (scales->given) {
+        auto codes = [](T t) { return t->scalar_type() == at::kFloat8_e4m3fn || t->scalar_type() == at::kByte; };
+        auto exps = [&](T t) {
+            return (t->scalar_type() == at::kFloat8_e8m0fnu || t->scalar_type() == at::kByte) && t->is_contiguous() &&
+                   t->sizes() == kc->sizes().slice(0, nd - 1);
+        };
+        want(codes(kc) && codes(vc) && kc->is_contiguous() && vc->is_contiguous(),
+             "caches with scales: contiguous float8_e4m3fn (or uint8 codes)");
+        want(exps(ks) && exps(vs), "k_scale, v_scale: contiguous float8_e8m0fnu (or uint8) of the caches' shape without D");
+        scales->s.k = ks->data_ptr();
+        scales->s.v = vs->data_ptr();
+    } else {
+        want(kc->scalar_type() == at::kBFloat16 && vc->scalar_type() == at::kBFloat16 && kc->is_contiguous() &&
+                 vc->is_contiguous(),
+             "expected contiguous bf16 caches");
+    }
     want(table->scalar_type() == at::kInt && table->dim() == 2 && table->is_contiguous(),
          "page_table: contiguous int32 [n_seqs, max_pages]");
     bsa_page_cache c{};
@@ -326,21 +348,25 @@ bsa_page_cache pool(T kc, T vc, T table, bool layers) {
     return c;
 }
 
-// side arguments (11), k_cache, v_cache, page_table, seq_ids, slots, out
+// side arguments (11), k_cache, v_cache, page_table, seq_ids, slots, out, k_scale, v_scale
 PyObject* cache_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
-    return guarded(n, 17, [&]() -> PyObject* {
+    return guarded(n, 19, [&]() -> PyObject* {
         Side s = side(o, false);
         T kc = tensor(o[11], "k_cache"), vc = tensor(o[12], "v_cache"), table = tensor(o[13], "page_table");
         T seq = tensor(o[14], "seq_ids"), slot = tensor(o[15], "slots");
-        const bsa_page_cache c = pool(kc, vc, table, false);
-        same_device(s.q, {kc, vc, table, seq, slot});
+        T ks = tensor_or_none(o[17], "k_scale"), vs = tensor_or_none(o[18], "v_scale");
+        Scales sc;
+        const bsa_page_cache c = pool(kc, vc, table, false, ks, vs, &sc);
+        same_device(s.q, {kc, vc, table, seq, slot, ks, vs});
         want(s.v && c.Hkv == s.Hkv && c.D == s.D, "k and v need the cache's heads and head size");
         ints(seq, {s.N}, "seq_ids");
         ints(slot, {s.N}, "slots");
         const c10::cuda::CUDAGuard guard(s.dev);
         const int64_t shape[3] = {s.N, s.Hq, s.D};
         at::Tensor q = output(tensor_or_none(o[16], "out"), shape, s.dev);
-        const int st = bsa_cache_append(&s.a, &c, data<int32_t>(seq), data<int32_t>(slot), q.data_ptr(), current_stream(s.dev));
+        const bsa_stream_t on = current_stream(s.dev);
+        const int st = sc.given ? bsa_cache_append_fp8(&s.a, &c, &sc.s, data<int32_t>(seq), data<int32_t>(slot), q.data_ptr(), on)
+                                : bsa_cache_append(&s.a, &c, data<int32_t>(seq), data<int32_t>(slot), q.data_ptr(), on);
         return st ? status(st) : wrap(q);
     });
 }
@@ -354,7 +380,8 @@ PyObject* tree_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
         T out = tensor_or_none(o[10], "out"), lse = tensor_or_none(o[11], "lse");
         want(q->dim() == 4 && q->scalar_type() == at::kBFloat16 && q->is_contiguous(), "q: contiguous bf16 [B, T, Hq, D]");
         const int64_t B = q->size(0), Tn = q->size(1), Hq = q->size(2), D = q->size(3);
-        const bsa_page_cache c = pool(kc, vc, table, false);
+        Scales sc;
+        const bsa_page_cache c = pool(kc, vc, table, false, nullptr, nullptr, &sc);
         const c10::Device dev = same_device(q, {kc, vc, table, ctx, dl, mask, rp, ci, out, lse});
         want(c.n_seqs == B && c.D == D, "page_table needs one row per sequence, the caches q's head size");
         ints(ctx, {B}, "context_len");
@@ -395,14 +422,15 @@ PyObject* tree_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
     });
 }
 
-// k_cache, v_cache, page_table, context_len, accepted, n_accepted, new_len
+// k_cache, v_cache, page_table, context_len, accepted, n_accepted, new_len, k_scale, v_scale
 PyObject* cache_accept(PyObject*, PyObject* const* o, Py_ssize_t n) {
-    return guarded(n, 7, [&]() -> PyObject* {
+    return guarded(n, 9, [&]() -> PyObject* {
         T kc = tensor(o[0], "k_cache"), vc = tensor(o[1], "v_cache"), table = tensor(o[2], "page_table");
         T ctx = tensor(o[3], "context_len"), acc = tensor(o[4], "accepted"), na = tensor(o[5], "n_accepted");
-        T given = tensor_or_none(o[6], "new_len");
-        const bsa_page_cache c = pool(kc, vc, table, true);
-        const c10::Device dev = same_device(kc, {vc, table, ctx, acc, na, given});
+        T given = tensor_or_none(o[6], "new_len"), ks = tensor_or_none(o[7], "k_scale"), vs = tensor_or_none(o[8], "v_scale");
+        Scales sc;
+        const bsa_page_cache c = pool(kc, vc, table, true, ks, vs, &sc);
+        const c10::Device dev = same_device(kc, {vc, table, ctx, acc, na, given, ks, vs});
         want(acc->dim() == 2, "accepted: int32 [n_seqs, T]");
         const int64_t S = c.n_seqs, Tn = acc->size(1);
         ints(ctx, {S}, "context_len");
@@ -411,20 +439,25 @@ PyObject* cache_accept(PyObject*, PyObject* const* o, Py_ssize_t n) {
         if (given) ints(given, {S}, "new_len");
         const c10::cuda::CUDAGuard guard(dev);
         at::Tensor r = given ? *given : new_tensor({S}, at::kInt, dev);
-        const int st = bsa_cache_accept(&c, data<int32_t>(ctx), data<int32_t>(acc), data<int32_t>(na), size32(Tn),
-                                        r.data_ptr<int32_t>(), current_stream(dev));
+        const int32_t *x = data<int32_t>(ctx), *y = data<int32_t>(acc), *z = data<int32_t>(na), t = size32(Tn);
+        const bsa_stream_t on = current_stream(dev);
+        const int st = sc.given ? bsa_cache_accept_fp8(&c, &sc.s, x, y, z, t, r.data_ptr<int32_t>(), on)
+                                : bsa_cache_accept(&c, x, y, z, t, r.data_ptr<int32_t>(), on);
         return st ? status(st) : wrap(r);
     });
 }
 
-// fork (True or False), page_table, page_ref, three request vectors (in the C call's order), k_cache, v_cache
+// fork (True or False), page_table, page_ref, three request vectors (in the C call's order), k_cache, v_cache,
+// k_scale, v_scale
 PyObject* cache_request(PyObject*, PyObject* const* o, Py_ssize_t n) {
-    return guarded(n, 8, [&]() -> PyObject* {
+    return guarded(n, 10, [&]() -> PyObject* {
         const bool fork = bool_arg(o[0]);
         T table = tensor(o[1], "page_table"), ref = tensor(o[2], "page_ref"), kc = tensor(o[6], "k_cache"), vc = tensor(o[7], "v_cache");
         T r[3] = {tensor(o[3], "requests"), tensor(o[4], "requests"), tensor(o[5], "requests")};
-        const bsa_page_cache c = pool(kc, vc, table, true);
-        const c10::Device dev = same_device(kc, {vc, table, ref, r[0], r[1], r[2]});
+        T ks = tensor_or_none(o[8], "k_scale"), vs = tensor_or_none(o[9], "v_scale");
+        Scales sc;
+        const bsa_page_cache c = pool(kc, vc, table, true, ks, vs, &sc);
+        const c10::Device dev = same_device(kc, {vc, table, ref, r[0], r[1], r[2], ks, vs});
         ints(ref, {c.n_pages}, "page_ref");
         const int64_t N = r[0]->numel();
         for (T t : r) ints(t, {N}, "requests");
@@ -433,34 +466,120 @@ PyObject* cache_request(PyObject*, PyObject* const* o, Py_ssize_t n) {
         if (N == 0) return wrap(granted);
         const int64_t bytes = bsa_cache_pages_workspace(size32(N), c.n_seqs, c.n_pages);
         at::Tensor ws = new_tensor({bytes}, at::kByte, dev);
-        const int st = (fork ? bsa_cache_fork : bsa_cache_resize)(&c, data<int32_t>(ref), (int32_t)N, data<int32_t>(r[0]),
-                                                                  data<int32_t>(r[1]), data<int32_t>(r[2]),
-                                                                  granted.data_ptr<int32_t>(), ws.data_ptr(), bytes,
-                                                                  current_stream(dev));
+        const int32_t *x = data<int32_t>(r[0]), *y = data<int32_t>(r[1]), *z = data<int32_t>(r[2]);
+        int32_t *rc = data<int32_t>(ref), *got = granted.data_ptr<int32_t>();
+        const bsa_stream_t on = current_stream(dev);
+        const int st =
+            sc.given ? (fork ? bsa_cache_fork_fp8 : bsa_cache_resize_fp8)(&c, &sc.s, rc, (int32_t)N, x, y, z, got,
+                                                                          ws.data_ptr(), bytes, on)
+                     : (fork ? bsa_cache_fork : bsa_cache_resize)(&c, rc, (int32_t)N, x, y, z, got, ws.data_ptr(), bytes, on);
         return st ? status(st) : wrap(granted);
     });
 }
 
-// page_table, page_ref, k_cache, v_cache
+// page_table, page_ref, k_cache, v_cache, k_scale, v_scale
 PyObject* cache_compact(PyObject*, PyObject* const* o, Py_ssize_t n) {
-    return guarded(n, 4, [&]() -> PyObject* {
+    return guarded(n, 6, [&]() -> PyObject* {
         T table = tensor(o[0], "page_table"), ref = tensor(o[1], "page_ref"), kc = tensor(o[2], "k_cache"), vc = tensor(o[3], "v_cache");
-        const bsa_page_cache c = pool(kc, vc, table, true);
-        const c10::Device dev = same_device(kc, {vc, table, ref});
+        T ks = tensor_or_none(o[4], "k_scale"), vs = tensor_or_none(o[5], "v_scale");
+        Scales sc;
+        const bsa_page_cache c = pool(kc, vc, table, true, ks, vs, &sc);
+        const c10::Device dev = same_device(kc, {vc, table, ref, ks, vs});
         ints(ref, {c.n_pages}, "page_ref");
         const c10::cuda::CUDAGuard guard(dev);
         at::Tensor r = new_tensor({c.n_pages}, at::kInt, dev);
         const int64_t bytes = bsa_cache_pages_workspace(0, c.n_seqs, c.n_pages);
         at::Tensor ws = new_tensor({bytes}, at::kByte, dev);
-        const int st = bsa_cache_compact(&c, data<int32_t>(ref), r.data_ptr<int32_t>(), ws.data_ptr(), bytes, current_stream(dev));
+        int32_t *rc = data<int32_t>(ref), *to = r.data_ptr<int32_t>();
+        const bsa_stream_t on = current_stream(dev);
+        const int st = sc.given ? bsa_cache_compact_fp8(&c, &sc.s, rc, to, ws.data_ptr(), bytes, on)
+                                : bsa_cache_compact(&c, rc, to, ws.data_ptr(), bytes, on);
         return st ? status(st) : wrap(r);
+    });
+}
+
+// k_cache, v_cache, page_table, seq_ids, lens or None, n, first or None, kv_repeat, k_scale, v_scale, out k, out v
+PyObject* cache_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        T kc = tensor(o[0], "k_cache"), vc = tensor(o[1], "v_cache"), table = tensor(o[2], "page_table");
+        T seq = tensor(o[3], "seq_ids"), len = tensor_or_none(o[4], "lens"), first = tensor_or_none(o[6], "first");
+        T ks = tensor_or_none(o[8], "k_scale"), vs = tensor_or_none(o[9], "v_scale");
+        T ok = tensor_or_none(o[10], "out"), ov = tensor_or_none(o[11], "out");
+        Scales sc;
+        const bsa_page_cache c = pool(kc, vc, table, false, ks, vs, &sc);
+        const c10::Device dev = same_device(kc, {vc, table, seq, len, first, ks, vs, ok, ov});
+        bsa_read_args a{};
+        const int64_t R = seq->numel();
+        a.R = size32(R);
+        a.n = int_arg(o[5], "n");
+        a.kv_repeat = int_arg(o[7], "kv_repeat");
+        ints(seq, {R}, "seq_ids");
+        if (len) ints(len, {R}, "lens");
+        if (first) ints(first, {R}, "first");
+        if (a.n < 0 || a.kv_repeat < 1) return status(BSA_ERR_INVALID_ARG);
+        want((ok != nullptr) == (ov != nullptr), "out: both tensors or none");
+        const c10::cuda::CUDAGuard guard(dev);
+        const int64_t shape[4] = {R, (int64_t)c.Hkv * a.kv_repeat, a.n, c.D};
+        at::Tensor k = output(ok, shape, dev), v = output(ov, shape, dev);
+        a.seq_ids = data<int32_t>(seq);
+        a.len = data<int32_t>(len);
+        a.first = data<int32_t>(first);
+        a.k = k.data_ptr();
+        a.v = v.data_ptr();
+        const int st = bsa_cache_read(&a, &c, sc.ptr(), current_stream(dev));
+        return st ? status(st) : wrap_all({k, v});
+    });
+}
+
+// q, k_cache, v_cache, page_table, context_len, q_ptr or None, window, sinks, k_scale, v_scale, scale or None, out, lse
+PyObject* chunk_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject* {
+        T q = tensor(o[0], "q"), kc = tensor(o[1], "k_cache"), vc = tensor(o[2], "v_cache"), table = tensor(o[3], "page_table");
+        T ctx = tensor(o[4], "context_len"), qp = tensor_or_none(o[5], "q_ptr");
+        T ks = tensor_or_none(o[8], "k_scale"), vs = tensor_or_none(o[9], "v_scale");
+        T out = tensor_or_none(o[11], "out"), lse = tensor_or_none(o[12], "lse");
+        want(q->dim() == 3 && q->scalar_type() == at::kBFloat16 && q->is_contiguous(), "q: contiguous bf16 [tokens, Hq, D]");
+        const int64_t N = q->size(0), Hq = q->size(1), D = q->size(2);
+        Scales sc;
+        const bsa_page_cache c = pool(kc, vc, table, false, ks, vs, &sc);
+        const c10::Device dev = same_device(q, {kc, vc, table, ctx, qp, ks, vs, out, lse});
+        want(c.D == D, "the caches need q's head size");
+        const int64_t B = c.n_seqs;
+        ints(ctx, {B}, "context_len");
+        if (qp) ints(qp, {B + 1}, "q_ptr");
+        want(qp || N == B, "q_ptr: needed where the sequences do not bring one token each");
+        bsa_chunk_args a{};
+        a.B = size32(B);
+        a.tokens = size32(N);
+        a.Hq = size32(Hq);
+        a.window = int_arg(o[6], "window");
+        a.sinks = int_arg(o[7], "sinks");
+        a.scale = o[10] == Py_None ? (float)(1.0 / std::sqrt((double)std::max<int64_t>(D, 1))) : float_arg(o[10]);
+        const c10::cuda::CUDAGuard guard(dev);
+        at::Tensor r = output(out, q->sizes(), dev), l;
+        if (lse) {
+            ints(lse, {N, Hq}, "lse", at::kFloat);
+            l = *lse;
+        } else {
+            l = new_tensor({N, Hq}, at::kFloat, dev);
+        }
+        const int64_t bytes = bsa_chunk_attention_workspace(a.B, a.tokens, a.Hq, c.Hkv, c.D);
+        at::Tensor ws = new_tensor({bytes}, at::kByte, dev);
+        a.q = q->data_ptr();
+        a.q_ptr = data<int32_t>(qp);
+        a.context_len = data<int32_t>(ctx);
+        a.out = r.data_ptr();
+        a.lse = l.data_ptr<float>();
+        const int st = bsa_chunk_attention(&a, &c, sc.ptr(), ws.data_ptr(), bytes, current_stream(dev));
+        return st ? status(st) : wrap_all({r, l});
     });
 }
 
 #define CALL(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {CALL(qk_norm_rope),  CALL(qk_norm_rope_backward), CALL(cache_append),
                           CALL(tree_attention), CALL(cache_accept),         CALL(cache_request),
-                          CALL(cache_compact),  {nullptr, nullptr, 0, nullptr}};
+                          CALL(cache_compact),  CALL(cache_read),           CALL(chunk_attention),
+                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bsa_torch", "Compiled marshalling (see rope.py and paged.py).", -1,
                        kMethods,              nullptr,       nullptr, nullptr, nullptr};
 

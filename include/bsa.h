@@ -779,6 +779,97 @@ int bsa_cache_fork(const bsa_page_cache *c, int32_t *page_ref, int32_t n, const 
 int bsa_cache_compact(const bsa_page_cache *c, int32_t *page_ref, int32_t *new_page, void *workspace,
                       int64_t workspace_bytes, bsa_stream_t stream);
 
+/*
+ * 8-bit pools
+ * -----------
+ * A cache of half the bytes: bsa_page_cache.k and v are e4m3 codes [layers,
+ * n_pages, Hkv, page, D], and every row of a key head has a scale of its own,
+ * a power of two, in bsa_page_scales.  A row y is held as code * 2^e with
+ *   e = the smallest integer in [-100, 118] with max |y| <= 448 * 2^e,
+ *   code = e4m3(y * 2^-e)  (nearest, ties to even, saturating; NaN stays NaN),
+ * the scale's byte being e + 127 (e8m0).  code * 2^e is a bf16 number exactly.
+ * The _fp8 calls are their namesakes on such pools: bsa_cache_append_fp8
+ * quantises the normed and rotated keys, and the values, from fp32 with that
+ * one rounding (queries stay bf16); the page calls move codes and scales.
+ */
+typedef struct {
+    void *k, *v;             /* device bytes [layers, n_pages, Hkv, page], 16-byte aligned */
+} bsa_page_scales;
+
+int bsa_cache_append_fp8(const bsa_norm_rope_args *a, const bsa_page_cache *c, const bsa_page_scales *scales,
+                         const int32_t *seq_ids, const int32_t *slots, void *q_out, bsa_stream_t stream);
+int bsa_cache_accept_fp8(const bsa_page_cache *c, const bsa_page_scales *scales, const int32_t *context_len,
+                         const int32_t *accepted, const int32_t *n_accepted, int32_t T, int32_t *new_len,
+                         bsa_stream_t stream);
+int bsa_cache_resize_fp8(const bsa_page_cache *c, const bsa_page_scales *scales, int32_t *page_ref, int32_t n,
+                         const int32_t *seqs, const int32_t *keep, const int32_t *capacity, int32_t *granted,
+                         void *workspace, int64_t workspace_bytes, bsa_stream_t stream);
+int bsa_cache_fork_fp8(const bsa_page_cache *c, const bsa_page_scales *scales, int32_t *page_ref, int32_t n,
+                       const int32_t *src, const int32_t *dst, const int32_t *len, int32_t *granted, void *workspace,
+                       int64_t workspace_bytes, bsa_stream_t stream);
+int bsa_cache_compact_fp8(const bsa_page_cache *c, const bsa_page_scales *scales, int32_t *page_ref,
+                          int32_t *new_page, void *workspace, int64_t workspace_bytes, bsa_stream_t stream);
+
+/*
+ * Reading a cache back: slots first[i] .. first[i] + len[i] - 1 of sequence
+ * seq_ids[i] as rows 0 .. len[i] - 1 of the head-major contiguous K and V that
+ * bsa_forward takes, key heads repeated; rows len[i] .. n - 1 are zeros (bsa_forward's
+ * padding).  scales NULL: bf16 pools, the rows as they are; else 8-bit ones,
+ * code * 2^e in bf16.
+ *   seq_ids   device [R]: row of the page table; < 0: nothing to read, all zeros
+ *   first     device [R]; NULL: 0
+ *   len       device [R], 0 .. n; NULL: n
+ *   k, v      device bf16 [R, Hkv*kv_repeat, n, D], 16-byte aligned
+ * A slot that has no page, a sequence or a length out of range is reported (bit
+ * 32); its rows are zeros.  R and n may be 0 (nothing to do).
+ */
+typedef struct {
+    int32_t R, n, kv_repeat;
+    const int32_t *seq_ids, *first, *len;
+    void *k, *v;
+} bsa_read_args;
+int bsa_cache_read(const bsa_read_args *a, const bsa_page_cache *c, const bsa_page_scales *scales,
+                   bsa_stream_t stream);
+
+/*
+ * Attention of new tokens over a paged cache: a chunk of a prompt behind a
+ * cached prefix, one token (decoding), or a batch of both.  The new tokens are
+ * packed: sequence b's are rows q_ptr[b] .. q_ptr[b+1] - 1 of q, in slots
+ * context_len[b] and on, where bsa_cache_append has written their keys and values.
+ * The token in slot s attends to the slots u <= s; with a window > 0 only to
+ * those with u > s - window or u < sinks (the first tokens of a sequence, which
+ * stay visible).
+ *   q            device bf16 [tokens, Hq, D];  query head h reads key head h / (Hq / Hkv)
+ *   q_ptr        device [B+1]; NULL: one token a sequence (tokens = B).  A sequence whose
+ *                entries decrease or leave [0, tokens] brings none and is reported (bit 4).
+ *   context_len  device [B]
+ *   scales       NULL: bf16 pools; else 8-bit ones
+ *   out          device bf16 [tokens, Hq, D];  lse  device fp32 [tokens, Hq] (natural log;
+ *                -inf and O = 0 for a row that sees nothing).  Rows of no sequence are
+ *                left as they were.
+ * Slots behind a sequence's new tokens, and pages of other sequences, may hold
+ * anything, NaN included; pages that no new token sees need not be there (-1).
+ * K and V must be finite in a sequence's slots up to its last new token, in the
+ * pages that one of its new tokens sees.  A slot that a token should see and that
+ * lies in no page is reported (bit 32) and not seen.
+ * Limits: Hq a multiple of Hkv, Hq / Hkv <= 128; window, sinks >= 0; Hkv * (max_pages *
+ * page / 128) * (tokens * (Hq / Hkv) / 128 + B) below about 2^30.
+ *   workspace    device, bsa_chunk_attention_workspace(...) bytes, 256-byte aligned.
+ *                Calls that overlap on the GPU need workspaces of their own.
+ */
+typedef struct {
+    int32_t B, tokens, Hq;
+    const void *q;
+    const int32_t *q_ptr, *context_len;
+    void *out;
+    float *lse;
+    float scale;
+    int32_t window, sinks;   /* window 0: every slot up to the token's own */
+} bsa_chunk_args;
+int64_t bsa_chunk_attention_workspace(int32_t B, int32_t tokens, int32_t Hq, int32_t Hkv, int32_t D);
+int bsa_chunk_attention(const bsa_chunk_args *a, const bsa_page_cache *c, const bsa_page_scales *scales,
+                        void *workspace, int64_t workspace_bytes, bsa_stream_t stream);
+
 /* Human-readable text of a bsa_status (static storage). */
 const char *bsa_status_string(int status);
 
