@@ -15,17 +15,21 @@
 // 1,400 for its bytes.  Here a warp reads its 16 keys from shared memory once,
 // converts them in registers and multiplies: 2 bytes of traffic per byte.
 //
-// Work: a step is 128 slots; an item the steps of one key head of one sequence;
+// Work: a step is 256 slots (128 with more than 8 rows); an item the steps of one key head of one sequence;
 // the steps of the batch, cut into equal ranges, one per CTA.  An item that a
 // range boundary cuts leaves unnormalised fp32 parts that the merge joins in range
 // order: no atomics, results do not depend on timing.
 //
 // One CTA per SM: a producer warp walks the range, resolves pages and TMA-loads K
-// and V tiles into a ring; NW consumer warps, each with 16 keys of a step, a
-// running maximum, sum and accumulator of its own (so steps need no exchange), and
-// with 16 warps two steps at a time.  At an item's end the warps meet in shared
-// memory.  P is multiplied as two bf16 parts, high and low, so that its rounding
-// (2^-17) does not add to the result's.
+// and V tiles into a ring; eight consumer warps, each with 16 keys of every tile, a
+// running maximum, sum and accumulator of its own, so steps need no exchange.  At
+// an item's end the warps meet in shared memory.
+// bf16 rows: P is multiplied as two bf16 parts, high and low, so that its rounding
+// (2^-17) does not add to the result's.  8-bit rows: fp16 products, since a
+// code is an fp16 number (one conversion instruction for two; to bf16 it takes
+// four and a product) and P rounds at 2^-12 in it.
+
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -40,24 +44,29 @@ constexpr int kShortUnits = 1024;   // sequences of a launch (their prefix sums 
 constexpr int kShortSmem = 232448;
 constexpr int kShortCtrl = 7168;
 constexpr int kShortMaxSlots = 16;
+constexpr int kShortInfos = 4;      // step descriptions ahead
+constexpr int kWarps = 8;           // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };
 
 struct ShortInfo {
-    int flags, step;    // step of the item
-    int base, have;     // first slot; halves that lie in a page
+    int flags;          // and from kHaveBit on, per tile, the halves that lie in a page
+    int base[2];        // first slot of each tile
+    // of the item, read with its first step
     int row0, rows, h;  // first token, query rows, key head
     int ctx, end;       // slot of the first new token, slot behind the last one
     int part;           // -1: write the output, else the partial slot
 };
+constexpr int kHaveBit = 8;
 
 struct ShortCtrl {
     uint64_t t_full[kShortMaxSlots], t_empty[kShortMaxSlots];
-    uint64_t i_empty[kShortMaxSlots / 2];
+    uint64_t i_empty[kShortInfos];
     uint64_t st_full, x_full;  // all consumers posted their sums, their parts of O
-    ShortInfo info[kShortMaxSlots / 2];
-    float2 stats[16][16];      // [warp][row]; 8 warps x 16 rows or 16 x 8 are used
-    int red[18];
+    ShortInfo info[kShortInfos];
+    float2 stats[kWarps][16];  // [warp][row]
+    int red[kWarps + 1];
     WaitFlag wf;
     int prefix[kShortUnits + 1];
 };
@@ -74,26 +83,26 @@ struct ShortParams {
 
 template <int D, bool Q8, int NT>
 struct ShortCfg {
-    static constexpr int NW = NT == 1 ? 16 : 8;       // consumer warps
-    static constexpr int THREADS = (NW + 1) * 32;
+    static constexpr int SUB = NT == 1 ? 2 : 1;       // tiles of a step
     static constexpr int ROWB = Q8 ? D : 128;         // bytes of a row of a box
     static constexpr int NBOX = Q8 ? 1 : D / 64;
     static constexpr int BOX = kTile * ROWB;
     static constexpr int TILE = NBOX * BOX;
     static constexpr int PITCH = D + 4;               // floats of an exchanged row
-    static constexpr int XCH = NW * 8 * NT * PITCH * 4;
+    static constexpr int XCH = kWarps * 8 * NT * PITCH * 4;
     static constexpr int FIXED = XCH + kShortCtrl + (Q8 ? kShortMaxSlots * kTile : 0);
     static constexpr int FIT = (kShortSmem - FIXED) / TILE;
     static constexpr int SLOTS = FIT > kShortMaxSlots ? kShortMaxSlots : FIT;
     static constexpr int SMEM = SLOTS * TILE + FIXED;
-    static_assert(SLOTS >= 4, "ring too small");
+    static_assert(SLOTS >= 2 * SUB, "ring too small");
 };
 
-// Steps of a short sequence's item; 0: it has no new tokens or is not short.
+// Steps (of SUB tiles) of a short sequence's item; 0: it has no new tokens or is not short.
+template <int SUB>
 __device__ __forceinline__ int short_steps(const ChunkCommon& p, int b, bool report) {
     const Seq s = sequence(p, b, report);
     if (s.n == 0 || s.n * (int64_t)p.G > kShortRows) return 0;
-    return visible_span(p, s.ctx, s.ctx + s.n).steps;
+    return (visible_span(p, s.ctx, s.ctx + s.n).steps + SUB - 1) / SUB;
 }
 
 // ---------------------------------------------------------------- producer
@@ -102,9 +111,9 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                                uint8_t* sS, ShortCtrl* c, int lo, int hi, int per, volatile WaitFlag* wf) {
     using C = ShortCfg<D, Q8, NT>;
     const ChunkCommon& cc = p.c;
-    const int lane = threadIdx.x & 31, Hkv = cc.Hkv, ppt = kTile / cc.page;
+    const int lane = threadIdx.x & 31, Hkv = cc.Hkv, ppt = kTile / cc.page, pps = C::SUB * ppt;
     const bool leader = elect_one();
-    const uint32_t infos = (uint32_t)p.n_slots / 2;
+    constexpr uint32_t infos = kShortInfos;
     uint32_t slot = 0, phase = 0, nload = 0, g = 0;
     bool ok = true, ended = false;
     PartMeta mt{-1, 0, per, 0, 0, 0, {0, 0}};
@@ -129,15 +138,20 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
             const bool whole = s0 == 0 && start + s1 == end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
             if (start < lo) mt = PartMeta{start, end, per, sq.row0, sq.n, h, {0, 0}};
-            for (int e0 = s0 * ppt; e0 < s1 * ppt && ok; e0 += 32) {
+            for (int e0 = s0 * pps; e0 < s1 * pps && ok; e0 += 32) {
                 // 32 pages resolved at a time
-                const int e = e0 + lane, est = e / ppt;
-                const int j = sp.tile(est) * ppt + e % ppt;
-                const int y = est < s1 ? page_row(cc, b, h, j, vis0, seq_end) : -1;
-                const int cnt = min(32, s1 * ppt - e0);
-                for (int q = 0; q < cnt && ok; q += ppt) {
-                    const int st = (e0 + q) / ppt;
-                    const int y0 = __shfl_sync(0xffffffffu, y, q), y1 = __shfl_sync(0xffffffffu, y, q + ppt - 1);
+                const int e = e0 + lane, tl = e / ppt;
+                const int j = sp.tile(tl) * ppt + e % ppt;
+                const int y = e < s1 * pps && tl < sp.steps ? page_row(cc, b, h, j, vis0, seq_end) : -1;
+                const int cnt = min(32, s1 * pps - e0);
+                for (int q = 0; q < cnt && ok; q += pps) {
+                    const int st = (e0 + q) / pps;
+                    int y0[C::SUB], y1[C::SUB];  // rows of each tile's halves
+#pragma unroll
+                    for (int x = 0; x < C::SUB; ++x) {
+                        y0[x] = __shfl_sync(0xffffffffu, y, q + x * ppt);
+                        y1[x] = __shfl_sync(0xffffffffu, y, q + x * ppt + ppt - 1);
+                    }
                     const uint32_t is = g % infos;
                     if (g >= infos && !warp_wait(&c->i_empty[is], ((g / infos) & 1) ^ 1, wf)) {
                         ok = false;
@@ -145,16 +159,20 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                     }
                     if (leader) {
                         ShortInfo& f = c->info[is];
-                        const int first = sp.tile(st) * kTile;
-                        const int have = ppt == 1 ? (y0 >= 0 ? 3 : 0) : (y0 >= 0 ? 1 : 0) | (y1 >= 0 ? 2 : 0);
-                        // every row sees all of it: up to the first token, inside the last one's window
-                        const bool plain = have == 3 && first + kTile <= sq.ctx + 1 &&
-                                           (cc.window <= 0 || first > seq_end - 1 - cc.window ||
-                                            first + kTile <= cc.sinks);
-                        f.flags = (st == s0 ? kFirst : 0) | (st + 1 == s1 ? kLast : 0) | (plain ? 0 : kMask);
-                        f.step = st - s0;
-                        f.base = first;
-                        f.have = have;
+                        bool plain = true;
+                        int have = 0;
+#pragma unroll
+                        for (int x = 0; x < C::SUB; ++x) {
+                            const int first = sp.tile(st * C::SUB + x) * kTile;
+                            const int hv = ppt == 1 ? (y0[x] >= 0 ? 3 : 0) : (y0[x] >= 0 ? 1 : 0) | (y1[x] >= 0 ? 2 : 0);
+                            // every row sees all of it: up to the first token, inside the last one's window
+                            plain &= hv == 3 && first + kTile <= sq.ctx + 1 &&
+                                     (cc.window <= 0 || first > seq_end - 1 - cc.window || first + kTile <= cc.sinks);
+                            have |= hv << (2 * x);
+                            f.base[x] = first;
+                        }
+                        f.flags = (st == s0 ? kFirst : 0) | (st + 1 == s1 ? kLast : 0) | (plain ? 0 : kMask) |
+                                  have << kHaveBit;
                         f.row0 = sq.row0;
                         f.rows = sq.n * cc.G;
                         f.h = h;
@@ -165,27 +183,29 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                     __syncwarp();
                     ++g;
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
+                    for (int kv = 0; kv < 2 * C::SUB; ++kv) {
+                        const bool val = kv >= C::SUB;
+                        const int r0 = y0[kv % C::SUB], r1 = y1[kv % C::SUB];
                         if (nload >= (uint32_t)p.n_slots && !warp_wait(&c->t_empty[slot], phase ^ 1, wf)) {
                             ok = false;
                             break;
                         }
                         if (leader) {
                             uint64_t* bar = &c->t_full[slot];
-                            const uint8_t* sc = kv ? cc.vs : cc.ks;
+                            const uint8_t* sc = val ? cc.vs : cc.ks;
                             uint32_t bytes = C::TILE;
-                            if (Q8) bytes += (y0 >= 0 ? cc.page : 0) + (ppt == 2 && y1 >= 0 ? cc.page : 0);
+                            if (Q8) bytes += (r0 >= 0 ? cc.page : 0) + (ppt == 2 && r1 >= 0 ? cc.page : 0);
                             mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
                             for (int x = 0; x < C::NBOX; ++x) {
                                 uint8_t* dst = sT + slot * C::TILE + x * C::BOX;
-                                tma_load_2d(dst, kv ? tv : tk, bar, x * 64, y0 >= 0 ? y0 : -cc.page);
+                                tma_load_2d(dst, val ? tv : tk, bar, x * 64, r0 >= 0 ? r0 : -cc.page);
                                 if (ppt == 2)
-                                    tma_load_2d(dst + 64 * C::ROWB, kv ? tv : tk, bar, x * 64, y1 >= 0 ? y1 : -cc.page);
+                                    tma_load_2d(dst + 64 * C::ROWB, val ? tv : tk, bar, x * 64, r1 >= 0 ? r1 : -cc.page);
                             }
                             if (Q8) {
-                                if (y0 >= 0) bulk_load(sS + slot * kTile, sc + y0, cc.page, bar);
-                                if (ppt == 2 && y1 >= 0) bulk_load(sS + slot * kTile + 64, sc + y1, cc.page, bar);
+                                if (r0 >= 0) bulk_load(sS + slot * kTile, sc + r0, cc.page, bar);
+                                if (ppt == 2 && r1 >= 0) bulk_load(sS + slot * kTile + 64, sc + r1, cc.page, bar);
                             }
                         }
                         ++nload;
@@ -232,12 +252,35 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
 }
 
 // ---------------------------------------------------------------- consumers
+// F16: fp16 operands, else bf16.
+template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (the low or high half of w) as fp16, exactly.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, int high) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+        : "=r"(r)
+        : "r"(high ? w >> 16 : w));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -271,50 +314,86 @@ template <int D, bool Q8, int NT>
 __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const uint8_t* sS, float* xch, ShortCtrl* c,
                                volatile WaitFlag* wf) {
     using C = ShortCfg<D, Q8, NT>;
-    constexpr int KS = D / 16;
+    constexpr int KS = D / 16, SUB = C::SUB;
     const ChunkCommon& cc = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, cq = lane & 3;
-    const int slab = (warp & 7) * 16, group = warp >> 3;
-    const uint32_t infos = (uint32_t)p.n_slots / 2;
+    const int slab = warp * 16;
     uint32_t qf[KS][NT][2];
     float o[KS][NT][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2], sl[NT][2];
+    int vref = 0;  // 8-bit: the scale byte that O counts in (0: none yet)
+    int row0 = 0, rows = 0, h = 0, ctx = 0, end = 0, part = 0;
     uint32_t slot = 0, phase = 0, items = 0;
-    auto next = [&](uint32_t& s, uint32_t& ph) {
-        if (++s == (uint32_t)p.n_slots) {
-            s = 0;
-            ph ^= 1;
-        }
-    };
     for (uint32_t gs = 0;; ++gs) {
         if (!warp_wait(&c->t_full[slot], phase, wf)) return;
-        const uint32_t is = gs % infos;
-        const ShortInfo f = c->info[is];
+        const uint32_t is = gs % kShortInfos;
+        const ShortInfo& f = c->info[is];
+        const int flags = f.flags;
+        int base[SUB];
+#pragma unroll
+        for (int x = 0; x < SUB; ++x) base[x] = f.base[x];
+        if (flags & kFirst) {
+            row0 = f.row0;
+            rows = f.rows;
+            h = f.h;
+            ctx = f.ctx;
+            end = f.end;
+            part = f.part;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->i_empty[is]);
-        if (f.flags & kEnd) return;
-        const uint32_t kslot = slot;
-        next(slot, phase);
-        const uint32_t vslot = slot, vphase = phase;
-        next(slot, phase);
-        if (f.flags & kFirst) {
+        if (flags & kEnd) return;
+        uint32_t ts[2 * SUB], tp[2 * SUB];  // slots and phases of the K and V tiles
+#pragma unroll
+        for (int x = 0; x < 2 * SUB; ++x) {
+            ts[x] = slot;
+            tp[x] = phase;
+            if (++slot == (uint32_t)p.n_slots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        if (flags & kFirst) {
+            vref = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int r = 8 * nt + g;
-                const bool on = r < f.rows;
+                const bool on = r < rows;
                 const __nv_bfloat16* src =
-                    p.q + ((int64_t)(f.row0 + (on ? r / cc.G : 0)) * cc.Hq + f.h * cc.G + (on ? r % cc.G : 0)) * D;
+                    p.q + ((int64_t)(row0 + (on ? r / cc.G : 0)) * cc.Hq + h * cc.G + (on ? r % cc.G : 0)) * D;
+                uint4 v[KS / 2];
 #pragma unroll
                 for (int q = 0; q < KS / 2; ++q) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (on) v = *reinterpret_cast<const uint4*>(src + q_chunk<D, Q8>(cq, q));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t a = word(v, 2 * i), b = word(v, 2 * i + 1);
-                        qf[2 * q + i][nt][0] = Q8 ? __byte_perm(a, b, 0x5410) : a;
-                        qf[2 * q + i][nt][1] = Q8 ? __byte_perm(a, b, 0x7632) : b;
-                    }
+                    v[q] = make_uint4(0, 0, 0, 0);
+                    if (on) v[q] = *reinterpret_cast<const uint4*>(src + q_chunk<D, Q8>(cq, q));
                 }
+                int up = 0;
+                if (Q8) {
+                    // fp16 with the row's largest magnitude at 2^14: no bf16 value of the
+                    // row above 2^-29 of it is rounded
+                    float top = 0.f;
+#pragma unroll
+                    for (int q = 0; q < KS / 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            top = fmax3(top, fabsf(__uint_as_float(word(v[q], i) << 16)),
+                                        fabsf(__uint_as_float(word(v[q], i) & 0xffff0000u)));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    up = min(14 + 127 - (int)(__float_as_uint(top) >> 23), 126);
+                }
+                const float qs = exp2_int(up);
+#pragma unroll
+                for (int q = 0; q < KS / 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = word(v[q], i);
+                        qf[2 * q + (i >> 1)][nt][i & 1] =
+                            Q8 ? pack_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xffff0000u) * qs) : w;
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)  // the lane's columns of S^T are rows 2 cq and 2 cq + 1
+                    sl[nt][i] = cc.scale_log2 * exp2_int(-__shfl_sync(0xffffffffu, up, (2 * cq + i) * 4));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     m[nt][i] = -INFINITY;
@@ -326,137 +405,189 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                     for (int i = 0; i < 4; ++i) o[t][nt][i] = 0.f;
             }
         }
-        if (C::NW == 8 || (f.step & 1) == group) {
-            float s[NT][4];
+        float s[SUB][NT][4];
+        uint32_t kb[SUB][2];  // 8-bit: the scale bytes of keys g and g + 8
+#pragma unroll
+        for (int x = 0; x < SUB; ++x) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-            const uint8_t* kt = sT + kslot * C::TILE;
-            if (Q8) {
-                uint32_t f1[2], f2_[2];
-                bool two = false;
+                for (int i = 0; i < 4; ++i) s[x][nt][i] = 0.f;
+            if (x > 0 && !warp_wait(&c->t_full[ts[x]], tp[x], wf)) return;
+        }
+        if (Q8) {
+            uint4 kr[SUB][2][D / 64];
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t e = sS[kslot * kTile + slab + g + 8 * r];
-                    f1[r] = scale_first(e) * 0x10001u;
-                    f2_[r] = scale_rest(e) * 0x10001u;
-                    two |= e > kOneStep;
+                    kb[x][r] = sS[ts[x] * kTile + slab + g + 8 * r];
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        kr[x][r][i] = *reinterpret_cast<const uint4*>(
+                            chunk_at<C::ROWB>(sT + ts[x] * C::TILE, slab + g + 8 * r, (D / 64) * cq + i));
                 }
-                two = __any_sync(0xffffffffu, two);
-                uint4 kr[2][D / 64];
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+            for (int j = 0; j < KS; ++j)
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        kr[r][x] = *reinterpret_cast<const uint4*>(
-                            chunk_at<C::ROWB>(kt, slab + g + 8 * r, (D / 64) * cq + x));
+                for (int x = 0; x < SUB; ++x) {
+                    const uint32_t w0 = word(kr[x][0][j / 4], j % 4), w1 = word(kr[x][1][j / 4], j % 4);
+                    const uint32_t a[4] = {codes_f16(w0, 0), codes_f16(w1, 0), codes_f16(w0, 1), codes_f16(w1, 1)};
 #pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    uint32_t a[4];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t w = word(kr[r][j / 4], j % 4);
-                        a[r] = mul_bf16x2(spread_even(w), f1[r]);
-                        a[2 + r] = mul_bf16x2(spread_odd(w), f1[r]);
-                        if (two) {
-                            a[r] = mul_bf16x2(a[r], f2_[r]);
-                            a[2 + r] = mul_bf16x2(a[2 + r], f2_[r]);
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[j][nt][0], qf[j][nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[x][nt], a, qf[j][nt][0], qf[j][nt][1]);
                 }
-            } else {
+        } else {
 #pragma unroll
-                for (int q = 0; q < KS / 2; ++q) {
+            for (int q = 0; q < KS / 2; ++q)
+#pragma unroll
+                for (int x = 0; x < SUB; ++x) {
                     uint4 kr[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        kr[r] = *reinterpret_cast<const uint4*>(
-                            chunk_at<128>(kt + (q >> 1) * C::BOX, slab + g + 8 * r, 2 * cq + (q & 1)));
+                        kr[r] = *reinterpret_cast<const uint4*>(chunk_at<128>(
+                            sT + ts[x] * C::TILE + (q >> 1) * C::BOX, slab + g + 8 * r, 2 * cq + (q & 1)));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t a[4] = {word(kr[0], 2 * i), word(kr[1], 2 * i), word(kr[0], 2 * i + 1),
                                                word(kr[1], 2 * i + 1)};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[2 * q + i][nt][0], qf[2 * q + i][nt][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<false>(s[x][nt], a, qf[2 * q + i][nt][0], qf[2 * q + i][nt][1]);
                     }
                 }
+        }
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+            for (int x = 0; x < SUB; ++x) mbar_arrive(&c->t_empty[ts[x]]);
+        }
+        // s[x][nt]: key g rows 2 cq, 2 cq + 1; key g + 8 the same rows
+        bool grow = false;
+#pragma unroll
+        for (int x = 0; x < SUB; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // 2^e (a byte of an unwritten slot is hidden below, whatever comes of it)
+                const float ke = Q8 ? __uint_as_float(kb[x][i >> 1] << 23) : 1.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[x][nt][i] *= Q8 ? sl[nt][i & 1] * ke : sl[nt][i & 1];
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->t_empty[kslot]);
-            // s[nt]: key g rows 2 cq, 2 cq + 1; key g + 8 the same rows
-            uint32_t hi[NT][2], lo[NT][2];
-            bool grow = false;
+        if (flags & kMask) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[nt][i] *= cc.scale_log2;
-                    if (f.flags & kMask) {
-                        const int r = 8 * nt + 2 * cq + (i & 1), key = slab + g + 8 * (i >> 1), u = f.base + key;
-                        const int pos = f.ctx + r / cc.G;
-                        const bool see = r < f.rows && ((f.have >> (key >> 6)) & 1) && u <= pos &&
-                                         (cc.window <= 0 || u > pos - cc.window || u < cc.sinks);
-                        if (!see) s[nt][i] = -INFINITY;
-                    }
-                    grow |= s[nt][i] > m[nt][i & 1] + 8.f;
-                }
-            // the reference follows the maximum only where it grows by more than 2^8
-            if (__any_sync(0xffffffffu, grow)) {
+            for (int x = 0; x < SUB; ++x)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float x = fmaxf(s[nt][i], s[nt][i + 2]);
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        x = fmaxf(x, m[nt][i]);
-                        const float w = x == -INFINITY ? 1.f : ex2_approx(m[nt][i] - x);
-                        m[nt][i] = x;
-                        l[nt][i] *= w;
-#pragma unroll
-                        for (int t = 0; t < KS; ++t) {
-                            o[t][nt][i] *= w;
-                            o[t][nt][i + 2] *= w;
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * nt + 2 * cq + (i & 1), key = slab + g + 8 * (i >> 1), u = base[x] + key;
+                        const int pos = ctx + r / cc.G;
+                        const bool see = r < rows && ((flags >> (kHaveBit + 2 * x + (key >> 6))) & 1) && u <= pos &&
+                                         (cc.window <= 0 || u > pos - cc.window || u < cc.sinks);
+                        if (!see) s[x][nt][i] = -INFINITY;
                     }
+        }
+#pragma unroll
+        for (int x = 0; x < SUB; ++x)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) grow |= s[x][nt][i] > m[nt][i & 1] + 8.f;
+        // the reference follows the maximum only where it grows by more than 2^8
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float top = m[nt][i];
+#pragma unroll
+                    for (int x = 0; x < SUB; ++x) top = fmax3(top, s[x][nt][i], s[x][nt][i + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const float w = top == -INFINITY ? 1.f : ex2_approx(m[nt][i] - top);
+                    m[nt][i] = top;
+                    l[nt][i] *= w;
+#pragma unroll
+                    for (int t = 0; t < KS; ++t) {
+                        o[t][nt][i] *= w;
+                        o[t][nt][i + 2] *= w;
+                    }
+                }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float ref = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
+#pragma unroll
+                for (int x = 0; x < SUB; ++x) {
+                    s[x][nt][i] = ex2_approx(s[x][nt][i] - ref);
+                    l[nt][i & 1] += s[x][nt][i];
+                }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float e[4];
+        for (int x = 0; x < SUB; ++x)
+            if (!warp_wait(&c->t_full[ts[SUB + x]], tp[SUB + x], wf)) return;
+        if (Q8) {
+            // Values are fp16 codes; their scales go into the weights, relative to the
+            // largest one met (with room for the next ones): 2^7 p 2^(e - ref) is at most
+            // 2^14, and down to 2^-21 of what a weight of 1 gives it is a normal number.
+            uint32_t vb[SUB][2], top = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float ref = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
-                    e[i] = ex2_approx(s[nt][i] - ref);
-                    l[nt][i & 1] += e[i];
-                }
+            for (int x = 0; x < SUB; ++x)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t h2 = pack_bf16x2(e[2 * k], e[2 * k + 1]);
-                    const uint32_t l2 = pack_bf16x2(e[2 * k] - __uint_as_float(h2 << 16),
-                                                    e[2 * k + 1] - __uint_as_float(h2 & 0xffff0000u));
-                    hi[nt][k] = transpose8x8(h2);
-                    lo[nt][k] = transpose8x8(l2);
+                    const int key = slab + g + 8 * k;
+                    vb[x][k] = sS[ts[SUB + x] * kTile + key];
+                    if ((flags & kMask) &&
+                        !(((flags >> (kHaveBit + 2 * x + (key >> 6))) & 1) && base[x] + key < end))
+                        vb[x][k] = 0;
+                    top = max(top, vb[x][k]);
                 }
+            if (__any_sync(0xffffffffu, (int)top > vref)) {
+                const int to = (int)__reduce_max_sync(0xffffffffu, top) + 1;
+                const float w = vref ? exp2_int(max(vref - to, -126)) : 0.f;
+                vref = to;
+#pragma unroll
+                for (int t = 0; t < KS; ++t)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[t][nt][i] *= w;
             }
-            if (!warp_wait(&c->t_full[vslot], vphase, wf)) return;
-            const uint8_t* vt = sT + vslot * C::TILE;
-            // keys 2 cq, 2 cq + 1 and 2 cq + 8, 2 cq + 9
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float w = exp2_int(max((int)vb[x][k] - vref + 7, -126));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) s[x][nt][2 * k + i] *= w;
+                }
+        }
+        uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
+#pragma unroll
+        for (int x = 0; x < SUB; ++x)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float a = s[x][nt][2 * k], b = s[x][nt][2 * k + 1];
+                    if (Q8) {
+                        hi[x][nt][k] = transpose8x8(pack_f16x2(a, b));
+                    } else {
+                        const uint32_t h2 = pack_bf16x2(a, b);
+                        hi[x][nt][k] = transpose8x8(h2);
+                        lo[x][nt][k] = transpose8x8(
+                            pack_bf16x2(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u)));
+                    }
+                }
+        // keys 2 cq, 2 cq + 1 and 2 cq + 8, 2 cq + 9
+#pragma unroll
+        for (int x = 0; x < SUB; ++x) {
+            const uint8_t* vt = sT + ts[SUB + x] * C::TILE;
             if (Q8) {
                 constexpr int W = D / 32;  // words of the lane's values in a key's row
-                uint32_t f1[2], f2_[2];
-                bool two = false;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t ea = sS[vslot * kTile + slab + 2 * cq + 8 * k];
-                    const uint32_t eb = sS[vslot * kTile + slab + 2 * cq + 8 * k + 1];
-                    f1[k] = scale_first(ea) | scale_first(eb) << 16;
-                    f2_[k] = scale_rest(ea) | scale_rest(eb) << 16;
-                    two |= ea > kOneStep || eb > kOneStep;
-                }
-                two = __any_sync(0xffffffffu, two);
                 uint32_t vw[4][W];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -464,52 +595,49 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                     if (D == 128) {
                         const uint4 v = *reinterpret_cast<const uint4*>(chunk_at<C::ROWB>(vt, row, g));
 #pragma unroll
-                        for (int x = 0; x < W; ++x) vw[k][x] = word(v, x);
+                        for (int i = 0; i < W; ++i) vw[k][i] = word(v, i);
                     } else {
                         const uint2 v = *reinterpret_cast<const uint2*>(chunk_at<C::ROWB>(vt, row, g >> 1) + 8 * (g & 1));
                         vw[k][0] = v.x;
                         vw[k][1] = v.y;
                     }
+                    // codes behind the last token may be NaN, and 0 * NaN is none of the sum
+                    if ((flags & kMask) && base[x] + row >= end) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) vw[k][i] = 0;
+                    }
                 }
 #pragma unroll
-                for (int x = 0; x < W; ++x)
+                for (int i = 0; i < W; ++i)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {  // tile 2 x + t: bytes 2 t and 2 t + 1 of the word
+                    for (int t = 0; t < 2; ++t) {  // tile 2 i + t: bytes 2 t and 2 t + 1 of the word, key by key
                         uint32_t a[4];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int by = 2 * t + r;
-                                const uint32_t two_keys =
-                                    __byte_perm(vw[2 * k][x], vw[2 * k + 1][x], (4 + by) << 12 | by << 4);
-                                uint32_t v = mul_bf16x2(spread_odd(two_keys), f1[k]);
-                                if (two) v = mul_bf16x2(v, f2_[k]);
-                                a[r + 2 * k] = v;
-                            }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(o[2 * x + t][nt], a, hi[nt][0], hi[nt][1]);
-                            mma16816(o[2 * x + t][nt], a, lo[nt][0], lo[nt][1]);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t w = __byte_perm(vw[2 * k][i], vw[2 * k + 1][i], t ? 0x7362 : 0x5140);
+                            a[2 * k] = codes_f16(w, 0);
+                            a[2 * k + 1] = codes_f16(w, 1);
                         }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[2 * i + t][nt], a, hi[x][nt][0], hi[x][nt][1]);
                     }
             } else {
                 uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                if (f.flags & kMask) {
+                if (flags & kMask) {
                     // rows behind the last token may hold NaN, and 0 * NaN is none of the sum
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int u = f.base + slab + 2 * cq + 8 * k;
-                        keep[k] = (u < f.end ? 0xffffu : 0u) | (u + 1 < f.end ? 0xffff0000u : 0u);
+                        const int u = base[x] + slab + 2 * cq + 8 * k;
+                        keep[k] = (u < end ? 0xffffu : 0u) | (u + 1 < end ? 0xffff0000u : 0u);
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
+                for (int bx = 0; bx < D / 64; ++bx) {
                     uint4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         v[k] = *reinterpret_cast<const uint4*>(
-                            chunk_at<128>(vt + x * C::BOX, slab + 2 * cq + 8 * (k >> 1) + (k & 1), g));
+                            chunk_at<128>(vt + bx * C::BOX, slab + 2 * cq + 8 * (k >> 1) + (k & 1), g));
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         uint32_t a[4];
@@ -521,16 +649,16 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(o[4 * x + t][nt], a, hi[nt][0], hi[nt][1]);
-                            mma16816(o[4 * x + t][nt], a, lo[nt][0], lo[nt][1]);
+                            mma16816<false>(o[4 * bx + t][nt], a, hi[x][nt][0], hi[x][nt][1]);
+                            mma16816<false>(o[4 * bx + t][nt], a, lo[x][nt][0], lo[x][nt][1]);
                         }
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c->t_empty[vslot]);
+            if (lane == 0) mbar_arrive(&c->t_empty[ts[SUB + x]]);
         }
-        if (!(f.flags & kLast)) continue;
+        if (!(flags & kLast)) continue;
         // The item's end: all warps' sums and accumulators meet.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -550,8 +678,9 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 const int r = 8 * nt + 2 * cq + i;
                 float top = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < C::NW; ++w) top = fmaxf(top, c->stats[w][r].x);
-                const float w = top == -INFINITY ? 0.f : ex2_approx(m[nt][i] - top);
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, c->stats[w][r].x);
+                float w = top == -INFINITY ? 0.f : ex2_approx(m[nt][i] - top);
+                if (Q8) w = vref ? w * exp2_int(vref - 127 - 7) : 0.f;
                 float* dst = xch + (warp * 8 * NT + r) * C::PITCH;
 #pragma unroll
                 for (int t = 0; t < KS / 2; ++t)
@@ -563,14 +692,14 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
         if (lane == 0) mbar_arrive(&c->x_full);
         if (!warp_wait(&c->x_full, items & 1, wf)) return;
         ++items;
-        for (int x = threadIdx.x; x < f.rows * (D / 4); x += C::NW * 32) {
+        for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
             const int r = x / (D / 4), d = x % (D / 4) * 4;
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < C::NW; ++w) top = fmaxf(top, c->stats[w][r].x);
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, c->stats[w][r].x);
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < C::NW; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
                 const float2 ml = c->stats[w][r];
                 if (top > -INFINITY) sum += ex2_approx(ml.x - top) * ml.y;
                 const float4 a = *reinterpret_cast<const float4*>(xch + (w * 8 * NT + r) * C::PITCH + d);
@@ -579,14 +708,14 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 v.z += a.z;
                 v.w += a.w;
             }
-            if (f.part < 0) {
+            if (part < 0) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const int64_t orow = (int64_t)(f.row0 + r / cc.G) * cc.Hq + f.h * cc.G + r % cc.G;
+                const int64_t orow = (int64_t)(row0 + r / cc.G) * cc.Hq + h * cc.G + r % cc.G;
                 *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(cc.out) + orow * D + d) =
                     make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
                 if (d == 0) cc.lse[orow] = lse_of(top, sum);
             } else {
-                const int64_t prow = (int64_t)f.part * kShortRows + r;
+                const int64_t prow = (int64_t)part * kShortRows + r;
                 *reinterpret_cast<float4*>(p.part_o + prow * D + d) = v;
                 if (d == 0) p.part_ml[prow] = make_float2(top, sum);
             }
@@ -596,7 +725,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
 
 // ---------------------------------------------------------------- kernel
 template <int D, bool Q8, int NT>
-__global__ void __launch_bounds__(ShortCfg<D, Q8, NT>::THREADS, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     short_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const ShortParams p) {
     using C = ShortCfg<D, Q8, NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -618,30 +747,30 @@ __global__ void __launch_bounds__(ShortCfg<D, Q8, NT>::THREADS, 1)
         const int x = threadIdx.x;
         if (x < kShortMaxSlots) {
             mbar_init(&c->t_full[x], 1);
-            mbar_init(&c->t_empty[x], 8);  // the eight warps whose step it is
-        } else if (x < kShortMaxSlots + kShortMaxSlots / 2) {
-            mbar_init(&c->i_empty[x - kShortMaxSlots], C::NW);
+            mbar_init(&c->t_empty[x], kWarps);
+        } else if (x < kShortMaxSlots + kShortInfos) {
+            mbar_init(&c->i_empty[x - kShortMaxSlots], kWarps);
         } else if (x == 32) {
-            mbar_init(&c->st_full, C::NW);
-            mbar_init(&c->x_full, C::NW);
+            mbar_init(&c->st_full, kWarps);
+            mbar_init(&c->x_full, kWarps);
             c->wf.abort = 0;
             c->wf.limit_ns = p.c.wait_limit_ns;
             c->prefix[0] = 0;
         }
         fence_mbar_init();
     }
-    if (warp == C::NW && lane == 0) {
+    if (warp == kWarps && lane == 0) {
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
     // Nothing before this line reads or writes global memory.
     griddep_wait();
     // prefix sums of the sequences' steps per item: every thread a run of them, then a scan
-    const int run = (p.units + C::THREADS - 1) / C::THREADS;
+    const int run = (p.units + kThreads - 1) / kThreads;
     const int u0 = min(p.units, (int)threadIdx.x * run), u1 = min(p.units, u0 + run);
     int sum = 0;
     for (int u = u0; u < u1; ++u) {
-        sum += short_steps(p.c, p.unit0 + u, blockIdx.x == 0);
+        sum += short_steps<C::SUB>(p.c, p.unit0 + u, blockIdx.x == 0);
         c->prefix[u + 1] = sum;
     }
     int incl = sum;
@@ -659,7 +788,7 @@ __global__ void __launch_bounds__(ShortCfg<D, Q8, NT>::THREADS, 1)
     const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
     volatile WaitFlag* wf = &c->wf;
-    if (warp == C::NW)
+    if (warp == kWarps)
         short_producer<D, Q8, NT>(&tk, &tv, p, sT, sS, c, lo, hi, per, wf);
     else
         short_consumer<D, Q8, NT>(p, sT, sS, xch, c, wf);
@@ -688,7 +817,7 @@ int go(const ShortLaunch& L, const CUtensorMap& tk, const CUtensorMap& tv, cudaS
     for (int u0 = 0; u0 < L.c.B; u0 += chunk) {
         p.unit0 = u0;
         p.units = std::min(chunk, L.c.B - u0);
-        cudaError_t e = launch_after(short_kernel<D, Q8, NT>, dim3((unsigned)ctas), C::THREADS, C::SMEM, s, tk, tv, p);
+        cudaError_t e = launch_after(short_kernel<D, Q8, NT>, dim3((unsigned)ctas), kThreads, C::SMEM, s, tk, tv, p);
         if (e != cudaSuccess) return BSA_ERR_CUDA;
         if (ctas < 2) continue;
         e = launch_after(chunk_merge_kernel<D, kShortRows, 1>, dim3((unsigned)ctas - 1, (unsigned)(8 * NT)), 256, 0, s,

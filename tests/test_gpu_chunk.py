@@ -6,8 +6,11 @@ A = sum p |v| / sum p:
     that is at most M = max over keys of scale * sum_d |q_d k_d|: D M 2^-24;
     the exponent's product, subtraction and 2^x: |x| 2^-23 + 2^-22, |x| <= 2 M
     -> relative error of a weight  e = (D + 4 * 2) M 2^-24 + 2^-21
-  p is rounded to bf16 once, 2^-8 (sequences of more than 16 rows a key head), or
-    held in two bf16 parts, 2^-16; fp32 accumulation: steps * 2^-24, inside 2^-16
+  p is rounded to bf16 once, 2^-8 (sequences of more than 16 rows a key head); in
+    shorter ones it is held in two bf16 parts, 2^-16, or, times the 8-bit row's
+    scale, rounded to fp16 once, 2^-11 (below fp16's normal numbers, 2^-21 of what a
+    weight of 1 gives at the largest scale met: off by 2^-32 of that, inside 2^-16);
+    fp32 accumulation: steps * 2^-24, inside 2^-16
   O: A (p's + 2 e + 2^-16) + |O| 2^-8 (its own rounding)
   LSE: e + 2^-21 (|LSE| + 1)
 8-bit rows are what they are (code * 2^e): the reference reads the same values.
@@ -69,7 +72,8 @@ class Case:
         for b, (r, n) in enumerate(zip(self.q_ptr, self.new)):
             if n:
                 part = [x[r:r + n] for x in self.ref]
-                check_attention(o[r:r + n], lse[r:r + n], part, self.D, 2.0 ** -16 if self.short[b] else 2.0 ** -8)
+                p = 2.0 ** -8 if not self.short[b] else 2.0 ** -11 if self.cache.q8 else 2.0 ** -16
+                check_attention(o[r:r + n], lse[r:r + n], part, self.D, p)
 
 
 both = pytest.mark.parametrize("q8", [False, True], ids=["bf16", "q8"])
