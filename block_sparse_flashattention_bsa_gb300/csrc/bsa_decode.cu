@@ -21,9 +21,9 @@
 // order: no atomics, results do not depend on timing.
 //
 // One CTA per SM: a producer warp walks the range, resolves pages and TMA-loads K
-// and V tiles into a ring; eight consumer warps, each with 16 keys of every tile, a
-// running maximum, sum and accumulator of its own, so steps need no exchange.  At
-// an item's end the warps meet in shared memory.
+// and V tiles into a ring; eleven consumer warps take units of 16 keys (of both tiles
+// of a step) in turn, each with a running maximum, sum and accumulator of its own,
+// so steps need no exchange.  At an item's end the warps meet in shared memory.
 // bf16 rows: P is multiplied as two bf16 parts, high and low, so that its rounding
 // (2^-17) does not add to the result's.  8-bit rows: fp16 products, since a
 // code is an fp16 number (one conversion instruction for two; to bf16 it takes
@@ -45,26 +45,32 @@ constexpr int kShortSmem = 232448;
 constexpr int kShortCtrl = 7168;
 constexpr int kShortMaxSlots = 16;
 constexpr int kShortInfos = 4;      // step descriptions ahead
-constexpr int kWarps = 8;           // consumer warps
+constexpr int kWarps = 11;          // consumer warps
+constexpr int kShortItems = 4;      // item descriptions ahead
 constexpr int kThreads = (kWarps + 1) * 32;
 
-enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8 };
+enum : int { kMask = 1, kOne = 2 };  // of a step: some row sees a part of it only; it is one tile
+constexpr int kHaveBit = 2;
 
-struct ShortInfo {
+struct ShortInfo {      // a step
     int flags;          // and from kHaveBit on, per tile, the halves that lie in a page
     int base[2];        // first slot of each tile
-    // of the item, read with its first step
+    int slot;           // ring slot of the first K tile, bit 31: its phase
+};
+struct ShortItem {
+    int step0, steps;   // its steps of this CTA; steps < 0: no more items
     int row0, rows, h;  // first token, query rows, key head
     int ctx, end;       // slot of the first new token, slot behind the last one
     int part;           // -1: write the output, else the partial slot
 };
-constexpr int kHaveBit = 8;
 
 struct ShortCtrl {
     uint64_t t_full[kShortMaxSlots], t_empty[kShortMaxSlots];
-    uint64_t i_empty[kShortInfos];
+    uint64_t i_full[kShortInfos], i_empty[kShortInfos];
+    uint64_t it_full[kShortItems], it_empty[kShortItems];
     uint64_t st_full, x_full;  // all consumers posted their sums, their parts of O
     ShortInfo info[kShortInfos];
+    ShortItem item[kShortItems];
     float2 stats[kWarps][16];  // [warp][row]
     int red[kWarps + 1];
     WaitFlag wf;
@@ -83,7 +89,7 @@ struct ShortParams {
 
 template <int D, bool Q8, int NT>
 struct ShortCfg {
-    static constexpr int SUB = NT == 1 ? 2 : 1;       // tiles of a step
+    static constexpr int SUB = NT == 1 ? 2 : 1;       // tiles of a step, at most
     static constexpr int ROWB = Q8 ? D : 128;         // bytes of a row of a box
     static constexpr int NBOX = Q8 ? 1 : D / 64;
     static constexpr int BOX = kTile * ROWB;
@@ -97,26 +103,37 @@ struct ShortCfg {
     static_assert(SLOTS >= 2 * SUB, "ring too small");
 };
 
-// Steps (of SUB tiles) of a short sequence's item; 0: it has no new tokens or is not short.
-template <int SUB>
-__device__ __forceinline__ int short_steps(const ChunkCommon& p, int b, bool report) {
+// Steps (of `sub` tiles) of a short sequence's item; 0: it has no new tokens or is not short.
+__device__ __forceinline__ int short_steps(const ChunkCommon& p, int b, int sub, bool report) {
     const Seq s = sequence(p, b, report);
     if (s.n == 0 || s.n * (int64_t)p.G > kShortRows) return 0;
-    return (visible_span(p, s.ctx, s.ctx + s.n).steps + SUB - 1) / SUB;
+    return (visible_span(p, s.ctx, s.ctx + s.n).steps + sub - 1) / sub;
 }
 
 // ---------------------------------------------------------------- producer
 template <int D, bool Q8, int NT>
 __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, const ShortParams& p, uint8_t* sT,
-                               uint8_t* sS, ShortCtrl* c, int lo, int hi, int per, volatile WaitFlag* wf) {
+                               uint8_t* sS, ShortCtrl* c, int lo, int hi, int per, int sub, volatile WaitFlag* wf) {
     using C = ShortCfg<D, Q8, NT>;
     const ChunkCommon& cc = p.c;
-    const int lane = threadIdx.x & 31, Hkv = cc.Hkv, ppt = kTile / cc.page, pps = C::SUB * ppt;
+    const int lane = threadIdx.x & 31, Hkv = cc.Hkv, ppt = kTile / cc.page, pps = sub * ppt;
     const bool leader = elect_one();
     constexpr uint32_t infos = kShortInfos;
-    uint32_t slot = 0, phase = 0, nload = 0, g = 0;
-    bool ok = true, ended = false;
+    uint32_t slot = 0, phase = 0, nload = 0, g = 0, ni = 0;
+    bool ok = true;
     PartMeta mt{-1, 0, per, 0, 0, 0, {0, 0}};
+    // the next item's description, as soon as there is room
+    auto announce = [&](const ShortItem& it) -> bool {
+        const uint32_t x = ni % kShortItems;
+        if (ni >= kShortItems && !warp_wait(&c->it_empty[x], ((ni / kShortItems) & 1) ^ 1, wf)) return false;
+        if (leader) {
+            c->item[x] = it;
+            mbar_arrive(&c->it_full[x]);
+        }
+        __syncwarp();
+        ++ni;
+        return true;
+    };
     if (lo < hi) {
         int u = 0;  // the sequence that holds step lo: last one whose first step is not behind it
         for (int span = p.units; span > 1;) {
@@ -138,6 +155,10 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
             const bool whole = s0 == 0 && start + s1 == end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
             if (start < lo) mt = PartMeta{start, end, per, sq.row0, sq.n, h, {0, 0}};
+            if (!announce(ShortItem{(int)g, s1 - s0, sq.row0, sq.n * cc.G, h, sq.ctx, seq_end, part})) {
+                ok = false;
+                break;
+            }
             for (int e0 = s0 * pps; e0 < s1 * pps && ok; e0 += 32) {
                 // 32 pages resolved at a time
                 const int e = e0 + lane, tl = e / ppt;
@@ -152,6 +173,7 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                         y0[x] = __shfl_sync(0xffffffffu, y, q + x * ppt);
                         y1[x] = __shfl_sync(0xffffffffu, y, q + x * ppt + ppt - 1);
                     }
+                    const int nx = min(sub, max(1, sp.steps - st * sub));  // its tiles
                     const uint32_t is = g % infos;
                     if (g >= infos && !warp_wait(&c->i_empty[is], ((g / infos) & 1) ^ 1, wf)) {
                         ok = false;
@@ -163,7 +185,8 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                         int have = 0;
 #pragma unroll
                         for (int x = 0; x < C::SUB; ++x) {
-                            const int first = sp.tile(st * C::SUB + x) * kTile;
+                            if (x >= nx) continue;
+                            const int first = sp.tile(st * sub + x) * kTile;
                             const int hv = ppt == 1 ? (y0[x] >= 0 ? 3 : 0) : (y0[x] >= 0 ? 1 : 0) | (y1[x] >= 0 ? 2 : 0);
                             // every row sees all of it: up to the first token, inside the last one's window
                             plain &= hv == 3 && first + kTile <= sq.ctx + 1 &&
@@ -171,21 +194,17 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                             have |= hv << (2 * x);
                             f.base[x] = first;
                         }
-                        f.flags = (st == s0 ? kFirst : 0) | (st + 1 == s1 ? kLast : 0) | (plain ? 0 : kMask) |
-                                  have << kHaveBit;
-                        f.row0 = sq.row0;
-                        f.rows = sq.n * cc.G;
-                        f.h = h;
-                        f.ctx = sq.ctx;
-                        f.end = seq_end;
-                        f.part = part;
+                        f.flags = (plain ? 0 : kMask) | (nx == 1 ? kOne : 0) | have << kHaveBit;
+                        f.slot = (int)(slot | phase << 31);
+                        mbar_arrive(&c->i_full[is]);
                     }
                     __syncwarp();
                     ++g;
 #pragma unroll
-                    for (int kv = 0; kv < 2 * C::SUB; ++kv) {
+                    for (int kv = 0; kv < 2 * C::SUB; ++kv) {  // K tiles, then V tiles
                         const bool val = kv >= C::SUB;
                         const int r0 = y0[kv % C::SUB], r1 = y1[kv % C::SUB];
+                        if (kv % C::SUB >= nx) continue;
                         if (nload >= (uint32_t)p.n_slots && !warp_wait(&c->t_empty[slot], phase ^ 1, wf)) {
                             ok = false;
                             break;
@@ -227,27 +246,14 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
             }
         }
     }
-    if (ok) {
-        // the end mark, with a slot's barrier
-        const uint32_t is = g % infos;
-        if ((g < infos || warp_wait(&c->i_empty[is], ((g / infos) & 1) ^ 1, wf)) &&
-            (nload < (uint32_t)p.n_slots || warp_wait(&c->t_empty[slot], phase ^ 1, wf)) && leader) {
-            c->info[is].flags = kEnd;
-            mbar_arrive(&c->t_full[slot]);
-            ended = true;
-        }
-    }
+    if (ok) announce(ShortItem{0, -1, 0, 0, 0, 0, 0, 0});
     if (lane == 0) p.meta[blockIdx.x] = mt;
     __syncwarp();
     if (leader) {
-        // copies still in flight must land before the CTA exits (the end mark used
-        // the slot of the oldest one, which was consumed before)
+        // copies still in flight must land before the CTA exits
         const uint32_t ns = (uint32_t)p.n_slots;
-        const uint32_t from = nload > ns ? nload - ns : 0;
-        for (uint32_t n = from; n < nload; ++n) {
-            if (ended && n % ns == nload % ns) continue;
+        for (uint32_t n = nload > ns ? nload - ns : 0; n < nload; ++n)
             mbar_wait_drain(&c->t_full[n % ns], (n / ns) & 1);
-        }
     }
 }
 
@@ -271,11 +277,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // Two e4m3 codes (the low or high half of w) as fp16, exactly.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w, int high) {
     uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "mov.b32 {lo, hi}, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-        : "=r"(r)
-        : "r"(high ? w >> 16 : w));
+    if (high)
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %1;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+            : "=r"(r)
+            : "r"(w));
+    else
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %1;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+            : "=r"(r)
+            : "r"(w));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -317,44 +330,19 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
     constexpr int KS = D / 16, SUB = C::SUB;
     const ChunkCommon& cc = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, cq = lane & 3;
-    const int slab = warp * 16;
     uint32_t qf[KS][NT][2];
     float o[KS][NT][4];
     float m[NT][2], l[NT][2], sl[NT][2];
-    int vref = 0;  // 8-bit: the scale byte that O counts in (0: none yet)
-    int row0 = 0, rows = 0, h = 0, ctx = 0, end = 0, part = 0;
-    uint32_t slot = 0, phase = 0, items = 0;
-    for (uint32_t gs = 0;; ++gs) {
-        if (!warp_wait(&c->t_full[slot], phase, wf)) return;
-        const uint32_t is = gs % kShortInfos;
-        const ShortInfo& f = c->info[is];
-        const int flags = f.flags;
-        int base[SUB];
-#pragma unroll
-        for (int x = 0; x < SUB; ++x) base[x] = f.base[x];
-        if (flags & kFirst) {
-            row0 = f.row0;
-            rows = f.rows;
-            h = f.h;
-            ctx = f.ctx;
-            end = f.end;
-            part = f.part;
-        }
+    for (uint32_t items = 0;; ++items) {
+        const uint32_t ii = items % kShortItems;
+        if (!warp_wait(&c->it_full[ii], (items / kShortItems) & 1, wf)) return;
+        const ShortItem it = c->item[ii];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->i_empty[is]);
-        if (flags & kEnd) return;
-        uint32_t ts[2 * SUB], tp[2 * SUB];  // slots and phases of the K and V tiles
-#pragma unroll
-        for (int x = 0; x < 2 * SUB; ++x) {
-            ts[x] = slot;
-            tp[x] = phase;
-            if (++slot == (uint32_t)p.n_slots) {
-                slot = 0;
-                phase ^= 1;
-            }
-        }
-        if (flags & kFirst) {
-            vref = 0;
+        if (lane == 0) mbar_arrive(&c->it_empty[ii]);
+        if (it.steps < 0) return;
+        const int row0 = it.row0, rows = it.rows, h = it.h, ctx = it.ctx, end = it.end, part = it.part;
+        int vref = 0;  // 8-bit: the scale byte that O counts in (0: none yet)
+        {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int r = 8 * nt + g;
@@ -405,260 +393,298 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                     for (int i = 0; i < 4; ++i) o[t][nt][i] = 0.f;
             }
         }
-        float s[SUB][NT][4];
-        uint32_t kb[SUB][2];  // 8-bit: the scale bytes of keys g and g + 8
+        // Eight units of 16 keys (of each of its tiles) to a step; the warps take them in turn.
+        const uint32_t u0 = (uint32_t)it.step0 * 8, u1 = u0 + (uint32_t)it.steps * 8;
+        for (uint32_t unit = u0 + (warp + kWarps - u0 % kWarps) % kWarps; unit < u1; unit += kWarps) {
+            const uint32_t gs = unit >> 3, is = gs % kShortInfos;
+            const int slab = (int)(unit & 7) * 16;
+            if (!warp_wait(&c->i_full[is], (gs / kShortInfos) & 1, wf)) return;
+            const int flags = c->info[is].flags;
+            int base[SUB];
 #pragma unroll
-        for (int x = 0; x < SUB; ++x) {
+            for (int x = 0; x < SUB; ++x) base[x] = c->info[is].base[x];
+            uint32_t slot = (uint32_t)c->info[is].slot & 0x7fffffffu, phase = (uint32_t)c->info[is].slot >> 31;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->i_empty[is]);
+            const int nx = flags & kOne ? 1 : SUB;
+            uint32_t ts[2 * SUB], tp[2 * SUB];  // slots and phases of the K and V tiles
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int x = 0; x < 2 * SUB; ++x) {
+                if (x % SUB >= nx) {  // not there: what the one before it holds is read and not used
+                    ts[x] = ts[x - 1];
+                    tp[x] = tp[x - 1];
+                    continue;
+                }
+                ts[x] = slot;
+                tp[x] = phase;
+                if (++slot == (uint32_t)p.n_slots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            float s[SUB][NT][4];
+            uint32_t kb[SUB][2];  // 8-bit: the scale bytes of keys g and g + 8
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[x][nt][i] = 0.f;
-            if (x > 0 && !warp_wait(&c->t_full[ts[x]], tp[x], wf)) return;
-        }
-        if (Q8) {
-            uint4 kr[SUB][2][D / 64];
+            for (int x = 0; x < SUB; ++x) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[x][nt][i] = 0.f;
+                if (x < nx && !warp_wait(&c->t_full[ts[x]], tp[x], wf)) return;
+            }
+            if (Q8) {
+                uint4 kr[SUB][2][D / 64];
+#pragma unroll
+                for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        kb[x][r] = sS[ts[x] * kTile + slab + g + 8 * r];
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i)
+                            kr[x][r][i] = *reinterpret_cast<const uint4*>(
+                                chunk_at<C::ROWB>(sT + ts[x] * C::TILE, slab + g + 8 * r, (D / 64) * cq + i));
+                    }
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+#pragma unroll
+                    for (int x = 0; x < SUB; ++x) {
+                        const uint32_t w0 = word(kr[x][0][j / 4], j % 4), w1 = word(kr[x][1][j / 4], j % 4);
+                        const uint32_t a[4] = {codes_f16(w0, 0), codes_f16(w1, 0), codes_f16(w0, 1), codes_f16(w1, 1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[x][nt], a, qf[j][nt][0], qf[j][nt][1]);
+                    }
+            } else {
+#pragma unroll
+                for (int q = 0; q < KS / 2; ++q)
+#pragma unroll
+                    for (int x = 0; x < SUB; ++x) {
+                        uint4 kr[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            kr[r] = *reinterpret_cast<const uint4*>(chunk_at<128>(
+                                sT + ts[x] * C::TILE + (q >> 1) * C::BOX, slab + g + 8 * r, 2 * cq + (q & 1)));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t a[4] = {word(kr[0], 2 * i), word(kr[1], 2 * i), word(kr[0], 2 * i + 1),
+                                                   word(kr[1], 2 * i + 1)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(s[x][nt], a, qf[2 * q + i][nt][0], qf[2 * q + i][nt][1]);
+                        }
+                    }
+            }
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < SUB; ++x)
+                    if (x < nx) mbar_arrive(&c->t_empty[ts[x]]);
+            }
+            // s[x][nt]: key g rows 2 cq, 2 cq + 1; key g + 8 the same rows
+            bool grow = false;
 #pragma unroll
             for (int x = 0; x < SUB; ++x)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    kb[x][r] = sS[ts[x] * kTile + slab + g + 8 * r];
+                for (int i = 0; i < 4; ++i) {
+                    // 2^e (a byte of an unwritten slot is hidden below, whatever comes of it)
+                    const float ke = Q8 ? __uint_as_float(kb[x][i >> 1] << 23) : 1.f;
 #pragma unroll
-                    for (int i = 0; i < D / 64; ++i)
-                        kr[x][r][i] = *reinterpret_cast<const uint4*>(
-                            chunk_at<C::ROWB>(sT + ts[x] * C::TILE, slab + g + 8 * r, (D / 64) * cq + i));
+                    for (int nt = 0; nt < NT; ++nt) s[x][nt][i] *= Q8 ? sl[nt][i & 1] * ke : sl[nt][i & 1];
                 }
+            if (flags & kMask) {
 #pragma unroll
-            for (int j = 0; j < KS; ++j)
+                for (int x = 0; x < SUB; ++x)
 #pragma unroll
-                for (int x = 0; x < SUB; ++x) {
-                    const uint32_t w0 = word(kr[x][0][j / 4], j % 4), w1 = word(kr[x][1][j / 4], j % 4);
-                    const uint32_t a[4] = {codes_f16(w0, 0), codes_f16(w1, 0), codes_f16(w0, 1), codes_f16(w1, 1)};
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[x][nt], a, qf[j][nt][0], qf[j][nt][1]);
-                }
-        } else {
-#pragma unroll
-            for (int q = 0; q < KS / 2; ++q)
-#pragma unroll
-                for (int x = 0; x < SUB; ++x) {
-                    uint4 kr[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        kr[r] = *reinterpret_cast<const uint4*>(chunk_at<128>(
-                            sT + ts[x] * C::TILE + (q >> 1) * C::BOX, slab + g + 8 * r, 2 * cq + (q & 1)));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t a[4] = {word(kr[0], 2 * i), word(kr[1], 2 * i), word(kr[0], 2 * i + 1),
-                                               word(kr[1], 2 * i + 1)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<false>(s[x][nt], a, qf[2 * q + i][nt][0], qf[2 * q + i][nt][1]);
-                    }
-                }
-        }
-        __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-            for (int x = 0; x < SUB; ++x) mbar_arrive(&c->t_empty[ts[x]]);
-        }
-        // s[x][nt]: key g rows 2 cq, 2 cq + 1; key g + 8 the same rows
-        bool grow = false;
-#pragma unroll
-        for (int x = 0; x < SUB; ++x)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // 2^e (a byte of an unwritten slot is hidden below, whatever comes of it)
-                const float ke = Q8 ? __uint_as_float(kb[x][i >> 1] << 23) : 1.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s[x][nt][i] *= Q8 ? sl[nt][i & 1] * ke : sl[nt][i & 1];
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * nt + 2 * cq + (i & 1), key = slab + g + 8 * (i >> 1), u = base[x] + key;
+                            const int pos = ctx + r / cc.G;
+                            const bool see = r < rows && ((flags >> (kHaveBit + 2 * x + (key >> 6))) & 1) && u <= pos &&
+                                             (cc.window <= 0 || u > pos - cc.window || u < cc.sinks);
+                            if (!see) s[x][nt][i] = -INFINITY;
+                        }
             }
-        if (flags & kMask) {
+            if (nx < SUB) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[SUB - 1][nt][i] = -INFINITY;
+            }
 #pragma unroll
             for (int x = 0; x < SUB; ++x)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 8 * nt + 2 * cq + (i & 1), key = slab + g + 8 * (i >> 1), u = base[x] + key;
-                        const int pos = ctx + r / cc.G;
-                        const bool see = r < rows && ((flags >> (kHaveBit + 2 * x + (key >> 6))) & 1) && u <= pos &&
-                                         (cc.window <= 0 || u > pos - cc.window || u < cc.sinks);
-                        if (!see) s[x][nt][i] = -INFINITY;
-                    }
-        }
+                    for (int i = 0; i < 4; ++i) grow |= s[x][nt][i] > m[nt][i & 1] + 8.f;
+            // the reference follows the maximum only where it grows by more than 2^8
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int x = 0; x < SUB; ++x)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                    for (int i = 0; i < 2; ++i) {
+                        float top = m[nt][i];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) grow |= s[x][nt][i] > m[nt][i & 1] + 8.f;
-        // the reference follows the maximum only where it grows by more than 2^8
-        if (__any_sync(0xffffffffu, grow)) {
+                        for (int x = 0; x < SUB; ++x) top = fmax3(top, s[x][nt][i], s[x][nt][i + 2]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const float w = top == -INFINITY ? 1.f : ex2_approx(m[nt][i] - top);
+                        m[nt][i] = top;
+                        l[nt][i] *= w;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float top = m[nt][i];
-#pragma unroll
-                    for (int x = 0; x < SUB; ++x) top = fmax3(top, s[x][nt][i], s[x][nt][i + 2]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const float w = top == -INFINITY ? 1.f : ex2_approx(m[nt][i] - top);
-                    m[nt][i] = top;
-                    l[nt][i] *= w;
-#pragma unroll
-                    for (int t = 0; t < KS; ++t) {
-                        o[t][nt][i] *= w;
-                        o[t][nt][i + 2] *= w;
-                    }
-                }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ref = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
-#pragma unroll
-                for (int x = 0; x < SUB; ++x) {
-                    s[x][nt][i] = ex2_approx(s[x][nt][i] - ref);
-                    l[nt][i & 1] += s[x][nt][i];
-                }
-            }
-#pragma unroll
-        for (int x = 0; x < SUB; ++x)
-            if (!warp_wait(&c->t_full[ts[SUB + x]], tp[SUB + x], wf)) return;
-        if (Q8) {
-            // Values are fp16 codes; their scales go into the weights, relative to the
-            // largest one met (with room for the next ones): 2^7 p 2^(e - ref) is at most
-            // 2^14, and down to 2^-21 of what a weight of 1 gives it is a normal number.
-            uint32_t vb[SUB][2], top = 0;
-#pragma unroll
-            for (int x = 0; x < SUB; ++x)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int key = slab + g + 8 * k;
-                    vb[x][k] = sS[ts[SUB + x] * kTile + key];
-                    if ((flags & kMask) &&
-                        !(((flags >> (kHaveBit + 2 * x + (key >> 6))) & 1) && base[x] + key < end))
-                        vb[x][k] = 0;
-                    top = max(top, vb[x][k]);
-                }
-            if (__any_sync(0xffffffffu, (int)top > vref)) {
-                const int to = (int)__reduce_max_sync(0xffffffffu, top) + 1;
-                const float w = vref ? exp2_int(max(vref - to, -126)) : 0.f;
-                vref = to;
-#pragma unroll
-                for (int t = 0; t < KS; ++t)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[t][nt][i] *= w;
-            }
-#pragma unroll
-            for (int x = 0; x < SUB; ++x)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float w = exp2_int(max((int)vb[x][k] - vref + 7, -126));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) s[x][nt][2 * k + i] *= w;
-                }
-        }
-        uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
-#pragma unroll
-        for (int x = 0; x < SUB; ++x)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float a = s[x][nt][2 * k], b = s[x][nt][2 * k + 1];
-                    if (Q8) {
-                        hi[x][nt][k] = transpose8x8(pack_f16x2(a, b));
-                    } else {
-                        const uint32_t h2 = pack_bf16x2(a, b);
-                        hi[x][nt][k] = transpose8x8(h2);
-                        lo[x][nt][k] = transpose8x8(
-                            pack_bf16x2(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u)));
-                    }
-                }
-        // keys 2 cq, 2 cq + 1 and 2 cq + 8, 2 cq + 9
-#pragma unroll
-        for (int x = 0; x < SUB; ++x) {
-            const uint8_t* vt = sT + ts[SUB + x] * C::TILE;
-            if (Q8) {
-                constexpr int W = D / 32;  // words of the lane's values in a key's row
-                uint32_t vw[4][W];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = slab + 2 * cq + 8 * (k >> 1) + (k & 1);
-                    if (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(chunk_at<C::ROWB>(vt, row, g));
-#pragma unroll
-                        for (int i = 0; i < W; ++i) vw[k][i] = word(v, i);
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(chunk_at<C::ROWB>(vt, row, g >> 1) + 8 * (g & 1));
-                        vw[k][0] = v.x;
-                        vw[k][1] = v.y;
-                    }
-                    // codes behind the last token may be NaN, and 0 * NaN is none of the sum
-                    if ((flags & kMask) && base[x] + row >= end) {
-#pragma unroll
-                        for (int i = 0; i < W; ++i) vw[k][i] = 0;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {  // tile 2 i + t: bytes 2 t and 2 t + 1 of the word, key by key
-                        uint32_t a[4];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t w = __byte_perm(vw[2 * k][i], vw[2 * k + 1][i], t ? 0x7362 : 0x5140);
-                            a[2 * k] = codes_f16(w, 0);
-                            a[2 * k + 1] = codes_f16(w, 1);
+                        for (int t = 0; t < KS; ++t) {
+                            o[t][nt][i] *= w;
+                            o[t][nt][i + 2] *= w;
                         }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[2 * i + t][nt], a, hi[x][nt][0], hi[x][nt][1]);
                     }
-            } else {
-                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                if (flags & kMask) {
-                    // rows behind the last token may hold NaN, and 0 * NaN is none of the sum
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float ref = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
+#pragma unroll
+                    for (int x = 0; x < SUB; ++x) {
+                        s[x][nt][i] = ex2_approx(s[x][nt][i] - ref);
+                        l[nt][i & 1] += s[x][nt][i];
+                    }
+                }
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
+                if (x < nx && !warp_wait(&c->t_full[ts[SUB + x]], tp[SUB + x], wf)) return;
+            if (Q8) {
+                // Values are fp16 codes; their scales go into the weights, relative to the
+                // largest one met (with room for the next ones): 2^7 p 2^(e - ref) is at most
+                // 2^14, and down to 2^-21 of what a weight of 1 gives it is a normal number.
+                uint32_t vb[SUB][2], top = 0;
+#pragma unroll
+                for (int x = 0; x < SUB; ++x)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int u = base[x] + slab + 2 * cq + 8 * k;
-                        keep[k] = (u < end ? 0xffffu : 0u) | (u + 1 < end ? 0xffff0000u : 0u);
+                        const int key = slab + g + 8 * k;
+                        vb[x][k] = sS[ts[SUB + x] * kTile + key];
+                        if ((flags & kMask) &&
+                            !(((flags >> (kHaveBit + 2 * x + (key >> 6))) & 1) && base[x] + key < end))
+                            vb[x][k] = 0;
+                        if (x >= nx) vb[x][k] = 0;
+                        top = max(top, vb[x][k]);
                     }
+                if (__any_sync(0xffffffffu, (int)top > vref)) {
+                    const int to = (int)__reduce_max_sync(0xffffffffu, top) + 1;
+                    const float w = vref ? exp2_int(max(vref - to, -126)) : 0.f;
+                    vref = to;
+#pragma unroll
+                    for (int t = 0; t < KS; ++t)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[t][nt][i] *= w;
                 }
 #pragma unroll
-                for (int bx = 0; bx < D / 64; ++bx) {
-                    uint4 v[4];
+                for (int x = 0; x < SUB; ++x)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = *reinterpret_cast<const uint4*>(
-                            chunk_at<128>(vt + bx * C::BOX, slab + 2 * cq + 8 * (k >> 1) + (k & 1), g));
+                    for (int k = 0; k < 2; ++k) {
+                        const float w = exp2_int(max((int)vb[x][k] - vref + 7, -126));
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        uint32_t a[4];
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) s[x][nt][2 * k + i] *= w;
+                    }
+            }
+            uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float a = s[x][nt][2 * k], b = s[x][nt][2 * k + 1];
+                        if (Q8) {
+                            hi[x][nt][k] = transpose8x8(pack_f16x2(a, b));
+                        } else {
+                            const uint32_t h2 = pack_bf16x2(a, b);
+                            hi[x][nt][k] = transpose8x8(h2);
+                            lo[x][nt][k] = transpose8x8(
+                                pack_bf16x2(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u)));
+                        }
+                    }
+            // keys 2 cq, 2 cq + 1 and 2 cq + 8, 2 cq + 9
+#pragma unroll
+            for (int x = 0; x < SUB; ++x) {
+                if (x >= nx) continue;
+                const uint8_t* vt = sT + ts[SUB + x] * C::TILE;
+                if (Q8) {
+                    constexpr int W = D / 32;  // words of the lane's values in a key's row
+                    uint32_t vw[4][W];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = slab + 2 * cq + 8 * (k >> 1) + (k & 1);
+                        if (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(chunk_at<C::ROWB>(vt, row, g));
+#pragma unroll
+                            for (int i = 0; i < W; ++i) vw[k][i] = word(v, i);
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(chunk_at<C::ROWB>(vt, row, g >> 1) + 8 * (g & 1));
+                            vw[k][0] = v.x;
+                            vw[k][1] = v.y;
+                        }
+                        // codes behind the last token may be NaN, and 0 * NaN is none of the sum
+                        if ((flags & kMask) && base[x] + row >= end) {
+#pragma unroll
+                            for (int i = 0; i < W; ++i) vw[k][i] = 0;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {  // tile 2 i + t: bytes 2 t and 2 t + 1 of the word, key by key
+                            uint32_t a[4];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t w = __byte_perm(vw[2 * k][i], vw[2 * k + 1][i], t ? 0x7362 : 0x5140);
+                                a[2 * k] = codes_f16(w, 0);
+                                a[2 * k + 1] = codes_f16(w, 1);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[2 * i + t][nt], a, hi[x][nt][0], hi[x][nt][1]);
+                        }
+                } else {
+                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+                    if (flags & kMask) {
+                        // rows behind the last token may hold NaN, and 0 * NaN is none of the sum
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t va = word(v[2 * k], t), vb = word(v[2 * k + 1], t);
-                            a[2 * k] = __byte_perm(va, vb, 0x5410) & keep[k];
-                            a[2 * k + 1] = __byte_perm(va, vb, 0x7632) & keep[k];
+                            const int u = base[x] + slab + 2 * cq + 8 * k;
+                            keep[k] = (u < end ? 0xffffu : 0u) | (u + 1 < end ? 0xffff0000u : 0u);
                         }
+                    }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816<false>(o[4 * bx + t][nt], a, hi[x][nt][0], hi[x][nt][1]);
-                            mma16816<false>(o[4 * bx + t][nt], a, lo[x][nt][0], lo[x][nt][1]);
+                    for (int bx = 0; bx < D / 64; ++bx) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = *reinterpret_cast<const uint4*>(
+                                chunk_at<128>(vt + bx * C::BOX, slab + 2 * cq + 8 * (k >> 1) + (k & 1), g));
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            uint32_t a[4];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t va = word(v[2 * k], t), vb = word(v[2 * k + 1], t);
+                                a[2 * k] = __byte_perm(va, vb, 0x5410) & keep[k];
+                                a[2 * k + 1] = __byte_perm(va, vb, 0x7632) & keep[k];
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816<false>(o[4 * bx + t][nt], a, hi[x][nt][0], hi[x][nt][1]);
+                                mma16816<false>(o[4 * bx + t][nt], a, lo[x][nt][0], lo[x][nt][1]);
+                            }
                         }
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->t_empty[ts[SUB + x]]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->t_empty[ts[SUB + x]]);
         }
-        if (!(flags & kLast)) continue;
         // The item's end: all warps' sums and accumulators meet.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -691,7 +717,6 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->x_full);
         if (!warp_wait(&c->x_full, items & 1, wf)) return;
-        ++items;
         for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
             const int r = x / (D / 4), d = x % (D / 4) * 4;
             float top = -INFINITY, sum = 0.f;
@@ -747,9 +772,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = threadIdx.x;
         if (x < kShortMaxSlots) {
             mbar_init(&c->t_full[x], 1);
-            mbar_init(&c->t_empty[x], kWarps);
+            mbar_init(&c->t_empty[x], 8);  // a warp for each of its units
         } else if (x < kShortMaxSlots + kShortInfos) {
-            mbar_init(&c->i_empty[x - kShortMaxSlots], kWarps);
+            mbar_init(&c->i_full[x - kShortMaxSlots], 1);
+            mbar_init(&c->i_empty[x - kShortMaxSlots], 8);
+        } else if (x < kShortMaxSlots + kShortInfos + kShortItems) {
+            mbar_init(&c->it_full[x - kShortMaxSlots - kShortInfos], 1);
+            mbar_init(&c->it_empty[x - kShortMaxSlots - kShortInfos], kWarps);
         } else if (x == 32) {
             mbar_init(&c->st_full, kWarps);
             mbar_init(&c->x_full, kWarps);
@@ -768,28 +797,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     // prefix sums of the sequences' steps per item: every thread a run of them, then a scan
     const int run = (p.units + kThreads - 1) / kThreads;
     const int u0 = min(p.units, (int)threadIdx.x * run), u1 = min(p.units, u0 + run);
-    int sum = 0;
-    for (int u = u0; u < u1; ++u) {
-        sum += short_steps<C::SUB>(p.c, p.unit0 + u, blockIdx.x == 0);
-        c->prefix[u + 1] = sum;
-    }
-    int incl = sum;
+    auto sums = [&](int sub, bool report) {
+        int sum = 0;
+        for (int u = u0; u < u1; ++u) {
+            sum += short_steps(p.c, p.unit0 + u, sub, report);
+            c->prefix[u + 1] = sum;
+        }
+        int incl = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) c->red[warp] = incl;
+        __syncthreads();
+        const int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? c->red[lane] : 0);
+        for (int u = u0; u < u1; ++u) c->prefix[u + 1] += before;
+        __syncthreads();
+    };
+    int sub = C::SUB;
+    sums(sub, blockIdx.x == 0);
+    if (C::SUB > 1 && 2 * (int64_t)c->prefix[p.units] * p.c.Hkv <= (int)gridDim.x) {
+        // fewer steps than half of the SMs: single tiles
+        __syncthreads();
+        sub = 1;
+        sums(sub, false);
     }
-    if (lane == 31) c->red[warp] = incl;
-    __syncthreads();
-    const int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? c->red[lane] : 0);
-    for (int u = u0; u < u1; ++u) c->prefix[u + 1] += before;
-    __syncthreads();
     const int total = c->prefix[p.units] * p.c.Hkv;
     const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
     volatile WaitFlag* wf = &c->wf;
     if (warp == kWarps)
-        short_producer<D, Q8, NT>(&tk, &tv, p, sT, sS, c, lo, hi, per, wf);
+        short_producer<D, Q8, NT>(&tk, &tv, p, sT, sS, c, lo, hi, per, sub, wf);
     else
         short_consumer<D, Q8, NT>(p, sT, sS, xch, c, wf);
     __syncwarp();
