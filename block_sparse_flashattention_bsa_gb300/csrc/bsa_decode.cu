@@ -21,9 +21,10 @@
 // order: no atomics, results do not depend on timing.
 //
 // One CTA per SM: a producer warp walks the range, resolves pages and TMA-loads K
-// and V tiles into a ring; eleven consumer warps take units of 16 keys (of both tiles
-// of a step) in turn, each with a running maximum, sum and accumulator of its own,
-// so steps need no exchange.  At an item's end the warps meet in shared memory.
+// and V tiles into a ring, and an item's queries; ten consumer warps take units of 16
+// keys (of both tiles of a step) in turn, each with a running maximum, sum and
+// accumulator of its own, so steps need no exchange; what they have at an item's end
+// one more warp joins while they go on.
 // bf16 rows: P is multiplied as two bf16 parts, high and low, so that its rounding
 // (2^-17) does not add to the result's.  8-bit rows: fp16 products, since a
 // code is an fp16 number (one conversion instruction for two; to bf16 it takes
@@ -45,9 +46,10 @@ constexpr int kShortSmem = 232448;
 constexpr int kShortCtrl = 7168;
 constexpr int kShortMaxSlots = 16;
 constexpr int kShortInfos = 4;      // step descriptions ahead
-constexpr int kWarps = 11;          // consumer warps
-constexpr int kShortItems = 4;      // item descriptions ahead
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 10;          // consumer warps
+constexpr int kJoiner = kWarps, kProducer = kWarps + 1;
+constexpr int kShortItems = 2;      // items ahead
+constexpr int kThreads = (kWarps + 2) * 32;
 
 enum : int { kMask = 1, kOne = 2 };  // of a step: some row sees a part of it only; it is one tile
 constexpr int kHaveBit = 2;
@@ -68,11 +70,11 @@ struct ShortCtrl {
     uint64_t t_full[kShortMaxSlots], t_empty[kShortMaxSlots];
     uint64_t i_full[kShortInfos], i_empty[kShortInfos];
     uint64_t it_full[kShortItems], it_empty[kShortItems];
-    uint64_t st_full, x_full;  // all consumers posted their sums, their parts of O
+    uint64_t x_full, x_empty;  // all consumers posted their part of an item; it has been read
     ShortInfo info[kShortInfos];
     ShortItem item[kShortItems];
     float2 stats[kWarps][16];  // [warp][row]
-    int red[kWarps + 1];
+    int red[kThreads / 32];
     WaitFlag wf;
     int prefix[kShortUnits + 1];
 };
@@ -96,7 +98,8 @@ struct ShortCfg {
     static constexpr int TILE = NBOX * BOX;
     static constexpr int PITCH = D + 4;               // floats of an exchanged row
     static constexpr int XCH = kWarps * 8 * NT * PITCH * 4;
-    static constexpr int FIXED = XCH + kShortCtrl + (Q8 ? kShortMaxSlots * kTile : 0);
+    static constexpr int QROWS = 8 * NT, QBUF = kShortItems * QROWS * D * 2;  // items' queries
+    static constexpr int FIXED = XCH + QBUF + kShortCtrl + (Q8 ? kShortMaxSlots * kTile : 0);
     static constexpr int FIT = (kShortSmem - FIXED) / TILE;
     static constexpr int SLOTS = FIT > kShortMaxSlots ? kShortMaxSlots : FIT;
     static constexpr int SMEM = SLOTS * TILE + FIXED;
@@ -113,7 +116,8 @@ __device__ __forceinline__ int short_steps(const ChunkCommon& p, int b, int sub,
 // ---------------------------------------------------------------- producer
 template <int D, bool Q8, int NT>
 __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, const ShortParams& p, uint8_t* sT,
-                               uint8_t* sS, ShortCtrl* c, int lo, int hi, int per, int sub, volatile WaitFlag* wf) {
+                               uint8_t* sS, __nv_bfloat16* sQ, ShortCtrl* c, int lo, int hi, int per, int sub,
+                               volatile WaitFlag* wf) {
     using C = ShortCfg<D, Q8, NT>;
     const ChunkCommon& cc = p.c;
     const int lane = threadIdx.x & 31, Hkv = cc.Hkv, ppt = kTile / cc.page, pps = sub * ppt;
@@ -122,13 +126,22 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
     uint32_t slot = 0, phase = 0, nload = 0, g = 0, ni = 0;
     bool ok = true;
     PartMeta mt{-1, 0, per, 0, 0, 0, {0, 0}};
-    // the next item's description, as soon as there is room
+    // the next item's description and queries, as soon as there is room
     auto announce = [&](const ShortItem& it) -> bool {
         const uint32_t x = ni % kShortItems;
         if (ni >= kShortItems && !warp_wait(&c->it_empty[x], ((ni / kShortItems) & 1) ^ 1, wf)) return false;
         if (leader) {
             c->item[x] = it;
-            mbar_arrive(&c->it_full[x]);
+            if (it.steps > 0) {
+                const int n = it.rows / cc.G;  // a token's heads are neighbours
+                mbar_arrive_expect_tx(&c->it_full[x], (uint32_t)(it.rows * D * 2));
+                for (int t = 0; t < n; ++t)
+                    bulk_load(sQ + (x * C::QROWS + t * cc.G) * D,
+                              p.q + ((int64_t)(it.row0 + t) * cc.Hq + it.h * cc.G) * D, (uint32_t)(cc.G * D * 2),
+                              &c->it_full[x]);
+            } else {
+                mbar_arrive(&c->it_full[x]);
+            }
         }
         __syncwarp();
         ++ni;
@@ -254,6 +267,8 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
         const uint32_t ns = (uint32_t)p.n_slots;
         for (uint32_t n = nload > ns ? nload - ns : 0; n < nload; ++n)
             mbar_wait_drain(&c->t_full[n % ns], (n / ns) & 1);
+        for (uint32_t n = ni > kShortItems ? ni - kShortItems : 0; n < ni; ++n)
+            mbar_wait_drain(&c->it_full[n % kShortItems], (n / kShortItems) & 1);
     }
 }
 
@@ -324,8 +339,8 @@ __device__ __forceinline__ int o_value(int g, int i) {
 }
 
 template <int D, bool Q8, int NT>
-__device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const uint8_t* sS, float* xch, ShortCtrl* c,
-                               volatile WaitFlag* wf) {
+__device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const uint8_t* sS, const __nv_bfloat16* sQ,
+                               float* xch, ShortCtrl* c, volatile WaitFlag* wf) {
     using C = ShortCfg<D, Q8, NT>;
     constexpr int KS = D / 16, SUB = C::SUB;
     const ChunkCommon& cc = p.c;
@@ -336,19 +351,19 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
     for (uint32_t items = 0;; ++items) {
         const uint32_t ii = items % kShortItems;
         if (!warp_wait(&c->it_full[ii], (items / kShortItems) & 1, wf)) return;
-        const ShortItem it = c->item[ii];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->it_empty[ii]);
-        if (it.steps < 0) return;
-        const int row0 = it.row0, rows = it.rows, h = it.h, ctx = it.ctx, end = it.end, part = it.part;
+        const int step0 = c->item[ii].step0, steps = c->item[ii].steps, rows = c->item[ii].rows;
+        const int ctx = c->item[ii].ctx, end = c->item[ii].end;
+        if (steps < 0) return;
         int vref = 0;  // 8-bit: the scale byte that O counts in (0: none yet)
-        {
+        // Eight units of 16 keys (of each of its tiles) to a step; the warps take them in turn.
+        const uint32_t u0 = (uint32_t)step0 * 8, u1 = u0 + (uint32_t)steps * 8;
+        const uint32_t mine = u0 + (warp + kWarps - u0 % kWarps) % kWarps;
+        if (mine < u1) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int r = 8 * nt + g;
                 const bool on = r < rows;
-                const __nv_bfloat16* src =
-                    p.q + ((int64_t)(row0 + (on ? r / cc.G : 0)) * cc.Hq + h * cc.G + (on ? r % cc.G : 0)) * D;
+                const __nv_bfloat16* src = sQ + (ii * C::QROWS + r) * D;
                 uint4 v[KS / 2];
 #pragma unroll
                 for (int q = 0; q < KS / 2; ++q) {
@@ -393,9 +408,9 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                     for (int i = 0; i < 4; ++i) o[t][nt][i] = 0.f;
             }
         }
-        // Eight units of 16 keys (of each of its tiles) to a step; the warps take them in turn.
-        const uint32_t u0 = (uint32_t)it.step0 * 8, u1 = u0 + (uint32_t)it.steps * 8;
-        for (uint32_t unit = u0 + (warp + kWarps - u0 % kWarps) % kWarps; unit < u1; unit += kWarps) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->it_empty[ii]);
+        for (uint32_t unit = mine; unit < u1; unit += kWarps) {
             const uint32_t gs = unit >> 3, is = gs % kShortInfos;
             const int slab = (int)(unit & 7) * 16;
             if (!warp_wait(&c->i_full[is], (gs / kShortInfos) & 1, wf)) return;
@@ -685,66 +700,85 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 if (lane == 0) mbar_arrive(&c->t_empty[ts[SUB + x]]);
             }
         }
-        // The item's end: all warps' sums and accumulators meet.
+        // The item's end: the warp's sums and accumulator go to the joining warp.
+        if (!warp_wait(&c->x_empty, (items & 1) ^ 1, wf)) return;
+        if (mine < u1) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
-                if (g == 0) c->stats[warp][8 * nt + 2 * cq + i] = make_float2(m[nt][i], l[nt][i]);
-            }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->st_full);
-        if (!warp_wait(&c->st_full, items & 1, wf)) return;
+                    for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
+                    const int r = 8 * nt + 2 * cq + i;
+                    if (g == 0) c->stats[warp][r] = make_float2(m[nt][i], l[nt][i]);
+                    const float w = !Q8 ? 1.f : vref ? exp2_int(vref - 127 - 7) : 0.f;
+                    float* dst = xch + (warp * 8 * NT + r) * C::PITCH;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * nt + 2 * cq + i;
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, c->stats[w][r].x);
-                float w = top == -INFINITY ? 0.f : ex2_approx(m[nt][i] - top);
-                if (Q8) w = vref ? w * exp2_int(vref - 127 - 7) : 0.f;
-                float* dst = xch + (warp * 8 * NT + r) * C::PITCH;
-#pragma unroll
-                for (int t = 0; t < KS / 2; ++t)
-                    *reinterpret_cast<float4*>(dst + o_value<D, Q8>(g, t)) =
-                        make_float4(w * o[2 * t][nt][i], w * o[2 * t][nt][i + 2], w * o[2 * t + 1][nt][i],
-                                    w * o[2 * t + 1][nt][i + 2]);
-            }
+                    for (int t = 0; t < KS / 2; ++t)
+                        *reinterpret_cast<float4*>(dst + o_value<D, Q8>(g, t)) =
+                            make_float4(w * o[2 * t][nt][i], w * o[2 * t][nt][i + 2], w * o[2 * t + 1][nt][i],
+                                        w * o[2 * t + 1][nt][i + 2]);
+                }
+        } else if (lane < 8 * NT) {
+            c->stats[warp][lane] = make_float2(-INFINITY, 0.f);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->x_full);
+    }
+}
+
+// ---------------------------------------------------------------- joining warp
+// One warp adds an item's parts up and writes it out, while the others are at the
+// next item (all of them at it, between two barriers, and Q loaded by each warp: 96
+// ragged sequences up to 8,192 slots, 8 key heads of 128, 8-bit rows 160 us; 147 so).
+template <int D, bool Q8, int NT>
+__device__ void short_joiner(const ShortParams& p, const float* xch, ShortCtrl* c, volatile WaitFlag* wf) {
+    using C = ShortCfg<D, Q8, NT>;
+    constexpr int LPR = D / 4;  // lanes of a row
+    const ChunkCommon& cc = p.c;
+    const int lane = threadIdx.x & 31, d = lane % LPR * 4;
+    for (uint32_t items = 0;; ++items) {
+        const uint32_t ii = items % kShortItems;
+        if (!warp_wait(&c->it_full[ii], (items / kShortItems) & 1, wf)) return;
+        const ShortItem it = c->item[ii];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->it_empty[ii]);
+        if (it.steps < 0) return;
         if (!warp_wait(&c->x_full, items & 1, wf)) return;
-        for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
-            const int r = x / (D / 4), d = x % (D / 4) * 4;
+        for (int r = lane / LPR; r < it.rows; r += 32 / LPR) {
+            float2 ml[kWarps];
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, c->stats[w][r].x);
+            for (int w = 0; w < kWarps; ++w) {
+                ml[w] = c->stats[w][r];
+                top = fmaxf(top, ml[w].x);
+            }
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = c->stats[w][r];
-                if (top > -INFINITY) sum += ex2_approx(ml.x - top) * ml.y;
+                if (ml[w].x == -INFINITY) continue;  // saw nothing of the row
+                const float f = ex2_approx(ml[w].x - top);
+                sum += f * ml[w].y;
                 const float4 a = *reinterpret_cast<const float4*>(xch + (w * 8 * NT + r) * C::PITCH + d);
-                v.x += a.x;
-                v.y += a.y;
-                v.z += a.z;
-                v.w += a.w;
+                v.x += f * a.x;
+                v.y += f * a.y;
+                v.z += f * a.z;
+                v.w += f * a.w;
             }
-            if (part < 0) {
+            if (it.part < 0) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const int64_t orow = (int64_t)(row0 + r / cc.G) * cc.Hq + h * cc.G + r % cc.G;
+                const int64_t orow = (int64_t)(it.row0 + r / cc.G) * cc.Hq + it.h * cc.G + r % cc.G;
                 *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(cc.out) + orow * D + d) =
                     make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
                 if (d == 0) cc.lse[orow] = lse_of(top, sum);
             } else {
-                const int64_t prow = (int64_t)part * kShortRows + r;
+                const int64_t prow = (int64_t)it.part * kShortRows + r;
                 *reinterpret_cast<float4*>(p.part_o + prow * D + d) = v;
                 if (d == 0) p.part_ml[prow] = make_float2(top, sum);
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->x_empty);
     }
 }
 
@@ -765,7 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sT = smem;
     float* xch = reinterpret_cast<float*>(sT + C::SLOTS * C::TILE);
     uint8_t* sS = reinterpret_cast<uint8_t*>(xch) + C::XCH;
-    ShortCtrl* c = reinterpret_cast<ShortCtrl*>(sS + (Q8 ? kShortMaxSlots * kTile : 0));
+    __nv_bfloat16* sQ = reinterpret_cast<__nv_bfloat16*>(sS + (Q8 ? kShortMaxSlots * kTile : 0));
+    ShortCtrl* c = reinterpret_cast<ShortCtrl*>(reinterpret_cast<uint8_t*>(sQ) + C::QBUF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
     {
@@ -778,17 +813,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&c->i_empty[x - kShortMaxSlots], 8);
         } else if (x < kShortMaxSlots + kShortInfos + kShortItems) {
             mbar_init(&c->it_full[x - kShortMaxSlots - kShortInfos], 1);
-            mbar_init(&c->it_empty[x - kShortMaxSlots - kShortInfos], kWarps);
+            mbar_init(&c->it_empty[x - kShortMaxSlots - kShortInfos], kWarps + 1);  // and the joining warp
         } else if (x == 32) {
-            mbar_init(&c->st_full, kWarps);
             mbar_init(&c->x_full, kWarps);
+            mbar_init(&c->x_empty, 1);
             c->wf.abort = 0;
             c->wf.limit_ns = p.c.wait_limit_ns;
             c->prefix[0] = 0;
         }
         fence_mbar_init();
     }
-    if (warp == kWarps && lane == 0) {
+    if (warp == kProducer && lane == 0) {
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
@@ -827,10 +862,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
     volatile WaitFlag* wf = &c->wf;
-    if (warp == kWarps)
-        short_producer<D, Q8, NT>(&tk, &tv, p, sT, sS, c, lo, hi, per, sub, wf);
+    if (warp == kProducer)
+        short_producer<D, Q8, NT>(&tk, &tv, p, sT, sS, sQ, c, lo, hi, per, sub, wf);
+    else if (warp == kJoiner)
+        short_joiner<D, Q8, NT>(p, xch, c, wf);
     else
-        short_consumer<D, Q8, NT>(p, sT, sS, xch, c, wf);
+        short_consumer<D, Q8, NT>(p, sT, sS, sQ, xch, c, wf);
     __syncwarp();
     __syncthreads();
     if (threadIdx.x == 0 && c->wf.abort) atomicOr(p.c.err, ERR_TIMEOUT);
