@@ -55,6 +55,7 @@ struct StepInfo {
     int row0, n, h;      // first token (row of q), tokens, key head of the item
     int pos0, end;       // slot of its first token, slot behind the sequence's last one
     int part;            // -1: write the output, else the partial slot
+    int vslot;           // ring slot of its V tile, bit 31: its phase
 };
 
 // A row group of the plan: two tiles of tokens of one sequence.
@@ -72,8 +73,8 @@ struct Ctrl {
     uint64_t q_full[2], q_empty[2];
     uint64_t qi_full[kQAhead], qi_empty[kQAhead];
     uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t i_empty[kInfos];
-    uint64_t fix_full, drain;
+    uint64_t i_full[kInfos], i_empty[kInfos];
+    uint64_t fix_full[kInfos], drain;
     volatile uint32_t issued;        // steps the producer has issued
     int2 qitem[kQAhead];             // first query head and token of an item; x < 0: no more
     StepInfo info[kInfos];
@@ -257,6 +258,8 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
                         f.pos0 = first;
                         f.end = sq.ctx + sq.n;
                         f.part = part;
+                        f.vslot = slot + 1 == NS ? (int)((phase ^ 1) << 31) : (int)((slot + 1) | phase << 31);
+                        mbar_arrive(&c->i_full[is]);
                     }
                     __syncwarp();
                     ++g;
@@ -307,6 +310,7 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
         if ((g < kInfos || warp_wait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf)) &&
             (nload < NS || warp_wait(&empty[slot], phase ^ 1, wf)) && leader) {
             c->info[is].flags = kEnd;
+            mbar_arrive(&c->i_full[is]);
             mbar_arrive(&full[slot]);
             ended = true;
         }
@@ -384,7 +388,7 @@ __device__ void mma_lane(uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem, volat
     constexpr uint64_t KDESC = sdesc_sw128_base(16, 1024), VDESC = sdesc_sw128_base(C::BOX, 1024);
     constexpr uint32_t IQK = idesc_bf16_f32(128, kTile, false), IPV = idesc_bf16_f32(128, D, true);
     if (elect_one()) {
-        uint32_t slot = 0, phase = 0, vslot = 0, vphase = 0, items = 0, fixes = 0;
+        uint32_t slot = 0, phase = 0, vslot = 0, vphase = 0, items = 0;
         bool pend = false;
         int pflags = 0;
         auto next = [&]() {
@@ -407,10 +411,7 @@ __device__ void mma_lane(uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem, volat
         auto pv = [&](int t, uint32_t g) -> bool {
             if (t == 0) {
                 if (!mbar_wait(&c->t_full[vslot], vphase, wf)) return false;
-                if (!Q8 && (pflags & kFix)) {
-                    if (!mbar_wait(&c->fix_full, fixes & 1, wf)) return false;
-                    ++fixes;
-                }
+                if (!Q8 && (pflags & kFix) && !mbar_wait(&c->fix_full[g % kInfos], (g / kInfos) & 1, wf)) return false;
             }
             if (!mbar_wait(&c->p_full[t], g & 1, wf)) return false;
             tc_fence_after();
@@ -464,37 +465,32 @@ __device__ void mma_lane(uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem, volat
 
 // ---------------------------------------------------------------- fixer
 // bf16: V rows behind the last token become zeros before the product reads them.
+// It has a barrier of its own for the descriptions: no product waits for it at
+// most steps, so a tile's barrier may be two phases on when it comes to look.
 template <int D>
 __device__ void fixer(uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
     using C = Cfg<D, false>;
     const int lane = threadIdx.x & 31;
-    uint32_t slot = 0, phase = 0;
-    auto next = [&]() {
-        if (++slot == (uint32_t)C::NT) {
-            slot = 0;
-            phase ^= 1;
-        }
-    };
     for (uint32_t g = 0;; ++g) {
-        if (!warp_wait(&c->t_full[slot], phase, wf)) return;
         const uint32_t is = g % kInfos;
-        const int flags = c->info[is].flags, left = c->info[is].end - c->info[is].base;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->i_empty[is]);
+        if (!warp_wait(&c->i_full[is], (g / kInfos) & 1, wf)) return;
+        const int flags = c->info[is].flags, from = max(c->info[is].end - c->info[is].base, 0);
+        const uint32_t vs = (uint32_t)c->info[is].vslot;
         if (flags & kEnd) return;
-        next();
         if (flags & kFix) {
-            if (!warp_wait(&c->t_full[slot], phase, wf)) return;
-            const int from = max(left, 0);
+            const uint32_t slot = vs & 0x7fffffffu;
+            if (!warp_wait(&c->t_full[slot], vs >> 31, wf)) return;
 #pragma unroll
             for (int x = 0; x < C::NBOX; ++x)
                 for (int i = from * 8 + lane; i < kTile * 8; i += 32)
                     reinterpret_cast<uint4*>(sT + slot * C::TILE + x * C::BOX)[i] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->fix_full);
         }
-        next();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&c->fix_full[is]);  // at every step, so that its phase goes with the step
+            mbar_arrive(&c->i_empty[is]);
+        }
     }
 }
 
@@ -743,7 +739,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             mbar_init(&c->r_full[x], 1);
             mbar_init(&c->r_empty[x], 4);
         } else if (x >= 32 && x < 32 + kInfos) {
+            mbar_init(&c->i_full[x - 32], 1);
             mbar_init(&c->i_empty[x - 32], Q8 ? 8 : 9);  // the softmax warps and the fixer
+            mbar_init(&c->fix_full[x - 32], 1);
         } else if (x >= 64 && x < 66) {
             mbar_init(&c->q_full[x - 64], 1);
             mbar_init(&c->q_empty[x - 64], 1);
@@ -754,7 +752,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             mbar_init(&c->qi_full[x - 96], 1);
             mbar_init(&c->qi_empty[x - 96], 1);
         } else if (x == 128) {
-            mbar_init(&c->fix_full, 1);
             mbar_init(&c->drain, 1);
             c->wf.abort = 0;
             c->wf.limit_ns = p.c.wait_limit_ns;
