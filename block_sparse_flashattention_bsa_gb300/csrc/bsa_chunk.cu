@@ -22,11 +22,11 @@
 //              registers, P back over it in bf16.  O is rescaled in TMEM only when
 //              the maximum grows by more than 2^8.
 //   warp 8     producer: walks the range, resolves pages, TMA-loads K / V tiles
-//   warp 9     MMA: S = Q K^T and O += P V on tcgen05; while one tile's softmax
-//              runs, the other tile's products do:
-//              ... PV_A(j-1) QK_A(j) PV_B(j-1) QK_B(j) PV_A(j) ...
-//   warp 10    loads an item's Q tiles as soon as the item before has used its own
-//   warp 11    bf16: zeroes V rows behind the last token (they may hold NaN)
+//   warps 9, 10  MMA of tile A, B: S = Q K^T and O += P V on tcgen05, 64 slots at a
+//              time, two S buffers to a tile: a tile's scores are two halves of a step
+//              ahead of its product
+//   warp 11    loads an item's Q tiles as soon as the item before has used its own
+//   warp 12    bf16: zeroes V rows behind the last token (they may hold NaN)
 //   warps 12-15  8-bit: convert tiles to bf16 (code * 2^e, exact), thread = row
 
 #include <algorithm>
@@ -43,8 +43,9 @@ constexpr int kSmem = 232448;
 constexpr int kCtrl = 2560;
 constexpr int kInfos = 4;
 constexpr int kQAhead = 4;
-constexpr int kMaxTiles = 12;
-constexpr int kProducer = 8, kMma = 9, kQLoader = 10, kFixer = 11, kConverter = 12;
+constexpr int kMaxTiles = 16;
+constexpr int kHalf = 64;     // key slots of a tile: half of a step
+constexpr int kProducer = 8, kMma = 9, kQLoader = 11, kFixer = 12, kConverter = 12;
 constexpr int kRows = 256;  // rows of an item
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8, kFix = 16 };
@@ -55,7 +56,6 @@ struct StepInfo {
     int row0, n, h;      // first token (row of q), tokens, key head of the item
     int pos0, end;       // slot of its first token, slot behind the sequence's last one
     int part;            // -1: write the output, else the partial slot
-    int vslot;           // ring slot of its V tile, bit 31: its phase
 };
 
 // A row group of the plan: two tiles of tokens of one sequence.
@@ -67,14 +67,21 @@ struct PlanHead {
     int pad[62];
 };
 
+// Tiles of 64 slots are loaded in the order in which the products take them, x
+// counting halves of steps: K(0) K(1) V(0) K(2) V(1) K(3) ..., so that a V tile takes
+// no room long before its turn (K and V of whole steps left 64 KB of loads in
+// flight, a step of 3,100 cycles whatever the products and the softmax took).
+__device__ __forceinline__ uint32_t v_tile(uint32_t x) { return 2 * x + 2; }  // its number in that order
+
 struct Ctrl {
     uint64_t t_full[kMaxTiles], t_empty[kMaxTiles];   // bf16 tiles
     uint64_t r_full[kMaxTiles], r_empty[kMaxTiles];   // 8-bit tiles
     uint64_t q_full[2], q_empty[2];
     uint64_t qi_full[kQAhead], qi_empty[kQAhead];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [tile][half of a step]
+    uint64_t o_full[2];
     uint64_t i_full[kInfos], i_empty[kInfos];
-    uint64_t fix_full[kInfos], drain;
+    uint64_t fix_full[kInfos][2], drain[2];
     volatile uint32_t issued;        // steps the producer has issued
     int2 qitem[kQAhead];             // first query head and token of an item; x < 0: no more
     StepInfo info[kInfos];
@@ -95,20 +102,19 @@ struct ChunkParams {
 
 template <int D, bool Q8>
 struct Cfg {
-    static constexpr int THREADS = Q8 ? 512 : 384;
+    static constexpr int THREADS = 512;
     static constexpr int NBOX = D / 64;
     static constexpr int QBOX = 128 * 128, QTILE = NBOX * QBOX;
-    static constexpr int BOX = kTile * 128, TILE = NBOX * BOX;
-    static constexpr int RAW = kTile * D;              // an 8-bit tile
+    static constexpr int BOX = kHalf * 128, TILE = NBOX * BOX;
+    static constexpr int RAW = kHalf * D;              // an 8-bit tile
     static constexpr int FREE = kSmem - kCtrl - 2 * QTILE;
-    // 8-bit: three bf16 tiles, the rest holds what is in flight
-    static constexpr int NRAW = Q8 ? ((FREE - 3 * TILE) / (RAW + kTile) > kMaxTiles ? kMaxTiles
-                                                                                    : (FREE - 3 * TILE) / (RAW + kTile))
-                                   : 0;
-    static constexpr int NT = Q8 ? 3 : (FREE / TILE > kMaxTiles ? kMaxTiles : FREE / TILE);
-    static constexpr int SMEM = 2 * QTILE + NT * TILE + NRAW * (RAW + kTile) + kCtrl;
+    // 8-bit: six bf16 tiles, the rest holds what is in flight
+    static constexpr int RAWFIT = (FREE - 6 * TILE) / (RAW + kHalf);
+    static constexpr int NRAW = !Q8 ? 0 : RAWFIT > kMaxTiles ? kMaxTiles : RAWFIT;
+    static constexpr int NT = Q8 ? 6 : FREE / TILE > kMaxTiles ? kMaxTiles : FREE / TILE;
+    static constexpr int SMEM = 2 * QTILE + NT * TILE + NRAW * (RAW + kHalf) + kCtrl;
     static constexpr int O_COL = 2 * kTile;
-    static_assert(SMEM <= kSmem && NT >= 3 && (!Q8 || NRAW >= 2), "shared memory");
+    static_assert(SMEM <= kSmem && NT >= 6 && (!Q8 || NRAW >= 6), "shared memory");
 };
 
 // ---------------------------------------------------------------- plan
@@ -186,15 +192,34 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
                          Ctrl* c, int S1, int n_groups, int lo, int hi, int per, volatile WaitFlag* wf) {
     using C = Cfg<D, Q8>;
     constexpr uint32_t NS = Q8 ? C::NRAW : C::NT;
-    constexpr int ROWB = Q8 ? D : 128, NBOX = Q8 ? 1 : C::NBOX, BOX = kTile * ROWB, TILE = NBOX * BOX;
+    constexpr int ROWB = Q8 ? D : 128, NBOX = Q8 ? 1 : C::NBOX, BOX = kHalf * ROWB, TILE = NBOX * BOX;
     const ChunkCommon& cc = p.c;
     uint64_t* full = Q8 ? c->r_full : c->t_full;
     uint64_t* empty = Q8 ? c->r_empty : c->t_empty;
     const int lane = threadIdx.x & 31, ppt = kTile / cc.page;
     const bool leader = elect_one();
     uint32_t slot = 0, phase = 0, nload = 0, g = 0, nq = 0;
-    bool ok = true, ended = false;
+    bool ok = true;
     PartMeta mt{-1, 0, per, 0, 0, 0, {0, 0}};
+    int v0 = -1, v1 = -1;  // rows of the V tiles still to load, of the step before
+    // the next tile, from row y on (-1: nothing is there, zeros)
+    auto load = [&](bool val, int y) -> bool {
+        if (nload >= NS && !warp_wait(&empty[slot], phase ^ 1, wf)) return false;
+        if (leader) {
+            const bool sc = Q8 && y >= 0;
+            mbar_arrive_expect_tx(&full[slot], TILE + (sc ? kHalf : 0));
+#pragma unroll
+            for (int x = 0; x < NBOX; ++x)
+                tma_load_2d(sT + slot * TILE + x * BOX, val ? tv : tk, &full[slot], x * 64, y >= 0 ? y : -kHalf);
+            if (sc) bulk_load(sS + slot * kHalf, (val ? cc.vs : cc.ks) + y, kHalf, &full[slot]);
+        }
+        ++nload;
+        if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
+        }
+        return true;
+    };
     if (lo < hi) {
         int h = lo / S1;
         const int in = lo - h * S1;
@@ -258,43 +283,18 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
                         f.pos0 = first;
                         f.end = sq.ctx + sq.n;
                         f.part = part;
-                        f.vslot = slot + 1 == NS ? (int)((phase ^ 1) << 31) : (int)((slot + 1) | phase << 31);
                         mbar_arrive(&c->i_full[is]);
                     }
                     __syncwarp();
+                    const int k1 = ppt == 2 ? y1 : y0 >= 0 ? y0 + kHalf : -1;
+                    if (g > 0) ok = load(true, v0);
+                    ok = ok && load(false, y0);
+                    if (g > 0) ok = ok && load(true, v1);
+                    ok = ok && load(false, k1);
+                    v0 = y0;
+                    v1 = k1;
                     ++g;
                     if (leader) c->issued = g;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (nload >= NS && !warp_wait(&empty[slot], phase ^ 1, wf)) {
-                            ok = false;
-                            break;
-                        }
-                        if (leader) {
-                            const uint8_t* sc = kv ? cc.vs : cc.ks;
-                            uint32_t bytes = TILE;
-                            if (Q8) bytes += (y0 >= 0 ? cc.page : 0) + (ppt == 2 && y1 >= 0 ? cc.page : 0);
-                            mbar_arrive_expect_tx(&full[slot], bytes);
-#pragma unroll
-                            for (int x = 0; x < NBOX; ++x) {
-                                uint8_t* dst = sT + slot * TILE + x * BOX;
-                                tma_load_2d(dst, kv ? tv : tk, &full[slot], x * 64, y0 >= 0 ? y0 : -cc.page);
-                                if (ppt == 2)
-                                    tma_load_2d(dst + 64 * ROWB, kv ? tv : tk, &full[slot], x * 64,
-                                                y1 >= 0 ? y1 : -cc.page);
-                            }
-                            if (Q8) {
-                                if (y0 >= 0) bulk_load(sS + slot * kTile, sc + y0, cc.page, &full[slot]);
-                                if (ppt == 2 && y1 >= 0)
-                                    bulk_load(sS + slot * kTile + 64, sc + y1, cc.page, &full[slot]);
-                            }
-                        }
-                        ++nload;
-                        if (++slot == NS) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
-                    }
                 }
             }
             pos = start + s1;
@@ -305,14 +305,24 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
         }
     }
     if (ok) {
-        // the end mark, with a slot's barrier; the converters and the MMA lane pass it on
+        // the end mark in the place of the next K tile; the converters and the MMA lanes pass it on
         const uint32_t is = g % kInfos;
-        if ((g < kInfos || warp_wait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf)) &&
-            (nload < NS || warp_wait(&empty[slot], phase ^ 1, wf)) && leader) {
-            c->info[is].flags = kEnd;
-            mbar_arrive(&c->i_full[is]);
-            mbar_arrive(&full[slot]);
-            ended = true;
+        if (g > 0) ok = load(true, v0);
+        ok = ok && (g < kInfos || warp_wait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf));
+        ok = ok && (nload < NS || warp_wait(&empty[slot], phase ^ 1, wf));
+        if (ok) {
+            if (leader) {
+                c->info[is].flags = kEnd;
+                mbar_arrive(&c->i_full[is]);
+                mbar_arrive(&full[slot]);
+            }
+            __syncwarp();
+            ++nload;
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+            if (g > 0) load(true, v1);
         }
         if ((nq < kQAhead || warp_wait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) && leader) {
             c->qitem[nq % kQAhead] = make_int2(-1, 0);
@@ -322,12 +332,8 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
     if (lane == 0) p.meta[blockIdx.x] = mt;
     __syncwarp();
     if (leader) {
-        // copies still in flight must land before the CTA exits (the end mark used
-        // the slot of the oldest one, which was consumed before)
-        for (uint32_t x = nload > NS ? nload - NS : 0; x < nload; ++x) {
-            if (ended && x % NS == nload % NS) continue;
-            mbar_wait_drain(&full[x % NS], (x / NS) & 1);
-        }
+        // copies still in flight must land before the CTA exits
+        for (uint32_t x = nload > NS ? nload - NS : 0; x < nload; ++x) mbar_wait_drain(&full[x % NS], (x / NS) & 1);
     }
 }
 
@@ -382,83 +388,81 @@ __device__ void q_loader(const CUtensorMap* tq, const ChunkParams& p, uint8_t* s
 }
 
 // ---------------------------------------------------------------- MMA
+// One lane for each tile: issuing takes a lane as long as half of the products do.
+//   ... PV(x-2) QK(x) PV(x-1) QK(x+1) ...
+// A tile's scores are two halves of a step ahead of its product, so that its
+// softmax never waits for the product of the half before.
 template <int D, bool Q8>
-__device__ void mma_lane(uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem, volatile WaitFlag* wf) {
+__device__ void mma_lane(int t, uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem, volatile WaitFlag* wf) {
     using C = Cfg<D, Q8>;
     constexpr uint64_t KDESC = sdesc_sw128_base(16, 1024), VDESC = sdesc_sw128_base(C::BOX, 1024);
-    constexpr uint32_t IQK = idesc_bf16_f32(128, kTile, false), IPV = idesc_bf16_f32(128, D, true);
+    constexpr uint64_t QDESC = KDESC;
+    constexpr uint32_t IQK = idesc_bf16_f32(128, kHalf, false), IPV = idesc_bf16_f32(128, D, true);
     if (elect_one()) {
-        uint32_t slot = 0, phase = 0, vslot = 0, vphase = 0, items = 0;
-        bool pend = false;
-        int pflags = 0;
+        uint32_t slot = 0, phase = 0, items = 0;
+        int flags = 0, pflags = 0;  // of this step and of the one before
+        const uint64_t qd = QDESC + (smem_u32(sQ + t * C::QTILE) >> 4);
+        const uint32_t t_o = tmem + C::O_COL + t * D;
         auto next = [&]() {
             if (++slot == (uint32_t)C::NT) {
                 slot = 0;
                 phase ^= 1;
             }
         };
-        auto qk = [&](int t, uint32_t ks) {
-            const uint64_t kd = KDESC + (smem_u32(sT + ks * C::TILE) >> 4);
-            const uint64_t qd = KDESC + (smem_u32(sQ + t * C::QTILE) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = (uint64_t)(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4);
-                mma_ss(tmem + t * kTile, qd + off, kd + off, IQK, kk > 0);
-            }
-            mma_commit(&c->s_full[t]);
-            mbar_arrive(&c->s_full[t]);
-        };
-        auto pv = [&](int t, uint32_t g) -> bool {
-            if (t == 0) {
-                if (!mbar_wait(&c->t_full[vslot], vphase, wf)) return false;
-                if (!Q8 && (pflags & kFix) && !mbar_wait(&c->fix_full[g % kInfos], (g / kInfos) & 1, wf)) return false;
-            }
-            if (!mbar_wait(&c->p_full[t], g & 1, wf)) return false;
+        // O += P V of half y, whose V tile is the next one; its step's flags are pf
+        auto pv = [&](uint32_t y, int pf) -> bool {
+            const uint32_t hf = y & 1, g = y >> 1;
+            if (!mbar_wait(&c->t_full[slot], phase, wf)) return false;
+            if (!Q8 && (pf & kFix) && !mbar_wait(&c->fix_full[g % kInfos][hf], (g / kInfos) & 1, wf)) return false;
+            if (!mbar_wait(&c->p_full[t][hf], g & 1, wf)) return false;
             tc_fence_after();
-            const uint64_t vd = VDESC + (smem_u32(sT + vslot * C::TILE) >> 4);
+            const uint64_t vd = VDESC + (smem_u32(sT + slot * C::TILE) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_ts(tmem + C::O_COL + t * D, tmem + t * kTile + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), IPV,
-                       ((pflags & kFirst) && kk == 0) ? 0u : 1u);
-            if (t == 1) mma_commit(&c->t_empty[vslot]);
-            if (pflags & kLast) mma_commit(&c->o_full[t]);
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ts(t_o, tmem + t * kTile + hf * kHalf + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), IPV,
+                       ((pf & kFirst) && hf == 0 && kk == 0) ? 0u : 1u);
+            mma_commit(&c->pv_done[t][hf]);
+            mma_commit(&c->t_empty[slot]);
+            if (hf == 1 && (pf & kLast)) mma_commit(&c->o_full[t]);
+            next();
             return true;
         };
-        for (uint32_t g = 0;; ++g) {
-            if (pend && !pv(0, g - 1)) break;
+        for (uint32_t x = 0;; ++x) {
+            const uint32_t hf = x & 1;
+            if (x >= 2 && !pv(x - 2, pflags)) break;
             if (!mbar_wait(&c->t_full[slot], phase, wf)) break;
-            const int flags = c->info[g % kInfos].flags;
-            if (flags & kEnd) {
-                if (pend && !pv(1, g - 1)) break;
-                for (int t = 0; t < 2; ++t) {
-                    mbar_arrive(&c->s_full[t]);
-                    mbar_arrive(&c->s_full[t]);
+            if (hf == 0) {
+                flags = c->info[(x >> 1) % kInfos].flags;
+                if (flags & kEnd) {
+                    next();
+                    if (x >= 2 && !pv(x - 1, pflags)) break;
+                    mbar_arrive(&c->s_full[t][0]);
+                    mbar_arrive(&c->s_full[t][0]);
+                    break;
                 }
-                break;
+                if ((flags & kFirst) && !mbar_wait(&c->q_full[t], items & 1, wf)) break;
             }
-            const uint32_t ks = slot;
-            if ((flags & kFirst) && !mbar_wait(&c->q_full[0], items & 1, wf)) break;
             tc_fence_after();
-            qk(0, ks);
-            if (flags & kLast) mma_commit(&c->q_empty[0]);
-            if (pend && !pv(1, g - 1)) break;
-            if ((flags & kFirst) && !mbar_wait(&c->q_full[1], items & 1, wf)) break;
-            tc_fence_after();
-            qk(1, ks);
-            mma_commit(&c->t_empty[ks]);
-            if (flags & kLast) {
-                mma_commit(&c->q_empty[1]);
-                ++items;
+            // S of the half's 64 slots, into the half's buffer
+            const uint64_t kd = KDESC + (smem_u32(sT + slot * C::TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tmem + t * kTile + hf * kHalf, qd + (uint64_t)(((kk >> 2) * C::QBOX + (kk & 3) * 32) >> 4),
+                       kd + (uint64_t)(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4), IQK, kk > 0);
+            mma_commit(&c->s_full[t][hf]);
+            mbar_arrive(&c->s_full[t][hf]);
+            mma_commit(&c->t_empty[slot]);
+            next();
+            if (hf == 1) {
+                if (flags & kLast) {
+                    mma_commit(&c->q_empty[t]);
+                    ++items;
+                }
+                pflags = flags;
             }
-            next();
-            vslot = slot;
-            vphase = phase;
-            next();
-            pflags = flags;
-            pend = true;
         }
-        mma_commit(&c->drain);
-        mbar_wait_drain(&c->drain, 0);
+        mma_commit(&c->drain[t]);
+        mbar_wait_drain(&c->drain[t], 0);
     }
     __syncwarp();
 }
@@ -474,65 +478,78 @@ __device__ void fixer(uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
     for (uint32_t g = 0;; ++g) {
         const uint32_t is = g % kInfos;
         if (!warp_wait(&c->i_full[is], (g / kInfos) & 1, wf)) return;
-        const int flags = c->info[is].flags, from = max(c->info[is].end - c->info[is].base, 0);
-        const uint32_t vs = (uint32_t)c->info[is].vslot;
+        const int flags = c->info[is].flags, held = c->info[is].end - c->info[is].base;
         if (flags & kEnd) return;
-        if (flags & kFix) {
-            const uint32_t slot = vs & 0x7fffffffu;
-            if (!warp_wait(&c->t_full[slot], vs >> 31, wf)) return;
 #pragma unroll
-            for (int x = 0; x < C::NBOX; ++x)
-                for (int i = from * 8 + lane; i < kTile * 8; i += 32)
-                    reinterpret_cast<uint4*>(sT + slot * C::TILE + x * C::BOX)[i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
+        for (int hf = 0; hf < 2; ++hf) {
+            const int from = max(held - hf * kHalf, 0);
+            if ((flags & kFix) && from < kHalf) {
+                const uint32_t n = v_tile(2 * g + hf), slot = n % C::NT;
+                if (!warp_wait(&c->t_full[slot], (n / C::NT) & 1, wf)) return;
+#pragma unroll
+                for (int x = 0; x < C::NBOX; ++x)
+                    for (int i = from * 8 + lane; i < kHalf * 8; i += 32)
+                        reinterpret_cast<uint4*>(sT + slot * C::TILE + x * C::BOX)[i] = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->fix_full[is][hf]);  // at every step, so that its phase goes with the step
         }
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&c->fix_full[is]);  // at every step, so that its phase goes with the step
-            mbar_arrive(&c->i_empty[is]);
-        }
+        if (lane == 0) mbar_arrive(&c->i_empty[is]);
     }
 }
 
 // ---------------------------------------------------------------- converters
-// Thread = row of a tile: its codes times 2^e, in bf16, into the tile that the
-// products read; 16-byte pieces, both sides in their copy's swizzle.
+// Two threads to a row of a tile: its codes times 2^e, in bf16, into the tile that
+// the products read; 16-byte pieces, both sides in their copy's swizzle.
 template <int D>
 __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
     using C = Cfg<D, true>;
-    const int lane = threadIdx.x & 31, row = threadIdx.x - kConverter * 32;
+    constexpr int CH = D / 32;  // 16-byte pieces of half a row
+    const int lane = threadIdx.x & 31, id = threadIdx.x - kConverter * 32, row = id >> 1, side = id & 1;
     uint32_t rs = 0, rphase = 0, ts = 0, tphase = 1;
+    bool ended = false;
+    int held = 0, pheld = 0;  // slots up to the last token, of this step and of the one before
     for (uint32_t n = 0;; ++n) {
         if (!warp_wait(&c->r_full[rs], rphase, wf)) return;
+        // number n is K(x) or V(x)
+        const bool val = n >= 2 && (n & 1) == 0;
+        const uint32_t x = n < 2 ? n : val ? (n - 2) >> 1 : (n + 1) >> 1;
+        bool end = false;
+        if (!val && (x & 1) == 0) {
+            const StepInfo& f = c->info[(x >> 1) % kInfos];
+            end = f.flags & kEnd;
+            pheld = held;
+            held = f.flags & kFix ? f.end - f.base : kTile;
+        }
+        // V(x) of an odd x comes after the next step's first K
+        const int keep = val ? (x & 1 ? pheld - kHalf : held) : kHalf;
         if (!warp_wait(&c->t_empty[ts], tphase, wf)) return;
-        const bool end = (n & 1) == 0 && (c->info[(n >> 1) % kInfos].flags & kEnd);
         if (!end) {
             const uint8_t* src = sR + rs * C::RAW + row * D;
-            uint8_t* dst = sT + ts * C::TILE + row * 128;
-            const uint32_t e = sS[rs * kTile + row];
-            const uint32_t f1 = scale_first(e) * 0x10001u, f2_ = scale_rest(e) * 0x10001u;
-            const bool two = __any_sync(0xffffffffu, e > kOneStep);
+            const uint32_t e = sS[rs * kHalf + row];
+            // 2^e (bytes that are never written: any finite factor)
+            const float f = __uint_as_float((uint32_t)min(max((int)e, 127 + kMinExp), 127 + kMaxExp) << 23);
             const int rx = D == 64 ? (row >> 1) & 3 : row & 7, wx = row & 7;
-            uint4 v[D / 16];
+            uint4 v[CH];
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) v[i] = *reinterpret_cast<const uint4*>(src + ((i ^ rx) << 4));
+            for (int i = 0; i < CH; ++i) v[i] = *reinterpret_cast<const uint4*>(src + (((side * CH + i) ^ rx) << 4));
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
+            for (int i = 0; i < CH; ++i) {
+                // V rows behind the last token may be NaN, and 0 * NaN is none of the sum
+                if (row >= keep) v[i] = make_uint4(0, 0, 0, 0);
                 const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                 uint32_t o[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o[2 * k] = mul_bf16x2(spread_odd(__byte_perm(w[k], 0, 0x1404)), f1);
-                    o[2 * k + 1] = mul_bf16x2(spread_odd(__byte_perm(w[k], 0, 0x3424)), f1);
+                for (int k = 0; k < 8; ++k) {
+                    const f2 y = mul2(codes_f32(w[k >> 1], k & 1), {f, f});
+                    o[k] = pack_bf16x2(y.x, y.y);
                 }
-                if (two) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2_);
-                }
-                uint8_t* box = dst + (i >> 2) * C::BOX;
-                const int ch = (i & 3) * 2;
-                *reinterpret_cast<uint4*>(box + ((ch ^ wx) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(box + (((ch + 1) ^ wx) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                const int q = side * CH + i;  // of the row's pieces of 16 values
+                uint8_t* dst = sT + ts * C::TILE + (q >> 2) * C::BOX + row * 128;
+                const int ch = (q & 3) * 2;
+                *reinterpret_cast<uint4*>(dst + ((ch ^ wx) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ wx) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
             fence_proxy_async_smem();
         }
@@ -541,7 +558,8 @@ __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctr
             mbar_arrive(&c->r_empty[rs]);
             mbar_arrive(&c->t_full[ts]);
         }
-        if (end) return;
+        if (ended || (end && x == 0)) return;
+        ended = end;  // one V tile is left, if there was any step
         if (++rs == (uint32_t)C::NRAW) {
             rs = 0;
             rphase ^= 1;
@@ -566,60 +584,60 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
     float m = -INFINITY, l = 0.f;
     uint32_t items = 0;
     const f2 sl2 = {cc.scale_log2, cc.scale_log2};
-    for (uint32_t g = 0;; ++g) {
-        if (!warp_wait(&c->s_full[t], g & 1, wf)) return;
+    // x counts halves of steps, 64 slots each
+    for (uint32_t x = 0;; ++x) {
+        const uint32_t g = x >> 1, hf = x & 1, is = g % kInfos;
+        if (!warp_wait(&c->s_full[t][hf], g & 1, wf)) return;
         tc_fence_after();
-        const uint32_t is = g % kInfos;
         const StepInfo& f = c->info[is];
         const int flags = f.flags;
         if (flags & kEnd) return;
-        if (flags & kFirst) {
+        const bool first = hf == 0 && (flags & kFirst);
+        if (first) {
             m = -INFINITY;
             l = 0.f;
         }
-        // Columns 64 .. 127 first, then 0 .. 63, which stay in registers for the
-        // weights (P of columns c goes over columns c / 2, so 0 .. 63 come first there).
+        const uint32_t t_x = t_s + hf * 64;
         uint32_t s[2][32];
-        Seen seen;
-        if (flags & kMask) seen = seen_slots(cc, f.base, in_tile && tok < f.n ? f.pos0 + tok : -1, f.have);
-        auto load = [&](int half) {
+        tmem_ld32(t_x, s[0]);
+        tmem_ld32(t_x + 32, s[1]);
+        tmem_wait_ld();
+        reg_fence(s[0]);
+        reg_fence(s[1]);
+        if (flags & kMask) {
+            const unsigned long long vis =
+                seen_slots(cc, f.base + 64 * (int)hf, in_tile && tok < f.n ? f.pos0 + tok : -1, (f.have >> hf) & 1);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) tmem_ld32(t_s + half * 64 + x * 32, s[x]);
-            tmem_wait_ld();
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t v = (uint32_t)(vis >> (32 * i));
+                if (__all_sync(0xffffffffu, v == 0xffffffffu)) continue;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) reg_fence(s[x]);
-            if (flags & kMask) {
-                const unsigned long long vis = half ? seen.w[1] : seen.w[0];
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int q = 0; q < 32; ++q)
-                        if (!(((uint32_t)(vis >> (32 * x)) >> q) & 1u)) s[x][q] = __float_as_uint(-INFINITY);
+                for (int q = 0; q < 32; ++q)
+                    if (!((v >> q) & 1u)) s[i][q] = __float_as_uint(-INFINITY);
             }
-        };
+        }
         float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-            load(half);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int q = 0; q < 32; q += 2)
-                    a[(q >> 1) & 3] = fmax3(a[(q >> 1) & 3], __uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1]));
-        }
+            for (int q = 0; q < 32; q += 2)
+                a[(q >> 1) & 3] = fmax3(a[(q >> 1) & 3], __uint_as_float(s[i][q]), __uint_as_float(s[i][q + 1]));
         const float top = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * cc.scale_log2;
         // The reference follows the maximum only where it grows by more than 2^8
-        // (exact after the final division).  The product before this step's scores
-        // has completed: O is at rest.
+        // (exact after the final division).
         if (__any_sync(0xffffffffu, top > m + 8.f)) {
             const float up = fmaxf(m, top);
             const float w = up == -INFINITY ? 1.f : ex2_approx(m - up);
-            if (!(flags & kFirst)) {
+            if (!first) {
+                // O is at rest once the half before has been added; nothing follows before p_full
+                const uint32_t y = x - 1;
+                if (!warp_wait(&c->pv_done[t][y & 1], (y >> 1) & 1, wf)) return;
+                tc_fence_after();
                 const f2 w2 = {w, w};
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
+                for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
-                    tmem_ld32(t_o + x * 32, o);
+                    tmem_ld32(t_o + i * 32, o);
                     tmem_wait_ld();
                     reg_fence(o);
 #pragma unroll
@@ -628,7 +646,7 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
                         o[2 * q] = __float_as_uint(v.x);
                         o[2 * q + 1] = __float_as_uint(v.y);
                     }
-                    tmem_st32(t_o + x * 32, o);
+                    tmem_st32(t_o + i * 32, o);
                 }
             }
             l *= w;
@@ -638,34 +656,29 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
         const f2 nm2 = {-ref, -ref};
         f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half) load(1);
+        for (int i = 0; i < 2; ++i) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const f2 v = fma2({__uint_as_float(s[x][2 * q]), __uint_as_float(s[x][2 * q + 1])}, sl2, nm2);
-                    const f2 e = {ex2_approx(v.x), ex2_approx(v.y)};
-                    sum[q & 1] = add2(sum[q & 1], e);
-                    pk[q] = pack_bf16x2(e.x, e.y);
-                }
-                tmem_st16(t_s + half * 32 + x * 16, pk);
+            for (int q = 0; q < 16; ++q) {
+                const f2 v = fma2({__uint_as_float(s[i][2 * q]), __uint_as_float(s[i][2 * q + 1])}, sl2, nm2);
+                const f2 e = {ex2_approx(v.x), ex2_approx(v.y)};
+                sum[q & 1] = add2(sum[q & 1], e);
+                pk[q] = pack_bf16x2(e.x, e.y);
             }
+            tmem_st16(t_x + i * 16, pk);
         }
         const f2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
-        const int n = f.n, part = f.part;
+        const int n = f.n, part = f.part, h = f.h;
         const int64_t row0 = f.row0;
-        const int h = f.h;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(&c->i_empty[is]);
-            mbar_arrive(&c->p_full[t]);
+            mbar_arrive(&c->p_full[t][hf]);
+            if (hf) mbar_arrive(&c->i_empty[is]);
         }
-        if (!(flags & kLast)) continue;
+        if (!hf || !(flags & kLast)) continue;
         // The item's end: its row, normalised, or a part of it.
         if (!warp_wait(&c->o_full[t], items & 1, wf)) return;
         tc_fence_after();
@@ -681,15 +694,15 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
                 p.part_ml[prow] = make_float2(m, l);
         }
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
+        for (int y = 0; y < D / 32; ++y) {
             uint32_t o[32];
             __syncwarp();
-            tmem_ld32(t_o + x * 32, o);
+            tmem_ld32(t_o + y * 32, o);
             tmem_wait_ld();
             reg_fence(o);
             if (!live) continue;
             if (part < 0) {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cc.out) + orow * D + x * 32);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cc.out) + orow * D + y * 32);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t v[4];
@@ -699,7 +712,7 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
                     dst[q] = make_uint4(v[0], v[1], v[2], v[3]);
                 }
             } else {
-                uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + x * 32);
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + y * 32);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
             }
@@ -728,31 +741,36 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     uint8_t* sT = sQ + 2 * C::QTILE;
     uint8_t* sR = sT + C::NT * C::TILE;
     uint8_t* sS = sR + C::NRAW * C::RAW;
-    Ctrl* c = reinterpret_cast<Ctrl*>(sS + C::NRAW * kTile);
+    Ctrl* c = reinterpret_cast<Ctrl*>(sS + C::NRAW * kHalf);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
     {
         const int x = threadIdx.x;
         if (x < kMaxTiles) {
             mbar_init(&c->t_full[x], Q8 ? 4 : 1);  // the converters' warps, or the copy
-            mbar_init(&c->t_empty[x], 1);
+            mbar_init(&c->t_empty[x], 2);  // both tiles' products
             mbar_init(&c->r_full[x], 1);
             mbar_init(&c->r_empty[x], 4);
         } else if (x >= 32 && x < 32 + kInfos) {
             mbar_init(&c->i_full[x - 32], 1);
             mbar_init(&c->i_empty[x - 32], Q8 ? 8 : 9);  // the softmax warps and the fixer
-            mbar_init(&c->fix_full[x - 32], 1);
+            mbar_init(&c->fix_full[x - 32][0], 1);
+            mbar_init(&c->fix_full[x - 32][1], 1);
         } else if (x >= 64 && x < 66) {
             mbar_init(&c->q_full[x - 64], 1);
             mbar_init(&c->q_empty[x - 64], 1);
-            mbar_init(&c->s_full[x - 64], 2);  // the scores' commit and the MMA lane itself
-            mbar_init(&c->p_full[x - 64], 4);
+            for (int hf = 0; hf < 2; ++hf) {
+                mbar_init(&c->s_full[x - 64][hf], 2);  // the scores' commit and the MMA lane itself
+                mbar_init(&c->p_full[x - 64][hf], 4);
+                mbar_init(&c->pv_done[x - 64][hf], 1);
+            }
             mbar_init(&c->o_full[x - 64], 1);
         } else if (x >= 96 && x < 96 + kQAhead) {
             mbar_init(&c->qi_full[x - 96], 1);
             mbar_init(&c->qi_empty[x - 96], 1);
         } else if (x == 128) {
-            mbar_init(&c->drain, 1);
+            mbar_init(&c->drain[0], 1);
+            mbar_init(&c->drain[1], 1);
             c->wf.abort = 0;
             c->wf.limit_ns = p.c.wait_limit_ns;
             c->issued = 0;
@@ -782,23 +800,23 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     const int total = S1 * p.c.Hkv;
     const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
-    // 8-bit: 128 registers a thread at launch; the softmax's 256 threads take 184,
-    // the others' 256 keep 72: 184 + 72 = 2 * 128.
+    // 128 registers a thread at launch; the softmax's 256 threads take 184, the
+    // others' 256 keep 72: 184 + 72 = 2 * 128.
     if (warp < 8) {
-        if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         softmax<D, Q8>(p, c, tmem, wf);
     } else {
-        if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kProducer)
             producer<D, Q8>(&tk, &tv, p, Q8 ? sR : sT, sS, c, S1, n_groups, lo, hi, per, wf);
-        else if (warp == kMma)
-            mma_lane<D, Q8>(sQ, sT, c, tmem, wf);
+        else if (warp == kMma || warp == kMma + 1)
+            mma_lane<D, Q8>(warp - kMma, sQ, sT, c, tmem, wf);
         else if (warp == kQLoader)
             q_loader<D>(&tq, p, sQ, c, wf);
-        else if (warp == kFixer) {
-            if (!Q8) fixer<D>(sT, c, wf);
-        } else
+        else if (Q8)
             converter<D>(sR, sS, sT, c, wf);
+        else if (warp == kFixer)
+            fixer<D>(sT, c, wf);
     }
     __syncwarp();
     tc_fence_before();
@@ -852,7 +870,7 @@ int go(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cons
     static std::atomic<uint64_t> raised{0};
     if (raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<D, Q8>), C::SMEM, &raised) != cudaSuccess)
         return BSA_ERR_CUDA;
-    if (Q8) {
+    {
         // the register split takes all of what 512 threads of 128 are given: with less it would wait forever
         static std::atomic<int> regs{0};
         if (regs.load() == 0) {
@@ -955,8 +973,8 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
     const uint64_t krows = (uint64_t)c->n_pages * c->Hkv * c->page;
     auto encode = scales ? encode_rows_e4m3 : encode_rows_bf16;
     if ((st = encode_token_rows_bf16(&tq, a->q, (uint64_t)a->tokens, a->Hq, c->D, G, cp.tq)) != BSA_OK) return st;
-    if ((st = encode(&tk, c->k, krows, c->D, c->page)) != BSA_OK) return st;
-    if ((st = encode(&tv, c->v, krows, c->D, c->page)) != BSA_OK) return st;
+    if ((st = encode(&tk, c->k, krows, c->D, kHalf)) != BSA_OK) return st;
+    if ((st = encode(&tv, c->v, krows, c->D, kHalf)) != BSA_OK) return st;
     if (launch_after(plan_kernel, dim3(1), 1024, 0, s, p, reinterpret_cast<PlanHead*>(ws + w.head),
                      reinterpret_cast<Group*>(ws + w.groups), w.cap, cp.tq) != cudaSuccess)
         return BSA_ERR_CUDA;

@@ -82,24 +82,15 @@ __device__ __forceinline__ Span visible_span(const ChunkCommon& p, int first, in
     return s;
 }
 
-// Slots u that a token in slot pos sees among base .. base + 127, as bits of two words.
-struct Seen {
-    unsigned long long w[2];
-};
+// Slots u that a token in slot pos sees among base .. base + 63, as bits; none where
+// they lie in no page (have 0).
 __device__ __forceinline__ unsigned long long below(int n) {  // bits 0 .. n - 1
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
-// have: bit h set where the tile's half h lies in a page.
-__device__ __forceinline__ Seen seen_slots(const ChunkCommon& p, int base, int pos, int have) {
-    Seen s;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int b = base + 64 * h;
-        unsigned long long m = below(pos + 1 - b);
-        if (p.window > 0) m &= ~below(max(pos - p.window + 1, 0) - b) | below(p.sinks - b);
-        s.w[h] = (have >> h) & 1 ? m : 0ull;
-    }
-    return s;
+__device__ __forceinline__ unsigned long long seen_slots(const ChunkCommon& p, int base, int pos, int have) {
+    unsigned long long m = below(pos + 1 - base);
+    if (p.window > 0) m &= ~below(max(pos - p.window + 1, 0) - base) | below(p.sinks - base);
+    return have ? m : 0ull;
 }
 
 // Page j of sequence b for tokens that see from slot lo to slot end - 1 (and the

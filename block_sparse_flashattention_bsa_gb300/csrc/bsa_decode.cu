@@ -289,23 +289,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 codes (the low or high half of w) as fp16, exactly.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w, int high) {
-    uint32_t r;
-    if (high)
-        asm("{\n\t.reg .b16 lo, hi;\n\t"
-            "mov.b32 {lo, hi}, %1;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
-            : "=r"(r)
-            : "r"(w));
-    else
-        asm("{\n\t.reg .b16 lo, hi;\n\t"
-            "mov.b32 {lo, hi}, %1;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-            : "=r"(r)
-            : "r"(w));
-    return r;
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);

@@ -10,6 +10,7 @@
 // the smallest code a normal bf16 number, kMaxExp keeps 448 * 2^e finite in bf16.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "bsa_ptx.cuh"
@@ -32,30 +33,28 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Codes to bf16 without a conversion instruction (there is none from e4m3): the
-// code's exponent and mantissa bits, put at bf16's, stand for its value times
-// 2^-120 (subnormal codes too), and a bf16 product with 2^(120 + e) gives
-// code * 2^e exactly.  A NaN code comes out as 480 * 2^e.
-__device__ __forceinline__ uint32_t spread_odd(uint32_t w) {  // bytes 1 and 3
-    return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
-}
-__device__ __forceinline__ uint32_t spread_even(uint32_t w) {  // bytes 0 and 2
-    return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+// Two e4m3 codes (the low or high half of w) as fp16, exactly.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, int high) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    if (high)
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %1;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+            : "=r"(r)
+            : "r"(w));
+    else
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %1;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+            : "=r"(r)
+            : "r"(w));
     return r;
 }
-// 2^(120 + e) of a scale byte as bf16 bits; exponents that one bf16 factor
-// cannot reach (e above 7) need scale_rest() as a second one.  Bytes outside
-// what is ever written (a slot that nothing was written to) give finite factors.
-__device__ __forceinline__ uint32_t scale_first(uint32_t byte) {
-    return (uint32_t)::min(::max((int)byte + 120, 127 + 120 + kMinExp), 254) << 7;
+// The same in fp32.
+__device__ __forceinline__ f2 codes_f32(uint32_t w, int high) {
+    const uint32_t h = codes_f16(w, high);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return {f.x, f.y};
 }
-__device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
-    return (uint32_t)(127 + ::min(::max((int)byte - 127 - 7, 0), kMaxExp - 7)) << 7;
-}
-constexpr uint32_t kOneStep = 127 + 7;  // scale bytes up to this need one factor
 
 }  // namespace bsa
