@@ -71,7 +71,8 @@ struct PlanHead {
 // counting halves of steps: K(0) K(1) V(0) K(2) V(1) K(3) ..., so that a V tile takes
 // no room long before its turn (K and V of whole steps left 64 KB of loads in
 // flight, a step of 3,100 cycles whatever the products and the softmax took).
-__device__ __forceinline__ uint32_t v_tile(uint32_t x) { return 2 * x + 2; }  // its number in that order
+__device__ __forceinline__ uint32_t v_tile(uint32_t x) { return 2 * x + 2; }  // their numbers in that order
+__device__ __forceinline__ uint32_t k_tile(uint32_t x) { return x < 2 ? x : 2 * x - 1; }
 
 struct Ctrl {
     uint64_t t_full[kMaxTiles], t_empty[kMaxTiles];   // bf16 tiles
@@ -500,54 +501,47 @@ __device__ void fixer(uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
 }
 
 // ---------------------------------------------------------------- converters
-// Two threads to a row of a tile: its codes times 2^e, in bf16, into the tile that
-// the products read; 16-byte pieces, both sides in their copy's swizzle.
+// Four warps, one to each tile of a step (K and V of either half), so that four
+// tiles are under way at a time: codes times 2^e, in bf16, into the tile that the
+// products read; 16-byte pieces, both sides in their copy's swizzle.
 template <int D>
 __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
     using C = Cfg<D, true>;
-    constexpr int CH = D / 32;  // 16-byte pieces of half a row
-    const int lane = threadIdx.x & 31, id = threadIdx.x - kConverter * 32, row = id >> 1, side = id & 1;
-    uint32_t rs = 0, rphase = 0, ts = 0, tphase = 1;
-    bool ended = false;
-    int held = 0, pheld = 0;  // slots up to the last token, of this step and of the one before
-    for (uint32_t n = 0;; ++n) {
-        if (!warp_wait(&c->r_full[rs], rphase, wf)) return;
-        // number n is K(x) or V(x)
-        const bool val = n >= 2 && (n & 1) == 0;
-        const uint32_t x = n < 2 ? n : val ? (n - 2) >> 1 : (n + 1) >> 1;
-        bool end = false;
-        if (!val && (x & 1) == 0) {
-            const StepInfo& f = c->info[(x >> 1) % kInfos];
-            end = f.flags & kEnd;
-            pheld = held;
-            held = f.flags & kFix ? f.end - f.base : kTile;
-        }
-        // V(x) of an odd x comes after the next step's first K
-        const int keep = val ? (x & 1 ? pheld - kHalf : held) : kHalf;
-        if (!warp_wait(&c->t_empty[ts], tphase, wf)) return;
+    constexpr int LPR = D / 16, RPP = 32 / LPR;  // lanes of a row (a 16-byte piece each), rows at a time
+    const int lane = threadIdx.x & 31, id = (threadIdx.x >> 5) - kConverter, hf = id & 1, piece = lane % LPR;
+    const bool val = id >= 2;
+    for (uint32_t g = 0;; ++g) {
+        const uint32_t is = g % kInfos, x = 2 * g + hf, n = val ? v_tile(x) : k_tile(x);
+        if (!warp_wait(&c->i_full[is], (g / kInfos) & 1, wf)) return;
+        const int flags = c->info[is].flags, left = c->info[is].end - c->info[is].base - hf * kHalf;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->i_empty[is]);
+        const bool end = flags & kEnd;
+        if (end && id != 0) return;  // the end mark stands in the place of the next K tile
+        const uint32_t rs = n % C::NRAW, ts = n % C::NT;
+        if (!warp_wait(&c->r_full[rs], (n / C::NRAW) & 1, wf)) return;
+        if (!warp_wait(&c->t_empty[ts], ((n / C::NT) & 1) ^ 1, wf)) return;
         if (!end) {
-            const uint8_t* src = sR + rs * C::RAW + row * D;
-            const uint32_t e = sS[rs * kHalf + row];
-            // 2^e (bytes that are never written: any finite factor)
-            const float f = __uint_as_float((uint32_t)min(max((int)e, 127 + kMinExp), 127 + kMaxExp) << 23);
-            const int rx = D == 64 ? (row >> 1) & 3 : row & 7, wx = row & 7;
-            uint4 v[CH];
-#pragma unroll
-            for (int i = 0; i < CH; ++i) v[i] = *reinterpret_cast<const uint4*>(src + (((side * CH + i) ^ rx) << 4));
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                // V rows behind the last token may be NaN, and 0 * NaN is none of the sum
-                if (row >= keep) v[i] = make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            // V rows behind the last token may be NaN, and 0 * NaN is none of the sum
+            const int keep = val && (flags & kFix) ? left : kHalf;
+#pragma unroll 4
+            for (int r0 = 0; r0 < kHalf; r0 += RPP) {
+                const int row = r0 + lane / LPR;
+                const int rx = D == 64 ? (row >> 1) & 3 : row & 7, wx = row & 7;
+                uint4 v = *reinterpret_cast<const uint4*>(sR + rs * C::RAW + row * D + ((piece ^ rx) << 4));
+                // 2^e (bytes that are never written: any finite factor)
+                const uint32_t e = sS[rs * kHalf + row];
+                const float f = __uint_as_float((uint32_t)min(max((int)e, 127 + kMinExp), 127 + kMaxExp) << 23);
+                if (row >= keep) v = make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t o[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const f2 y = mul2(codes_f32(w[k >> 1], k & 1), {f, f});
                     o[k] = pack_bf16x2(y.x, y.y);
                 }
-                const int q = side * CH + i;  // of the row's pieces of 16 values
-                uint8_t* dst = sT + ts * C::TILE + (q >> 2) * C::BOX + row * 128;
-                const int ch = (q & 3) * 2;
+                uint8_t* dst = sT + ts * C::TILE + (piece >> 2) * C::BOX + row * 128;
+                const int ch = (piece & 3) * 2;
                 *reinterpret_cast<uint4*>(dst + ((ch ^ wx) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ wx) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
@@ -558,16 +552,7 @@ __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctr
             mbar_arrive(&c->r_empty[rs]);
             mbar_arrive(&c->t_full[ts]);
         }
-        if (ended || (end && x == 0)) return;
-        ended = end;  // one V tile is left, if there was any step
-        if (++rs == (uint32_t)C::NRAW) {
-            rs = 0;
-            rphase ^= 1;
-        }
-        if (++ts == (uint32_t)C::NT) {
-            ts = 0;
-            tphase ^= 1;
-        }
+        if (end) return;
     }
 }
 
@@ -634,7 +619,7 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
                 if (!warp_wait(&c->pv_done[t][y & 1], (y >> 1) & 1, wf)) return;
                 tc_fence_after();
                 const f2 w2 = {w, w};
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
                     tmem_ld32(t_o + i * 32, o);
@@ -693,7 +678,7 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
             else
                 p.part_ml[prow] = make_float2(m, l);
         }
-#pragma unroll
+#pragma unroll 1
         for (int y = 0; y < D / 32; ++y) {
             uint32_t o[32];
             __syncwarp();
@@ -747,13 +732,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     {
         const int x = threadIdx.x;
         if (x < kMaxTiles) {
-            mbar_init(&c->t_full[x], Q8 ? 4 : 1);  // the converters' warps, or the copy
+            mbar_init(&c->t_full[x], 1);  // its converter, or the copy
             mbar_init(&c->t_empty[x], 2);  // both tiles' products
             mbar_init(&c->r_full[x], 1);
-            mbar_init(&c->r_empty[x], 4);
+            mbar_init(&c->r_empty[x], 1);
         } else if (x >= 32 && x < 32 + kInfos) {
             mbar_init(&c->i_full[x - 32], 1);
-            mbar_init(&c->i_empty[x - 32], Q8 ? 8 : 9);  // the softmax warps and the fixer
+            mbar_init(&c->i_empty[x - 32], Q8 ? 12 : 9);  // the softmax warps, the converters or the fixer
             mbar_init(&c->fix_full[x - 32][0], 1);
             mbar_init(&c->fix_full[x - 32][1], 1);
         } else if (x >= 64 && x < 66) {
