@@ -11,10 +11,9 @@
 // exponentials (one a pair) and, for 8-bit rows, the conversions run beside them.
 //
 // Work: an item is two tiles of 128 rows of one key head of one sequence (both
-// tiles use every K / V tile that is loaded); a step 128 slots.  plan_kernel lists
-// the items' steps, heads outermost; the steps of the whole batch are cut into
-// equal ranges, one per CTA, so that one long chunk loads the SMs as evenly as
-// many short ones.  Items that a range boundary cuts leave unnormalised fp32
+// tiles use every K / V tile that is loaded); a step 128 slots.  The steps of the
+// whole batch are cut into equal ranges, one per CTA, so that one long chunk loads
+// the SMs as evenly as many short ones.  Items that a range boundary cuts leave unnormalised fp32
 // parts, which the merge joins in range order: results do not depend on timing.
 //
 // One CTA per SM:
@@ -58,21 +57,18 @@ struct StepInfo {
     int part;            // -1: write the output, else the partial slot
 };
 
-// A row group of the plan: two tiles of tokens of one sequence.
-struct Group {
-    int b, t0, steps, cum;  // cum: steps of the groups before it
-};
-struct PlanHead {
-    int groups, steps;  // steps of all groups, of one key head
-    int pad[62];
-};
-
 // Tiles of 64 slots are loaded in the order in which the products take them, x
 // counting halves of steps: K(0) K(1) V(0) K(2) V(1) K(3) ..., so that a V tile takes
 // no room long before its turn (K and V of whole steps left 64 KB of loads in
 // flight, a step of 3,100 cycles whatever the products and the softmax took).
 __device__ __forceinline__ uint32_t v_tile(uint32_t x) { return 2 * x + 2; }  // their numbers in that order
 __device__ __forceinline__ uint32_t k_tile(uint32_t x) { return x < 2 ? x : 2 * x - 1; }
+
+struct Place {
+    int b, h, i;          // sequence, key head, group
+    int head, cum;        // steps of one of its key heads; of the head's groups before this one
+    int start;            // first step of the item
+};
 
 struct Ctrl {
     uint64_t t_full[kMaxTiles], t_empty[kMaxTiles];   // bf16 tiles
@@ -88,14 +84,15 @@ struct Ctrl {
     StepInfo info[kInfos];
     uint32_t tmem_base;
     WaitFlag wf;
+    Place place;                     // where the CTA's range starts
+    long long sums[32];
 };
 static_assert(sizeof(Ctrl) <= kCtrl, "control block too large");
 
 struct ChunkParams {
     ChunkCommon c;
     int32_t tq;                // tokens of a tile
-    const PlanHead* head;
-    const Group* groups;
+    int32_t least;             // sequences of fewer query rows of a key head are not worked on
     PartMeta* meta;
     float* part_o;             // [2 * grid][256][D]
     float2* part_ml;           // [2 * grid][256]
@@ -119,78 +116,55 @@ struct Cfg {
 };
 
 // ---------------------------------------------------------------- plan
-// One CTA: the row groups of the sequences that are not short, and the running
-// sum of their steps.  Sequences in order, a warp each (lanes are groups).
-__global__ void __launch_bounds__(1024) plan_kernel(const ChunkCommon p, PlanHead* head, Group* groups, int cap, int tq) {
-    __shared__ int red[32];
-    __shared__ int first[1024 + 1];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    griddep_launch_dependents();
-    griddep_wait();
-    int done = 0;  // groups of the sequences before
-    for (int b0 = 0; b0 < p.B; b0 += 1024) {
-        const int b = b0 + tid;
-        int cnt = 0;
-        if (b < p.B) {
-            const Seq s = sequence(p, b, true);
-            if (s.n * (int64_t)p.G > kShortRows) cnt = (s.n + 2 * tq - 1) / (2 * tq);
-        }
-        int incl = cnt;
+// An item's place in the order of all steps: sequences, their key heads, their
+// groups of two tiles of tokens.  Every CTA works out for itself where its range
+// starts (a kernel that listed the items for all: 5 us in front of this one).
+
+// Groups of sequence s; 0: it is not worked on here.
+__device__ __forceinline__ int group_count(const ChunkParams& p, const Seq& s) {
+    return s.n * (int64_t)p.c.G < p.least ? 0 : (s.n + 2 * p.tq - 1) / (2 * p.tq);
+}
+__device__ __forceinline__ int group_steps(const ChunkParams& p, const Seq& s, int i) {
+    const int t0 = i * 2 * p.tq;
+    return visible_span(p.c, s.ctx + t0, s.ctx + min(s.n, t0 + 2 * p.tq)).steps;
+}
+// Steps of one key head of sequences b0 + lane (0 from b1 on), a lane each; the
+// whole warp takes those of many groups.
+__device__ int head_steps(const ChunkParams& p, int b0, int b1, bool report) {
+    const int lane = threadIdx.x & 31;
+    Seq s{0, 0, 0};
+    if (b0 + lane < b1) s = sequence(p.c, b0 + lane, report);
+    const int n = group_count(p, s);
+    int sum = 0;
+    if (n <= 4)
+        for (int i = 0; i < n; ++i) sum += group_steps(p, s, i);
+    for (unsigned m = __ballot_sync(0xffffffffu, n > 4); m; m &= m - 1) {
+        const int from = __ffs(m) - 1;
+        Seq w;
+        w.row0 = 0;
+        w.n = __shfl_sync(0xffffffffu, s.n, from);
+        w.ctx = __shfl_sync(0xffffffffu, s.ctx, from);
+        const int cnt = __shfl_sync(0xffffffffu, n, from);
+        int x = 0;
+        for (int i = lane; i < cnt; i += 32) x += group_steps(p, w, i);
+        x = __reduce_add_sync(0xffffffffu, x);
+        if (lane == from) sum = x;
+    }
+    return sum;
+}
+__device__ __forceinline__ int inclusive_sum(int v) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) red[warp] = incl;
-        __syncthreads();
-        incl += __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
-        first[tid] = done + incl - cnt;
-        if (tid == 1023) first[1024] = done + incl;
-        __syncthreads();
-        for (int u = warp; u < min(1024, p.B - b0); u += 32) {
-            const int at = first[u], n = first[u + 1] - at;
-            if (n == 0) continue;
-            const Seq s = sequence(p, b0 + u, false);
-            for (int i = lane; i < n && at + i < cap; i += 32) {
-                const int t0 = i * 2 * tq, pos = s.ctx + t0;
-                groups[at + i] = Group{b0 + u, t0, visible_span(p, pos, s.ctx + min(s.n, t0 + 2 * tq)).steps, 0};
-            }
-        }
-        done = first[1024];
-        __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)(threadIdx.x & 31) >= o) v += x;
     }
-    if (done > cap) {  // overlapping sequences: more rows than there are
-        if (tid == 0) atomicOr(p.err, ERR_CAPACITY);
-        done = cap;
-    }
-    __threadfence_block();
-    __syncthreads();
-    int before = 0;
-    for (int g0 = 0; g0 < done; g0 += 1024) {
-        const int g = g0 + tid, steps = g < done ? groups[g].steps : 0;
-        int incl = steps;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) red[warp] = incl;
-        __syncthreads();
-        incl += __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
-        if (g < done) groups[g].cum = before + incl - steps;
-        before += __reduce_add_sync(0xffffffffu, red[lane]);
-        __syncthreads();
-    }
-    if (tid == 0) {
-        head->groups = done;
-        head->steps = before;
-    }
+    return v;
 }
 
 // ---------------------------------------------------------------- producer
 template <int D, bool Q8>
 __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const ChunkParams& p, uint8_t* sT, uint8_t* sS,
-                         Ctrl* c, int S1, int n_groups, int lo, int hi, int per, volatile WaitFlag* wf) {
+                         Ctrl* c, int lo, int hi, int per, volatile WaitFlag* wf) {
     using C = Cfg<D, Q8>;
     constexpr uint32_t NS = Q8 ? C::NRAW : C::NT;
     constexpr int ROWB = Q8 ? D : 128, NBOX = Q8 ? 1 : C::NBOX, BOX = kHalf * ROWB, TILE = NBOX * BOX;
@@ -222,35 +196,45 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
         return true;
     };
     if (lo < hi) {
-        int h = lo / S1;
-        const int in = lo - h * S1;
-        int u = 0;  // the group that holds step lo of head h: last one whose first step is not behind it
-        for (int span = n_groups; span > 1;) {
-            const int stride = (span + 31) >> 5, off = lane * stride;
-            const bool le = off < span && p.groups[u + off].cum <= in;
-            u += (__popc(__ballot_sync(0xffffffffu, le)) - 1) * stride;
-            span = min(stride, n_groups - u);
+        // c->place: the sequence that step lo lies in, and its first step; then the head, and
+        // the group: the last one whose first step is not behind it
+        Place at = c->place;
+        Seq sq = sequence(cc, at.b, false);
+        int n_groups = group_count(p, sq);
+        at.h = (lo - at.start) / at.head;
+        const int in = lo - at.start - at.h * at.head;
+        at.i = at.cum = 0;
+        for (int i0 = 0, before = 0; i0 < n_groups; i0 += 32) {
+            const int st = i0 + lane < n_groups ? group_steps(p, sq, i0 + lane) : 0;
+            const int incl = before + inclusive_sum(st), cum = incl - st;
+            const unsigned le = __ballot_sync(0xffffffffu, i0 + lane < n_groups && cum <= in);
+            if (le) {
+                const int x = 31 - __clz(le);
+                at.i = i0 + x;
+                at.cum = __shfl_sync(0xffffffffu, cum, x);
+            }
+            before = __shfl_sync(0xffffffffu, incl, 31);
+            if (before > in) break;
         }
+        at.start += at.h * at.head + at.cum;
         int pos = lo;
         while (ok && pos < hi) {
-            const Group gr = p.groups[u];
-            const int b = gr.b;
-            const Seq sq = sequence(cc, b, false);
-            const int n = min(sq.n - gr.t0, 2 * p.tq), first = sq.ctx + gr.t0, last = first + n;
+            const int b = at.b, h = at.h, t0 = at.i * 2 * p.tq;
+            const int n = min(sq.n - t0, 2 * p.tq), first = sq.ctx + t0, last = first + n;
             const int vis0 = first_slot(cc, first);
             const Span sp = visible_span(cc, first, last);
-            const int start = h * S1 + gr.cum, end = start + gr.steps;
+            const int start = at.start, end = start + sp.steps;
             const int s0 = pos - start, s1 = min(end, hi) - start;
             const bool whole = s0 == 0 && start + s1 == end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
-            if (start < lo) mt = PartMeta{start, end, per, sq.row0 + gr.t0, n, h, {0, 0}};
+            if (start < lo) mt = PartMeta{start, end, per, sq.row0 + t0, n, h, {0, 0}};
             // the Q loader's turn, as soon as its buffers are free
             if (nq >= kQAhead && !warp_wait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
                 ok = false;
                 break;
             }
             if (leader) {
-                c->qitem[nq % kQAhead] = make_int2(h * cc.G, sq.row0 + gr.t0);
+                c->qitem[nq % kQAhead] = make_int2(h * cc.G, sq.row0 + t0);
                 mbar_arrive(&c->qi_full[nq % kQAhead]);
             }
             ++nq;
@@ -278,7 +262,7 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
                                   (base + kTile > sq.ctx + sq.n ? kFix : 0);
                         f.base = base;
                         f.have = have;
-                        f.row0 = sq.row0 + gr.t0;
+                        f.row0 = sq.row0 + t0;
                         f.n = n;
                         f.h = h;
                         f.pos0 = first;
@@ -299,9 +283,16 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
                 }
             }
             pos = start + s1;
-            if (++u == n_groups && pos < hi) {
-                u = 0;
-                ++h;
+            at.start = end;
+            if (++at.i == n_groups && pos < hi) {
+                at.i = 0;
+                if (++at.h == cc.Hkv) {
+                    at.h = 0;
+                    do {
+                        sq = sequence(cc, ++at.b, false);
+                        n_groups = group_count(p, sq);
+                    } while (n_groups == 0);
+                }
             }
         }
     }
@@ -781,10 +772,37 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = c->tmem_base;
     volatile WaitFlag* wf = &c->wf;
-    const int S1 = p.head->steps, n_groups = p.head->groups;
-    const int total = S1 * p.c.Hkv;
+    // steps of all sequences, a run of 32 after another to a warp; then the range's start
+    constexpr int NW = C::THREADS / 32;
+    const int each = (p.c.B + 32 * NW - 1) / (32 * NW) * 32;  // sequences of a warp
+    const int b0 = min(p.c.B, warp * each), b1 = min(p.c.B, b0 + each);
+    long long mine = 0;
+    for (int b = b0; b < b1; b += 32) mine += head_steps(p, b, b1, blockIdx.x == 0);  // this lane's
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) c->sums[warp] = mine;
+    __syncthreads();
+    long long all = 0, ahead = 0;
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) ahead += c->sums[w];
+        all += c->sums[w];
+    }
+    if (all * p.c.Hkv > 1 << 30) {  // only where sequences overlap: their rows make no sense
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.c.err, ERR_BAD_ROW);
+        all = 0;
+    }
+    const int total = (int)all * p.c.Hkv;
     const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int lo = min(total, (int)blockIdx.x * per), hi = min(total, lo + per);
+    if (lo < hi && ahead * p.c.Hkv <= lo && lo < (ahead + mine) * p.c.Hkv) {
+        int before = (int)ahead * p.c.Hkv;
+        for (int b = b0; b < b1; b += 32) {
+            const int st = head_steps(p, b, b1, false), incl = inclusive_sum(st), first = before + (incl - st) * p.c.Hkv;
+            if (first <= lo && lo < first + st * p.c.Hkv) c->place = Place{b + lane, 0, 0, st, 0, first};
+            before += __shfl_sync(0xffffffffu, incl, 31) * p.c.Hkv;
+        }
+    }
+    __syncthreads();
     // 128 registers a thread at launch; the softmax's 256 threads take 184, the
     // others' 256 keep 72: 184 + 72 = 2 * 128.
     if (warp < 8) {
@@ -793,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kProducer)
-            producer<D, Q8>(&tk, &tv, p, Q8 ? sR : sT, sS, c, S1, n_groups, lo, hi, per, wf);
+            producer<D, Q8>(&tk, &tv, p, Q8 ? sR : sT, sS, c, lo, hi, per, wf);
         else if (warp == kMma || warp == kMma + 1)
             mma_lane<D, Q8>(warp - kMma, sQ, sT, c, tmem, wf);
         else if (warp == kQLoader)
@@ -819,8 +837,7 @@ int tile_tokens(int G) { return 128 / G; }
 
 // The workspace: both kernels' part descriptions, the plan, the parts.
 struct Layout {
-    int64_t short_meta, short_o, short_ml, meta, head, groups, o, ml, bytes;
-    int32_t cap;
+    int64_t short_meta, short_o, short_ml, meta, o, ml, bytes;
 };
 int64_t up(int64_t x) { return (x + 255) / 256 * 256; }
 Layout layout(int64_t B, int64_t tokens, int G, int D) {
@@ -836,12 +853,7 @@ Layout layout(int64_t B, int64_t tokens, int G, int D) {
     w.short_o = take(parts * kShortRows * D * 4);
     w.short_ml = take(parts * kShortRows * 8);
     if (tokens * G > kShortRows) {
-        // a sequence's groups: its tokens over 2 tq, rounded up
-        const int64_t cap = tokens / (2 * tile_tokens(G)) + std::min(B, tokens);
-        w.cap = (int32_t)std::min<int64_t>(cap, INT32_MAX);
         w.meta = take(kChunkMaxCtas * (int64_t)sizeof(PartMeta));
-        w.head = take(sizeof(PlanHead));
-        w.groups = take(cap * (int64_t)sizeof(Group));
         w.o = take(parts * kRows * D * 4);
         w.ml = take(parts * kRows * 8);
     }
@@ -850,7 +862,8 @@ Layout layout(int64_t B, int64_t tokens, int G, int D) {
 }
 
 template <int D, bool Q8>
-int go(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, int ctas, cudaStream_t s) {
+int go(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, const PartSet& few,
+       int few_rows, int ctas, cudaStream_t s) {
     using C = Cfg<D, Q8>;
     static std::atomic<uint64_t> raised{0};
     if (raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<D, Q8>), C::SMEM, &raised) != cudaSuccess)
@@ -867,8 +880,8 @@ int go(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cons
     }
     cudaError_t e = launch_after(chunk_kernel<D, Q8>, dim3((unsigned)ctas), C::THREADS, C::SMEM, s, tq, tk, tv, p);
     if (e == cudaSuccess && ctas > 1)
-        e = launch_after(chunk_merge_kernel<D, kRows, 8>, dim3((unsigned)ctas - 1, kRows / 8), 256, 0, s, p.c, p.meta,
-                         p.part_o, p.part_ml, p.tq);
+        e = launch_after(chunk_merge_kernel<D>, dim3((unsigned)ctas - 1, (unsigned)(few_rows + kRows / 32)), 256, 0, s, p.c,
+                         few, PartSet{p.meta, p.part_o, p.part_ml}, few_rows, p.tq);
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -901,10 +914,11 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
     if (a->B == 0 || a->tokens == 0) return BSA_OK;
     const int G = a->Hq / c->Hkv;
     const Layout w = layout(a->B, a->tokens, G, c->D);
-    // the steps of the chunks stay below 2^30 (sums and range ends fit an int)
+    // the steps of the chunks stay below 2^30 (sums and range ends fit an int): a sequence has
+    // its tokens over 2 tq, rounded up, groups (the kernel refuses sequences that overlap so far)
     const int64_t most = ((int64_t)c->max_pages * c->page + kTile - 1) / kTile;
-    if (c->Hkv * most > 1 << 30 || (w.cap > 0 && w.cap * (double)most * c->Hkv > (double)(1 << 30)))
-        return BSA_ERR_INVALID_ARG;
+    const double groups = (double)a->tokens / (2 * tile_tokens(G)) + a->B;
+    if (c->Hkv * most > 1 << 30 || groups * most * c->Hkv > (double)(1 << 30)) return BSA_ERR_INVALID_ARG;
     if (!workspace || !al(workspace, 256)) return BSA_ERR_INVALID_ARG;
     if (workspace_bytes < w.bytes) return BSA_ERR_CAPACITY;
     ChunkCommon p{};
@@ -931,8 +945,13 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
     p.wait_limit_ns = wait_limit_ns();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    // single tokens of more heads than a short sequence's rows are chunks too
-    if (G <= kShortRows) {
+    // Short sequences have a kernel of their own, unless there is but one sequence and it
+    // can be a chunk; single tokens of more heads than its rows are chunks too.
+    const bool all_short = !a->q_ptr || (int64_t)a->tokens * G <= kShortRows;  // if their heads allow
+    const bool some_short = G <= kShortRows && (all_short || a->B > 1);
+    PartSet few{};
+    int few_rows = 0;
+    if (some_short) {
         ShortLaunch L{};
         L.c = p;
         L.k = c->k;
@@ -943,14 +962,16 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
         L.meta = reinterpret_cast<PartMeta*>(ws + w.short_meta);
         L.part_o = reinterpret_cast<float*>(ws + w.short_o);
         L.part_ml = reinterpret_cast<float2*>(ws + w.short_ml);
+        L.merge = all_short;
         if ((st = launch_short(L, s)) != BSA_OK) return st;
-        if (!a->q_ptr || (int64_t)a->tokens * G <= kShortRows) return BSA_OK;  // there is no other sequence
+        if (all_short) return BSA_OK;
+        few = PartSet{L.meta, L.part_o, L.part_ml};
+        few_rows = short_rows(p);
     }
     ChunkParams cp{};
     cp.c = p;
     cp.tq = tile_tokens(G);
-    cp.head = reinterpret_cast<const PlanHead*>(ws + w.head);
-    cp.groups = reinterpret_cast<const Group*>(ws + w.groups);
+    cp.least = some_short ? kShortRows + 1 : 1;
     cp.meta = reinterpret_cast<PartMeta*>(ws + w.meta);
     cp.part_o = reinterpret_cast<float*>(ws + w.o);
     cp.part_ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -960,12 +981,9 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
     if ((st = encode_token_rows_bf16(&tq, a->q, (uint64_t)a->tokens, a->Hq, c->D, G, cp.tq)) != BSA_OK) return st;
     if ((st = encode(&tk, c->k, krows, c->D, kHalf)) != BSA_OK) return st;
     if ((st = encode(&tv, c->v, krows, c->D, kHalf)) != BSA_OK) return st;
-    if (launch_after(plan_kernel, dim3(1), 1024, 0, s, p, reinterpret_cast<PlanHead*>(ws + w.head),
-                     reinterpret_cast<Group*>(ws + w.groups), w.cap, cp.tq) != cudaSuccess)
-        return BSA_ERR_CUDA;
     const int ctas = std::min(sms, kChunkMaxCtas);
-    if (c->D == 128) return scales ? go<128, true>(tq, tk, tv, cp, ctas, s) : go<128, false>(tq, tk, tv, cp, ctas, s);
-    return scales ? go<64, true>(tq, tk, tv, cp, ctas, s) : go<64, false>(tq, tk, tv, cp, ctas, s);
+    auto launch = c->D == 128 ? (scales ? go<128, true> : go<128, false>) : (scales ? go<64, true> : go<64, false>);
+    return launch(tq, tk, tv, cp, few, few_rows, ctas, s);
 }
 
 }  // extern "C"

@@ -132,74 +132,44 @@ struct ShortLaunch {
     PartMeta* meta;
     float* part_o;
     float2* part_ml;
+    bool merge;            // else the caller joins the parts (of the last launch, if there are several)
 };
 // Sequences whose new tokens make at most kShortRows rows of a key head (csrc/bsa_decode.cu).
 int launch_short(const ShortLaunch& L, cudaStream_t s);
+// Rows of a key head that its sequences can have, at most.
+inline int short_rows(const ChunkCommon& c) {
+    return c.G <= 8 && (!c.q_ptr || (int64_t)c.tokens * c.G <= 8) ? 8 : kShortRows;
+}
 
-// Joins the parts that the boundary in front of range x + 1 is the first to cut:
-// with parts i in range order, m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i /
-// sum w_i l_i.  A CTA takes RB rows, 8 / RB warps to a row (each every (8 / RB)-th
-// part).  Rows of an item: ROWS, in tiles of 128 with tq tokens of G rows each
-// (ROWS = 16: one tile).  Bound by dependent reads from the L2.
-template <int D, int ROWS, int RB>
-__global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkCommon p, const PartMeta* meta, const float* part_o,
-                                                          const float2* part_ml, int tq) {
-    constexpr int WPR = 8 / RB, C = D / 32;
-    __shared__ float red[WPR > 1 ? WPR : 1][D + 1];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const PartMeta mt = meta[blockIdx.x + 1];
-    const int first = blockIdx.x;
-    if (mt.start < 0 || mt.start < first * mt.per) return;  // not cut here, or by an earlier boundary too
-    const int last = (mt.end - 1) / mt.per;
-    const int r = blockIdx.y * RB + warp / WPR, part = warp % WPR;
-    const int i = r & 127, t = (r >> 7) * tq + i / p.G;
-    const bool on = r < ROWS && i < tq * p.G && t < mt.n;
-    if (WPR == 1 && !on) return;
-    auto slot_of = [&](int k) { return 2 * k + (k == first && mt.start > first * mt.per ? 1 : 0); };
-    float m = -INFINITY, l = 0.f, acc[C];
-#pragma unroll
-    for (int x = 0; x < C; ++x) acc[x] = 0.f;
-    if (on) {
-        for (int k = first + lane; k <= last; k += 32) m = fmaxf(m, part_ml[(int64_t)slot_of(k) * ROWS + r].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ref = m > -INFINITY ? m : 0.f;
-#pragma unroll 4
-        for (int k = first + part; k <= last; k += WPR) {
-            const int64_t pr = (int64_t)slot_of(k) * ROWS + r;
-            const float2 ml = part_ml[pr];
-            const float w = ex2_approx(ml.x - ref);  // 0 for a part that saw nothing
-            l += w * ml.y;
-            const float* src = part_o + pr * D + lane * C;
-            if (C == 4) {
-                const float4 o = *reinterpret_cast<const float4*>(src);
-                acc[0] += w * o.x;
-                acc[1] += w * o.y;
-                acc[C - 2] += w * o.z;
-                acc[C - 1] += w * o.w;
-            } else {
-                const float2 o = *reinterpret_cast<const float2*>(src);
-                acc[0] += w * o.x;
-                acc[1] += w * o.y;
-            }
-        }
+// Joins the parts of items that range boundaries cut, in range order: with parts i,
+// m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.  A warp to a row (chunks:
+// to four at a time, whose loads are all under way together; short sequences, which
+// can have a part from every CTA: eight warps to a row, every eighth part each).
+// Bound by dependent reads from the L2.
+struct PartSet {
+    const PartMeta* meta;
+    const float* o;       // [2 * ctas][rows][D]
+    const float2* ml;     // [2 * ctas][rows]
+};
+// The item that the boundary in front of range x + 1 is the first to cut: its
+// parts are those of ranges x .. last.
+struct CutItem {
+    PartMeta mt;
+    int first, last;
+    __device__ __forceinline__ bool find(const PartMeta* meta, int x) {
+        mt = meta[x + 1];
+        first = x;
+        if (mt.start < 0 || mt.start < x * mt.per) return false;  // not cut here, or by an earlier boundary too
+        last = (mt.end - 1) / mt.per;
+        return true;
     }
-    if (WPR > 1) {
-#pragma unroll
-        for (int x = 0; x < C; ++x) red[part][lane * C + x] = acc[x];
-        if (lane == 0) red[part][D] = l;
-        __syncthreads();
-        if (part > 0 || !on) return;
-        for (int w = 1; w < WPR; ++w) {
-#pragma unroll
-            for (int x = 0; x < C; ++x) acc[x] += red[w][lane * C + x];
-            l += red[w][D];
-        }
-    }
+    __device__ __forceinline__ int slot(int k) const { return 2 * k + (k == first && mt.start > first * mt.per ? 1 : 0); }
+};
+
+template <int D>
+__device__ __forceinline__ void store_row(const ChunkCommon& p, int64_t orow, int lane, const float* acc, float m, float l) {
+    constexpr int C = D / 32;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t orow = (int64_t)(mt.row0 + t) * p.Hq + mt.h * p.G + i % p.G;
     if (lane == 0) p.lse[orow] = lse_of(m, l);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D;
     if (C == 4)
@@ -207,6 +177,105 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkCommon p, c
             make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[C - 2] * inv, acc[C - 1] * inv));
     else
         reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+}
+template <int D>
+__device__ __forceinline__ void add_part(float* acc, const float* src, float w) {
+    constexpr int C = D / 32;
+    if (C == 4) {
+        const float4 o = *reinterpret_cast<const float4*>(src);
+        acc[0] += w * o.x;
+        acc[1] += w * o.y;
+        acc[C - 2] += w * o.z;
+        acc[C - 1] += w * o.w;
+    } else {
+        const float2 o = *reinterpret_cast<const float2*>(src);
+        acc[0] += w * o.x;
+        acc[1] += w * o.y;
+    }
+}
+
+// blockIdx.y < rows_short: row blockIdx.y of a short sequence's item; behind those, 32
+// rows of a chunk's item (256 rows, two tiles of tq tokens).
+template <int D>
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkCommon p, const PartSet few, const PartSet many,
+                                                          int rows_short, int tq) {
+    constexpr int C = D / 32, R = 4;
+    __shared__ float red[8][D + 1];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    CutItem it;
+    if ((int)blockIdx.y < rows_short) {
+        if (!it.find(few.meta, blockIdx.x)) return;
+        const int r = blockIdx.y;
+        if (r >= it.mt.n * p.G) return;
+        float m = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+        for (int x = 0; x < C; ++x) acc[x] = 0.f;
+        for (int k = it.first + lane; k <= it.last; k += 32) m = fmaxf(m, few.ml[(int64_t)it.slot(k) * kShortRows + r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = m > -INFINITY ? m : 0.f;
+#pragma unroll 4
+        for (int k = it.first + warp; k <= it.last; k += 8) {
+            const int64_t pr = (int64_t)it.slot(k) * kShortRows + r;
+            const float2 ml = few.ml[pr];
+            const float w = ex2_approx(ml.x - ref);  // 0 for a part that saw nothing
+            l += w * ml.y;
+            add_part<D>(acc, few.o + pr * D + lane * C, w);
+        }
+#pragma unroll
+        for (int x = 0; x < C; ++x) red[warp][lane * C + x] = acc[x];
+        if (lane == 0) red[warp][D] = l;
+        __syncthreads();
+        if (warp > 0) return;
+        for (int w = 1; w < 8; ++w) {
+#pragma unroll
+            for (int x = 0; x < C; ++x) acc[x] += red[w][lane * C + x];
+            l += red[w][D];
+        }
+        store_row<D>(p, (int64_t)(it.mt.row0 + r / p.G) * p.Hq + it.mt.h * p.G + r % p.G, lane, acc, m, l);
+        return;
+    }
+    if (!it.find(many.meta, blockIdx.x)) return;
+    const int r0 = ((int)blockIdx.y - rows_short) * 8 * R + warp * R;
+    const int t0 = (r0 >> 7) * tq, i0 = r0 & 127;  // first token of the tile, row in it
+    bool on[R];
+    float m[R], l[R], acc[R][C];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        on[q] = i0 + q < tq * p.G && t0 + (i0 + q) / p.G < it.mt.n;
+        m[q] = -INFINITY;
+        l[q] = 0.f;
+#pragma unroll
+        for (int x = 0; x < C; ++x) acc[q][x] = 0.f;
+    }
+    if (!on[0]) return;  // nor are the rows behind it
+    for (int k = it.first + lane; k <= it.last; k += 32)
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (on[q]) m[q] = fmaxf(m[q], many.ml[(int64_t)it.slot(k) * 256 + r0 + q].x);
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m[q] = fmaxf(m[q], __shfl_xor_sync(0xffffffffu, m[q], o));
+#pragma unroll 2
+    for (int k = it.first; k <= it.last; ++k) {
+        const int64_t pr = (int64_t)it.slot(k) * 256 + r0;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            if (!on[q]) continue;
+            const float2 ml = many.ml[pr + q];
+            const float w = ex2_approx(ml.x - (m[q] > -INFINITY ? m[q] : 0.f));
+            l[q] += w * ml.y;
+            add_part<D>(acc[q], many.o + (pr + q) * D + lane * C, w);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+        if (on[q])
+            store_row<D>(p, (int64_t)(it.mt.row0 + t0 + (i0 + q) / p.G) * p.Hq + it.mt.h * p.G + (i0 + q) % p.G, lane,
+                         acc[q], m[q], l[q]);
 }
 
 }  // namespace bsa

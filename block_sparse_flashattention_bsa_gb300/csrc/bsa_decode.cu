@@ -878,9 +878,10 @@ int go(const ShortLaunch& L, const CUtensorMap& tk, const CUtensorMap& tv, cudaS
         p.units = std::min(chunk, L.c.B - u0);
         cudaError_t e = launch_after(short_kernel<D, Q8, NT>, dim3((unsigned)ctas), kThreads, C::SMEM, s, tk, tv, p);
         if (e != cudaSuccess) return BSA_ERR_CUDA;
-        if (ctas < 2) continue;
-        e = launch_after(chunk_merge_kernel<D, kShortRows, 1>, dim3((unsigned)ctas - 1, (unsigned)(8 * NT)), 256, 0, s,
-                         p.c, p.meta, p.part_o, p.part_ml, 128);
+        if (ctas < 2 || (!L.merge && u0 + chunk >= L.c.B)) continue;
+        const PartSet few{p.meta, p.part_o, p.part_ml};
+        e = launch_after(chunk_merge_kernel<D>, dim3((unsigned)ctas - 1, (unsigned)(8 * NT)), 256, 0, s, p.c, few,
+                         PartSet{}, 8 * NT, 0);
         if (e != cudaSuccess) return BSA_ERR_CUDA;
     }
     return BSA_OK;
@@ -896,8 +897,7 @@ int launch_short(const ShortLaunch& L, cudaStream_t s) {
     int st;
     if ((st = encode(&tk, L.k, krows, L.D, L.c.page)) != BSA_OK) return st;
     if ((st = encode(&tv, L.v, krows, L.D, L.c.page)) != BSA_OK) return st;
-    // one 8-column tile of query rows where no short sequence can have more
-    const bool one = L.c.G <= 8 && (!L.c.q_ptr || (int64_t)L.c.tokens * L.c.G <= 8);
+    const bool one = short_rows(L.c) == 8;  // one 8-column tile of query rows
     if (L.D == 128)
         return one ? (q8 ? go<128, true, 1>(L, tk, tv, s) : go<128, false, 1>(L, tk, tv, s))
                    : (q8 ? go<128, true, 2>(L, tk, tv, s) : go<128, false, 2>(L, tk, tv, s));
