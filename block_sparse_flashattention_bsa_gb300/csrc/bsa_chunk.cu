@@ -100,7 +100,8 @@ struct ChunkParams {
 
 template <int D, bool Q8>
 struct Cfg {
-    static constexpr int THREADS = 512;
+    static constexpr int THREADS = Q8 ? 640 : 512;
+    static constexpr int CONV = 2;                     // converting warps of a tile
     static constexpr int NBOX = D / 64;
     static constexpr int QBOX = 128 * 128, QTILE = NBOX * QBOX;
     static constexpr int BOX = kHalf * 128, TILE = NBOX * BOX;
@@ -492,15 +493,17 @@ __device__ void fixer(uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
 }
 
 // ---------------------------------------------------------------- converters
-// Four warps, one to each tile of a step (K and V of either half), so that four
-// tiles are under way at a time: codes times 2^e, in bf16, into the tile that the
+// Eight warps, two to each tile of a step (K and V of either half), so that four
+// tiles are under way at a time (64 rows of 128 codes take a warp 3,600 cycles
+// beside two softmax warps, a step 4,500 with one warp to a tile): codes times 2^e, in bf16, into the tile that the
 // products read; 16-byte pieces, both sides in their copy's swizzle.
 template <int D>
 __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
     using C = Cfg<D, true>;
     constexpr int LPR = D / 16, RPP = 32 / LPR;  // lanes of a row (a 16-byte piece each), rows at a time
     const int lane = threadIdx.x & 31, id = (threadIdx.x >> 5) - kConverter, hf = id & 1, piece = lane % LPR;
-    const bool val = id >= 2;
+    const bool val = id & 2;
+    const int from = (id >> 2) * (kHalf / C::CONV);  // this warp's rows
     for (uint32_t g = 0;; ++g) {
         const uint32_t is = g % kInfos, x = 2 * g + hf, n = val ? v_tile(x) : k_tile(x);
         if (!warp_wait(&c->i_full[is], (g / kInfos) & 1, wf)) return;
@@ -508,7 +511,7 @@ __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctr
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->i_empty[is]);
         const bool end = flags & kEnd;
-        if (end && id != 0) return;  // the end mark stands in the place of the next K tile
+        if (end && (id & 3)) return;  // the end mark stands in the place of the next K tile
         const uint32_t rs = n % C::NRAW, ts = n % C::NT;
         if (!warp_wait(&c->r_full[rs], (n / C::NRAW) & 1, wf)) return;
         if (!warp_wait(&c->t_empty[ts], ((n / C::NT) & 1) ^ 1, wf)) return;
@@ -516,7 +519,7 @@ __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctr
             // V rows behind the last token may be NaN, and 0 * NaN is none of the sum
             const int keep = val && (flags & kFix) ? left : kHalf;
 #pragma unroll 4
-            for (int r0 = 0; r0 < kHalf; r0 += RPP) {
+            for (int r0 = from; r0 < from + kHalf / C::CONV; r0 += RPP) {
                 const int row = r0 + lane / LPR;
                 const int rx = D == 64 ? (row >> 1) & 3 : row & 7, wx = row & 7;
                 uint4 v = *reinterpret_cast<const uint4*>(sR + rs * C::RAW + row * D + ((piece ^ rx) << 4));
@@ -723,13 +726,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     {
         const int x = threadIdx.x;
         if (x < kMaxTiles) {
-            mbar_init(&c->t_full[x], 1);  // its converter, or the copy
+            mbar_init(&c->t_full[x], Q8 ? C::CONV : 1);  // its converters, or the copy
             mbar_init(&c->t_empty[x], 2);  // both tiles' products
             mbar_init(&c->r_full[x], 1);
-            mbar_init(&c->r_empty[x], 1);
+            mbar_init(&c->r_empty[x], C::CONV);
         } else if (x >= 32 && x < 32 + kInfos) {
             mbar_init(&c->i_full[x - 32], 1);
-            mbar_init(&c->i_empty[x - 32], Q8 ? 12 : 9);  // the softmax warps, the converters or the fixer
+            mbar_init(&c->i_empty[x - 32], 8 + (Q8 ? 4 * C::CONV : 1));  // the softmax warps, the converters or the fixer
             mbar_init(&c->fix_full[x - 32][0], 1);
             mbar_init(&c->fix_full[x - 32][1], 1);
         } else if (x >= 64 && x < 66) {
@@ -803,13 +806,19 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
         }
     }
     __syncthreads();
-    // 128 registers a thread at launch; the softmax's 256 threads take 184, the
-    // others' 256 keep 72: 184 + 72 = 2 * 128.
+    // A split of the launch's registers: bf16 512 x 128 = 256 x 184 + 256 x 72, 8-bit
+    // 640 x 96 = 256 x 144 + 384 x 64.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        if (Q8)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         softmax<D, Q8>(p, c, tmem, wf);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (Q8)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kProducer)
             producer<D, Q8>(&tk, &tv, p, Q8 ? sR : sT, sS, c, lo, hi, per, wf);
         else if (warp == kMma || warp == kMma + 1)
@@ -876,7 +885,7 @@ int go(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cons
             if (cudaFuncGetAttributes(&at, chunk_kernel<D, Q8>) != cudaSuccess) return BSA_ERR_CUDA;
             regs.store(at.numRegs);
         }
-        if (regs.load() < 128) return BSA_ERR_UNSUPPORTED;
+        if (regs.load() < (Q8 ? 96 : 128)) return BSA_ERR_UNSUPPORTED;
     }
     cudaError_t e = launch_after(chunk_kernel<D, Q8>, dim3((unsigned)ctas), C::THREADS, C::SMEM, s, tq, tk, tv, p);
     if (e == cudaSuccess && ctas > 1)
