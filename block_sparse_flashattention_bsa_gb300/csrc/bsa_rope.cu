@@ -13,6 +13,7 @@
 // fraction is good to 2^-53 of a turn per position); its top 32 bits give the
 // angle in [-pi, pi), where sin.approx / cos.approx are within 2^-20 of the
 // true values.  That is 2^11 times finer than the bf16 rounding of the result.
+// Keys that are written as 8-bit codes take them to fp32's precision.
 //
 // Gradients, with dy the rotated-back gradient (by -t f, times gain), g = dy * w:
 //   dx = r g - x r^3 mean(g x),   dw = sum over rows of dy * x * r
@@ -129,14 +130,22 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// cos and sin of this lane's 8 pairs at position pos, times gain.
-template <int LPR, bool IL>
+// cos and sin of this lane's 8 pairs at position pos, times gain.  FINE: to fp32's
+// precision (2^-20 is far below a bf16 rounding, but moves one in 10^5 values that
+// go straight to an 8-bit code to the next one).
+template <int LPR, bool IL, bool FINE = false>
 __device__ __forceinline__ void lane_angles(const unsigned long long* turns, int s, int pos, float gain, float* cs,
                                             float* sn) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int i = IL ? 4 * s + e + (e < 4 ? 0 : 4 * LPR - 4) : 8 * s + e;
         const unsigned long long t = turns[i] * (unsigned long long)(long long)pos;
+        if (FINE) {
+            sincospif((float)(int)(unsigned)(t >> 32) * 4.656612873077392578125e-10f, &sn[e], &cs[e]);  // 2^-31
+            cs[e] *= gain;
+            sn[e] *= gain;
+            continue;
+        }
         const float a = (float)(int)(unsigned)(t >> 32) * 1.46291807926715968e-9f;  // 2 pi / 2^32
         cs[e] = __cosf(a) * gain;
         sn[e] = __sinf(a) * gain;
@@ -405,7 +414,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_append_kernel(const
         }
         if (turn) {
             float c[8], s[8];
-            lane_angles<LPR, IL>(turns, ln.s, t.pos, p.gain, c, s);
+            if (Q8 && kind == 1)
+                lane_angles<LPR, IL, true>(turns, ln.s, t.pos, p.gain, c, s);
+            else
+                lane_angles<LPR, IL>(turns, ln.s, t.pos, p.gain, c, s);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 cs[e] = {c[2 * e], c[2 * e + 1]};
