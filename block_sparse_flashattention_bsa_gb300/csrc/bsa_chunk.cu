@@ -20,12 +20,12 @@
 //   warps 0-3, 4-7  softmax of tile A, B: thread = row (TMEM lane).  S in
 //              registers, P back over it in bf16.  O is rescaled in TMEM only when
 //              the maximum grows by more than 2^8.
-//   warp 8     producer: walks the range, resolves pages, TMA-loads K / V tiles
+//   warp 8     producer: walks the range, resolves pages, TMA-loads K / V tiles;
+//              bf16: zeroes V rows behind the last token (they may hold NaN)
 //   warps 9, 10  MMA of tile A, B: S = Q K^T and O += P V on tcgen05, 64 slots at a
 //              time, two S buffers to a tile: a tile's scores are two halves of a step
 //              ahead of its product
 //   warp 11    loads an item's Q tiles as soon as the item before has used its own
-//   warp 12    bf16: zeroes V rows behind the last token (they may hold NaN)
 //   warps 12-15  8-bit: convert tiles to bf16 (code * 2^e, exact), thread = row
 
 #include <algorithm>
@@ -44,7 +44,7 @@ constexpr int kInfos = 4;
 constexpr int kQAhead = 4;
 constexpr int kMaxTiles = 16;
 constexpr int kHalf = 64;     // key slots of a tile: half of a step
-constexpr int kProducer = 8, kMma = 9, kQLoader = 11, kFixer = 12, kConverter = 12;
+constexpr int kProducer = 8, kMma = 9, kQLoader = 11, kConverter = 12;
 constexpr int kRows = 256;  // rows of an item
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kEnd = 8, kFix = 16 };
@@ -78,8 +78,9 @@ struct Ctrl {
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [tile][half of a step]
     uint64_t o_full[2];
     uint64_t i_full[kInfos], i_empty[kInfos];
-    uint64_t fix_full[kInfos][2], drain[2];
+    uint64_t fix_full[kInfos][2], drain[2];  // fix_full: a half's V rows behind the last token are zeros
     volatile uint32_t issued;        // steps the producer has issued
+    volatile uint32_t first[2];      // 8-bit: halves of K(0) that are converted
     int2 qitem[kQAhead];             // first query head and token of an item; x < 0: no more
     StepInfo info[kInfos];
     uint32_t tmem_base;
@@ -107,13 +108,14 @@ struct Cfg {
     static constexpr int BOX = kHalf * 128, TILE = NBOX * BOX;
     static constexpr int RAW = kHalf * D;              // an 8-bit tile
     static constexpr int FREE = kSmem - kCtrl - 2 * QTILE;
-    // 8-bit: six bf16 tiles, the rest holds what is in flight
-    static constexpr int RAWFIT = (FREE - 6 * TILE) / (RAW + kHalf);
+    // 8-bit: eight bf16 tiles, the rest holds what is in flight; both in fours, so that
+    // a slot's tiles are all converted by the same two warps
+    static constexpr int RAWFIT = (FREE - 8 * TILE) / (RAW + kHalf) / 4 * 4;
     static constexpr int NRAW = !Q8 ? 0 : RAWFIT > kMaxTiles ? kMaxTiles : RAWFIT;
-    static constexpr int NT = Q8 ? 6 : FREE / TILE > kMaxTiles ? kMaxTiles : FREE / TILE;
+    static constexpr int NT = Q8 ? 8 : FREE / TILE > kMaxTiles ? kMaxTiles : FREE / TILE;
     static constexpr int SMEM = 2 * QTILE + NT * TILE + NRAW * (RAW + kHalf) + kCtrl;
     static constexpr int O_COL = 2 * kTile;
-    static_assert(SMEM <= kSmem && NT >= 6 && (!Q8 || NRAW >= 6), "shared memory");
+    static_assert(SMEM <= kSmem && NT >= 6 && (!Q8 || NRAW >= 4), "shared memory");
 };
 
 // ---------------------------------------------------------------- plan
@@ -196,6 +198,26 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
         }
         return true;
     };
+    // V of half hf of the step before (number g - 1): its load, and what its last rows need
+    int v_held = kTile;  // its slots up to the last token
+    auto load_v = [&](int hf, int y, uint32_t g) -> bool {
+        const uint32_t s = slot, ph = phase;
+        if (!load(true, y)) return false;
+        if (Q8) return true;
+        const int from = max(v_held - hf * kHalf, 0);
+        if (from < kHalf) {
+            // rows behind the last token may hold NaN, and 0 * NaN is none of the sum
+            if (!warp_wait(&full[s], ph, wf)) return false;
+#pragma unroll
+            for (int x = 0; x < NBOX; ++x)
+                for (int i = from * 8 + lane; i < kHalf * 8; i += 32)
+                    reinterpret_cast<uint4*>(sT + s * TILE + x * BOX)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (leader) mbar_arrive(&c->fix_full[(g - 1) % kInfos][hf]);  // at every step: its phase goes with the step
+        return true;
+    };
     if (lo < hi) {
         // c->place: the sequence that step lo lies in, and its first step; then the head, and
         // the group: the last one whose first step is not behind it
@@ -273,12 +295,14 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
                     }
                     __syncwarp();
                     const int k1 = ppt == 2 ? y1 : y0 >= 0 ? y0 + kHalf : -1;
-                    if (g > 0) ok = load(true, v0);
+                    if (g > 0) ok = load_v(0, v0, g);
                     ok = ok && load(false, y0);
-                    if (g > 0) ok = ok && load(true, v1);
+                    if (g > 0) ok = ok && load_v(1, v1, g);
                     ok = ok && load(false, k1);
                     v0 = y0;
                     v1 = k1;
+                    const int base = sp.tile(st) * kTile;
+                    v_held = base + kTile > sq.ctx + sq.n ? sq.ctx + sq.n - base : kTile;
                     ++g;
                     if (leader) c->issued = g;
                 }
@@ -300,7 +324,7 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
     if (ok) {
         // the end mark in the place of the next K tile; the converters and the MMA lanes pass it on
         const uint32_t is = g % kInfos;
-        if (g > 0) ok = load(true, v0);
+        if (g > 0) ok = load_v(0, v0, g);
         ok = ok && (g < kInfos || warp_wait(&c->i_empty[is], ((g / kInfos) & 1) ^ 1, wf));
         ok = ok && (nload < NS || warp_wait(&empty[slot], phase ^ 1, wf));
         if (ok) {
@@ -311,11 +335,11 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
             }
             __syncwarp();
             ++nload;
-            if (++slot == NS) {
+                if (++slot == NS) {
                 slot = 0;
                 phase ^= 1;
             }
-            if (g > 0) load(true, v1);
+            if (g > 0) load_v(1, v1, g);
         }
         if ((nq < kQAhead || warp_wait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) && leader) {
             c->qitem[nq % kQAhead] = make_int2(-1, 0);
@@ -460,38 +484,6 @@ __device__ void mma_lane(int t, uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem
     __syncwarp();
 }
 
-// ---------------------------------------------------------------- fixer
-// bf16: V rows behind the last token become zeros before the product reads them.
-// It has a barrier of its own for the descriptions: no product waits for it at
-// most steps, so a tile's barrier may be two phases on when it comes to look.
-template <int D>
-__device__ void fixer(uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
-    using C = Cfg<D, false>;
-    const int lane = threadIdx.x & 31;
-    for (uint32_t g = 0;; ++g) {
-        const uint32_t is = g % kInfos;
-        if (!warp_wait(&c->i_full[is], (g / kInfos) & 1, wf)) return;
-        const int flags = c->info[is].flags, held = c->info[is].end - c->info[is].base;
-        if (flags & kEnd) return;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int from = max(held - hf * kHalf, 0);
-            if ((flags & kFix) && from < kHalf) {
-                const uint32_t n = v_tile(2 * g + hf), slot = n % C::NT;
-                if (!warp_wait(&c->t_full[slot], (n / C::NT) & 1, wf)) return;
-#pragma unroll
-                for (int x = 0; x < C::NBOX; ++x)
-                    for (int i = from * 8 + lane; i < kHalf * 8; i += 32)
-                        reinterpret_cast<uint4*>(sT + slot * C::TILE + x * C::BOX)[i] = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->fix_full[is][hf]);  // at every step, so that its phase goes with the step
-        }
-        if (lane == 0) mbar_arrive(&c->i_empty[is]);
-    }
-}
-
 // ---------------------------------------------------------------- converters
 // Eight warps, two to each tile of a step (K and V of either half), so that four
 // tiles are under way at a time (64 rows of 128 codes take a warp 3,600 cycles
@@ -513,6 +505,10 @@ __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctr
         const bool end = flags & kEnd;
         if (end && (id & 3)) return;  // the end mark stands in the place of the next K tile
         const uint32_t rs = n % C::NRAW, ts = n % C::NT;
+        // A barrier's parity tells a phase from its neighbours only: who skips phases may
+        // take one for another.  These warps see every phase of their slots' barriers, but
+        // for K(0), which stands where V(-1) would: it has landed once it is converted.
+        if (g == 0 && id % 4 == 3 && (!reached(&c->first[0], 1, wf) || !reached(&c->first[1], 1, wf))) return;
         if (!warp_wait(&c->r_full[rs], (n / C::NRAW) & 1, wf)) return;
         if (!warp_wait(&c->t_empty[ts], ((n / C::NT) & 1) ^ 1, wf)) return;
         if (!end) {
@@ -545,6 +541,7 @@ __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctr
         if (lane == 0) {
             mbar_arrive(&c->r_empty[rs]);
             mbar_arrive(&c->t_full[ts]);
+            if (n == 0) c->first[id >> 2] = 1;
         }
         if (end) return;
     }
@@ -732,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             mbar_init(&c->r_empty[x], C::CONV);
         } else if (x >= 32 && x < 32 + kInfos) {
             mbar_init(&c->i_full[x - 32], 1);
-            mbar_init(&c->i_empty[x - 32], 8 + (Q8 ? 4 * C::CONV : 1));  // the softmax warps, the converters or the fixer
+            mbar_init(&c->i_empty[x - 32], 8 + (Q8 ? 4 * C::CONV : 0));  // the softmax warps and the converters
             mbar_init(&c->fix_full[x - 32][0], 1);
             mbar_init(&c->fix_full[x - 32][1], 1);
         } else if (x >= 64 && x < 66) {
@@ -753,6 +750,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             c->wf.abort = 0;
             c->wf.limit_ns = p.c.wait_limit_ns;
             c->issued = 0;
+            c->first[0] = c->first[1] = 0;
         }
         fence_mbar_init();
         for (int z = x; z < 2 * C::QTILE / 16; z += C::THREADS)
@@ -827,8 +825,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             q_loader<D>(&tq, p, sQ, c, wf);
         else if (Q8)
             converter<D>(sR, sS, sT, c, wf);
-        else if (warp == kFixer)
-            fixer<D>(sT, c, wf);
     }
     __syncwarp();
     tc_fence_before();

@@ -117,6 +117,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, wf));
 }
 
+// Whole warp: until the counter (which only grows) is at `want`.  A barrier's
+// parity tells a phase from its neighbours only, so who does not wait for every
+// phase of a barrier first makes sure that the phase it wants is the current one
+// or the one before: a tile's load was issued, so its slot's last use is over.
+__device__ __forceinline__ bool reached(volatile uint32_t* count, uint32_t want, volatile WaitFlag* wf) {
+    if (__any_sync(0xffffffffu, *count >= want)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (__any_sync(0xffffffffu, *count >= want)) return true;
+        if ((it & 31u) == 0) {
+            const bool late = globaltimer_ns() - t0 > wf->limit_ns;
+            if (late) wf->abort = 1;
+            if (__any_sync(0xffffffffu, late || wf->abort)) return false;
+        }
+    }
+}
+
 // Untiled bulk copy global -> shared (16-byte aligned, bytes % 16 == 0), counted on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(

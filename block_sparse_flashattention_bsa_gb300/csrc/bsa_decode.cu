@@ -57,7 +57,7 @@ constexpr int kHaveBit = 2;
 struct ShortInfo {      // a step
     int flags;          // and from kHaveBit on, per tile, the halves that lie in a page
     int base[2];        // first slot of each tile
-    int slot;           // ring slot of the first K tile, bit 31: its phase
+    uint32_t tile;      // number of its first K tile in the order of loads
 };
 struct ShortItem {
     int step0, steps;   // its steps of this CTA; steps < 0: no more items
@@ -76,6 +76,7 @@ struct ShortCtrl {
     float2 stats[kWarps][16];  // [warp][row]
     int red[kThreads / 32];
     WaitFlag wf;
+    volatile uint32_t loaded;  // tiles whose load was issued
     int prefix[kShortUnits + 1];
 };
 static_assert(sizeof(ShortCtrl) <= kShortCtrl, "control block too large");
@@ -103,6 +104,9 @@ struct ShortCfg {
     static constexpr int FIT = (kShortSmem - FIXED) / TILE;
     static constexpr int SLOTS = FIT > kShortMaxSlots ? kShortMaxSlots : FIT;
     static constexpr int SMEM = SLOTS * TILE + FIXED;
+    // A step is announced when all of its loads were issued, unless the ring is too short
+    // for that; then who waits for a tile looks for its load first (reached()).
+    static constexpr bool LATE = SLOTS >= 4 * SUB;
     static_assert(SLOTS >= 2 * SUB, "ring too small");
 };
 
@@ -208,8 +212,8 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                             f.base[x] = first;
                         }
                         f.flags = (plain ? 0 : kMask) | (nx == 1 ? kOne : 0) | have << kHaveBit;
-                        f.slot = (int)(slot | phase << 31);
-                        mbar_arrive(&c->i_full[is]);
+                        f.tile = nload;
+                        if (!C::LATE) mbar_arrive(&c->i_full[is]);
                     }
                     __syncwarp();
                     ++g;
@@ -241,11 +245,13 @@ __device__ void short_producer(const CUtensorMap* tk, const CUtensorMap* tv, con
                             }
                         }
                         ++nload;
+                        if (!C::LATE && leader) c->loaded = nload;
                         if (++slot == (uint32_t)p.n_slots) {
                             slot = 0;
                             phase ^= 1;
                         }
                     }
+                    if (C::LATE && ok && leader) mbar_arrive(&c->i_full[is]);
                 }
             }
             pos = start + s1;
@@ -401,25 +407,23 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
             int base[SUB];
 #pragma unroll
             for (int x = 0; x < SUB; ++x) base[x] = c->info[is].base[x];
-            uint32_t slot = (uint32_t)c->info[is].slot & 0x7fffffffu, phase = (uint32_t)c->info[is].slot >> 31;
+            uint32_t tile = c->info[is].tile;
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->i_empty[is]);
             const int nx = flags & kOne ? 1 : SUB;
-            uint32_t ts[2 * SUB], tp[2 * SUB];  // slots and phases of the K and V tiles
+            uint32_t ts[2 * SUB], tn[2 * SUB];  // slots and numbers of the K and V tiles
 #pragma unroll
             for (int x = 0; x < 2 * SUB; ++x) {
-                if (x % SUB >= nx) {  // not there: what the one before it holds is read and not used
-                    ts[x] = ts[x - 1];
-                    tp[x] = tp[x - 1];
-                    continue;
-                }
-                ts[x] = slot;
-                tp[x] = phase;
-                if (++slot == (uint32_t)p.n_slots) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                // one that is not there: what the one before it holds is read and not used
+                tn[x] = x % SUB >= nx ? tn[x - 1] : tile++;
+                ts[x] = tn[x] % C::SLOTS;
             }
+            // mostly all of the step's loads were issued by now
+            const bool issued = C::LATE || __any_sync(0xffffffffu, c->loaded >= tile);
+            auto landed = [&](int x) -> bool {
+                return (issued || reached(&c->loaded, tn[x] + 1, wf)) &&
+                       warp_wait(&c->t_full[ts[x]], (tn[x] / C::SLOTS) & 1, wf);
+            };
             float s[SUB][NT][4];
             uint32_t kb[SUB][2];  // 8-bit: the scale bytes of keys g and g + 8
 #pragma unroll
@@ -428,7 +432,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[x][nt][i] = 0.f;
-                if (x < nx && !warp_wait(&c->t_full[ts[x]], tp[x], wf)) return;
+                if (x < nx && !landed(x)) return;
             }
             if (Q8) {
                 uint4 kr[SUB][2][D / 64];
@@ -548,7 +552,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 }
 #pragma unroll
             for (int x = 0; x < SUB; ++x)
-                if (x < nx && !warp_wait(&c->t_full[ts[SUB + x]], tp[SUB + x], wf)) return;
+                if (x < nx && !landed(SUB + x)) return;
             if (Q8) {
                 // Values are fp16 codes; their scales go into the weights, relative to the
                 // largest one met (with room for the next ones): 2^7 p 2^(e - ref) is at most
@@ -802,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&c->x_empty, 1);
             c->wf.abort = 0;
             c->wf.limit_ns = p.c.wait_limit_ns;
+            c->loaded = 0;
             c->prefix[0] = 0;
         }
         fence_mbar_init();

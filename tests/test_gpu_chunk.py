@@ -6,11 +6,12 @@ A = sum p |v| / sum p:
     that is at most M = max over keys of scale * sum_d |q_d k_d|: D M 2^-24;
     the exponent's product, subtraction and 2^x: |x| 2^-23 + 2^-22, |x| <= 2 M
     -> relative error of a weight  e = (D + 4 * 2) M 2^-24 + 2^-21
-  p is rounded to bf16 once, 2^-8 (sequences of more than 16 rows a key head); in
-    shorter ones it is held in two bf16 parts, 2^-16, or, times the 8-bit row's
-    scale, rounded to fp16 once, 2^-11 (below fp16's normal numbers, 2^-21 of what a
-    weight of 1 gives at the largest scale met: off by 2^-32 of that, inside 2^-16);
-    fp32 accumulation: steps * 2^-24, inside 2^-16
+  p is rounded to bf16 once, 2^-8 (chunks, and the short sequences of a small batch
+    that has chunks too); in short sequences of up to 16 rows a key head it is held in
+    two bf16 parts, 2^-16, or, times the 8-bit row's scale, rounded to fp16 once,
+    2^-11 (below fp16's normal numbers, 2^-21 of what a weight of 1 gives at the largest
+    scale met: off by 2^-32 of that, inside 2^-16); fp32 accumulation: steps * 2^-24,
+    inside 2^-16
   O: A (p's + 2 e + 2^-16) + |O| 2^-8 (its own rounding)
   LSE: e + 2^-21 (|LSE| + 1)
 8-bit rows are what they are (code * 2^e): the reference reads the same values.
@@ -38,10 +39,12 @@ def bsa():
 
 
 class Case:
-    def __init__(self, ctx, new, Hq, Hkv, D, page, q8, window=0, sinks=0, seed=0, q_scale=1.0, spread=1.0, release=False):
+    def __init__(self, ctx, new, Hq, Hkv, D, page, q8, window=0, sinks=0, seed=0, q_scale=1.0, spread=1.0, release=False,
+                 table_extra=1):
         g = torch.Generator().manual_seed(seed + 1)
         self.ctx, self.new, self.window, self.sinks, self.D = list(ctx), list(new), window, sinks, D
-        self.cache = Cache([c + n for c, n in zip(ctx, new)], Hkv, D, page, q8, seed, spread=spread)
+        self.cache = Cache([c + n for c, n in zip(ctx, new)], Hkv, D, page, q8, seed, spread=spread,
+                           table_extra=table_extra)
         self.q_ptr = [0]
         for n in new:
             self.q_ptr.append(self.q_ptr[-1] + n)
@@ -52,7 +55,11 @@ class Case:
                 for j in range(-(-c // page)):
                     if (j + 1) * page <= c - window + 1 and j * page >= sinks:
                         self.cache.table[b, j] = -1
-        self.short = [n * (Hq // Hkv) <= 16 for n in new]
+        self.G = Hq // Hkv
+        # whose rows the short form takes: all, or those of a batch of some size
+        P = self.cache.table.shape[1] * page / 128
+        alone = sum(new) * self.G <= 16 or (max(new) == 1 and self.G <= 16)
+        self.short = [n * self.G <= 16 and (alone or len(ctx) * P * Hkv > 64 * 160) for n in new]
 
     def args(self, one=False):
         k, v, table, sc = self.cache.device()
@@ -88,6 +95,7 @@ def test_decoding(bsa, D, page, q8, G):
     ctx = [0, 1, 62, 63, 64, 127, 128, 129, 300, 1000, 2049]
     c = Case(ctx, [1] * len(ctx), 2 * G, 2, D, page, q8, seed=G)
     c.check(*c.run(bsa, one=True))
+    c.short = [False] * len(ctx)
     c.check(*c.run(bsa))  # the same with q_ptr
 
 
@@ -103,8 +111,11 @@ def test_decoding_sixteen_rows(bsa, D, q8, G):
 def test_few_tokens_short(bsa, q8):
     """Two to eight tokens of few heads: still the short form."""
     c = Case([0, 3, 120, 500, 129], [2, 8, 5, 3, 1], 4, 2, 128, 64, q8)
-    assert all(c.short)
     c.check(*c.run(bsa))
+    for n in (2, 5, 8):
+        c = Case([140], [n], 2, 1, 128, 64, q8, seed=n)
+        assert all(c.short)
+        c.check(*c.run(bsa))
 
 
 @both
@@ -112,6 +123,28 @@ def test_decoding_long_context(bsa, q8):
     """Over all SMs: every CTA has a part of the one item or two."""
     c = Case([40000], [1], 4, 1, 128, 128, q8)
     c.check(*c.run(bsa, one=True))
+
+
+@both
+def test_few_tokens_beside_chunks(bsa, q8):
+    """Small batches; then a table wide enough for both forms: each row to its own tolerance."""
+    new = [1, 2, 1, 70, 1, 4, 1, 1, 300, 1, 0, 1] * 2
+    c = Case([3000 + 7 * b for b in range(24)], new, 8, 4, 128, 64, q8)
+    c.check(*c.run(bsa))
+    c = Case([1000 + 97 * b for b in range(24)], new, 8, 4, 128, 64, q8, table_extra=200)
+    assert any(c.short) and not all(c.short)
+    for _ in range(5):
+        c.check(*c.run(bsa))
+
+
+@both
+def test_ends_of_sequences_in_flight(bsa, q8):
+    """Many items a CTA, each with a last tile of rows that are not there (NaN), again and again."""
+    for D, page in ((128, 64), (64, 128), (128, 128)):
+        c = Case([3000 + 7 * b for b in range(16)], [70, 1, 2, 130] * 4, 8, 4, D, page, q8)
+        for _ in range(5):
+            o, lse = c.run(bsa)
+        c.check(o, lse)
 
 
 @both
