@@ -950,10 +950,16 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
     p.wait_limit_ns = wait_limit_ns();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    // Short sequences have a kernel of their own, unless there is but one sequence and it
-    // can be a chunk; single tokens of more heads than its rows are chunks too.
+    // Short sequences have a kernel of their own where that pays: a row of a chunk's tile
+    // costs them nothing but time, a launch and the wait for it do.  Counted in steps of
+    // single sequences per SM, at most (the table's width), batches of which a tenth are
+    // chunks of 60 to 500 tokens, us with and without that kernel:
+    //   bf16   8: 57, 39   34: 90, 74   70: 163, 157   105: 182, 196   190: 345, 383
+    //   8-bit  8: 54, 42   34: 77, 96   70: 139, 204   (a chunk's step takes 2.5 times as long)
+    // Single tokens of more heads than its rows are chunks too.
     const bool all_short = !a->q_ptr || (int64_t)a->tokens * G <= kShortRows;  // if their heads allow
-    const bool some_short = G <= kShortRows && (all_short || a->B > 1);
+    const bool some_short =
+        G <= kShortRows && (all_short || (a->B > 1 && a->B * most * c->Hkv > (scales ? 16ll : 64ll) * sms));
     PartSet few{};
     int few_rows = 0;
     if (some_short) {
