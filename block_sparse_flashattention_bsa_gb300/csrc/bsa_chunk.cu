@@ -26,7 +26,7 @@
 //              time, two S buffers to a tile: a tile's scores are two halves of a step
 //              ahead of its product
 //   warp 11    loads an item's Q tiles as soon as the item before has used its own
-//   warps 12-15  8-bit: convert tiles to bf16 (code * 2^e, exact), thread = row
+//   warps 12-19  8-bit: convert tiles to bf16 (code * 2^e, exact)
 
 #include <algorithm>
 #include <cmath>
@@ -113,7 +113,11 @@ struct Cfg {
     static constexpr int RAWFIT = (FREE - 8 * TILE) / (RAW + kHalf) / 4 * 4;
     static constexpr int NRAW = !Q8 ? 0 : RAWFIT > kMaxTiles ? kMaxTiles : RAWFIT;
     static constexpr int NT = Q8 ? 8 : FREE / TILE > kMaxTiles ? kMaxTiles : FREE / TILE;
-    static constexpr int SMEM = 2 * QTILE + NT * TILE + NRAW * (RAW + kHalf) + kCtrl;
+    // Finished rows on their way out, 128 bytes of each of a warp's 32 rows, for stores of whole
+    // lines: an item's end 1.1 us, a part's 1.6 us, straight from the lanes 1.5 and 2.5.  Rows
+    // of 128 values leave no room for it, and have half as many ends to their steps.
+    static constexpr int STAGE = D == 64 ? 8 * 32 * 128 : 0;
+    static constexpr int SMEM = 2 * QTILE + NT * TILE + NRAW * (RAW + kHalf) + STAGE + kCtrl;
     static constexpr int O_COL = 2 * kTile;
     static_assert(SMEM <= kSmem && NT >= 6 && (!Q8 || NRAW >= 4), "shared memory");
 };
@@ -127,9 +131,11 @@ struct Cfg {
 __device__ __forceinline__ int group_count(const ChunkParams& p, const Seq& s) {
     return s.n * (int64_t)p.c.G < p.least ? 0 : (s.n + 2 * p.tq - 1) / (2 * p.tq);
 }
+// Steps of group i, and one for its end, which takes about as long (with windows of ten
+// steps to an item the last CTA was 6 % behind the others without it).
 __device__ __forceinline__ int group_steps(const ChunkParams& p, const Seq& s, int i) {
     const int t0 = i * 2 * p.tq;
-    return visible_span(p.c, s.ctx + t0, s.ctx + min(s.n, t0 + 2 * p.tq)).steps;
+    return visible_span(p.c, s.ctx + t0, s.ctx + min(s.n, t0 + 2 * p.tq)).steps + 1;
 }
 // Steps of one key head of sequences b0 + lane (0 from b1 on), a lane each; the
 // whole warp takes those of many groups.
@@ -246,21 +252,23 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
             const int n = min(sq.n - t0, 2 * p.tq), first = sq.ctx + t0, last = first + n;
             const int vis0 = first_slot(cc, first);
             const Span sp = visible_span(cc, first, last);
-            const int start = at.start, end = start + sp.steps;
+            const int start = at.start, end = start + sp.steps;  // then the step of its end
             const int s0 = pos - start, s1 = min(end, hi) - start;
             const bool whole = s0 == 0 && start + s1 == end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (pos == lo ? 0 : 1);
-            if (start < lo) mt = PartMeta{start, end, per, sq.row0 + t0, n, h, {0, 0}};
+            if (start < lo && lo < end) mt = PartMeta{start, end, per, sq.row0 + t0, n, h, {0, 0}};
             // the Q loader's turn, as soon as its buffers are free
-            if (nq >= kQAhead && !warp_wait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
+            if (s0 < s1 && nq >= kQAhead && !warp_wait(&c->qi_empty[nq % kQAhead], ((nq / kQAhead) & 1) ^ 1, wf)) {
                 ok = false;
                 break;
             }
-            if (leader) {
-                c->qitem[nq % kQAhead] = make_int2(h * cc.G, sq.row0 + t0);
-                mbar_arrive(&c->qi_full[nq % kQAhead]);
+            if (s0 < s1) {
+                if (leader) {
+                    c->qitem[nq % kQAhead] = make_int2(h * cc.G, sq.row0 + t0);
+                    mbar_arrive(&c->qi_full[nq % kQAhead]);
+                }
+                ++nq;
             }
-            ++nq;
             for (int e0 = s0 * ppt; e0 < s1 * ppt && ok; e0 += 32) {
                 const int e = e0 + lane, est = e / ppt;  // 32 pages resolved at a time
                 const int j = sp.tile(est) * ppt + e % ppt;
@@ -307,8 +315,7 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
                     if (leader) c->issued = g;
                 }
             }
-            pos = start + s1;
-            at.start = end;
+            pos = at.start = end + 1;
             if (++at.i == n_groups && pos < hi) {
                 at.i = 0;
                 if (++at.h == cc.Hkv) {
@@ -335,7 +342,7 @@ __device__ void producer(const CUtensorMap* tk, const CUtensorMap* tv, const Chu
             }
             __syncwarp();
             ++nload;
-                if (++slot == NS) {
+            if (++slot == NS) {
                 slot = 0;
                 phase ^= 1;
             }
@@ -486,9 +493,11 @@ __device__ void mma_lane(int t, uint8_t* sQ, uint8_t* sT, Ctrl* c, uint32_t tmem
 
 // ---------------------------------------------------------------- converters
 // Eight warps, two to each tile of a step (K and V of either half), so that four
-// tiles are under way at a time (64 rows of 128 codes take a warp 3,600 cycles
-// beside two softmax warps, a step 4,500 with one warp to a tile): codes times 2^e, in bf16, into the tile that the
-// products read; 16-byte pieces, both sides in their copy's swizzle.
+// tiles are under way at a time: codes times 2^e, in bf16, into the tile that the
+// products read; 16-byte pieces, both sides in their copy's swizzle.  They share the
+// schedulers with two softmax warps each and take as long as those do: 8,192 tokens
+// behind as many slots, 32 heads of 128, 1,325 us (1.25 PFLOP/s; bf16 pools 1.37 PFLOP/s;
+// a warp to a tile 1,545, two for all four 1,747).
 template <int D>
 __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctrl* c, volatile WaitFlag* wf) {
     using C = Cfg<D, true>;
@@ -549,7 +558,7 @@ __device__ void converter(const uint8_t* sR, const uint8_t* sS, uint8_t* sT, Ctr
 
 // ---------------------------------------------------------------- softmax
 template <int D, bool Q8>
-__device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile WaitFlag* wf) {
+__device__ void softmax(const ChunkParams& p, uint8_t* stage, Ctrl* c, uint32_t tmem, volatile WaitFlag* wf) {
     using C = Cfg<D, Q8>;
     const ChunkCommon& cc = p.c;
     const int t = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -676,6 +685,39 @@ __device__ void softmax(const ChunkParams& p, Ctrl* c, uint32_t tmem, volatile W
             tmem_ld32(t_o + y * 32, o);
             tmem_wait_ld();
             reg_fence(o);
+            if (C::STAGE > 0) {
+                // 16-byte pieces of the lane's row, in a swizzle; bf16 rows: two turns to a line
+                uint8_t* mine = stage + lane * 128;
+                if (part < 0) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * i]) * w, __uint_as_float(o[8 * q + 2 * i + 1]) * w);
+                        *reinterpret_cast<uint4*>(mine + ((((y & 1) * 4 + q) ^ (lane & 7)) << 4)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    if (!(y & 1)) continue;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4*>(mine + ((q ^ (lane & 7)) << 4)) =
+                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                }
+                __syncwarp();
+                const int piece = lane & 7;
+                char* dst = (part < 0 ? static_cast<char*>(cc.out) + (y >> 1) * 128
+                                      : reinterpret_cast<char*>(p.part_o) + y * 128) + piece * 16;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = 4 * k + (lane >> 3);
+                    const long long at = __shfl_sync(0xffffffffu, (long long)(!live ? -1 : part < 0 ? orow : prow), r);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+                    if (at >= 0) *reinterpret_cast<uint4*>(dst + at * (part < 0 ? D * 2 : D * 4)) = v;
+                }
+                continue;  // the next turn begins with a __syncwarp
+            }
             if (!live) continue;
             if (part < 0) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cc.out) + orow * D + y * 32);
@@ -717,7 +759,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     uint8_t* sT = sQ + 2 * C::QTILE;
     uint8_t* sR = sT + C::NT * C::TILE;
     uint8_t* sS = sR + C::NRAW * C::RAW;
-    Ctrl* c = reinterpret_cast<Ctrl*>(sS + C::NRAW * kHalf);
+    Ctrl* c = reinterpret_cast<Ctrl*>(sS + C::NRAW * kHalf + C::STAGE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
     {
@@ -778,7 +820,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     const int each = (p.c.B + 32 * NW - 1) / (32 * NW) * 32;  // sequences of a warp
     const int b0 = min(p.c.B, warp * each), b1 = min(p.c.B, b0 + each);
     long long mine = 0;
-    for (int b = b0; b < b1; b += 32) mine += head_steps(p, b, b1, blockIdx.x == 0);  // this lane's
+    int some = 0;
+    for (int b = b0; b < b1; b += 32) mine += some = head_steps(p, b, b1, blockIdx.x == 0);  // this lane's
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) c->sums[warp] = mine;
@@ -798,7 +841,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     if (lo < hi && ahead * p.c.Hkv <= lo && lo < (ahead + mine) * p.c.Hkv) {
         int before = (int)ahead * p.c.Hkv;
         for (int b = b0; b < b1; b += 32) {
-            const int st = head_steps(p, b, b1, false), incl = inclusive_sum(st), first = before + (incl - st) * p.c.Hkv;
+            const int st = each == 32 ? some : head_steps(p, b, b1, false), incl = inclusive_sum(st);
+            const int first = before + (incl - st) * p.c.Hkv;
             if (first <= lo && lo < first + st * p.c.Hkv) c->place = Place{b + lane, 0, 0, st, 0, first};
             before += __shfl_sync(0xffffffffu, incl, 31) * p.c.Hkv;
         }
@@ -811,7 +855,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        softmax<D, Q8>(p, c, tmem, wf);
+        softmax<D, Q8>(p, sS + C::NRAW * kHalf + warp * (C::STAGE / 8), c, tmem, wf);
     } else {
         if (Q8)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -923,7 +967,7 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
     // its tokens over 2 tq, rounded up, groups (the kernel refuses sequences that overlap so far)
     const int64_t most = ((int64_t)c->max_pages * c->page + kTile - 1) / kTile;
     const double groups = (double)a->tokens / (2 * tile_tokens(G)) + a->B;
-    if (c->Hkv * most > 1 << 30 || groups * most * c->Hkv > (double)(1 << 30)) return BSA_ERR_INVALID_ARG;
+    if (c->Hkv * most > 1 << 30 || groups * (most + 1) * c->Hkv > (double)(1 << 30)) return BSA_ERR_INVALID_ARG;
     if (!workspace || !al(workspace, 256)) return BSA_ERR_INVALID_ARG;
     if (workspace_bytes < w.bytes) return BSA_ERR_CAPACITY;
     ChunkCommon p{};
