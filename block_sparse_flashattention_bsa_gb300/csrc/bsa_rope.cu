@@ -141,9 +141,16 @@ __device__ __forceinline__ void lane_angles(const unsigned long long* turns, int
         const int i = IL ? 4 * s + e + (e < 4 ? 0 : 4 * LPR - 4) : 8 * s + e;
         const unsigned long long t = turns[i] * (unsigned long long)(long long)pos;
         if (FINE) {
-            sincospif((float)(int)(unsigned)(t >> 32) * 4.656612873077392578125e-10f, &sn[e], &cs[e]);  // 2^-31
-            cs[e] *= gain;
-            sn[e] *= gain;
+            // Whole quarter turns apart; the rest, a = within pi / 4, by its power series:
+            // the first terms left out are a^11 / 11! < 2^-28 a and a^12 / 12! < 2^-33
+            const uint32_t u = (uint32_t)(t >> 32), q = (u + (1u << 29)) >> 30;
+            const float a = (float)(int)(u - (q << 30)) * 1.46291807926715968e-9f, x = a * a;
+            const float s0 = fmaf(a * x, fmaf(x, fmaf(x, fmaf(x, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), a);
+            const float c0 = fmaf(
+                x, fmaf(x, fmaf(x, fmaf(x, fmaf(x, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+            const float c1 = q & 1 ? s0 : c0, s1 = q & 1 ? c0 : s0;
+            cs[e] = (q + 1) & 2 ? -gain * c1 : gain * c1;
+            sn[e] = q & 2 ? -gain * s1 : gain * s1;
             continue;
         }
         const float a = (float)(int)(unsigned)(t >> 32) * 1.46291807926715968e-9f;  // 2 pi / 2^32
