@@ -95,7 +95,7 @@ struct ChunkParams {
     int32_t tq;                // tokens of a tile
     int32_t least;             // sequences of fewer query rows of a key head are not worked on
     PartMeta* meta;
-    float* part_o;             // [2 * grid][256][D]
+    float* part_o;             // [2 * grid][D / 4][256][4]
     float2* part_ml;           // [2 * grid][256]
 };
 
@@ -114,8 +114,8 @@ struct Cfg {
     static constexpr int NRAW = !Q8 ? 0 : RAWFIT > kMaxTiles ? kMaxTiles : RAWFIT;
     static constexpr int NT = Q8 ? 8 : FREE / TILE > kMaxTiles ? kMaxTiles : FREE / TILE;
     // Finished rows on their way out, 128 bytes of each of a warp's 32 rows, for stores of whole
-    // lines: an item's end 1.1 us, a part's 1.6 us, straight from the lanes 1.5 and 2.5.  Rows
-    // of 128 values leave no room for it, and have half as many ends to their steps.
+    // lines: an item's end 1.1 us, straight from the lanes 1.5.  Rows of 128 values leave no
+    // room for it.
     static constexpr int STAGE = D == 64 ? 8 * 32 * 128 : 0;
     static constexpr int SMEM = 2 * QTILE + NT * TILE + NRAW * (RAW + kHalf) + STAGE + kCtrl;
     static constexpr int O_COL = 2 * kTile;
@@ -685,54 +685,41 @@ __device__ void softmax(const ChunkParams& p, uint8_t* stage, Ctrl* c, uint32_t 
             tmem_ld32(t_o + y * 32, o);
             tmem_wait_ld();
             reg_fence(o);
-            if (C::STAGE > 0) {
-                // 16-byte pieces of the lane's row, in a swizzle; bf16 rows: two turns to a line
-                uint8_t* mine = stage + lane * 128;
-                if (part < 0) {
+            if (part >= 0) {
+                if (!live) continue;
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o) + ((int64_t)part * (D / 4) + y * 8) * kRows + threadIdx.x;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * i]) * w, __uint_as_float(o[8 * q + 2 * i + 1]) * w);
-                        *reinterpret_cast<uint4*>(mine + ((((y & 1) * 4 + q) ^ (lane & 7)) << 4)) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                    if (!(y & 1)) continue;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        *reinterpret_cast<uint4*>(mine + ((q ^ (lane & 7)) << 4)) =
-                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                }
-                __syncwarp();
-                const int piece = lane & 7;
-                char* dst = (part < 0 ? static_cast<char*>(cc.out) + (y >> 1) * 128
-                                      : reinterpret_cast<char*>(p.part_o) + y * 128) + piece * 16;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = 4 * k + (lane >> 3);
-                    const long long at = __shfl_sync(0xffffffffu, (long long)(!live ? -1 : part < 0 ? orow : prow), r);
-                    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
-                    if (at >= 0) *reinterpret_cast<uint4*>(dst + at * (part < 0 ? D * 2 : D * 4)) = v;
-                }
-                continue;  // the next turn begins with a __syncwarp
+                for (int q = 0; q < 8; ++q)
+                    dst[q * kRows] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                continue;
             }
-            if (!live) continue;
-            if (part < 0) {
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * q]) * w, __uint_as_float(o[8 * q + 1]) * w),
+                                  pack_bf16x2(__uint_as_float(o[8 * q + 2]) * w, __uint_as_float(o[8 * q + 3]) * w),
+                                  pack_bf16x2(__uint_as_float(o[8 * q + 4]) * w, __uint_as_float(o[8 * q + 5]) * w),
+                                  pack_bf16x2(__uint_as_float(o[8 * q + 6]) * w, __uint_as_float(o[8 * q + 7]) * w));
+            if (C::STAGE == 0) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cc.out) + orow * D + y * 32);
+                if (live)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t v[4];
+                    for (int q = 0; q < 4; ++q) dst[q] = v[q];
+                continue;
+            }
+            // 16-byte pieces of the lane's row, in a swizzle; two turns fill a line
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * i]) * w, __uint_as_float(o[8 * q + 2 * i + 1]) * w);
-                    dst[q] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            } else {
-                uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + y * 32);
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((((y & 1) * 4 + q) ^ (lane & 7)) << 4)) = v[q];
+            if (!(y & 1)) continue;
+            __syncwarp();
+            char* dst = static_cast<char*>(cc.out) + (y >> 1) * 128 + (lane & 7) * 16;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int k = 0; k < 8; ++k) {
+                const int r = 4 * k + (lane >> 3);
+                const long long at = __shfl_sync(0xffffffffu, live ? (long long)orow : -1ll, r);
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane ^ r) & 7) << 4));
+                if (at >= 0) *reinterpret_cast<uint4*>(dst + at * (D * 2)) = x;
             }
         }
         __syncwarp();

@@ -159,13 +159,14 @@ inline int short_rows(const ChunkCommon& c) {
 }
 
 // Joins the parts of items that range boundaries cut, in range order: with parts i,
-// m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.  A warp to a row (chunks:
-// to four at a time, whose loads are all under way together; short sequences, which
-// can have a part from every CTA: eight warps to a row, every eighth part each).
-// Bound by dependent reads from the L2.
+// m = max m_i, w_i = 2^(m_i - m), O = sum w_i O_i / sum w_i l_i.  Chunks: a CTA to 32
+// rows, a lane to each, a warp to an eighth of the columns, which is how their parts lie
+// in memory: whole lines both written and read (with rows behind one another a part of
+// 128-wide rows took its CTA 5.3 us, now 2.0).  Short sequences, which can have a part from every CTA: eight warps to a row,
+// every eighth part each.  Bound by dependent reads from the L2.
 struct PartSet {
     const PartMeta* meta;
-    const float* o;       // [2 * ctas][rows][D]
+    const float* o;       // short sequences: [2 * ctas][16][D]; chunks: [2 * ctas][D / 4][256][4]
     const float2* ml;     // [2 * ctas][rows]
 };
 // The item that the boundary in front of range x + 1 is the first to cut: its
@@ -216,8 +217,9 @@ __device__ __forceinline__ void add_part(float* acc, const float* src, float w) 
 template <int D>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkCommon p, const PartSet few, const PartSet many,
                                                           int rows_short, int tq) {
-    constexpr int C = D / 32, R = 4;
+    constexpr int C = D / 32;
     __shared__ float red[8][D + 1];
+    __shared__ uint2 rows[32][D / 4 + 1];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -255,44 +257,51 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkCommon p, c
         return;
     }
     if (!it.find(many.meta, blockIdx.x)) return;
-    const int r0 = ((int)blockIdx.y - rows_short) * 8 * R + warp * R;
-    const int t0 = (r0 >> 7) * tq, i0 = r0 & 127;  // first token of the tile, row in it
-    bool on[R];
-    float m[R], l[R], acc[R][C];
+    const int r0 = ((int)blockIdx.y - rows_short) * 32;
+    // row of q that row r of the item is, times Hq, plus its head; < 0: none
+    auto place = [&](int r) -> int64_t {
+        const int i = r & 127, t = (r >> 7) * tq + i / p.G;  // row in its tile, token
+        return i < tq * p.G && t < it.mt.n ? (int64_t)(it.mt.row0 + t) * p.Hq + it.mt.h * p.G + i % p.G : -1;
+    };
+    const int64_t mine = place(r0 + lane);
+    if (!__any_sync(0xffffffffu, mine >= 0)) return;  // the same in every warp
+    float m = -INFINITY, l = 0.f, acc[C][4];
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-        on[q] = i0 + q < tq * p.G && t0 + (i0 + q) / p.G < it.mt.n;
-        m[q] = -INFINITY;
-        l[q] = 0.f;
+    for (int q = 0; q < C; ++q)
 #pragma unroll
-        for (int x = 0; x < C; ++x) acc[q][x] = 0.f;
-    }
-    if (!on[0]) return;  // nor are the rows behind it
-    for (int k = it.first + lane; k <= it.last; k += 32)
-#pragma unroll
-        for (int q = 0; q < R; ++q)
-            if (on[q]) m[q] = fmaxf(m[q], many.ml[(int64_t)it.slot(k) * 256 + r0 + q].x);
-#pragma unroll
-    for (int q = 0; q < R; ++q)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m[q] = fmaxf(m[q], __shfl_xor_sync(0xffffffffu, m[q], o));
+        for (int x = 0; x < 4; ++x) acc[q][x] = 0.f;
+    if (mine >= 0) {
+#pragma unroll 4
+        for (int k = it.first; k <= it.last; ++k) m = fmaxf(m, many.ml[(int64_t)it.slot(k) * 256 + r0 + lane].x);
+        const float ref = m > -INFINITY ? m : 0.f;
 #pragma unroll 2
-    for (int k = it.first; k <= it.last; ++k) {
-        const int64_t pr = (int64_t)it.slot(k) * 256 + r0;
+        for (int k = it.first; k <= it.last; ++k) {
+            const int64_t part = it.slot(k);
+            const float2 ml = many.ml[part * 256 + r0 + lane];
+            const float w = ex2_approx(ml.x - ref);  // 0 for a part that saw nothing
+            l += w * ml.y;
+            const float4* src = reinterpret_cast<const float4*>(many.o) + (part * (D / 4) + warp) * 256 + r0 + lane;
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            if (!on[q]) continue;
-            const float2 ml = many.ml[pr + q];
-            const float w = ex2_approx(ml.x - (m[q] > -INFINITY ? m[q] : 0.f));
-            l[q] += w * ml.y;
-            add_part<D>(acc[q], many.o + (pr + q) * D + lane * C, w);
+            for (int q = 0; q < C; ++q) {
+                const float4 o = src[q * 8 * 256];
+                acc[q][0] += w * o.x;
+                acc[q][1] += w * o.y;
+                acc[q][2] += w * o.z;
+                acc[q][3] += w * o.w;
+            }
         }
+        if (warp == 0) p.lse[mine] = lse_of(m, l);
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int q = 0; q < R; ++q)
-        if (on[q])
-            store_row<D>(p, (int64_t)(it.mt.row0 + t0 + (i0 + q) / p.G) * p.Hq + it.mt.h * p.G + (i0 + q) % p.G, lane,
-                         acc[q], m[q], l[q]);
+    for (int q = 0; q < C; ++q)
+        rows[lane][warp + 8 * q] = make_uint2(pack_bf16x2(acc[q][0] * inv, acc[q][1] * inv), pack_bf16x2(acc[q][2] * inv, acc[q][3] * inv));
+    __syncthreads();
+#pragma unroll
+    for (int x = threadIdx.x; x < 32 * (D / 4); x += 256) {
+        const int64_t at = place(r0 + x / (D / 4));
+        if (at >= 0) reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D)[x % (D / 4)] = rows[x / (D / 4)][x % (D / 4)];
+    }
 }
 
 }  // namespace bsa
