@@ -787,7 +787,8 @@ int bsa_cache_compact(const bsa_page_cache *c, int32_t *page_ref, int32_t *new_p
  * a power of two, in bsa_page_scales.  A row y is held as code * 2^e with
  *   e = the smallest integer in [-100, 118] with max |y| <= 448 * 2^e,
  *   code = e4m3(y * 2^-e)  (nearest, ties to even, saturating; NaN stays NaN),
- * the scale's byte being e + 127 (e8m0).  code * 2^e is a bf16 number exactly.
+ * the scale's byte being e + 127 (e8m0; the scales of rows that are attended to lie
+ * in 27 .. 245).  code * 2^e is a bf16 number exactly.
  * The _fp8 calls are their namesakes on such pools: bsa_cache_append_fp8
  * quantises the normed and rotated keys, and the values, from fp32 with that
  * one rounding (queries stay bf16); the page calls move codes and scales.
