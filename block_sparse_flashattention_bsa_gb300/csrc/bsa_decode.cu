@@ -15,7 +15,7 @@
 // 1,400 for its bytes.  Here a warp reads its 16 keys from shared memory once,
 // converts them in registers and multiplies: 2 bytes of traffic per byte.
 //
-// Work: a step is 256 slots (128 with more than 8 rows); an item the steps of one key head of one sequence;
+// Work: a step is 256 slots (128 with more than 8 rows, or few steps); an item the steps of one key head of one sequence;
 // the steps of the batch, cut into equal ranges, one per CTA.  An item that a
 // range boundary cuts leaves unnormalised fp32 parts that the merge joins in range
 // order: no atomics, results do not depend on timing.
@@ -337,13 +337,13 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
     uint32_t qf[KS][NT][2];
     float o[KS][NT][4];
     float m[NT][2], l[NT][2], sl[NT][2];
+    float rv[NT][2];  // 8-bit: what the rows' weights times V's scales are multiplied with, a power of two
     for (uint32_t items = 0;; ++items) {
         const uint32_t ii = items % kShortItems;
         if (!warp_wait(&c->it_full[ii], (items / kShortItems) & 1, wf)) return;
         const int step0 = c->item[ii].step0, steps = c->item[ii].steps, rows = c->item[ii].rows;
         const int ctx = c->item[ii].ctx, end = c->item[ii].end;
         if (steps < 0) return;
-        int vref = 0;  // 8-bit: the scale byte that O counts in (0: none yet)
         // Eight units of 16 keys (of each of its tiles) to a step; the warps take them in turn.
         const uint32_t u0 = (uint32_t)step0 * 8, u1 = u0 + (uint32_t)steps * 8;
         const uint32_t mine = u0 + (warp + kWarps - u0 % kWarps) % kWarps;
@@ -390,6 +390,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 for (int i = 0; i < 2; ++i) {
                     m[nt][i] = -INFINITY;
                     l[nt][i] = 0.f;
+                    rv[nt][i] = exp2_int(120);
                 }
 #pragma unroll
                 for (int t = 0; t < KS; ++t)
@@ -554,43 +555,62 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
             for (int x = 0; x < SUB; ++x)
                 if (x < nx && !landed(SUB + x)) return;
             if (Q8) {
-                // Values are fp16 codes; their scales go into the weights, relative to the
-                // largest one met (with room for the next ones): 2^7 p 2^(e - ref) is at most
-                // 2^14, and down to 2^-21 of what a weight of 1 gives it is a normal number.
-                uint32_t vb[SUB][2], top = 0;
+                // Values are fp16 codes; their scales go into the weights: p 2^e, times a power of
+                // two of the row's that keeps it below 2^15 and puts the largest one met at 2^6
+                // or more.  Down to 2^-20 of that one they are normal numbers, rounded at 2^-12.
+                float big[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) big[nt][0] = big[nt][1] = 0.f;
 #pragma unroll
                 for (int x = 0; x < SUB; ++x)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int key = slab + g + 8 * k;
-                        vb[x][k] = sS[ts[SUB + x] * kTile + key];
+                        uint32_t vb = sS[ts[SUB + x] * kTile + key];
                         if ((flags & kMask) &&
                             !(((flags >> (kHaveBit + 2 * x + (key >> 6))) & 1) && base[x] + key < end))
-                            vb[x][k] = 0;
-                        if (x >= nx) vb[x][k] = 0;
-                        top = max(top, vb[x][k]);
-                    }
-                if (__any_sync(0xffffffffu, (int)top > vref)) {
-                    const int to = (int)__reduce_max_sync(0xffffffffu, top) + 1;
-                    const float w = vref ? exp2_int(max(vref - to, -126)) : 0.f;
-                    vref = to;
-#pragma unroll
-                    for (int t = 0; t < KS; ++t)
+                            vb = 0;
+                        const float ve = __uint_as_float((x < nx ? vb : 0u) << 23);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) o[t][nt][i] *= w;
+                            for (int i = 0; i < 2; ++i) {
+                                s[x][nt][2 * k + i] *= ve;
+                                big[nt][i] = fmaxf(big[nt][i], s[x][nt][2 * k + i]);
+                            }
+                    }
+                bool over = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) over |= big[nt][i] * rv[nt][i] > 32768.f;
+                if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float top = big[nt][i];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                            if (!(top * rv[nt][i] > 32768.f)) continue;
+                            // exponents: top's at 6 and above
+                            const int was = 127 - (int)(__float_as_uint(rv[nt][i]) >> 23);
+                            const int to = (int)(__float_as_uint(top) >> 23) - 127 - 6;
+                            const float w = exp2_int(max(was - to, -126));
+                            rv[nt][i] = exp2_int(-to);
+#pragma unroll
+                            for (int t = 0; t < KS; ++t) {
+                                o[t][nt][i] *= w;
+                                o[t][nt][i + 2] *= w;
+                            }
+                        }
                 }
 #pragma unroll
                 for (int x = 0; x < SUB; ++x)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float w = exp2_int(max((int)vb[x][k] - vref + 7, -126));
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) s[x][nt][2 * k + i] *= w;
-                    }
+                        for (int i = 0; i < 4; ++i) s[x][nt][i] *= rv[nt][i & 1];
             }
             uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
 #pragma unroll
@@ -698,7 +718,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                     for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
                     const int r = 8 * nt + 2 * cq + i;
                     if (g == 0) c->stats[warp][r] = make_float2(m[nt][i], l[nt][i]);
-                    const float w = !Q8 ? 1.f : vref ? exp2_int(vref - 127 - 7) : 0.f;
+                    const float w = Q8 ? __uint_as_float((254u << 23) - __float_as_uint(rv[nt][i])) : 1.f;  // 1 / rv
                     float* dst = xch + (warp * 8 * NT + r) * C::PITCH;
 #pragma unroll
                     for (int t = 0; t < KS / 2; ++t)

@@ -9,9 +9,8 @@ A = sum p |v| / sum p:
   p is rounded to bf16 once, 2^-8 (chunks, and the short sequences of a small batch
     that has chunks too); in short sequences of up to 16 rows a key head it is held in
     two bf16 parts, 2^-16, or, times the 8-bit row's scale, rounded to fp16 once,
-    2^-11 (below fp16's normal numbers, 2^-21 of what a weight of 1 gives at the largest
-    scale met: off by 2^-32 of that, inside 2^-16); fp32 accumulation: steps * 2^-24,
-    inside 2^-16
+    2^-11 (below fp16's normal numbers, 2^-20 of the largest such product: off by 2^-31
+    of that, inside 2^-16); fp32 accumulation: steps * 2^-24, inside 2^-16
   O: A (p's + 2 e + 2^-16) + |O| 2^-8 (its own rounding)
   LSE: e + 2^-21 (|LSE| + 1)
 8-bit rows are what they are (code * 2^e): the reference reads the same values.

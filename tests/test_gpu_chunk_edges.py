@@ -9,7 +9,7 @@ another stream, a replay) the results are the same bits.
 import pytest
 import torch
 
-from paged_reference import E4M3, E8M0, Cache, attention, check_attention
+from paged_reference import E4M3, E8M0, Cache, attention, check_attention, quantise
 from test_gpu_chunk import Case, both, bsa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -85,6 +85,45 @@ def test_far_pages(bsa, q8):  # noqa: F811
     assert torch.equal(*z) and bsa.device_error() == 0
     for x, y in zip(big, pools):
         assert torch.equal(x.view(torch.uint8)[far - n:], y.view(torch.uint8))
+
+
+# ------------------------------------------------------------ values of far magnitudes
+def set_row(cache, b, slot, which, value):
+    """Every head's K or V row of a slot to one value."""
+    pg, at = int(cache.table[b, slot // cache.page]), slot % cache.page
+    y = torch.full((cache.D,), value, dtype=torch.float64)
+    pool = getattr(cache, which)
+    if cache.q8:
+        codes, e = quantise(y)
+        pool[pg, :, at] = codes
+        getattr(cache, which + "s")[pg, :, at] = e
+    else:
+        pool[pg, :, at] = y.bfloat16()
+
+
+@both
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_far_magnitudes(bsa, q8, n, D):  # noqa: F811
+    """Rows whose values are 2^50 times the others' and whose weight is 2^-78 (a window's hidden
+    rows: 2^100 and none) drown nothing; nor do heads that see large values the others."""
+    G, ctx, page = 4, 300, 64
+    g = torch.Generator().manual_seed(n)
+    for window in (0, 100):
+        cache = Cache([ctx + n], 1, D, page, q8, 5)
+        for slot in (7, 130, 290):
+            set_row(cache, 0, slot, "k", -48.0 / D ** 0.5)
+            set_row(cache, 0, slot, "v", 2.0 ** 50)
+        if window:
+            set_row(cache, 0, 195, "v", 2.0 ** 100)  # a page that is read, in front of every window
+        q = torch.randn(n, G, D, generator=g).abs().bfloat16()
+        q[:, 2] = -q[:, 2] / 4  # sees the large values
+        k, v, table, sc = cache.device()
+        ptr = None if n == 1 else i32([0, n])
+        o, lse = bsa.chunk_attention(q.cuda(), k, v, table, i32([ctx]), q_ptr=ptr, window=window, **sc)
+        assert bsa.device_error() == 0
+        ref = attention(cache, q, [0, n], [ctx], window, 0, D ** -0.5)
+        check_attention(o, lse, ref, D, 2.0 ** -8 if n > 1 else 2.0 ** -11 if q8 else 2.0 ** -16)
 
 
 # ------------------------------------------------------------ one call after another
