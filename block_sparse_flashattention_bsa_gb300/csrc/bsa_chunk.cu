@@ -813,11 +813,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) c->sums[warp] = mine;
     __syncthreads();
-    long long all = 0, ahead = 0;
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) ahead += c->sums[w];
-        all += c->sums[w];
+    long long ahead = lane < NW ? c->sums[lane] : 0;  // inclusive sums over the warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, ahead, o);
+        if (lane >= o) ahead += x;
     }
+    long long all = __shfl_sync(0xffffffffu, ahead, 31);
+    ahead = __shfl_sync(0xffffffffu, ahead, warp) - mine;
     if (all * p.c.Hkv > 1 << 30) {  // only where sequences overlap: their rows make no sense
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.c.err, ERR_BAD_ROW);
         all = 0;
