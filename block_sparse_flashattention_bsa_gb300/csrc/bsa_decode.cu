@@ -338,6 +338,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
     float o[KS][NT][4];
     float m[NT][2], l[NT][2], sl[NT][2];
     float rv[NT][2];  // 8-bit: what the rows' weights times V's scales are multiplied with, a power of two
+    float lv[NT][2];  // 8-bit: the product that rv was set for, times rv, against the present maximum
     for (uint32_t items = 0;; ++items) {
         const uint32_t ii = items % kShortItems;
         if (!warp_wait(&c->it_full[ii], (items / kShortItems) & 1, wf)) return;
@@ -391,6 +392,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                     m[nt][i] = -INFINITY;
                     l[nt][i] = 0.f;
                     rv[nt][i] = exp2_int(120);
+                    lv[nt][i] = 0.f;
                 }
 #pragma unroll
                 for (int t = 0; t < KS; ++t)
@@ -530,9 +532,24 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                         for (int x = 0; x < SUB; ++x) top = fmax3(top, s[x][nt][i], s[x][nt][i + 2]);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const float w = top == -INFINITY ? 1.f : ex2_approx(m[nt][i] - top);
+                        float w = top == -INFINITY ? 1.f : ex2_approx(m[nt][i] - top);
                         m[nt][i] = top;
                         l[nt][i] *= w;
+                        if (Q8) {
+                            // The products met so far shrink by w too, and rv rises with that (to 2^120 at
+                            // most), or what follows would be rounded against weights that are none any more.
+                            lv[nt][i] *= w;
+                            if (lv[nt][i] < 64.f) {
+                                const int at = (int)(__float_as_uint(rv[nt][i]) >> 23) - 127, room = 120 - at;
+                                const int k = lv[nt][i] > 0.f
+                                                  ? min(127 + 6 - (int)(__float_as_uint(lv[nt][i]) >> 23), room)
+                                                  : room;  // nothing is left of them: w is 0, or o
+                                const float up = exp2_int(min(k, 126));
+                                w *= up;
+                                lv[nt][i] *= up;
+                                rv[nt][i] = exp2_int(at + k);
+                            }
+                        }
 #pragma unroll
                         for (int t = 0; t < KS; ++t) {
                             o[t][nt][i] *= w;
@@ -556,8 +573,9 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 if (x < nx && !landed(SUB + x)) return;
             if (Q8) {
                 // Values are fp16 codes; their scales go into the weights: p 2^e, times a power of
-                // two of the row's that keeps it below 2^15 and puts the largest one met at 2^6
-                // or more.  Down to 2^-20 of that one they are normal numbers, rounded at 2^-12.
+                // two of the row's that keeps it below 2^15 and puts the largest one met, measured
+                // against the present maximum, at 2^6 or more.  Down to 2^-20 of that one they are
+                // normal numbers, rounded at 2^-12.
                 float big[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) big[nt][0] = big[nt][1] = 0.f;
@@ -598,6 +616,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                             const int to = (int)(__float_as_uint(top) >> 23) - 127 - 6;
                             const float w = exp2_int(max(was - to, -126));
                             rv[nt][i] = exp2_int(-to);
+                            lv[nt][i] = top * rv[nt][i];
 #pragma unroll
                             for (int t = 0; t < KS; ++t) {
                                 o[t][nt][i] *= w;
