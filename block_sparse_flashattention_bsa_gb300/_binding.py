@@ -98,7 +98,8 @@ class _ReadArgs(ctypes.Structure):
 class _ChunkArgs(ctypes.Structure):
     _fields_ = [(x, ctypes.c_int32) for x in ("B", "tokens", "Hq")]
     _fields_ += [(x, ctypes.c_void_p) for x in ("q", "q_ptr", "context_len", "out", "lse")]
-    _fields_ += [("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+    _fields_ += [("scale", ctypes.c_float)]
+    _fields_ += [(x, ctypes.c_int32) for x in ("window", "sinks", "max_context")]
 
 
 MAX_WINDOWS = 4

@@ -531,9 +531,9 @@ PyObject* cache_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
     });
 }
 
-// q, k_cache, v_cache, page_table, context_len, q_ptr or None, window, sinks, k_scale, v_scale, scale or None, out, lse
+// q, k_cache, v_cache, page_table, context_len, q_ptr or None, window, sinks, k_scale, v_scale, scale or None, out, lse, max_context
 PyObject* chunk_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
-    return guarded(n, 13, [&]() -> PyObject* {
+    return guarded(n, 14, [&]() -> PyObject* {
         T q = tensor(o[0], "q"), kc = tensor(o[1], "k_cache"), vc = tensor(o[2], "v_cache"), table = tensor(o[3], "page_table");
         T ctx = tensor(o[4], "context_len"), qp = tensor_or_none(o[5], "q_ptr");
         T ks = tensor_or_none(o[8], "k_scale"), vs = tensor_or_none(o[9], "v_scale");
@@ -554,6 +554,7 @@ PyObject* chunk_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
         a.Hq = size32(Hq);
         a.window = int_arg(o[6], "window");
         a.sinks = int_arg(o[7], "sinks");
+        a.max_context = int_arg(o[13], "max_context");
         a.scale = o[10] == Py_None ? (float)(1.0 / std::sqrt((double)std::max<int64_t>(D, 1))) : float_arg(o[10]);
         const c10::cuda::CUDAGuard guard(dev);
         at::Tensor r = output(out, q->sizes(), dev), l;

@@ -119,14 +119,18 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     context_len: torch.Tensor, q_ptr: Optional[torch.Tensor] = None, window: int = 0, sinks: int = 0,
                     k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                    lse: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+                    lse: Optional[torch.Tensor] = None, stream=None,
+                    max_context: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of new tokens over their sequences' pages: q [tokens,Hq,D] bf16
     (what `cache_append` returns), sequence b's rows q_ptr[b] .. q_ptr[b+1]-1
     (int32 [B+1]; None: one token a sequence) in slots context_len[b] and on.
     Slot s attends to the slots u <= s; with window > 0 only to those with
     u > s - window or u < sinks (pages that no token sees any more may be -1).
+    max_context: at least the slots of the longest sequence after this call (0: not
+    known, the table's width is taken).  Small batches of chunks and single tokens
+    under a wide table are faster with it; results do not depend on its being right.
 
     Returns (O bf16 [tokens,Hq,D], LSE fp32 [tokens,Hq]); rows of no sequence
     are left as they were."""
     return _call(compiled().chunk_attention, "bsa_chunk_attention", stream, q, k_cache, v_cache, page_table,
-                 context_len, q_ptr, window, sinks, k_scale, v_scale, scale, out, lse)
+                 context_len, q_ptr, window, sinks, k_scale, v_scale, scale, out, lse, max_context)

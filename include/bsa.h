@@ -853,7 +853,11 @@ int bsa_cache_read(const bsa_read_args *a, const bsa_page_cache *c, const bsa_pa
  * K and V must be finite in a sequence's slots up to its last new token, in the
  * pages that one of its new tokens sees.  A slot that a token should see and that
  * lies in no page is reported (bit 32) and not seen.
- * Limits: Hq a multiple of Hkv, Hq / Hkv <= 128; window, sinks >= 0; Hkv * (max_pages *
+ *   max_context  at least the slots of the longest sequence, its new tokens among them; 0:
+ *                not known, the page table's width is taken.  It says how much work there may
+ *                be, by which batches of chunks and short sequences are given one kernel or
+ *                two, and nothing else: with a wrong one the result is right all the same.
+ * Limits: Hq a multiple of Hkv, Hq / Hkv <= 128; window, sinks, max_context >= 0; Hkv * (max_pages *
  * page / 128) * (tokens * (Hq / Hkv) / 128 + B) below about 2^30.
  *   workspace    device, bsa_chunk_attention_workspace(...) bytes, 256-byte aligned.
  *                Calls that overlap on the GPU need workspaces of their own.
@@ -866,6 +870,7 @@ typedef struct {
     float *lse;
     float scale;
     int32_t window, sinks;   /* window 0: every slot up to the token's own */
+    int32_t max_context;
 } bsa_chunk_args;
 int64_t bsa_chunk_attention_workspace(int32_t B, int32_t tokens, int32_t Hq, int32_t Hkv, int32_t D);
 int bsa_chunk_attention(const bsa_chunk_args *a, const bsa_page_cache *c, const bsa_page_scales *scales,
