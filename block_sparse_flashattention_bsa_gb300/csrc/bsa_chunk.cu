@@ -992,10 +992,14 @@ int bsa_chunk_attention(const bsa_chunk_args* a, const bsa_page_cache* c, const 
     //   8-bit  8: 54, 42   34: 77, 96   70: 139, 204   (a chunk's step takes 2.5 times as long)
     // These hold where max_context, or else the table's width, is the longest context; under
     // a table for 131,072 slots and without max_context 8 sequences of up to 1,000 slots take
-    // 31 us instead of 20 (bf16) and 35 instead of 23 (8-bit).
+    // 31 us instead of 20 (bf16) and 35 instead of 23 (8-bit).  A window bounds the steps too:
+    // 8 sequences of up to 32,000 slots under one of 1,024, four steps per SM, 39 and 29 (bf16),
+    // 42 and 33 (8-bit); 24, 13 steps, 74 and 59, 70 and 69; 48, 25 steps, 109 and 99, 109 and 118.
     // Single tokens of more heads than its rows are chunks too.
     const bool all_short = !a->q_ptr || (int64_t)a->tokens * G <= kShortRows;  // if their heads allow
-    const int64_t longest = a->max_context > 0 ? std::min(most, ((int64_t)a->max_context + kTile - 1) / kTile) : most;
+    auto tiles = [](int64_t slots) { return (slots + kTile - 1) / kTile; };
+    int64_t longest = a->max_context > 0 ? std::min(most, tiles(a->max_context)) : most;
+    if (a->window > 0) longest = std::min(longest, tiles(a->window) + 1 + tiles(a->sinks));
     const bool some_short =
         G <= kShortRows && (all_short || (a->B > 1 && a->B * longest * c->Hkv > (scales ? 16ll : 64ll) * sms));
     PartSet few{};

@@ -61,3 +61,28 @@ def test_single_tokens_take_no_notice(bsa, q8):  # noqa: F811
     with pytest.raises((ValueError, RuntimeError, OverflowError)):
         bsa.chunk_attention(q, k, v, table, ctx, max_context=2 ** 31, **more)
     assert bsa.device_error() == 0
+
+
+@both
+@pytest.mark.parametrize("window,sinks", [(200, 4), (1000, 130)])
+def test_a_window_bounds_the_work_too(bsa, window, sinks, q8):  # noqa: F811
+    """However long the contexts may be, a few sequences under a window are one kernel's work."""
+    c = Case(CTX, NEW, 32, 8, 128, 64, q8, window, sinks)
+    (q, k, v, table, ctx), more = c.args()
+    o, lse = bsa.chunk_attention(q, k, v, table, ctx, **more)
+    c.check(o, lse)
+    o2, lse2 = bsa.chunk_attention(q, k, v, table_for(c, 131072), ctx, **more)
+    assert bsa.device_error() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@both
+def test_many_sequences_under_a_wide_window(bsa, q8):  # noqa: F811
+    """Enough work for two kernels, by the window's width: single tokens to the short kernel's tolerance."""
+    ctx, new = [(37 * b) % 300 for b in range(40)], [1, 1, 30, 1] * 10
+    c = Case(ctx, new, 16, 16, 64, 64, q8, 4000, 4)
+    (q, k, v, table, ctx), more = c.args()
+    o, lse = bsa.chunk_attention(q, k, v, table_for(c, 131072), ctx, **more)
+    assert bsa.device_error() == 0
+    c.short = [n == 1 for n in new]
+    c.check(o, lse)
