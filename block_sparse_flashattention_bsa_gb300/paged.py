@@ -128,7 +128,12 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     u > s - window or u < sinks (pages that no token sees any more may be -1).
     max_context: at least the slots of the longest sequence after this call (0: not
     known, the table's width is taken).  Small batches of chunks and single tokens
-    under a wide table are faster with it; results do not depend on its being right.
+    under a wide table are faster with it, and a wrong one gives right results too.
+
+    Weights are rounded to bf16 (2^-8) before they meet V.  Sequences of at most 16
+    rows of a key head have finer ones (bf16 pools 2^-16, 8-bit 2^-11) where all are
+    such or the batch has work enough for a kernel of their own: a row's last bits
+    may depend on the batch and the table's width (the rule is in ``include/bsa.h``).
 
     Returns (O bf16 [tokens,Hq,D], LSE fp32 [tokens,Hq]); rows of no sequence
     are left as they were."""

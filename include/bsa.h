@@ -855,8 +855,19 @@ int bsa_cache_read(const bsa_read_args *a, const bsa_page_cache *c, const bsa_pa
  * lies in no page is reported (bit 32) and not seen.
  *   max_context  at least the slots of the longest sequence, its new tokens among them; 0:
  *                not known, the page table's width is taken.  It says how much work there may
- *                be, by which batches of chunks and short sequences are given one kernel or
- *                two, and nothing else: with a wrong one the result is right all the same.
+ *                be (which kernel works on short sequences, below) and nothing else: with a
+ *                wrong one the result is right all the same.
+ * Precision: scores, the softmax's statistics and all sums are fp32.  A row's weights are
+ * rounded before they meet V: once to bf16 (2^-8 of a weight); finer for short sequences,
+ * those whose new tokens have at most 16 rows of a key head (tokens * (Hq / Hkv)), where a
+ * kernel of their own works on them: two bf16 parts (2^-16), or for 8-bit pools the weight
+ * times V's scale in fp16 (2^-11, or 2^-31 of the row's largest such product).  They have it
+ *   where every sequence is short for certain: q_ptr NULL, or tokens * (Hq / Hkv) <= 16;
+ *   in other batches where B > 1 and B * Hkv * S is above 64 (8-bit pools: 16) times the
+ *   GPU's SMs, S the steps of 128 slots that a token may see: those of max_context or of
+ *   the table, or if that is less ceil(window / 128) + 1 + ceil(sinks / 128).
+ * So the last bits of a row may change with the batch that it is in, the table's width and
+ * max_context; the order of its sums does too.  The same call gives the same bits.
  * Limits: Hq a multiple of Hkv, Hq / Hkv <= 128; window, sinks, max_context >= 0; Hkv * (max_pages *
  * page / 128) * (tokens * (Hq / Hkv) / 128 + B) below about 2^30.
  *   workspace    device, bsa_chunk_attention_workspace(...) bytes, 256-byte aligned.
