@@ -77,15 +77,17 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams p) 
                 bad = true;
                 continue;
             }
+            // Ordinary loads: this kernel may have started before the one that writes these rows
+            // ended, and the read-only path is for memory that nobody writes meanwhile.
             const int64_t row = ((int64_t)pg * p.Hkv + h) * p.page + slot % p.page;
             if (Q8) {
-                const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k) + row * LPR + c);
-                const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.v) + row * LPR + c);
+                const uint2 a = reinterpret_cast<const uint2*>(p.k)[row * LPR + c];
+                const uint2 b = reinterpret_cast<const uint2*>(p.v)[row * LPR + c];
                 val[0][u] = make_uint4(a.x, a.y, p.ks[row], 0);
                 val[1][u] = make_uint4(b.x, b.y, p.vs[row], 0);
             } else {
-                val[0][u] = __ldg(reinterpret_cast<const uint4*>(p.k) + row * LPR + c);
-                val[1][u] = __ldg(reinterpret_cast<const uint4*>(p.v) + row * LPR + c);
+                val[0][u] = reinterpret_cast<const uint4*>(p.k)[row * LPR + c];
+                val[1][u] = reinterpret_cast<const uint4*>(p.v)[row * LPR + c];
             }
         }
         if (bad) atomicOr(p.err, ERR_BAD_PAGE);
