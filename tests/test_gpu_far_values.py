@@ -110,3 +110,22 @@ def test_the_ends_of_the_scales(bsa, q8):  # noqa: F811
     size = [90.0 if s < half else -20.0 for s in range(N)]
     c = steep_cache(128, 8, 19, q8, score, size, 2)
     check(bsa, c, queries(19, 32, 128, 1.0, 3), q8)
+
+
+@both
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rise,fall", [(100, 80), (100, 20), (20, 100)])
+def test_chunks_of_them(bsa, q8, D, rise, fall):  # noqa: F811
+    """The same under chunks, whose weights are rounded to bf16."""
+    n, B, Hkv, G = 40, 3, 2, 4
+    score = [rise * s / N for s in range(N)]
+    size = [-fall * s / N for s in range(N)]
+    size[5] += 20
+    c = steep_cache(D, Hkv, B, q8, score, size, rise)
+    q = queries(B * n, Hkv * G, D, torch.tensor([1.0, 0.5, 0.25, 0.75] * (Hkv * G // 4)), D)
+    k, v, table, sc = c.device()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ctx, ptr = [N - n] * B, [n * b for b in range(B + 1)]
+    o, lse = bsa.chunk_attention(q.cuda(), k, v, table, i32(ctx), q_ptr=i32(ptr), **sc)
+    assert bsa.device_error() == 0
+    check_attention(o, lse, attention(c, q, ptr, ctx, 0, 0, D ** -0.5), D, 2.0 ** -8)
