@@ -26,9 +26,9 @@
 // accumulator of its own, so steps need no exchange; what they have at an item's end
 // one more warp joins while they go on.
 // bf16 rows: P is multiplied as two bf16 parts, high and low, so that its rounding
-// (2^-17) does not add to the result's.  8-bit rows: fp16 products, since a
+// (2^-16) does not add to the result's.  8-bit rows: fp16 products, since a
 // code is an fp16 number (one conversion instruction for two; to bf16 it takes
-// four and a product) and P rounds at 2^-12 in it.
+// four and a product) and P rounds at 2^-11 in it.
 
 #include <cuda_fp16.h>
 
@@ -575,7 +575,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                 // Values are fp16 codes; their scales go into the weights: p 2^e, times a power of
                 // two of the row's that keeps it below 2^15 and puts the largest one met, measured
                 // against the present maximum, at 2^6 or more.  Down to 2^-20 of that one they are
-                // normal numbers, rounded at 2^-12.
+                // normal numbers, rounded at 2^-11.
                 float big[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) big[nt][0] = big[nt][1] = 0.f;
@@ -756,7 +756,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
 // ---------------------------------------------------------------- joining warp
 // One warp adds an item's parts up and writes it out, while the others are at the
 // next item (all of them at it, between two barriers, and Q loaded by each warp: 96
-// ragged sequences up to 8,192 slots, 8 key heads of 128, 8-bit rows 160 us; 147 so).
+// ragged sequences up to 8,192 slots, 8 key heads of 128, 8-bit rows 160 us; 148 so).
 template <int D, bool Q8, int NT>
 __device__ void short_joiner(const ShortParams& p, const float* xch, ShortCtrl* c, volatile WaitFlag* wf) {
     using C = ShortCfg<D, Q8, NT>;

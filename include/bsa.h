@@ -791,7 +791,8 @@ int bsa_cache_compact(const bsa_page_cache *c, int32_t *page_ref, int32_t *new_p
  * in 27 .. 245).  code * 2^e is a bf16 number exactly.
  * The _fp8 calls are their namesakes on such pools: bsa_cache_append_fp8
  * quantises the normed and rotated keys, and the values, from fp32 with that
- * one rounding (queries stay bf16); the page calls move codes and scales.
+ * one rounding (queries stay bf16; two tokens of one slot may leave the codes of
+ * one under the scale of the other); the page calls move codes and scales.
  */
 typedef struct {
     void *k, *v;             /* device bytes [layers, n_pages, Hkv, page], 16-byte aligned */
@@ -851,7 +852,8 @@ int bsa_cache_read(const bsa_read_args *a, const bsa_page_cache *c, const bsa_pa
  * Slots behind a sequence's new tokens, and pages of other sequences, may hold
  * anything, NaN included; pages that no new token sees need not be there (-1).
  * K and V must be finite in a sequence's slots up to its last new token, in the
- * pages that one of its new tokens sees.  A slot that a token should see and that
+ * pages that one of its new tokens sees, V at most 2^90 where a token sees it (its
+ * sums before they are divided by the weights' are fp32).  A slot that a token should see and that
  * lies in no page is reported (bit 32) and not seen.
  *   max_context  at least the slots of the longest sequence, its new tokens among them; 0:
  *                not known, the page table's width is taken.  It says how much work there may

@@ -98,16 +98,16 @@ def test_growing_maxima_and_falling_values(bsa, q8, B, Hkv, G, D, rise, fall):  
 
 @both
 def test_the_ends_of_the_scales(bsa, q8):  # noqa: F811
-    """Values from 2^90 down to 2^-110 under scores that rise as fast: every power of two in between is
+    """Values from 2^86 down to 2^-114 under scores that rise as fast: every power of two in between is
     the largest product met at some slot."""
     score = [118.0 * s / N for s in range(N)]
-    size = [90 - 200.0 * s / N for s in range(N)]
+    size = [86 - 200.0 * s / N for s in range(N)]
     c = steep_cache(128, 8, 19, q8, score, size, 1)
     check(bsa, c, queries(19, 32, 128, 1.0, 2), q8)
     # scores first, then values
     half = N // 2
     score = [-118.0 if s < half else 0.0 for s in range(N)]
-    size = [90.0 if s < half else -20.0 for s in range(N)]
+    size = [86.0 if s < half else -20.0 for s in range(N)]
     c = steep_cache(128, 8, 19, q8, score, size, 2)
     check(bsa, c, queries(19, 32, 128, 1.0, 3), q8)
 
