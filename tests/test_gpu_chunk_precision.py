@@ -116,3 +116,13 @@ def test_few_rows_with_and_without_pointers(bsa, D, page, G, count, q8):  # noqa
     assert all(c.short)
     run(bsa, c, 2)
     assert all(c.short) == (count * G <= 16)
+
+
+@both
+@pytest.mark.parametrize("count", [1024, 1025, 2100])
+def test_more_sequences_than_a_launch_takes(bsa, count, q8):  # noqa: F811
+    """Short sequences of several launches beside chunks, whose join is the last launch's."""
+    ctx, new = [(53 * b) % 270 for b in range(count)], [0 if b % 11 == 3 else 40 if b % 97 == 5 else 1 for b in range(count)]
+    c = Case(ctx, new, 8, 4, 64, 64, q8)
+    run(bsa, c, 4, width=2048)
+    assert any(c.short) and not all(c.short)
