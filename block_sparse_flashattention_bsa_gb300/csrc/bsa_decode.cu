@@ -543,7 +543,7 @@ __device__ void short_consumer(const ShortParams& p, const uint8_t* sT, const ui
                                 const int at = (int)(__float_as_uint(rv[nt][i]) >> 23) - 127, room = 120 - at;
                                 const int k = lv[nt][i] > 0.f
                                                   ? min(127 + 6 - (int)(__float_as_uint(lv[nt][i]) >> 23), room)
-                                                  : room;  // nothing is left of them: w is 0, or o
+                                                  : room;  // nothing was met yet, or nothing is left of it (w is 0)
                                 const float up = exp2_int(min(k, 126));
                                 w *= up;
                                 lv[nt][i] *= up;

@@ -853,8 +853,8 @@ int bsa_cache_read(const bsa_read_args *a, const bsa_page_cache *c, const bsa_pa
  * anything, NaN included; pages that no new token sees need not be there (-1).
  * K and V must be finite in a sequence's slots up to its last new token, in the
  * pages that one of its new tokens sees, V at most 2^90 where a token sees it (its
- * sums before they are divided by the weights' are fp32).  A slot that a token should see and that
- * lies in no page is reported (bit 32) and not seen.
+ * sums before they are divided by the weights' are fp32).  A slot that a token
+ * should see and that lies in no page is reported (bit 32) and not seen.
  *   max_context  at least the slots of the longest sequence, its new tokens among them; 0:
  *                not known, the page table's width is taken.  It says how much work there may
  *                be (which kernel works on short sequences, below) and nothing else: with a
@@ -870,8 +870,8 @@ int bsa_cache_read(const bsa_read_args *a, const bsa_page_cache *c, const bsa_pa
  *   the table, or if that is less ceil(window / 128) + 1 + ceil(sinks / 128).
  * So the last bits of a row may change with the batch that it is in, the table's width and
  * max_context; the order of its sums does too.  The same call gives the same bits.
- * Limits: Hq a multiple of Hkv, Hq / Hkv <= 128; window, sinks, max_context >= 0; Hkv * (max_pages *
- * page / 128) * (tokens * (Hq / Hkv) / 128 + B) below about 2^30.
+ * Limits: Hq a multiple of Hkv, Hq / Hkv <= 128; window, sinks, max_context >= 0;
+ * Hkv * (max_pages * page / 128) * (tokens * (Hq / Hkv) / 128 + B) below about 2^30.
  *   workspace    device, bsa_chunk_attention_workspace(...) bytes, 256-byte aligned.
  *                Calls that overlap on the GPU need workspaces of their own.
  */
